@@ -9,6 +9,13 @@ raises.
     bufs = [torch.randn(1 << 20, device="cuda") for _ in range(8)]
     plan = ar.Plan(8, 1 << 20, "float32", "sum", "ring")
     plan.execute(bufs)            # every buffer now holds the sum
+
+What follows the allreduce in a training step works on lists of tensors:
+
+    grads = ar.Grads([p.grad for p in params])
+    record = grads.norm(max_norm=1.0)        # [norm, scale, nonfinite, clipped], on the device
+    opt = ar.AdamW(params, [p.grad for p in params], exp_avg, exp_avg_sq)
+    opt.step(1, lr=3e-4, clip=record)        # reads the scale on the device: no pass of its own, no sync
 """
 
 import ctypes
@@ -22,6 +29,7 @@ ORDERS = {"faithful": 0, "fp32acc": 1}
 GROUPS = {"cyclic": 0, "xor": 1}
 PHASES = {"allreduce": 0, "reduce_scatter": 1, "all_gather": 2}
 JIT = {"auto": 0, "on": 1, "off": -1}
+NORMS = {"l2": 0, "max": 1}
 ESIZE = {"int32": 4, "float32": 4, "bfloat16": 2}
 KERNEL_STREAM, KERNEL_STAGED, KERNEL_ELEMENTWISE, KERNEL_DAG_JIT, KERNEL_WORD_JIT, KERNEL_CHAIN_WORD = 1, 2, 4, 8, 16, 32
 KERNEL_COPY, KERNEL_FEW = 64, 128
@@ -80,8 +88,22 @@ class CostModel(ctypes.Structure):
                 ("gamma_us_per_byte", ctypes.c_double), ("delta_us_per_message", ctypes.c_double)]
 
 
+class TensorsInfo(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int), ("elems", ctypes.c_uint64), ("n_items", ctypes.c_uint64),
+                ("item_elems", ctypes.c_uint64), ("table_bytes", ctypes.c_uint64), ("tiling_ok", ctypes.c_int)]
+
+    def as_dict(self):
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+class AdamWParams(ctypes.Structure):
+    _fields_ = [("step", ctypes.c_uint64), ("lr", ctypes.c_double), ("beta1", ctypes.c_double),
+                ("beta2", ctypes.c_double), ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
+
+
 _lib = None
 _VP = ctypes.c_void_p
+_U64P, _INTP, _VPP = ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_void_p)
 _EXPORTS = {
     "ar_schedule_create": (ctypes.c_int, [ctypes.c_int, ctypes.c_uint64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                           ctypes.POINTER(Params), ctypes.POINTER(_VP)]),
@@ -109,6 +131,17 @@ _EXPORTS = {
     "ar_cost_select": (ctypes.c_int, [ctypes.c_int, ctypes.c_uint64, ctypes.c_int, ctypes.c_int,
                                       ctypes.POINTER(CostModel), ctypes.POINTER(ctypes.c_int),
                                       ctypes.POINTER(Params), ctypes.POINTER(ctypes.c_double)]),
+    "ar_tensors_lowering": (ctypes.c_int, [ctypes.c_int, _U64P, _INTP, ctypes.POINTER(TensorsInfo)]),
+    "ar_grads_create": (ctypes.c_int, [ctypes.c_int, _U64P, _INTP, _VPP, _INTP, _VPP, _VPP]),
+    "ar_grads_query": (ctypes.c_int, [_VP, ctypes.POINTER(TensorsInfo)]),
+    "ar_grads_destroy": (ctypes.c_int, [_VP]),
+    "ar_grad_norm": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_double, ctypes.c_double, _VP, _VP, _VP]),
+    "ar_grad_clip": (ctypes.c_int, [_VP, ctypes.c_int, ctypes.c_double, ctypes.c_double, _VP, _VP, _VP]),
+    "ar_adamw_create": (ctypes.c_int, [ctypes.c_int, _U64P, _INTP, _VPP, _INTP, _VPP, _VPP, _VPP, _VPP,
+                                       ctypes.POINTER(ctypes.c_float), _VPP]),
+    "ar_adamw_query": (ctypes.c_int, [_VP, ctypes.POINTER(TensorsInfo)]),
+    "ar_adamw_destroy": (ctypes.c_int, [_VP]),
+    "ar_adamw_step": (ctypes.c_int, [_VP, ctypes.POINTER(AdamWParams), _VP, _VP]),
 }
 
 
@@ -264,6 +297,169 @@ class Plan:
     def close(self):
         if getattr(self, "_h", None):
             lib().ar_plan_destroy(self._h)
+            self._h = None
+
+    __del__ = close
+
+
+# ------------------------------------------- after the allreduce: many tensors
+
+def _layout(t):
+    """The strides a dense tensor's elements lie at in memory, None for a
+    tensor with gaps, repeated elements or another order than dense."""
+    if t.is_contiguous():
+        return "contiguous"
+    want = 1
+    for size, stride in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n != 1), key=lambda x: x[1]):
+        if stride != want:
+            return None
+        want *= size
+    return tuple(t.stride())
+
+
+def _tensor_list(tensors, what, like=None, dtypes=("float32", "bfloat16")):
+    """Checked tensors as a list, with their element types; `like` tensors fix
+    every size and memory order."""
+    tensors = list(tensors)
+    if like is not None and len(tensors) != len(like):
+        raise ValueError(f"{what}: expected {len(like)} tensors, got {len(tensors)}")
+    types = []
+    for i, t in enumerate(tensors):
+        name = str(t.dtype).replace("torch.", "")
+        if name not in dtypes:
+            raise ValueError(f"{what}[{i}]: element type {name}, expected {' or '.join(dtypes)}")
+        if not t.is_cuda:
+            raise ValueError(f"{what}[{i}]: not a CUDA tensor")
+        layout = _layout(t)
+        if layout is None:
+            raise ValueError(f"{what}[{i}]: not dense (strides {t.stride()} of shape {tuple(t.shape)})")
+        if like is not None:
+            if t.numel() != like[i].numel():
+                raise ValueError(f"{what}[{i}]: expected {like[i].numel()} elements, got {t.numel()}")
+            if layout != _layout(like[i]) or (layout != "contiguous" and t.shape != like[i].shape):
+                raise ValueError(f"{what}[{i}]: its elements lie in another order in memory")
+        types.append(name)
+    return tensors, types
+
+
+def _counts(tensors):
+    return (ctypes.c_uint64 * len(tensors))(*[t.numel() for t in tensors])
+
+
+def _dtype_array(types):
+    return (ctypes.c_int * len(types))(*[DTYPES[t] for t in types])
+
+
+def _float_out(t, n, what):
+    """The device address of n float32 a call reads or writes."""
+    if str(t.dtype) != "torch.float32" or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: expected a contiguous float32 CUDA tensor of at least {n} elements")
+    return _VP(t.data_ptr())
+
+
+def tensors_lowering(counts, dtypes):
+    """Host only: the ranges a Grads handle over tensors of these sizes and
+    element types would work through (ar_tensors_lowering)."""
+    info = TensorsInfo()
+    n = len(counts)
+    _check(lib().ar_tensors_lowering(n, (ctypes.c_uint64 * n)(*counts), _dtype_array(dtypes), ctypes.byref(info)),
+           "ar_tensors_lowering")
+    return info.as_dict()
+
+
+class Grads:
+    """Gradient tensors bound for norms and clipping (float32 or bfloat16,
+    each its own; dense).  `out`: the tensors that clip() writes, of the same
+    sizes (None: in place).  The handle keeps references to all of them.
+
+    Both calls return the record, four floats on the device: norm, scale,
+    nonfinite, clipped.  Without `result` that is `self.record`, which the
+    next call overwrites."""
+
+    def __init__(self, grads, out=None):
+        import torch
+        self.grads, types = _tensor_list(grads, "grads")
+        self.out, out_types = (None, None) if out is None else _tensor_list(out, "out", like=self.grads)
+        self.record = torch.zeros(4, dtype=torch.float32, device="cuda")
+        h = _VP()
+        _check(lib().ar_grads_create(len(self.grads), _counts(self.grads), _dtype_array(types), _ptrs(self.grads),
+                                     None if out is None else _dtype_array(out_types),
+                                     None if out is None else _ptrs(self.out), ctypes.byref(h)), "ar_grads_create")
+        self._h = h
+
+    def info(self):
+        i = TensorsInfo()
+        _check(lib().ar_grads_query(self._h, ctypes.byref(i)), "ar_grads_query")
+        return i.as_dict()
+
+    def _run(self, call, where, max_norm, kind, pre_scale, result, per_tensor, stream):
+        result = self.record if result is None else result
+        norms = None if per_tensor is None else _float_out(per_tensor, len(self.grads), "per_tensor")
+        _check(call(self._h, NORMS[kind], pre_scale, max_norm, _float_out(result, 4, "result"), norms,
+                    _VP(_stream_handle(stream))), where)
+        return result
+
+    def norm(self, max_norm=float("inf"), kind="l2", pre_scale=1.0, result=None, per_tensor=None, stream=None):
+        """Enqueue the global norm of pre_scale times the gradients ("l2" or
+        "max"); `per_tensor` (float32, one per tensor) takes each tensor's."""
+        return self._run(lib().ar_grad_norm, "ar_grad_norm", max_norm, kind, pre_scale, result, per_tensor, stream)
+
+    def clip(self, max_norm, kind="l2", pre_scale=1.0, result=None, per_tensor=None, stream=None):
+        """Enqueue the norm, then every gradient times the record's scale, into
+        `out` or in place."""
+        return self._run(lib().ar_grad_clip, "ar_grad_clip", max_norm, kind, pre_scale, result, per_tensor, stream)
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().ar_grads_destroy(self._h)
+            self._h = None
+
+    __del__ = close
+
+
+class AdamW:
+    """Parameters (float32 or bfloat16) bound with their gradients, float32
+    moments and, for float32 parameters, optional bfloat16 copies for the
+    forward pass.  `decay`: one factor of the weight decay per tensor (None:
+    1).  The handle keeps references to all tensors."""
+
+    def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, decay=None):
+        self.params, ptypes = _tensor_list(params, "params")
+        self.grads, gtypes = _tensor_list(grads, "grads", like=self.params)
+        self.exp_avg, _ = _tensor_list(exp_avg, "exp_avg", like=self.params, dtypes=("float32",))
+        self.exp_avg_sq, _ = _tensor_list(exp_avg_sq, "exp_avg_sq", like=self.params, dtypes=("float32",))
+        self.copies = None
+        if copies is not None:
+            self.copies, _ = _tensor_list(copies, "copies", like=self.params, dtypes=("bfloat16",))
+        if decay is not None and len(decay) != len(self.params):
+            raise ValueError(f"decay: expected {len(self.params)} factors, got {len(decay)}")
+        n = len(self.params)
+        h = _VP()
+        _check(lib().ar_adamw_create(n, _counts(self.params), _dtype_array(ptypes), _ptrs(self.params),
+                                     _dtype_array(gtypes), _ptrs(self.grads), _ptrs(self.exp_avg),
+                                     _ptrs(self.exp_avg_sq), None if copies is None else _ptrs(self.copies),
+                                     None if decay is None else (ctypes.c_float * n)(*decay), ctypes.byref(h)),
+               "ar_adamw_create")
+        self._h = h
+
+    def info(self):
+        i = TensorsInfo()
+        _check(lib().ar_adamw_query(self._h, ctypes.byref(i)), "ar_adamw_query")
+        return i.as_dict()
+
+    def step(self, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, clip=None, stream=None):
+        """Enqueue update number `step` (from 1).  `clip`: the record of a norm
+        of these gradients; its scale multiplies them, and if it says
+        nonfinite nothing changes."""
+        if step < 1:
+            raise ValueError("step counts from 1")
+        p = AdamWParams(int(step), lr, beta1, beta2, eps, weight_decay)
+        record = None if clip is None else _float_out(clip, 4, "clip")
+        _check(lib().ar_adamw_step(self._h, ctypes.byref(p), record, _VP(_stream_handle(stream))), "ar_adamw_step")
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().ar_adamw_destroy(self._h)
             self._h = None
 
     __del__ = close

@@ -83,4 +83,23 @@ ar_status check_rank_buffers(int P, uint64_t n, int es, int device, void* const*
     return AR_OK;
 }
 
+ar_status check_spans(const std::vector<Span>& spans, int device) {
+    std::vector<std::pair<uintptr_t, uintptr_t>> at;
+    at.reserve(spans.size());
+    for (const Span& s : spans) {
+        if (s.bytes == 0) continue;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(s.p);
+        if (!a || a % s.es || a + s.bytes < a) return AR_ERR_INVALID_ARG;
+        at.emplace_back(a, a + s.bytes);
+    }
+    std::sort(at.begin(), at.end());
+    for (size_t i = 0; i + 1 < at.size(); ++i)
+        if (at[i].second > at[i + 1].first) return AR_ERR_INVALID_ARG;
+    for (const Span& s : spans)
+        if (s.bytes != 0 && !resident(s.p, s.bytes, device)) return AR_ERR_INVALID_ARG;
+    return AR_OK;
+}
+
+bool device_resident(const void* p, uint64_t bytes, int device) { return resident(p, bytes, device); }
+
 }  // namespace ar

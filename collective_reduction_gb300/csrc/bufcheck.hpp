@@ -5,6 +5,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <cstdint>
+#include <vector>
 
 #include "ar.h"
 
@@ -28,5 +29,20 @@ struct TraceRange {
 // every pointer is 16-byte aligned.  AR_ERR_INVALID_ARG on any failure.
 ar_status check_rank_buffers(int P, uint64_t n, int es, int device, void* const* bufs, bool residency,
                              bool* aligned16);
+
+// A buffer of `bytes` bytes of es-byte elements.
+struct Span {
+    const void* p;
+    uint64_t bytes;
+    int es;
+};
+
+// The same checks for buffers of unlike sizes: each non-null, aligned to its
+// element size, resident on `device` with its bytes inside its allocation,
+// and all pairwise disjoint.  A span of no bytes is not looked at.
+ar_status check_spans(const std::vector<Span>& spans, int device);
+
+// Device (or managed) memory of `device` that holds `bytes` bytes from p on.
+bool device_resident(const void* p, uint64_t bytes, int device);
 
 }  // namespace ar

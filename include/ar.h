@@ -370,6 +370,111 @@ ar_status ar_selftest_bounded_wait(uint32_t timeout_ms, void* stream);
  * synchronisation fails. */
 ar_status ar_plan_check(ar_plan_t plan);
 
+/* ---- after the allreduce: gradient norm, clipping, AdamW ------------------
+ * What a data-parallel step does with the gradients that an allreduce (or a
+ * reduce-scatter, for the owned chunks alone) has left on the device, before
+ * the parameters are used or gathered again ("All-Reduce, in depth", The
+ * APIs: DDP's gradient buckets; FSDP / ZeRO, which reduce-scatter gradients
+ * and all-gather parameters).  The pages stop at the collective; these calls
+ * have no counterpart on them.
+ *
+ * A handle binds N tensors: it checks their pointers once and uploads the
+ * ranges its kernels work through; the caller keeps the tensors where they
+ * are while the handle lives.  Element types are AR_FLOAT32 and AR_BFLOAT16,
+ * each tensor its own.  Pointers need only element alignment; tensors whose
+ * streams share one alignment take the vector path whatever it is.  A count
+ * of 0 is an empty tensor (its pointer is not looked at); N = 0 is valid.
+ * Calls launch kernels only (capturable in a CUDA graph once the handle
+ * exists), never synchronise and keep nothing between calls.  Calls on one
+ * handle must be ordered on one stream: they share the handle's workspace.
+ * The handle's device must be current (AR_ERR_INVALID_ARG otherwise).
+ * Repeated calls on equal inputs give equal bits. */
+typedef enum { AR_NORM_L2 = 0, AR_NORM_MAX = 1 } ar_norm_kind;
+
+typedef struct ar_grads_s* ar_grads_t;
+typedef struct ar_adamw_s* ar_adamw_t;
+
+typedef struct {
+    int n_tensors;
+    uint64_t elems;        /* over all tensors                                  */
+    uint64_t n_items;      /* ranges the kernels work through, one warp each    */
+    uint64_t item_elems;   /* elements of every range but a tensor's last       */
+    uint64_t table_bytes;  /* device memory the handle owns (0 without one)     */
+    int tiling_ok;         /* ar_tensors_lowering: the ranges tile every tensor */
+} ar_tensors_info;
+
+/* Host only: the ranges a gradient handle over these sizes would have, checked
+ * against the sizes by code apart from the one that makes them.  Errors as
+ * ar_grads_create. */
+ar_status ar_tensors_lowering(int n_tensors, const uint64_t* counts, const ar_dtype* dtypes, ar_tensors_info* out);
+
+/* Binds N gradient tensors, and the N tensors that ar_grad_clip writes: outs
+ * NULL (out_dtypes is then not looked at) scales in place; otherwise outs[t]
+ * takes tensor t scaled, in out_dtypes[t]; it may be grads[t] itself (same
+ * type).  AR_ERR_INVALID_ARG: null arrays or pointers, unknown types, N < 0,
+ * pointers off their element's alignment, memory that is not the current
+ * device's or ends before the tensor does, tensors that overlap.
+ * AR_ERR_UNSUPPORTED: AR_INT32, more than 2^20 tensors or 2^40 elements.
+ * AR_ERR_NOMEM, AR_ERR_CUDA. */
+ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype* grad_dtypes, void* const* grads,
+                          const ar_dtype* out_dtypes, void* const* outs, ar_grads_t* out);
+ar_status ar_grads_query(ar_grads_t h, ar_tensors_info* info);
+/* Frees the handle, not the tensors.  Synchronises the device first. */
+ar_status ar_grads_destroy(ar_grads_t h);
+
+/* The norm of all N tensors as one vector g, times the pre-scale c (one over
+ * the loss scale or the rank count; a float32-normal positive number):
+ *   AR_NORM_L2   c sqrt(sum g^2)        AR_NORM_MAX   c max |g|
+ * written to result, 4 floats of device memory:
+ *   [0] norm
+ *   [1] scale      c max_norm / norm if clipped, else c
+ *   [2] nonfinite  1 if any element is an infinity or NaN, else 0
+ *   [3] clipped    1 if norm > max_norm and nothing is nonfinite, else 0
+ * max_norm >= 0 (INFINITY: never clipped).  With a nonfinite element the norm
+ * is that infinity or NaN and nothing is clipped.  Squares are added so that
+ * no finite gradient overflows or underflows its sum (the norm itself rounds
+ * to float32).  tensor_norms: NULL, or N floats of device memory that take
+ * each tensor's norm times c.  No element: norm 0. */
+ar_status ar_grad_norm(ar_grads_t h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
+                       float* tensor_norms, void* stream);
+/* ar_grad_norm, then every element times result[1], rounded to nearest even
+ * in its output's type: global-norm clipping.  With a nonfinite element the
+ * factor is c: infinities and NaN stay where they are for whoever looks for
+ * them.  In place a factor of exactly 1 writes nothing. */
+ar_status ar_grad_clip(ar_grads_t h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
+                       float* tensor_norms, void* stream);
+
+/* Binds N parameters with their gradients, first and second moments and, for
+ * float32 parameters, bf16 copies that the forward pass reads (copies NULL:
+ * none).  decay: N host floats >= 0 that multiply the weight decay of each
+ * tensor (NULL: all 1; usually 0 for vectors).  All tensors are disjoint.
+ * Errors as ar_grads_create; copies of bf16 parameters: AR_ERR_INVALID_ARG. */
+ar_status ar_adamw_create(int n_tensors, const uint64_t* counts, const ar_dtype* param_dtypes, void* const* params,
+                          const ar_dtype* grad_dtypes, void* const* grads, float* const* exp_avg,
+                          float* const* exp_avg_sq, void* const* copies, const float* decay, ar_adamw_t* out);
+ar_status ar_adamw_query(ar_adamw_t h, ar_tensors_info* info);
+ar_status ar_adamw_destroy(ar_adamw_t h);
+
+typedef struct {
+    uint64_t step;        /* t, from 1: the number of this update          */
+    double lr;            /* >= 0                                          */
+    double beta1, beta2;  /* 0 <= beta < 1                                 */
+    double eps;           /* > 0 (a float32-normal number)                 */
+    double weight_decay;  /* >= 0                                          */
+} ar_adamw_params;
+
+/* One AdamW update, computed in float32 (decoupled weight decay; moments are
+ * float32, bf16 parameters round to nearest even once):
+ *   g = s grad,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+ * s = 1 with result NULL.  Otherwise result is the record of an earlier
+ * ar_grad_norm (device memory, read when the kernel runs): s = result[1],
+ * and when result[2] says that the gradients hold an infinity or NaN the
+ * call leaves every tensor as it is (its step number may be used again).
+ * After ar_grad_clip the gradients are scaled already: pass NULL, or the
+ * record would scale them twice. */
+ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* params, const float* result, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* ar_status_string(ar_status s);
 
