@@ -195,7 +195,8 @@ def _ptrs(bufs):
 def _stream_handle(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: making a Stream object of it costs 3 us, more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream
     return int(stream)
@@ -352,7 +353,8 @@ def _dtype_array(types):
 
 def _float_out(t, n, what):
     """The device address of n float32 a call reads or writes."""
-    if str(t.dtype) != "torch.float32" or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+    import torch
+    if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{what}: expected a contiguous float32 CUDA tensor of at least {n} elements")
     return _VP(t.data_ptr())
 
@@ -381,6 +383,7 @@ class Grads:
         self.grads, types = _tensor_list(grads, "grads")
         self.out, out_types = (None, None) if out is None else _tensor_list(out, "out", like=self.grads)
         self.record = torch.zeros(4, dtype=torch.float32, device="cuda")
+        self._record = _VP(self.record.data_ptr())
         h = _VP()
         _check(lib().ar_grads_create(len(self.grads), _counts(self.grads), _dtype_array(types), _ptrs(self.grads),
                                      None if out is None else _dtype_array(out_types),
@@ -393,11 +396,10 @@ class Grads:
         return i.as_dict()
 
     def _run(self, call, where, max_norm, kind, pre_scale, result, per_tensor, stream):
-        result = self.record if result is None else result
+        to = self._record if result is None else _float_out(result, 4, "result")
         norms = None if per_tensor is None else _float_out(per_tensor, len(self.grads), "per_tensor")
-        _check(call(self._h, NORMS[kind], pre_scale, max_norm, _float_out(result, 4, "result"), norms,
-                    _VP(_stream_handle(stream))), where)
-        return result
+        _check(call(self._h, NORMS[kind], pre_scale, max_norm, to, norms, _stream_handle(stream)), where)
+        return self.record if result is None else result
 
     def norm(self, max_norm=float("inf"), kind="l2", pre_scale=1.0, result=None, per_tensor=None, stream=None):
         """Enqueue the global norm of pre_scale times the gradients ("l2" or
@@ -455,7 +457,7 @@ class AdamW:
             raise ValueError("step counts from 1")
         p = AdamWParams(int(step), lr, beta1, beta2, eps, weight_decay)
         record = None if clip is None else _float_out(clip, 4, "clip")
-        _check(lib().ar_adamw_step(self._h, ctypes.byref(p), record, _VP(_stream_handle(stream))), "ar_adamw_step")
+        _check(lib().ar_adamw_step(self._h, ctypes.byref(p), record, _stream_handle(stream)), "ar_adamw_step")
 
     def close(self):
         if getattr(self, "_h", None):

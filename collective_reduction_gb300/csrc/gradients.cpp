@@ -6,34 +6,43 @@
 #include <cmath>
 #include <cstring>
 #include <new>
-#include <stdexcept>
+#include <vector>
 
 #include "bufcheck.hpp"
-
-namespace ar {
-
-void split_tensors(int n, const uint64_t* counts, uint64_t item_elems, std::vector<TensorRange>& ranges,
-                   std::vector<uint32_t>& first) {
-    ranges.clear();
-    first.assign(1, 0);
-    for (int t = 0; t < n; ++t) {
-        for (uint64_t at = 0; at < counts[t]; at += item_elems) {
-            const uint64_t left = counts[t] - at;
-            ranges.push_back({static_cast<uint32_t>(t), static_cast<uint32_t>(left < item_elems ? left : item_elems), at});
-        }
-        if (ranges.size() > 0x7FFFFFFFu) throw std::length_error("too many ranges");
-        first.push_back(static_cast<uint32_t>(ranges.size()));
-    }
-}
-
-}  // namespace ar
 
 namespace {
 
 constexpr int kMaxTensors = 1 << 20;
 constexpr uint64_t kMaxElems = uint64_t(1) << 40;
-constexpr uint64_t kGradItemElems = 4096;
-constexpr uint64_t kAdamItemElems = 1024;
+
+// One wave of warps on GB300's 152 SMs: the norm kernel runs 3 CTAs of 8 warps
+// on each, the AdamW kernel 4.  A set that gives every warp of a wave at most
+// one full range is split to fill one wave; beyond that the ranges stay at
+// their full size and CTAs follow one another.  Measured: a norm of 25 MB
+// takes 10.0 us split this way and 15.4 in ranges of 1024 elements; one of
+// 4.3 GB 597 us in ranges of 16384 elements, 796 of 4096; AdamW on 0.4M
+// elements 4.0 us, 8.4 in ranges of 1024.
+constexpr uint64_t kNormWave = 152 * 3 * ar::kGradWarps, kAdamWave = 152 * 4 * ar::kGradWarps;
+constexpr uint32_t kGradItemMax = 16384, kAdamItemStep = 256, kAdamItemMax = 1024;
+
+uint32_t item_elems(int n, const uint64_t* counts, uint64_t wave, uint32_t step, uint32_t most) {
+    uint64_t total = 0;
+    for (int t = 0; t < n; ++t) total += counts[t];
+    const uint64_t e = (total / wave / step + 1) * step;
+    return e < most ? static_cast<uint32_t>(e) : most;
+}
+uint32_t grad_item_elems(int n, const uint64_t* counts) {
+    return item_elems(n, counts, kNormWave, ar::kSmallItemElems, kGradItemMax);
+}
+uint32_t adam_item_elems(int n, const uint64_t* counts) {
+    return item_elems(n, counts, kAdamWave, kAdamItemStep, kAdamItemMax);
+}
+
+// Gradient bytes at the end of a set that the norm before a scaling asks L2 to
+// keep (of 129 MB, which also hold the scaled results on their way out).
+// Measured on 96 MB of gradients: 51.6 us with none, 46.7 with 48 or 64 MB,
+// 48.0 with 100; on 2.7 GB 1162 us and 1159.
+constexpr uint64_t kKeepBytes = 64ull << 20;
 
 ar_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
@@ -65,34 +74,63 @@ void fill_info(int n, const uint64_t* counts, uint64_t item_elems, size_t items,
     info->item_elems = item_elems;
 }
 
-struct DeviceBlob {
-    std::vector<char> host;
+// Device memory in parts, each on a 256-byte boundary.
+struct DeviceMemory {
     char* dev = nullptr;
-    size_t reserve(size_t bytes) {  // zeroed bytes on a 256-byte boundary; returns their offset
-        const size_t off = (host.size() + 255) / 256 * 256;
-        host.resize(off + bytes);
-        return off;
+    size_t bytes = 0;
+    size_t part(size_t n) {  // its offset
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
     }
+    cudaError_t allocate() { return cudaMalloc(&dev, bytes); }
     template <class T>
-    size_t put(const std::vector<T>& v) {
-        const size_t off = reserve(v.size() * sizeof(T));
-        if (!v.empty()) std::memcpy(host.data() + off, v.data(), v.size() * sizeof(T));
-        return off;
+    T* at(size_t offset) const {
+        return reinterpret_cast<T*>(dev + offset);
     }
-    cudaError_t upload() {
-        if (host.empty()) host.resize(256);
-        cudaError_t e = cudaMalloc(&dev, host.size());
-        if (e == cudaSuccess) e = cudaMemcpy(dev, host.data(), host.size(), cudaMemcpyHostToDevice);
-        return e;
-    }
-    template <class T>
-    T* at(size_t off) const {
-        return reinterpret_cast<T*>(dev + off);
-    }
-    ~DeviceBlob() {
+    ~DeviceMemory() {
         if (dev) cudaFree(dev);
     }
 };
+
+// The tensors' first items from their splits; their number, or 0 with *ok
+// false when there are more than the kernels index.
+template <class Tensor>
+uint32_t first_items(const std::vector<Tensor>& tensors, std::vector<uint32_t>& first, bool* ok) {
+    uint64_t n = 0;
+    first.assign(1, 0);
+    for (const Tensor& t : tensors) {
+        n += t.split.ranges();
+        if (n > 0x7FFFFFFFu) {
+            *ok = false;
+            return 0;
+        }
+        first.push_back(static_cast<uint32_t>(n));
+    }
+    *ok = true;
+    return static_cast<uint32_t>(n);
+}
+
+// Uploads the tensors and has the device write their items.
+template <class Tensor, class Item>
+cudaError_t upload_items(const std::vector<Tensor>& tensors, const std::vector<uint32_t>& first, uint32_t* d_first,
+                         Item* d_items) {
+    const uint32_t n_items = first.back();
+    cudaError_t e = cudaMemcpy(d_first, first.data(), first.size() * sizeof(uint32_t), cudaMemcpyHostToDevice);
+    if (e != cudaSuccess || n_items == 0) return e;
+    Tensor* d_tensors = nullptr;
+    e = cudaMalloc(&d_tensors, tensors.size() * sizeof(Tensor));
+    if (e == cudaSuccess)
+        e = cudaMemcpy(d_tensors, tensors.data(), tensors.size() * sizeof(Tensor), cudaMemcpyHostToDevice);
+    if (e == cudaSuccess)
+        e = ar::launch_items(d_tensors, d_first, static_cast<int>(tensors.size()), n_items, d_items, nullptr);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    cudaFree(d_tensors);
+    return e;
+}
+
+// A positive number that float32 holds without losing digits.
+bool float_normal(double x) { return x >= 1.17549436e-38 && x <= 3.4028234e38; }
 
 bool on_device(int device) {
     int now = -1;
@@ -107,46 +145,62 @@ bool float_buffer(const float* p, uint64_t n, int device) {
 }  // namespace
 
 struct ar_grads_s {
-    int n = 0, device = 0, num_sms = 0, grid = 0;
+    int n = 0, device = 0;
     ar_tensors_info info = {};
-    uint32_t n_items = 0;
-    DeviceBlob tables;     // items, first ranges, then the workspace below
+    uint32_t n_items = 0, keep_from = 0;
+    DeviceMemory memory;
     const ar::GradItem* items = nullptr;
     const uint32_t* first = nullptr;
     uint64_t* cta_partials = nullptr;
-    uint32_t* counter = nullptr;
+    uint64_t* group_partials = nullptr;
     uint64_t* item_partials = nullptr;
+    uint32_t* counters = nullptr;
 };
 
 struct ar_adamw_s {
     int device = 0;
     ar_tensors_info info = {};
     uint32_t n_items = 0;
-    DeviceBlob tables;
+    bool whole = true;
+    DeviceMemory memory;
     const ar::AdamItem* items = nullptr;
 };
 
 namespace {
 
+// The norm, and with `clip` the scaling by its record.
 ar_status run_norm(ar_grads_s* h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
-                   float* tensor_norms, cudaStream_t st) {
+                   float* tensor_norms, bool clip, cudaStream_t st) {
     if (!h || (kind != AR_NORM_L2 && kind != AR_NORM_MAX)) return AR_ERR_INVALID_ARG;
-    // a factor below float32's smallest normal would lose its digits
-    if (!(pre_scale >= 1.17549436e-38 && pre_scale <= 3.4028234e38) || !(max_norm >= 0.0)) return AR_ERR_INVALID_ARG;
+    if (!float_normal(pre_scale) || !(max_norm >= 0.0)) return AR_ERR_INVALID_ARG;
     if (!on_device(h->device) || !float_buffer(result, 4, h->device)) return AR_ERR_INVALID_ARG;
-    if (tensor_norms && h->n > 0 && !float_buffer(tensor_norms, h->n, h->device)) return AR_ERR_INVALID_ARG;
+    const bool norms = tensor_norms && h->n > 0;
+    if (norms && !float_buffer(tensor_norms, h->n, h->device)) return AR_ERR_INVALID_ARG;
     ar::NormArgs a = {};
     a.items = h->items;
     a.n_items = h->n_items;
+    a.keep_from = h->keep_from;
     a.kind = kind;
     a.cta_partials = h->cta_partials;
-    a.item_partials = tensor_norms ? h->item_partials : nullptr;
-    a.counter = h->counter;
+    a.group_partials = h->group_partials;
+    a.item_partials = norms ? h->item_partials : nullptr;
+    a.counters = h->counters;
     a.pre_scale = pre_scale;
     a.max_norm = max_norm;
     a.result = result;
-    cudaError_t e = ar::launch_norm(a, h->grid, st);
-    if (e == cudaSuccess && tensor_norms && h->n > 0) {
+    // one cluster holds the whole set (in the smallest ranges: a set in larger
+    // ones has enough elements for half a wave of them)
+    static_assert(kNormWave / 2 > ar::kSmallItems, "a set of kSmallItems ranges has the smallest ranges");
+    const bool small = h->n_items <= ar::kSmallItems;
+    cudaError_t e = small ? ar::launch_small(a, clip, st) : ar::launch_norm(a, clip, st);
+    if (e == cudaSuccess && clip && !small) {
+        ar::ScaleArgs b = {};
+        b.items = h->items;
+        b.n_items = h->n_items;
+        b.result = result;
+        e = ar::launch_scale(b, st);
+    }
+    if (e == cudaSuccess && norms) {
         ar::TensorNormArgs b = {};
         b.item_partials = h->item_partials;
         b.first = h->first;
@@ -167,28 +221,28 @@ ar_status ar_tensors_lowering(int n_tensors, const uint64_t* counts, const ar_dt
     std::memset(out, 0, sizeof(*out));
     const ar_status s = check_layout(n_tensors, counts, dtypes);
     if (s != AR_OK) return s;
-    try {
-        std::vector<ar::TensorRange> R;
-        std::vector<uint32_t> first;
-        ar::split_tensors(n_tensors, counts, kGradItemElems, R, first);
-        fill_info(n_tensors, counts, kGradItemElems, R.size(), out);
-        // the ranges against the sizes, apart from the loop that made them
-        std::vector<uint64_t> next(n_tensors, 0);
-        bool ok = first.size() == static_cast<size_t>(n_tensors) + 1 && first.back() == R.size();
-        for (size_t i = 0; i < R.size() && ok; ++i) {
-            const ar::TensorRange& r = R[i];
-            ok = r.tensor < static_cast<uint32_t>(n_tensors) && r.count > 0 && r.count <= kGradItemElems &&
-                 r.elem == next[r.tensor] && i >= first[r.tensor] && i < first[r.tensor + 1] && r.elem % 8 == 0;
-            if (ok) next[r.tensor] += r.count;
+    // every tensor's ranges against its size, for a tensor on a range boundary
+    // and for one off it
+    const uint32_t e = grad_item_elems(n_tensors, counts);
+    bool ok = true;
+    uint64_t items = 0;
+    for (int t = 0; t < n_tensors; ++t) {
+        const uint32_t off = 1 + static_cast<uint32_t>(t) % (ar::kRangeAlign / esize(dtypes[t]) - 1);
+        for (const uint32_t lead : {0u, off}) {
+            const ar::RangeSplit s{counts[t], e, lead};
+            uint64_t next = 0;
+            for (uint64_t k = 0; k < s.ranges(); ++k) {
+                const uint64_t lo = s.begin(k), hi = s.end(k);
+                ok = ok && lo == next && hi > lo && hi - lo <= e && (lo == 0 || (lo + lead) % e == 0);
+                next = hi;
+            }
+            ok = ok && next == counts[t];
+            if (lead == 0) items += s.ranges();
         }
-        for (int t = 0; t < n_tensors && ok; ++t) ok = next[t] == counts[t];
-        out->tiling_ok = ok ? 1 : 0;
-        return AR_OK;
-    } catch (const std::length_error&) {
-        return AR_ERR_UNSUPPORTED;
-    } catch (const std::bad_alloc&) {
-        return AR_ERR_NOMEM;
     }
+    fill_info(n_tensors, counts, e, items, out);
+    out->tiling_ok = ok ? 1 : 0;
+    return AR_OK;
 }
 
 ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype* grad_dtypes, void* const* grads,
@@ -204,7 +258,6 @@ ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype*
     try {
         h = new ar_grads_s();
         cudaError_t e = cudaGetDevice(&h->device);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
         if (e != cudaSuccess) {
             delete h;
             return cuda_status(e);
@@ -221,47 +274,65 @@ ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype*
             delete h;
             return s;
         }
-        std::vector<ar::TensorRange> R;
-        std::vector<uint32_t> first;
-        ar::split_tensors(n_tensors, counts, kGradItemElems, R, first);
-        std::vector<ar::GradItem> items;
-        items.reserve(R.size());
-        for (const ar::TensorRange& r : R) {
-            const ar_dtype gt = grad_dtypes[r.tensor], ot = outs ? out_dtypes[r.tensor] : gt;
-            void* dst = outs ? outs[r.tensor] : grads[r.tensor];
-            ar::GradItem it = {};
-            it.src = static_cast<const char*>(grads[r.tensor]) + r.elem * esize(gt);
-            it.dst = static_cast<char*>(dst) + r.elem * esize(ot);
-            it.count = r.count;
-            it.flags = (gt == AR_BFLOAT16 ? ar::kGradBf16 : 0) | (ot == AR_BFLOAT16 ? ar::kOutBf16 : 0) |
-                       (dst == grads[r.tensor] ? ar::kInPlace : 0);
-            items.push_back(it);
+        const uint32_t elems = grad_item_elems(n_tensors, counts);
+        std::vector<ar::GradTensor> tensors;
+        for (int t = 0; t < n_tensors; ++t) {
+            const ar_dtype gt = grad_dtypes[t], ot = outs ? out_dtypes[t] : gt;
+            void* dst = outs ? outs[t] : grads[t];
+            const uint32_t flags = (gt == AR_BFLOAT16 ? ar::kGradBf16 : 0) | (ot == AR_BFLOAT16 ? ar::kOutBf16 : 0) |
+                                   (dst == grads[t] ? ar::kInPlace : 0);
+            tensors.push_back({static_cast<const char*>(grads[t]), static_cast<char*>(dst),
+                               {counts[t], elems, ar::lead_elems(grads[t], esize(gt))}, flags});
         }
+        std::vector<uint32_t> first;
+        bool fits = false;
         h->n = n_tensors;
-        h->n_items = static_cast<uint32_t>(items.size());
-        h->grid = ar::norm_grid(h->n_items, h->num_sms);
-        fill_info(n_tensors, counts, kGradItemElems, items.size(), &h->info);
-        h->info.tiling_ok = 1;
-        const size_t o_items = h->tables.put(items), o_first = h->tables.put(first);
-        const size_t o_cta = h->tables.reserve(sizeof(uint64_t) * h->grid), o_counter = h->tables.reserve(256);
-        const size_t o_parts = h->tables.reserve(sizeof(uint64_t) * items.size());
-        e = h->tables.upload();
+        h->n_items = first_items(tensors, first, &fits);
+        if (!fits) {
+            delete h;
+            return AR_ERR_UNSUPPORTED;
+        }
+        // the items that make up the last kKeepBytes
+        h->keep_from = h->n_items;
+        uint64_t room = kKeepBytes;
+        for (int t = n_tensors - 1; t >= 0; --t) {
+            const uint64_t bytes = counts[t] * esize(grad_dtypes[t]);
+            if (bytes > room) {
+                const uint64_t part = room / (elems * esize(grad_dtypes[t])), all = tensors[t].split.ranges();
+                h->keep_from -= static_cast<uint32_t>(part < all ? part : all);
+                break;
+            }
+            h->keep_from = first[t];
+            room -= bytes;
+        }
+        const uint32_t groups = ar::norm_groups(h->n_items);
+        const size_t o_items = h->memory.part(sizeof(ar::GradItem) * h->n_items);
+        const size_t o_first = h->memory.part(sizeof(uint32_t) * first.size());
+        const size_t o_cta = h->memory.part(sizeof(uint64_t) * ar::grad_ctas(h->n_items));
+        const size_t o_group = h->memory.part(sizeof(uint64_t) * groups);
+        const size_t o_parts = h->memory.part(sizeof(uint64_t) * h->n_items);
+        const size_t o_counters = h->memory.part(sizeof(uint32_t) * (groups + 1));
+        e = h->memory.allocate();
+        if (e == cudaSuccess) {
+            h->items = h->memory.at<ar::GradItem>(o_items);
+            h->first = h->memory.at<uint32_t>(o_first);
+            h->cta_partials = h->memory.at<uint64_t>(o_cta);
+            h->group_partials = h->memory.at<uint64_t>(o_group);
+            h->item_partials = h->memory.at<uint64_t>(o_parts);
+            h->counters = h->memory.at<uint32_t>(o_counters);
+            e = cudaMemset(h->counters, 0, sizeof(uint32_t) * (groups + 1));
+        }
+        if (e == cudaSuccess)
+            e = upload_items(tensors, first, h->memory.at<uint32_t>(o_first), h->memory.at<ar::GradItem>(o_items));
         if (e != cudaSuccess) {
             delete h;
             return cuda_status(e);
         }
-        h->info.table_bytes = h->tables.host.size();
-        h->items = h->tables.at<ar::GradItem>(o_items);
-        h->first = h->tables.at<uint32_t>(o_first);
-        h->cta_partials = h->tables.at<uint64_t>(o_cta);
-        h->counter = h->tables.at<uint32_t>(o_counter);
-        h->item_partials = h->tables.at<uint64_t>(o_parts);
-        std::vector<char>().swap(h->tables.host);
+        fill_info(n_tensors, counts, elems, h->n_items, &h->info);
+        h->info.table_bytes = h->memory.bytes;
+        h->info.tiling_ok = 1;
         *out = h;
         return AR_OK;
-    } catch (const std::length_error&) {
-        delete h;
-        return AR_ERR_UNSUPPORTED;
     } catch (const std::bad_alloc&) {
         delete h;
         return AR_ERR_NOMEM;
@@ -284,20 +355,13 @@ ar_status ar_grads_destroy(ar_grads_t h) {
 ar_status ar_grad_norm(ar_grads_t h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
                        float* tensor_norms, void* stream) {
     ar::TraceRange trace("ar_grad_norm");
-    return run_norm(h, kind, pre_scale, max_norm, result, tensor_norms, static_cast<cudaStream_t>(stream));
+    return run_norm(h, kind, pre_scale, max_norm, result, tensor_norms, false, static_cast<cudaStream_t>(stream));
 }
 
 ar_status ar_grad_clip(ar_grads_t h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
                        float* tensor_norms, void* stream) {
     ar::TraceRange trace("ar_grad_clip");
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const ar_status s = run_norm(h, kind, pre_scale, max_norm, result, tensor_norms, st);
-    if (s != AR_OK || h->n_items == 0) return s;
-    ar::ScaleArgs a = {};
-    a.items = h->items;
-    a.n_items = h->n_items;
-    a.result = result;
-    return cuda_status(ar::launch_scale(a, st));
+    return run_norm(h, kind, pre_scale, max_norm, result, tensor_norms, true, static_cast<cudaStream_t>(stream));
 }
 
 ar_status ar_adamw_create(int n_tensors, const uint64_t* counts, const ar_dtype* param_dtypes, void* const* params,
@@ -336,42 +400,46 @@ ar_status ar_adamw_create(int n_tensors, const uint64_t* counts, const ar_dtype*
             delete h;
             return s;
         }
-        std::vector<ar::TensorRange> R;
-        std::vector<uint32_t> first;
-        ar::split_tensors(n_tensors, counts, kAdamItemElems, R, first);
-        std::vector<ar::AdamItem> items;
-        items.reserve(R.size());
-        for (const ar::TensorRange& r : R) {
-            const uint32_t t = r.tensor;
-            ar::AdamItem it = {};
-            it.p = static_cast<char*>(params[t]) + r.elem * esize(param_dtypes[t]);
-            it.g = static_cast<const char*>(grads[t]) + r.elem * esize(grad_dtypes[t]);
-            it.m = exp_avg[t] + r.elem;
-            it.v = exp_avg_sq[t] + r.elem;
-            it.w = copies ? static_cast<char*>(copies[t]) + r.elem * 2 : nullptr;
-            it.count = r.count;
-            it.flags = (param_dtypes[t] == AR_BFLOAT16 ? ar::kParamBf16 : 0) |
-                       (grad_dtypes[t] == AR_BFLOAT16 ? ar::kGradBf16 : 0) | (copies ? ar::kHasCopy : 0);
-            it.decay = decay ? decay[t] : 1.f;
-            items.push_back(it);
+        const uint32_t elems = adam_item_elems(n_tensors, counts);
+        std::vector<ar::AdamTensor> tensors;
+        for (int t = 0; t < n_tensors; ++t) {
+            const uint32_t pe = esize(param_dtypes[t]), ge = esize(grad_dtypes[t]);
+            const uint32_t flags = (pe == 2 ? ar::kParamBf16 : 0) | (ge == 2 ? ar::kGradBf16 : 0) |
+                                   (copies ? ar::kHasCopy : 0);
+            ar::AdamTensor a = {static_cast<char*>(params[t]), static_cast<const char*>(grads[t]), exp_avg[t],
+                                exp_avg_sq[t], copies ? static_cast<char*>(copies[t]) : nullptr,
+                                {counts[t], elems, ar::lead_elems(exp_avg[t], 4)}, flags, decay ? decay[t] : 1.f};
+            // the first moments' quads start `o` elements in: do the others'?
+            const uint64_t o = (16 - reinterpret_cast<uintptr_t>(a.m) % 16) % 16 / 4;
+            const auto quads = [o](const void* p, uint32_t es) {
+                return (reinterpret_cast<uintptr_t>(p) + o * es) % (4 * es) == 0;
+            };
+            h->whole = h->whole && (counts[t] == 0 || (quads(a.p, pe) && quads(a.g, ge) && quads(a.v, 4) &&
+                                                       (!copies || quads(a.w, 2))));
+            tensors.push_back(a);
         }
-        h->n_items = static_cast<uint32_t>(items.size());
-        fill_info(n_tensors, counts, kAdamItemElems, items.size(), &h->info);
-        h->info.tiling_ok = 1;
-        const size_t o_items = h->tables.put(items);
-        const cudaError_t up = h->tables.upload();
+        std::vector<uint32_t> first;
+        bool fits = false;
+        h->n_items = first_items(tensors, first, &fits);
+        if (!fits) {
+            delete h;
+            return AR_ERR_UNSUPPORTED;
+        }
+        const size_t o_items = h->memory.part(sizeof(ar::AdamItem) * h->n_items);
+        const size_t o_first = h->memory.part(sizeof(uint32_t) * first.size());
+        cudaError_t up = h->memory.allocate();
+        if (up == cudaSuccess)
+            up = upload_items(tensors, first, h->memory.at<uint32_t>(o_first), h->memory.at<ar::AdamItem>(o_items));
         if (up != cudaSuccess) {
             delete h;
             return cuda_status(up);
         }
-        h->info.table_bytes = h->tables.host.size();
-        h->items = h->tables.at<ar::AdamItem>(o_items);
-        std::vector<char>().swap(h->tables.host);
+        h->items = h->memory.at<ar::AdamItem>(o_items);
+        fill_info(n_tensors, counts, elems, h->n_items, &h->info);
+        h->info.table_bytes = h->memory.bytes;
+        h->info.tiling_ok = 1;
         *out = h;
         return AR_OK;
-    } catch (const std::length_error&) {
-        delete h;
-        return AR_ERR_UNSUPPORTED;
     } catch (const std::bad_alloc&) {
         delete h;
         return AR_ERR_NOMEM;
@@ -396,7 +464,7 @@ ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* p, const float* res
     if (!h || !p) return AR_ERR_INVALID_ARG;
     const auto finite = [](double x) { return x >= 0.0 && x <= 3.4028234e38; };
     if (p->step < 1 || !finite(p->lr) || !finite(p->weight_decay) || !finite(p->lr * p->weight_decay) ||
-        !finite(p->eps) || !(p->eps >= 1.17549436e-38) || !(p->beta1 >= 0.0 && p->beta1 < 1.0) ||
+        !float_normal(p->eps) || !(p->beta1 >= 0.0 && p->beta1 < 1.0) ||
         !(p->beta2 >= 0.0 && p->beta2 < 1.0))
         return AR_ERR_INVALID_ARG;
     const double t = static_cast<double>(p->step);
@@ -416,7 +484,7 @@ ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* p, const float* res
     a.inv_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
     a.eps = static_cast<float>(p->eps);
     a.lr_decay = static_cast<float>(p->lr * p->weight_decay);
-    return cuda_status(ar::launch_adamw(a, static_cast<cudaStream_t>(stream)));
+    return cuda_status(ar::launch_adamw(a, h->whole, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

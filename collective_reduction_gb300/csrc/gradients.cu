@@ -13,25 +13,67 @@ namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
+// How long the lines that a load brings in should stay in L2.
+__device__ __forceinline__ uint64_t keep_policy(bool last_out) {
+    uint64_t p;
+    if (last_out)
+        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    else
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 __device__ __forceinline__ uint4 load128(const char* p) {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
     return v;
 }
 
-__device__ __forceinline__ uint2 load64(const char* p) {
-    uint2 v;
-    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+__device__ __forceinline__ uint4 load128(const char* p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
     return v;
 }
 
-__device__ __forceinline__ void store128(char* p, uint4 v) {
-    asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
+// CS: the line is not used again (streaming)
+template <bool CS>
+__device__ __forceinline__ uint4 load_vec4(const char* p) {
+    if (!CS) return load128(p);
+    uint4 v;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
 }
 
-__device__ __forceinline__ void store64(char* p, uint2 v) {
-    asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+template <bool CS>
+__device__ __forceinline__ uint2 load_vec2(const char* p) {
+    uint2 v;
+    if (CS)
+        asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    else
+        asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+template <bool CS>
+__device__ __forceinline__ void store_vec4(char* p, uint4 v) {
+    if (CS)
+        asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+    else
+        asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+}
+
+template <bool CS>
+__device__ __forceinline__ void store_vec2(char* p, uint2 v) {
+    if (CS)
+        asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
+    else
+        asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(v.x), "r"(v.y) : "memory");
 }
 
 // One element as the bits of a float32.
@@ -58,24 +100,37 @@ __device__ __forceinline__ void store_elem(char* p, uint32_t i, float x) {
     }
 }
 
-// Four elements starting at element i (16 bytes of float32 or 8 of bfloat16).
-template <bool BF>
-__device__ __forceinline__ float4 load_quad(const char* p, uint32_t i) {
+// Four elements starting at element i: one access of 16 bytes of float32 or 8
+// of bfloat16 where `whole` says that they are aligned to it, else four.
+template <bool BF, bool CS = false>
+__device__ __forceinline__ float4 load_quad(const char* p, uint32_t i, bool whole) {
+    if (!whole)
+        return make_float4(__uint_as_float(load_elem<BF>(p, i)), __uint_as_float(load_elem<BF>(p, i + 1)),
+                           __uint_as_float(load_elem<BF>(p, i + 2)), __uint_as_float(load_elem<BF>(p, i + 3)));
     if (BF) {
-        const uint2 w = load64(p + 2ull * i);
+        const uint2 w = load_vec2<CS>(p + 2ull * i);
         return make_float4(bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y));
     }
-    const uint4 w = load128(p + 4ull * i);
+    const uint4 w = load_vec4<CS>(p + 4ull * i);
     return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
 }
 
-template <bool BF>
-__device__ __forceinline__ void store_quad(char* p, uint32_t i, float4 x) {
-    if (BF)
-        store64(p + 2ull * i, make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w)));
+template <bool BF, bool CS = false>
+__device__ __forceinline__ void store_quad(char* p, uint32_t i, float4 x, bool whole) {
+    if (!whole) {
+        store_elem<BF>(p, i, x.x), store_elem<BF>(p, i + 1, x.y);
+        store_elem<BF>(p, i + 2, x.z), store_elem<BF>(p, i + 3, x.w);
+    } else if (BF)
+        store_vec2<CS>(p + 2ull * i, make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w)));
     else
-        store128(p + 4ull * i, make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z),
+        store_vec4<CS>(p + 4ull * i, make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z),
                                           __float_as_uint(x.w)));
+}
+
+// Whether quads from element i on lie on their alignment.
+template <bool BF>
+__device__ __forceinline__ bool quad_aligned(const void* p, uint32_t i) {
+    return ((static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) + i * (BF ? 2 : 4)) & (BF ? 7 : 15)) == 0;
 }
 
 // Elements before the first whole vector of `bytes` bytes (a power of two).
@@ -183,7 +238,23 @@ struct SumSquares {
     __device__ __forceinline__ uint64_t bits() const {
         return static_cast<uint64_t>(__double_as_longlong(s));
     }
-    __device__ __forceinline__ double norm() const { return sqrt(s); }
+    // The root r and 1 / r.  float64 roots and divisions are long dependent
+    // chains here (0.3 us each of a call that takes 4): float32's reciprocal
+    // root of s 4^-k in [1, 4) and one Newton step in float64 give 2^-42.
+    __device__ __forceinline__ void root(double& r, double& inverse) const {
+        if (s == 0.0 || nonfinite()) {
+            r = inverse = s;  // the inverse is not used
+            return;
+        }
+        const uint64_t b = bits();
+        const int k = (static_cast<int>(b >> 52) - 1023) >> 1;  // s is at least 2^-298: a normal number
+        const double t = __longlong_as_double(static_cast<long long>(b - (static_cast<uint64_t>(2 * k) << 52)));
+        const double y = rsqrtf(static_cast<float>(t));
+        const double z = fma(y, fma(-0.5 * t * y, y, 0.5), y);
+        const auto power = [](int e) { return __longlong_as_double(static_cast<long long>(1023 + e) << 52); };
+        r = t * z * power(k);
+        inverse = z * power(-k);
+    }
     __device__ __forceinline__ bool nonfinite() const { return !(s <= 1.7976931348623157e308); }
 };
 
@@ -206,7 +277,10 @@ struct MaxAbs {
     __device__ __forceinline__ void add(uint32_t d) { m = max(m, d); }
     __device__ __forceinline__ void join(uint64_t other) { m = max(m, static_cast<uint32_t>(other)); }
     __device__ __forceinline__ uint64_t bits() const { return m; }
-    __device__ __forceinline__ double norm() const { return static_cast<double>(__uint_as_float(m)); }
+    __device__ __forceinline__ void root(double& r, double& inverse) const {
+        r = static_cast<double>(__uint_as_float(m));
+        inverse = 1.0 / r;
+    }
     __device__ __forceinline__ bool nonfinite() const { return m >= 0x7F800000u; }
 };
 
@@ -231,80 +305,229 @@ __device__ __forceinline__ void cta_join(Acc& a, uint64_t* sm) {
     }
 }
 
-// Lane's share of one item: whole 16-byte vectors, 8 in flight a thread, and
-// single elements before the first and after the last.
-template <class Acc, bool BF>
-__device__ __forceinline__ void norm_item(Acc& acc, const char* src, uint32_t count, uint32_t lane) {
-    constexpr uint32_t V = BF ? 8 : 4;
-    constexpr int U = 8;
-    const uint32_t head = min(count, head_elems<BF>(src, 16));
-    const uint32_t nv = (count - head) / V;
-    const uint32_t tail = count - head - nv * V;
-    const char* body = src + head * (BF ? 2 : 4);
-    uint32_t q = lane;
-    for (; q + 32 * (U - 1) < nv; q += 32 * U) {
-        uint4 x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = load128(body + 16ull * (q + 32 * u));
-        if (!acc.template feed<BF, U>(x)) acc.add(Acc::template again<BF, U>(body, q, nv));
-    }
-    if (q < nv) {
-        uint4 x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            x[u] = q + 32 * u < nv ? load128(body + 16ull * (q + 32 * u)) : make_uint4(0, 0, 0, 0);
-        if (!acc.template feed<BF, U>(x)) acc.add(Acc::template again<BF, U>(body, q, nv));
-    }
-    if (lane < head) acc.one(load_elem<BF>(src, lane));
-    if (lane < tail) acc.one(load_elem<BF>(src, count - tail + lane));
+// The record of a norm (and what every element is scaled by).
+struct Record {
+    float norm, scale, nonfinite, clipped;
+};
+
+template <class Acc>
+__device__ __forceinline__ Record make_record(const Acc& acc, double c, double max_norm) {
+    double r, inverse;
+    acc.root(r, inverse);
+    const bool bad = acc.nonfinite(), clipped = !bad && c * r > max_norm;
+    return {static_cast<float>(c * r), static_cast<float>(clipped ? max_norm * inverse : c), bad ? 1.f : 0.f,
+            clipped ? 1.f : 0.f};
 }
 
-// Every warp sums its items, every CTA its warps, and the CTA that finishes
-// last adds the CTAs' sums in their order: which warp takes which item is
-// fixed by the grid, so repeated calls give the same bits.
-template <class Acc>
-__global__ void __launch_bounds__(kGradThreads, kNormCtasPerSm) norm_kernel(const __grid_constant__ NormArgs a) {
+__device__ __forceinline__ void store_record(float* to, const Record& r) {
+    to[0] = r.norm;
+    to[1] = r.scale;
+    to[2] = r.nonfinite;
+    to[3] = r.clipped;
+}
+
+// An item's 16-byte vectors and the elements before and after them.
+template <bool BF>
+struct Vectors {
+    static constexpr uint32_t V = BF ? 8 : 4;
+    uint32_t head, n, tail;
+    const char* body;
+
+    __device__ __forceinline__ Vectors(const char* src, uint32_t count) {
+        head = min(count, head_elems<BF>(src, 16));
+        n = (count - head) / V;
+        tail = count - head - n * V;
+        body = src + head * (BF ? 2 : 4);
+    }
+};
+
+// Lane's share of one item, 8 vectors in flight a thread: at the kernel's 3
+// CTAs an SM that keeps 98 KB in flight on each.
+template <class Acc, bool BF, bool HINT>
+__device__ __forceinline__ void norm_item(Acc& acc, const char* src, uint32_t count, uint32_t lane, uint64_t policy) {
+    constexpr int U = 8;
+    const Vectors<BF> v(src, count);
+    auto load = [&](uint32_t q) { return HINT ? load128(v.body + 16ull * q, policy) : load128(v.body + 16ull * q); };
+    for (uint32_t q0 = 0; q0 < v.n; q0 += 32 * U) {
+        const uint32_t q = q0 + lane;
+        uint4 x[U];
+        if (q0 + 32 * U <= v.n) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = load(q + 32 * u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) x[u] = q + 32 * u < v.n ? load(q + 32 * u) : make_uint4(0, 0, 0, 0);
+        }
+        if (!acc.template feed<BF, U>(x)) acc.add(Acc::template again<BF, U>(v.body, q, v.n));
+    }
+    if (lane < v.head) acc.one(load_elem<BF>(src, lane));
+    if (lane < v.tail) acc.one(load_elem<BF>(src, count - v.tail + lane));
+}
+
+// Counts a CTA whose thread 0 has stored its sum; true in the one that came
+// last, whose threads then see every sum.
+__device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n, bool* flag) {
+    if (threadIdx.x == 0) {
+        uint32_t before;
+        asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"  // wraps to 0 for the next call
+                     : "=r"(before)
+                     : "l"(counter), "r"(n - 1)
+                     : "memory");
+        *flag = before == n - 1;
+    }
+    __syncthreads();
+    return *flag;
+}
+
+// Any number of items.  A warp sums one item, a CTA its warps.  Of every
+// kNormGroup CTAs the one that finishes last adds their sums, and the last of
+// those the groups' sums: each addition has its place whatever the order the
+// CTAs run in, so repeated calls give the same bits while the hardware deals
+// CTAs to SMs as they come free.  (One resident wave of CTAs looping over the
+// items instead left SMs idle for the last tenth: 5.9 TB/s against 7.2.)
+// CLIP: a scaling follows, in the reverse order.
+template <class Acc, bool CLIP>
+__global__ void __launch_bounds__(kGradThreads, 3) norm_kernel(const __grid_constant__ NormArgs a) {
     __shared__ uint64_t sm[kGradWarps];
-    __shared__ bool last;
+    __shared__ bool flag;
     const uint32_t lane = threadIdx.x & 31;
-    const uint32_t stride = gridDim.x * kGradWarps;
+    const uint32_t it = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    GradItem w = {};  // the items are the handle's own and constant: read while the kernel before still runs
+    if (it < a.n_items) w = a.items[it];
+    const uint64_t policy = CLIP ? keep_policy(it >= a.keep_from) : 0;
     griddep_wait();
     griddep_launch_dependents();
     Acc acc;
-    for (uint32_t it = blockIdx.x * kGradWarps + (threadIdx.x >> 5); it < a.n_items; it += stride) {
-        const GradItem w = a.items[it];
-        Acc part;
-        if (w.flags & kGradBf16)
-            norm_item<Acc, true>(part, w.src, w.count, lane);
-        else
-            norm_item<Acc, false>(part, w.src, w.count, lane);
-        acc.join(part.bits());
-        if (a.item_partials) {
-            warp_join(part);
-            if (lane == 0) a.item_partials[it] = part.bits();
-        }
-    }
-    cta_join<Acc, kGradWarps>(acc, sm);
-    if (threadIdx.x == 0) {
-        a.cta_partials[blockIdx.x] = acc.bits();
-        __threadfence();
-        last = atomicInc(a.counter, gridDim.x - 1) == gridDim.x - 1;  // wraps to 0 for the next call
+    if (w.flags & kGradBf16)
+        norm_item<Acc, true, CLIP>(acc, w.src, w.count, lane, policy);
+    else
+        norm_item<Acc, false, CLIP>(acc, w.src, w.count, lane, policy);
+    warp_join(acc);
+    if (lane == 0) {
+        if (a.item_partials && it < a.n_items) a.item_partials[it] = acc.bits();
+        sm[threadIdx.x >> 5] = acc.bits();
     }
     __syncthreads();
-    if (!last) return;
-    __threadfence();
-    Acc all;
-    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kGradThreads) all.join(__ldcg(a.cta_partials + i));
-    cta_join<Acc, kGradWarps>(all, sm);
     if (threadIdx.x == 0) {
-        const double c = a.pre_scale, norm = c * all.norm();
-        const bool bad = all.nonfinite();
-        const bool clipped = !bad && norm > a.max_norm;
-        a.result[0] = static_cast<float>(norm);
-        a.result[1] = static_cast<float>(clipped ? c * (a.max_norm / norm) : c);
-        a.result[2] = bad ? 1.f : 0.f;
-        a.result[3] = clipped ? 1.f : 0.f;
+        Acc b;
+#pragma unroll
+        for (int k = 0; k < kGradWarps; ++k) b.join(sm[k]);
+        a.cta_partials[blockIdx.x] = b.bits();
     }
+    const uint32_t group = blockIdx.x / kNormGroup, groups = (gridDim.x + kNormGroup - 1) / kNormGroup;
+    const uint32_t first = group * kNormGroup, size = min(kNormGroup, gridDim.x - first);
+    if (!last_of(a.counters + group, size, &flag)) return;
+    Acc all;
+#pragma unroll
+    for (uint32_t k = 0; k < kNormGroup; k += kGradThreads)
+        if (k + threadIdx.x < size) all.join(__ldcg(a.cta_partials + first + k + threadIdx.x));
+    cta_join<Acc, kGradWarps>(all, sm);
+    if (groups > 1) {
+        if (threadIdx.x == 0) a.group_partials[group] = all.bits();
+        if (!last_of(a.counters + groups, groups, &flag)) return;
+        all = Acc();
+        for (uint32_t i = threadIdx.x; i < groups; i += kGradThreads) all.join(__ldcg(a.group_partials + i));
+        cta_join<Acc, kGradWarps>(all, sm);
+    }
+    if (threadIdx.x == 0) store_record(a.result, make_record(all, a.pre_scale, a.max_norm));
+}
+
+// Small sets: one cluster, an item to a warp, the sums exchanged through the
+// CTAs' shared memory.  No counter in global memory, and with SCALE the
+// gradients wait in registers for the factor: one launch and one read where
+// the general path takes two of each.
+template <class Acc, bool SCALE>
+__global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ uint64_t sm[kSmallWarps], sums[kSmallCtas];
+    __shared__ float factor;
+    constexpr int U = kSmallItemElems / 128;  // float32 vectors of a full item, a lane's
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t it = blockIdx.x * kSmallWarps + warp;
+    GradItem w = {};
+    if (it < a.n_items) w = a.items[it];
+    griddep_wait();
+    griddep_launch_dependents();
+    const bool bf = w.flags & kGradBf16;
+    const uint32_t head = bf ? Vectors<true>(w.src, w.count).head : Vectors<false>(w.src, w.count).head;
+    const uint32_t n = (w.count - head) / (bf ? 8 : 4), tail = w.count - head - n * (bf ? 8 : 4);
+    const char* body = w.src + head * (bf ? 2 : 4);
+    uint4 x[U];
+    uint32_t edge[2] = {0, 0};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        x[u] = lane + 32 * u < n ? load128(body + 16ull * (lane + 32 * u)) : make_uint4(0, 0, 0, 0);
+    if (lane < head) edge[0] = bf ? load_elem<true>(w.src, lane) : load_elem<false>(w.src, lane);
+    if (lane < tail)
+        edge[1] = bf ? load_elem<true>(w.src, w.count - tail + lane) : load_elem<false>(w.src, w.count - tail + lane);
+    Acc acc;
+    if (bf) {
+        if (!acc.template feed<true, U>(x)) acc.add(Acc::template again<true, U>(body, lane, n));
+    } else {
+        if (!acc.template feed<false, U>(x)) acc.add(Acc::template again<false, U>(body, lane, n));
+    }
+    if (lane < head) acc.one(edge[0]);
+    if (lane < tail) acc.one(edge[1]);
+    warp_join(acc);
+    if (lane == 0) {
+        if (a.item_partials && it < a.n_items) a.item_partials[it] = acc.bits();
+        sm[warp] = acc.bits();
+    }
+    __syncthreads();
+    if (warp == 0) {
+        Acc b;
+        if (lane < kSmallWarps) b.join(sm[lane]);
+        warp_join(b);
+        const uint64_t mine = __shfl_sync(kFull, b.bits(), 0);
+        if (lane < gridDim.x) {  // this CTA's sum to CTA `lane`'s shared memory
+            uint32_t to;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(sums + blockIdx.x)), "r"(lane));
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(mine) : "memory");
+        }
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (threadIdx.x == 0) {
+        Acc all;
+        for (uint32_t c = 0; c < gridDim.x; ++c) all.join(sums[c]);
+        const Record r = make_record(all, a.pre_scale, a.max_norm);
+        factor = r.scale;
+        if (blockIdx.x == 0) store_record(a.result, r);
+    }
+    if (!SCALE) return;
+    __syncthreads();
+    const float f = factor;
+    if ((w.flags & kInPlace) && f == 1.f) return;
+    const bool ob = w.flags & kOutBf16;
+    const auto store = [&](uint32_t i, float4 v, bool whole) {
+        v = make_float4(__fmul_rn(v.x, f), __fmul_rn(v.y, f), __fmul_rn(v.z, f), __fmul_rn(v.w, f));
+        if (ob)
+            store_quad<true>(w.dst, i, v, whole);
+        else
+            store_quad<false>(w.dst, i, v, whole);
+    };
+    const bool whole = ob ? quad_aligned<true>(w.dst, head) : quad_aligned<false>(w.dst, head);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t q = lane + 32 * u;
+        if (q >= n) continue;
+        if (bf) {
+            store(head + 8 * q, make_float4(bf_lo(x[u].x), bf_hi(x[u].x), bf_lo(x[u].y), bf_hi(x[u].y)), whole);
+            store(head + 8 * q + 4, make_float4(bf_lo(x[u].z), bf_hi(x[u].z), bf_lo(x[u].w), bf_hi(x[u].w)), whole);
+        } else {
+            store(head + 4 * q, make_float4(__uint_as_float(x[u].x), __uint_as_float(x[u].y), __uint_as_float(x[u].z),
+                                            __uint_as_float(x[u].w)), whole);
+        }
+    }
+    const auto store_edge = [&](uint32_t i, uint32_t bits) {
+        const float v = __fmul_rn(__uint_as_float(bits), f);
+        if (ob)
+            store_elem<true>(w.dst, i, v);
+        else
+            store_elem<false>(w.dst, i, v);
+    };
+    if (lane < head) store_edge(lane, edge[0]);
+    if (lane < tail) store_edge(w.count - tail + lane, edge[1]);
 }
 
 // Norms of single tensors: a CTA adds one tensor's item sums.
@@ -318,58 +541,48 @@ __global__ void __launch_bounds__(kTensorNormThreads) tensor_norm_kernel(const _
 #pragma unroll 8
     for (uint32_t i = lo + threadIdx.x; i < hi; i += kTensorNormThreads) acc.join(a.item_partials[i]);
     cta_join<Acc, kTensorNormThreads / 32>(acc, sm);
-    if (threadIdx.x == 0) a.norms[blockIdx.x] = static_cast<float>(a.pre_scale * acc.norm());
+    if (threadIdx.x == 0) a.norms[blockIdx.x] = make_record(acc, a.pre_scale, 0.0).norm;
 }
 
 // ---------------------------------------------------------------- the scaling
 
-// dst = round(f * src) over one item: quads where both sides are whole
-// vectors after the same head, else element by element.
+// dst = round(f * src) over one item, in quads of four elements.
 template <bool SB, bool DB>
 __device__ __forceinline__ void scale_item(const char* src, char* dst, uint32_t count, float f, uint32_t lane) {
     constexpr int U = 8;
-    const uint32_t head = min(count, head_elems<DB>(dst, DB ? 8 : 16));
-    const uintptr_t s0 = reinterpret_cast<uintptr_t>(src) + head * (SB ? 2 : 4);
-    if (s0 % (SB ? 8 : 16) == 0) {
-        const uint32_t nq = (count - head) / 4;
-        const uint32_t done = head + nq * 4;
-        for (uint32_t q = lane; q < nq; q += 32 * U) {
-            float4 x[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (q + 32 * u < nq) x[u] = load_quad<SB>(src, head + 4 * (q + 32 * u));
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (q + 32 * u < nq)
-                    store_quad<DB>(dst, head + 4 * (q + 32 * u),
-                                   make_float4(__fmul_rn(x[u].x, f), __fmul_rn(x[u].y, f), __fmul_rn(x[u].z, f),
-                                               __fmul_rn(x[u].w, f)));
-        }
-        if (lane < head) store_elem<DB>(dst, lane, __fmul_rn(__uint_as_float(load_elem<SB>(src, lane)), f));
-        if (done + lane < count)
-            store_elem<DB>(dst, done + lane, __fmul_rn(__uint_as_float(load_elem<SB>(src, done + lane)), f));
-        return;
-    }
-    for (uint32_t q = lane; q < count; q += 32 * U) {
-        uint32_t x[U];
+    const uint32_t head = min(count, head_elems<SB>(src, SB ? 8 : 16));
+    const bool whole = quad_aligned<DB>(dst, head);
+    const uint32_t nq = (count - head) / 4;
+    const uint32_t done = head + nq * 4;
+    for (uint32_t q = lane; q < nq; q += 32 * U) {
+        float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (q + 32 * u < count) x[u] = load_elem<SB>(src, q + 32 * u);
+            if (q + 32 * u < nq) x[u] = load_quad<SB, true>(src, head + 4 * (q + 32 * u), true);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (q + 32 * u < count) store_elem<DB>(dst, q + 32 * u, __fmul_rn(__uint_as_float(x[u]), f));
+            if (q + 32 * u < nq)
+                store_quad<DB, true>(dst, head + 4 * (q + 32 * u),
+                               make_float4(__fmul_rn(x[u].x, f), __fmul_rn(x[u].y, f), __fmul_rn(x[u].z, f),
+                                           __fmul_rn(x[u].w, f)),
+                               whole);
     }
+    if (lane < head) store_elem<DB>(dst, lane, __fmul_rn(__uint_as_float(load_elem<SB>(src, lane)), f));
+    if (done + lane < count)
+        store_elem<DB>(dst, done + lane, __fmul_rn(__uint_as_float(load_elem<SB>(src, done + lane)), f));
 }
 
-// The items in the reverse of the norm's order: what the norm read last may
-// still be in L2.  In place, a factor of exactly 1 leaves nothing to do.
-__global__ void __launch_bounds__(kGradThreads) scale_kernel(const __grid_constant__ ScaleArgs a) {
+// The items in the reverse of the norm's order: the norm leaves its last ones
+// in L2.  Loads and stores are streaming (neither is used again), so the
+// results do not push out the gradients that wait there.
+// In place, a factor of exactly 1 leaves nothing to do.
+__global__ void __launch_bounds__(kGradThreads, 4) scale_kernel(const __grid_constant__ ScaleArgs a) {
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t w = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    GradItem it = {};
+    if (w < a.n_items) it = a.items[a.n_items - 1 - w];
     griddep_wait();
     griddep_launch_dependents();
-    if (w >= a.n_items) return;
-    const GradItem it = a.items[a.n_items - 1 - w];
     const float f = __ldcg(a.result + 1);
     if ((it.flags & kInPlace) && f == 1.f) return;
     const bool sb = it.flags & kGradBf16, db = it.flags & kOutBf16;
@@ -420,101 +633,171 @@ __device__ __forceinline__ void adam_elem(const AdamArgs& a, const AdamItem& it,
     if (COPY) store_elem<true>(it.w, i, p);
 }
 
-template <bool PB, bool GB, bool COPY>
+template <bool PB, bool GB, bool COPY, bool WHOLE>
 __device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamItem& it, float f, uint32_t lane) {
-    constexpr int U = 2;
+    constexpr int U = WHOLE ? 2 : 1;
     const float decay = __fmul_rn(a.lr_decay, it.decay);
     char* mp = reinterpret_cast<char*>(it.m);
     char* vp = reinterpret_cast<char*>(it.v);
     const uint32_t head = min(it.count, head_elems<false>(mp, 16));
-    auto whole = [&](const void* p, bool bf) {
-        return (reinterpret_cast<uintptr_t>(p) + head * (bf ? 2 : 4)) % (bf ? 8 : 16) == 0;
-    };
-    if (whole(it.p, PB) && whole(it.g, GB) && whole(vp, false) && (!COPY || whole(it.w, true))) {
-        const uint32_t nq = (it.count - head) / 4;
-        const uint32_t done = head + nq * 4;
-        for (uint32_t q = lane; q < nq; q += 32 * U) {
-            float4 p[U], g[U], m[U], v[U];
+    const bool pw = WHOLE || quad_aligned<PB>(it.p, head), gw = WHOLE || quad_aligned<GB>(it.g, head);
+    const bool vw = WHOLE || quad_aligned<false>(vp, head), ww = WHOLE || (COPY && quad_aligned<true>(it.w, head));
+    const uint32_t nq = (it.count - head) / 4;
+    const uint32_t done = head + nq * 4;
+    for (uint32_t q = lane; q < nq; q += 32 * U) {
+        float4 p[U], g[U], m[U], v[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t i = head + 4 * (q + 32 * u);
-                if (q + 32 * u < nq) {
-                    g[u] = load_quad<GB>(it.g, i);
-                    m[u] = load_quad<false>(mp, i);
-                    v[u] = load_quad<false>(vp, i);
-                    p[u] = load_quad<PB>(it.p, i);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t i = head + 4 * (q + 32 * u);
-                if (q + 32 * u < nq) {
-                    adam_quad(a, decay, f, p[u], g[u], m[u], v[u]);
-                    store_quad<PB>(it.p, i, p[u]);
-                    store_quad<false>(mp, i, m[u]);
-                    store_quad<false>(vp, i, v[u]);
-                    if (COPY) store_quad<true>(it.w, i, p[u]);
-                }
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = head + 4 * (q + 32 * u);
+            if (q + 32 * u < nq) {
+                g[u] = load_quad<GB>(it.g, i, gw);
+                m[u] = load_quad<false>(mp, i, true);
+                v[u] = load_quad<false>(vp, i, vw);
+                p[u] = load_quad<PB>(it.p, i, pw);
             }
         }
-        if (lane < head) adam_elem<PB, GB, COPY>(a, it, decay, f, lane);
-        if (done + lane < it.count) adam_elem<PB, GB, COPY>(a, it, decay, f, done + lane);
-        return;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t i = head + 4 * (q + 32 * u);
+            if (q + 32 * u < nq) {
+                adam_quad(a, decay, f, p[u], g[u], m[u], v[u]);
+                store_quad<PB>(it.p, i, p[u], pw);
+                store_quad<false>(mp, i, m[u], true);
+                store_quad<false>(vp, i, v[u], vw);
+                if (COPY) store_quad<true>(it.w, i, p[u], ww);
+            }
+        }
     }
-    for (uint32_t i = lane; i < it.count; i += 32) adam_elem<PB, GB, COPY>(a, it, decay, f, i);
+    if (lane < head) adam_elem<PB, GB, COPY>(a, it, decay, f, lane);
+    if (done + lane < it.count) adam_elem<PB, GB, COPY>(a, it, decay, f, done + lane);
 }
 
-// A warp updates one item.  With a record, nothing is touched when the
-// gradients held an infinity or NaN.
-__global__ void __launch_bounds__(kGradThreads) adamw_kernel(const __grid_constant__ AdamArgs a) {
+// A warp updates one item; with a record, nothing is touched when the
+// gradients held an infinity or NaN.  The items in the reverse of the norm's
+// order, whose last gradients may still be in L2.  Bound by HBM.
+// WHOLE: every stream moves in quads.  Two quads of each in flight a thread at
+// 4 CTAs an SM; a stream off its alignment takes single elements, which need
+// more warps instead: one quad, 6 CTAs.  (Measured, in us, both ways: a billion
+// float32 parameters 4584 and 4647; bf16 parameters with bf16 gradients packed
+// tight at odd sizes 492 and 455, norm included.)
+template <bool WHOLE>
+__global__ void __launch_bounds__(kGradThreads, WHOLE ? 4 : 6) adamw_kernel(const __grid_constant__ AdamArgs a) {
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t w = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    AdamItem it = {};
+    if (w < a.n_items) it = a.items[a.n_items - 1 - w];
     griddep_wait();
     griddep_launch_dependents();
     if (w >= a.n_items) return;
-    const AdamItem it = a.items[a.n_items - 1 - w];
     float f = 1.f;
     if (a.result) {
         f = __ldcg(a.result + 1);
         if (__ldcg(a.result + 2) != 0.f) return;
     }
     switch (it.flags & (kGradBf16 | kParamBf16 | kHasCopy)) {
-        case 0: return adam_item<false, false, false>(a, it, f, lane);
-        case kGradBf16: return adam_item<false, true, false>(a, it, f, lane);
-        case kHasCopy: return adam_item<false, false, true>(a, it, f, lane);
-        case kHasCopy | kGradBf16: return adam_item<false, true, true>(a, it, f, lane);
-        case kParamBf16: return adam_item<true, false, false>(a, it, f, lane);
-        default: return adam_item<true, true, false>(a, it, f, lane);
+        case 0: return adam_item<false, false, false, WHOLE>(a, it, f, lane);
+        case kGradBf16: return adam_item<false, true, false, WHOLE>(a, it, f, lane);
+        case kHasCopy: return adam_item<false, false, true, WHOLE>(a, it, f, lane);
+        case kHasCopy | kGradBf16: return adam_item<false, true, true, WHOLE>(a, it, f, lane);
+        case kParamBf16: return adam_item<true, false, false, WHOLE>(a, it, f, lane);
+        default: return adam_item<true, true, false, WHOLE>(a, it, f, lane);
     }
 }
 
+// ------------------------------------------------------------------ the items
+
+__device__ __forceinline__ GradItem make_item(const GradTensor& t, uint64_t lo, uint64_t hi) {
+    GradItem it = {};
+    it.src = t.src + lo * (t.flags & kGradBf16 ? 2 : 4);
+    it.dst = t.dst + lo * (t.flags & kOutBf16 ? 2 : 4);
+    it.count = static_cast<uint32_t>(hi - lo);
+    it.flags = t.flags;
+    return it;
+}
+
+__device__ __forceinline__ AdamItem make_item(const AdamTensor& t, uint64_t lo, uint64_t hi) {
+    AdamItem it = {};
+    it.p = t.p + lo * (t.flags & kParamBf16 ? 2 : 4);
+    it.g = t.g + lo * (t.flags & kGradBf16 ? 2 : 4);
+    it.m = t.m + lo;
+    it.v = t.v + lo;
+    it.w = t.flags & kHasCopy ? t.w + lo * 2 : nullptr;
+    it.count = static_cast<uint32_t>(hi - lo);
+    it.flags = t.flags;
+    it.decay = t.decay;
+    return it;
+}
+
+// Once per handle, a thread an item: the tensor whose items hold it, by
+// halving, and the item's place in it.
+template <class Tensor, class Item>
+__global__ void items_kernel(const Tensor* tensors, const uint32_t* first, int n, Item* items) {
+    const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= first[n]) return;
+    int lo = 0, hi = n;  // first[lo] <= i < first[hi]
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (first[mid] <= i)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Tensor t = tensors[lo];
+    const uint32_t k = i - first[lo];
+    items[i] = make_item(t, t.split.begin(k), t.split.end(k));
+}
+
+template <class Tensor, class Item>
+cudaError_t make_items(const Tensor* tensors, const uint32_t* first, int n, uint32_t n_items, Item* items,
+                       cudaStream_t st) {
+    items_kernel<<<(n_items + 255) / 256, 256, 0, st>>>(tensors, first, n, items);
+    return cudaGetLastError();
+}
+
 template <class Args>
-cudaError_t launch(void (*f)(Args), const Args& a, uint32_t grid, int block, cudaStream_t st) {
+cudaError_t launch(void (*f)(Args), const Args& a, uint32_t grid, int block, cudaStream_t st, bool cluster = false) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = AR_PDL;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = grid;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster ? 2 : 1;
     void* args[] = {const_cast<Args*>(&a)};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(f), args);
 }
 
-uint32_t ctas(uint32_t n_items) { return (n_items + kGradWarps - 1) / kGradWarps; }
-
 }  // namespace
 
-int norm_grid(uint32_t n_items, int num_sms) {
-    const uint32_t most = static_cast<uint32_t>(num_sms) * kNormCtasPerSm, want = ctas(n_items);
-    return static_cast<int>(want < 1 ? 1 : want < most ? want : most);
+cudaError_t launch_items(const GradTensor* tensors, const uint32_t* first, int n, uint32_t n_items, GradItem* items,
+                         cudaStream_t st) {
+    return make_items(tensors, first, n, n_items, items, st);
 }
 
-cudaError_t launch_norm(const NormArgs& a, int grid, cudaStream_t st) {
-    return launch(a.kind == AR_NORM_MAX ? norm_kernel<MaxAbs> : norm_kernel<SumSquares>, a,
-                  static_cast<uint32_t>(grid), kGradThreads, st);
+cudaError_t launch_items(const AdamTensor* tensors, const uint32_t* first, int n, uint32_t n_items, AdamItem* items,
+                         cudaStream_t st) {
+    return make_items(tensors, first, n, n_items, items, st);
+}
+
+cudaError_t launch_norm(const NormArgs& a, bool before_scale, cudaStream_t st) {
+    const bool max = a.kind == AR_NORM_MAX;
+    return launch(before_scale ? (max ? norm_kernel<MaxAbs, true> : norm_kernel<SumSquares, true>)
+                               : (max ? norm_kernel<MaxAbs, false> : norm_kernel<SumSquares, false>),
+                  a, grad_ctas(a.n_items), kGradThreads, st);
+}
+
+cudaError_t launch_small(const NormArgs& a, bool scale, cudaStream_t st) {
+    const bool max = a.kind == AR_NORM_MAX;
+    const uint32_t ctas = a.n_items == 0 ? 1 : (a.n_items + kSmallWarps - 1) / kSmallWarps;
+    return launch(scale ? (max ? small_kernel<MaxAbs, true> : small_kernel<SumSquares, true>)
+                        : (max ? small_kernel<MaxAbs, false> : small_kernel<SumSquares, false>),
+                  a, ctas, kSmallThreads, st, true);
 }
 
 cudaError_t launch_tensor_norms(const TensorNormArgs& a, int n_tensors, cudaStream_t st) {
@@ -523,11 +806,11 @@ cudaError_t launch_tensor_norms(const TensorNormArgs& a, int n_tensors, cudaStre
 }
 
 cudaError_t launch_scale(const ScaleArgs& a, cudaStream_t st) {
-    return launch(scale_kernel, a, ctas(a.n_items), kGradThreads, st);
+    return launch(scale_kernel, a, grad_ctas(a.n_items), kGradThreads, st);
 }
 
-cudaError_t launch_adamw(const AdamArgs& a, cudaStream_t st) {
-    return launch(adamw_kernel, a, ctas(a.n_items), kGradThreads, st);
+cudaError_t launch_adamw(const AdamArgs& a, bool whole, cudaStream_t st) {
+    return launch(whole ? adamw_kernel<true> : adamw_kernel<false>, a, grad_ctas(a.n_items), kGradThreads, st);
 }
 
 }  // namespace ar

@@ -5,31 +5,63 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <vector>
 
 #include "ar.h"
 
 namespace ar {
 
-// A range of one tensor that one warp works through.  Every item of a tensor
-// but its last holds the handle's item_elems elements, so all start at the
-// same place within a 16-byte vector as the tensor does.
-struct TensorRange {
-    uint32_t tensor;
-    uint32_t count;
-    uint64_t elem;
+// A handle splits every tensor into ranges that a warp each works through.
+// Range k of a tensor ends before element (k + 1) item_elems - lead and starts
+// where range k - 1 ends: a tensor that begins `lead` elements past an
+// alignment boundary (lead < item_elems) has a short first range, and every
+// later one starts on a boundary.
+struct RangeSplit {
+    uint64_t count;
+    uint32_t item_elems;
+    uint32_t lead;
+
+    __host__ __device__ uint64_t ranges() const {
+        return count == 0 ? 0 : (count + lead + item_elems - 1) / item_elems;
+    }
+    __host__ __device__ uint64_t begin(uint64_t k) const { return k == 0 ? 0 : k * item_elems - lead; }
+    __host__ __device__ uint64_t end(uint64_t k) const {
+        const uint64_t e = (k + 1) * item_elems - lead;
+        return e < count ? e : count;
+    }
 };
 
-// The ranges of n tensors in order, none empty; first[t] is the index of
-// tensor t's first range (first[n] their number).
-void split_tensors(int n, const uint64_t* counts, uint64_t item_elems, std::vector<TensorRange>& ranges,
-                   std::vector<uint32_t>& first);
+// Ranges start on this boundary of their leading stream (the gradients; for
+// AdamW the first moments): a warp's 512-byte loads then cover whole lines.
+constexpr uint32_t kRangeAlign = 128;
+inline uint32_t lead_elems(const void* p, uint32_t es) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) % kRangeAlign) / es;
+}
 
-// Item flags: element types of the streams (bit set: bfloat16, else float32),
-// and whether a scaled item overwrites its own gradients.
+// Flags: element types of the streams (bit set: bfloat16, else float32), and
+// whether a scaled tensor overwrites its own gradients.
 constexpr uint32_t kGradBf16 = 1, kOutBf16 = 2, kInPlace = 4, kParamBf16 = 8, kHasCopy = 16;
 
-// One range of a gradient (src) and of the tensor that takes it scaled (dst).
+// A gradient and the tensor that takes it scaled.
+struct GradTensor {
+    const char* src;
+    char* dst;
+    RangeSplit split;
+    uint32_t flags;
+};
+
+// A parameter, its gradient, moments and optional bf16 copy.
+struct AdamTensor {
+    char* p;
+    const char* g;
+    float* m;
+    float* v;
+    char* w;
+    RangeSplit split;
+    uint32_t flags;
+    float decay;  // this tensor's multiple of the weight decay
+};
+
+// One range of them.
 struct alignas(16) GradItem {
     const char* src;
     char* dst;
@@ -38,7 +70,6 @@ struct alignas(16) GradItem {
     uint64_t pad;
 };
 
-// One range of a parameter, its gradient, moments and optional bf16 copy.
 struct alignas(16) AdamItem {
     char* p;
     const char* g;
@@ -47,34 +78,46 @@ struct alignas(16) AdamItem {
     char* w;
     uint32_t count;
     uint32_t flags;
-    float decay;  // this tensor's multiple of the weight decay
+    float decay;
     uint32_t pad[3];
 };
 
-constexpr int kGradThreads = 256;                   // 8 warps, an item each at a time
+constexpr int kGradThreads = 256;  // 8 warps, an item each
 constexpr int kGradWarps = kGradThreads / 32;
-constexpr int kNormCtasPerSm = 4;                   // the norm kernel's persistent grid
-constexpr int kTensorNormThreads = 512;
+constexpr int kTensorNormThreads = 128;
+// CTAs whose sums one CTA adds up (four a thread) on the way to the norm
+constexpr uint32_t kNormGroup = 4 * kGradThreads;
+// Small sets: one cluster, a range of at most kSmallItemElems to each warp
+constexpr int kSmallThreads = 512;
+constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallCtas = 8;
+constexpr uint32_t kSmallItems = kSmallWarps * kSmallCtas;
+constexpr uint32_t kSmallItemElems = 1024;
 
-// What the norm kernels leave for the host's caller and for the kernels after
-// them: the norm, the factor, and two truth values.
+inline uint32_t grad_ctas(uint32_t n_items) {
+    return n_items <= kGradWarps ? 1 : (n_items + kGradWarps - 1) / kGradWarps;
+}
+inline uint32_t norm_groups(uint32_t n_items) { return (grad_ctas(n_items) + kNormGroup - 1) / kNormGroup; }
+
 struct NormArgs {
     const GradItem* items;
     uint32_t n_items;
-    int kind;                // AR_NORM_L2 or AR_NORM_MAX
-    uint64_t* cta_partials;  // one per CTA of the grid
-    uint64_t* item_partials; // one per item, or null: no norms of single tensors
-    uint32_t* counter;       // CTAs done; 0 between calls
+    uint32_t keep_from;        // before a scaling: items from here on stay in L2 for it
+    int kind;                  // AR_NORM_L2 or AR_NORM_MAX
+    uint64_t* cta_partials;    // one per CTA
+    uint64_t* group_partials;  // one per kNormGroup CTAs
+    uint64_t* item_partials;   // one per item, or null: no norms of single tensors
+    uint32_t* counters;        // CTAs done of each group, then groups done; 0 between calls
     double pre_scale, max_norm;
-    float* result;           // 4 floats
+    float* result;             // norm, scale, nonfinite, clipped
 };
 
 struct TensorNormArgs {
     const uint64_t* item_partials;
-    const uint32_t* first;   // n + 1
+    const uint32_t* first;     // n + 1: each tensor's first item
     int kind;
     double pre_scale;
-    float* norms;            // n
+    float* norms;              // n
 };
 
 struct ScaleArgs {
@@ -86,20 +129,28 @@ struct ScaleArgs {
 struct AdamArgs {
     const AdamItem* items;
     uint32_t n_items;
-    const float* result;     // the norm's record, or null: factor 1
-    float beta1, omb1;       // omb: one minus beta, rounded from 64 bits
+    const float* result;       // the norm's record, or null: factor 1
+    float beta1, omb1;         // omb: one minus beta, rounded from 64 bits
     float beta2, omb2;
-    float step_size;         // lr / (1 - beta1^t)
-    float inv_bc2;           // 1 / sqrt(1 - beta2^t)
+    float step_size;           // lr / (1 - beta1^t)
+    float inv_bc2;             // 1 / sqrt(1 - beta2^t)
     float eps;
-    float lr_decay;          // lr times the weight decay
+    float lr_decay;            // lr times the weight decay
 };
 
-// CTAs of the norm kernel's grid for n_items on num_sms SMs.
-int norm_grid(uint32_t n_items, int num_sms);
-cudaError_t launch_norm(const NormArgs& a, int grid, cudaStream_t st);
+// Writes the items of n tensors; first[t] is tensor t's first item (n + 1).
+cudaError_t launch_items(const GradTensor* tensors, const uint32_t* first, int n, uint32_t n_items, GradItem* items,
+                         cudaStream_t st);
+cudaError_t launch_items(const AdamTensor* tensors, const uint32_t* first, int n, uint32_t n_items, AdamItem* items,
+                         cudaStream_t st);
+
+cudaError_t launch_norm(const NormArgs& a, bool before_scale, cudaStream_t st);
 cudaError_t launch_tensor_norms(const TensorNormArgs& a, int n_tensors, cudaStream_t st);
 cudaError_t launch_scale(const ScaleArgs& a, cudaStream_t st);
-cudaError_t launch_adamw(const AdamArgs& a, cudaStream_t st);
+// The norm and, with `scale`, the scaling in one launch: at most kSmallItems
+// items of at most kSmallItemElems elements.
+cudaError_t launch_small(const NormArgs& a, bool scale, cudaStream_t st);
+// whole: every stream of every tensor can be read and written in quads.
+cudaError_t launch_adamw(const AdamArgs& a, bool whole, cudaStream_t st);
 
 }  // namespace ar
