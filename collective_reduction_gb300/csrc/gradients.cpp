@@ -12,18 +12,20 @@
 
 namespace {
 
+constexpr double kFloatMax = 3.4028234e38;
 constexpr int kMaxTensors = 1 << 20;
 constexpr uint64_t kMaxElems = uint64_t(1) << 40;
 
 // One wave of warps on GB300's 152 SMs: the norm kernel runs 3 CTAs of 8 warps
-// on each, the AdamW kernel 4.  A set that gives every warp of a wave at most
-// one full range is split to fill one wave; beyond that the ranges stay at
-// their full size and CTAs follow one another.  Measured: a norm of 25 MB
-// takes 10.0 us split this way and 15.4 in ranges of 1024 elements; one of
-// 4.3 GB 597 us in ranges of 16384 elements, 796 of 4096; AdamW on 0.4M
-// elements 4.0 us, 8.4 in ranges of 1024.
-constexpr uint64_t kNormWave = 152 * 3 * ar::kGradWarps, kAdamWave = 152 * 4 * ar::kGradWarps;
-constexpr uint32_t kGradItemMax = 16384, kAdamItemStep = 256, kAdamItemMax = 1024;
+// on each, the AdamW kernel 4.  A set with less than a full range for every
+// warp of a wave is split to fill one wave; beyond that the ranges stay at
+// their full size.  Measured: a norm of 25 MB takes 9.8 us split this way and
+// 15.4 in ranges of 1024 elements; one of 4.2 GB in bf16 583 us in ranges of
+// 12288 elements, 587 and 597 of 8192 and 16384, in float32 1148 us, 1178 and
+// 1167; AdamW on 0.4M elements 3.9 us, 8.4 in ranges of 1024; on a billion,
+// the norm included, 4526 us in ranges of 512, 4545 and 4565 of 768 and 1024.
+constexpr uint64_t kNormWave = 152 * ar::kNormCtasPerSm * ar::kGradWarps, kAdamWave = 152 * 4 * ar::kGradWarps;
+constexpr uint32_t kGradItemMax = 12288, kAdamItemStep = 256, kAdamItemMax = 512;
 
 uint32_t item_elems(int n, const uint64_t* counts, uint64_t wave, uint32_t step, uint32_t most) {
     uint64_t total = 0;
@@ -38,10 +40,11 @@ uint32_t adam_item_elems(int n, const uint64_t* counts) {
     return item_elems(n, counts, kAdamWave, kAdamItemStep, kAdamItemMax);
 }
 
-// Gradient bytes at the end of a set that the norm before a scaling asks L2 to
-// keep (of 129 MB, which also hold the scaled results on their way out).
-// Measured on 96 MB of gradients: 51.6 us with none, 46.7 with 48 or 64 MB,
-// 48.0 with 100; on 2.7 GB 1162 us and 1159.
+// Gradient bytes at the end of a set that a norm asks L2 to keep (of 129 MB)
+// when it has a bound, for then the scaling or the update reads the gradients
+// next, last ones first.  Measured: clipping 96 MB into other tensors 51.6 us
+// with none, 46.7 with 48 or 64 MB, 48.0 with 100; the norm and AdamW on 244 MB
+// of bf16 gradients 447 us with none, 439 with 64 MB.
 constexpr uint64_t kKeepBytes = 64ull << 20;
 
 ar_status cuda_status(cudaError_t e) {
@@ -130,7 +133,7 @@ cudaError_t upload_items(const std::vector<Tensor>& tensors, const std::vector<u
 }
 
 // A positive number that float32 holds without losing digits.
-bool float_normal(double x) { return x >= 1.17549436e-38 && x <= 3.4028234e38; }
+bool float_normal(double x) { return x >= 1.17549436e-38 && x <= kFloatMax; }
 
 bool on_device(int device) {
     int now = -1;
@@ -145,16 +148,15 @@ bool float_buffer(const float* p, uint64_t n, int device) {
 }  // namespace
 
 struct ar_grads_s {
-    int n = 0, device = 0;
+    int n = 0, device = 0, num_sms = 0;
     ar_tensors_info info = {};
     uint32_t n_items = 0, keep_from = 0;
+    uint32_t least_es = 4;  // bytes of the gradients' smallest element type
     DeviceMemory memory;
     const ar::GradItem* items = nullptr;
     const uint32_t* first = nullptr;
-    uint64_t* cta_partials = nullptr;
-    uint64_t* group_partials = nullptr;
-    uint64_t* item_partials = nullptr;
-    uint32_t* counters = nullptr;
+    uint64_t* partials = nullptr;
+    uint32_t* drawn = nullptr;
 };
 
 struct ar_adamw_s {
@@ -181,33 +183,30 @@ ar_status run_norm(ar_grads_s* h, ar_norm_kind kind, double pre_scale, double ma
     a.n_items = h->n_items;
     a.keep_from = h->keep_from;
     a.kind = kind;
-    a.cta_partials = h->cta_partials;
-    a.group_partials = h->group_partials;
-    a.item_partials = norms ? h->item_partials : nullptr;
-    a.counters = h->counters;
+    a.partials = h->partials;
+    a.drawn = h->drawn;
     a.pre_scale = pre_scale;
     a.max_norm = max_norm;
     a.result = result;
+    a.first = h->first;
+    a.tensor_norms = tensor_norms;
+    a.n_tensors = norms ? h->n : 0;
     // one cluster holds the whole set (in the smallest ranges: a set in larger
     // ones has enough elements for half a wave of them)
     static_assert(kNormWave / 2 > ar::kSmallItems, "a set of kSmallItems ranges has the smallest ranges");
     const bool small = h->n_items <= ar::kSmallItems;
-    cudaError_t e = small ? ar::launch_small(a, clip, st) : ar::launch_norm(a, clip, st);
+    a.record_ctas = small ? 0 : ar::kFinishCtas;
+    cudaError_t e = small ? ar::launch_small(a, clip, st) : ar::launch_norm(a, max_norm <= kFloatMax, h->num_sms, st);
+    if (e == cudaSuccess && (!small || norms)) e = ar::launch_finish(a, st);
     if (e == cudaSuccess && clip && !small) {
         ar::ScaleArgs b = {};
         b.items = h->items;
         b.n_items = h->n_items;
+        b.item_warps = 1;
+        while (b.item_warps < ar::kGradWarps && b.item_warps * 2 * 4096 <= h->info.item_elems * h->least_es)
+            b.item_warps *= 2;  // 4 KB of gradients at least to each
         b.result = result;
         e = ar::launch_scale(b, st);
-    }
-    if (e == cudaSuccess && norms) {
-        ar::TensorNormArgs b = {};
-        b.item_partials = h->item_partials;
-        b.first = h->first;
-        b.kind = kind;
-        b.pre_scale = pre_scale;
-        b.norms = tensor_norms;
-        e = ar::launch_tensor_norms(b, h->n, st);
     }
     return cuda_status(e);
 }
@@ -258,6 +257,7 @@ ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype*
     try {
         h = new ar_grads_s();
         cudaError_t e = cudaGetDevice(&h->device);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
         if (e != cudaSuccess) {
             delete h;
             return cuda_status(e);
@@ -279,6 +279,7 @@ ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype*
         for (int t = 0; t < n_tensors; ++t) {
             const ar_dtype gt = grad_dtypes[t], ot = outs ? out_dtypes[t] : gt;
             void* dst = outs ? outs[t] : grads[t];
+            if (gt == AR_BFLOAT16) h->least_es = 2;
             const uint32_t flags = (gt == AR_BFLOAT16 ? ar::kGradBf16 : 0) | (ot == AR_BFLOAT16 ? ar::kOutBf16 : 0) |
                                    (dst == grads[t] ? ar::kInPlace : 0);
             tensors.push_back({static_cast<const char*>(grads[t]), static_cast<char*>(dst),
@@ -305,22 +306,17 @@ ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype*
             h->keep_from = first[t];
             room -= bytes;
         }
-        const uint32_t groups = ar::norm_groups(h->n_items);
         const size_t o_items = h->memory.part(sizeof(ar::GradItem) * h->n_items);
         const size_t o_first = h->memory.part(sizeof(uint32_t) * first.size());
-        const size_t o_cta = h->memory.part(sizeof(uint64_t) * ar::grad_ctas(h->n_items));
-        const size_t o_group = h->memory.part(sizeof(uint64_t) * groups);
-        const size_t o_parts = h->memory.part(sizeof(uint64_t) * h->n_items);
-        const size_t o_counters = h->memory.part(sizeof(uint32_t) * (groups + 1));
+        const size_t o_partials = h->memory.part(sizeof(uint64_t) * h->n_items);
+        const size_t o_drawn = h->memory.part(sizeof(uint32_t) * 32 * ar::kNormLists);
         e = h->memory.allocate();
         if (e == cudaSuccess) {
             h->items = h->memory.at<ar::GradItem>(o_items);
             h->first = h->memory.at<uint32_t>(o_first);
-            h->cta_partials = h->memory.at<uint64_t>(o_cta);
-            h->group_partials = h->memory.at<uint64_t>(o_group);
-            h->item_partials = h->memory.at<uint64_t>(o_parts);
-            h->counters = h->memory.at<uint32_t>(o_counters);
-            e = cudaMemset(h->counters, 0, sizeof(uint32_t) * (groups + 1));
+            h->partials = h->memory.at<uint64_t>(o_partials);
+            h->drawn = h->memory.at<uint32_t>(o_drawn);
+            e = cudaMemset(h->drawn, 0, sizeof(uint32_t) * 32 * ar::kNormLists);
         }
         if (e == cudaSuccess)
             e = upload_items(tensors, first, h->memory.at<uint32_t>(o_first), h->memory.at<ar::GradItem>(o_items));
@@ -376,7 +372,7 @@ ar_status ar_adamw_create(int n_tensors, const uint64_t* counts, const ar_dtype*
     if (n_tensors > 0 && (!params || !grads || !exp_avg || !exp_avg_sq)) return AR_ERR_INVALID_ARG;
     for (int t = 0; t < n_tensors; ++t) {
         if (copies && param_dtypes[t] != AR_FLOAT32) return AR_ERR_INVALID_ARG;
-        if (decay && !(decay[t] >= 0.f && decay[t] <= 3.4028234e38f)) return AR_ERR_INVALID_ARG;
+        if (decay && !(decay[t] >= 0.f && decay[t] <= kFloatMax)) return AR_ERR_INVALID_ARG;
     }
     ar_adamw_s* h = nullptr;
     try {
@@ -462,7 +458,7 @@ ar_status ar_adamw_destroy(ar_adamw_t h) {
 ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* p, const float* result, void* stream) {
     ar::TraceRange trace("ar_adamw_step");
     if (!h || !p) return AR_ERR_INVALID_ARG;
-    const auto finite = [](double x) { return x >= 0.0 && x <= 3.4028234e38; };
+    const auto finite = [](double x) { return x >= 0.0 && x <= kFloatMax; };
     if (p->step < 1 || !finite(p->lr) || !finite(p->weight_decay) || !finite(p->lr * p->weight_decay) ||
         !float_normal(p->eps) || !(p->beta1 >= 0.0 && p->beta1 < 1.0) ||
         !(p->beta2 >= 0.0 && p->beta2 < 1.0))

@@ -364,72 +364,93 @@ __device__ __forceinline__ void norm_item(Acc& acc, const char* src, uint32_t co
     if (lane < v.tail) acc.one(load_elem<BF>(src, count - v.tail + lane));
 }
 
-// Counts a CTA whose thread 0 has stored its sum; true in the one that came
-// last, whose threads then see every sum.
-__device__ __forceinline__ bool last_of(uint32_t* counter, uint32_t n, bool* flag) {
-    if (threadIdx.x == 0) {
-        uint32_t before;
-        asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"  // wraps to 0 for the next call
-                     : "=r"(before)
-                     : "l"(counter), "r"(n - 1)
-                     : "memory");
-        *flag = before == n - 1;
-    }
-    __syncthreads();
-    return *flag;
-}
-
-// Any number of items.  A warp sums one item, a CTA its warps.  Of every
-// kNormGroup CTAs the one that finishes last adds their sums, and the last of
-// those the groups' sums: each addition has its place whatever the order the
-// CTAs run in, so repeated calls give the same bits while the hardware deals
-// CTAs to SMs as they come free.  (One resident wave of CTAs looping over the
-// items instead left SMs idle for the last tenth: 5.9 TB/s against 7.2.)
-// CLIP: a scaling follows, in the reverse order.
-template <class Acc, bool CLIP>
-__global__ void __launch_bounds__(kGradThreads, 3) norm_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ uint64_t sm[kGradWarps];
-    __shared__ bool flag;
+// Any number of items, on one resident wave of CTAs.  A warp takes an item at a
+// time and leaves its sum in the item's place; finish_kernel adds them up in
+// their order, so repeated calls give the same bits whichever warp took which.
+// More items than warps are dealt to kNormLists lists, and a CTA's warps draw
+// from one of them, after a first two items each that are fixed: the SMs do
+// not all read at one rate (with equal shares some idled for the last tenth).
+// One list would do but for its counter: an item every 3 ns is what one
+// address gives out.  Item and draw are fetched one item ahead.
+// KEEP: a reader of the gradients follows, in the reverse order.
+template <class Acc, bool KEEP>
+__global__ void __launch_bounds__(kGradThreads, kNormCtasPerSm) norm_kernel(const __grid_constant__ NormArgs a) {
     const uint32_t lane = threadIdx.x & 31;
-    const uint32_t it = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    const uint32_t lists = a.n_items > gridDim.x * kGradWarps ? kNormLists : 1, list = blockIdx.x % lists;
+    const uint32_t warps = (gridDim.x - list + lists - 1) / lists * kGradWarps;  // that draw from this list
+    uint32_t it = list + lists * (blockIdx.x / lists * kGradWarps + (threadIdx.x >> 5)), next = it + lists * warps;
     GradItem w = {};  // the items are the handle's own and constant: read while the kernel before still runs
     if (it < a.n_items) w = a.items[it];
-    const uint64_t policy = CLIP ? keep_policy(it >= a.keep_from) : 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    while (it < a.n_items) {
+        GradItem ahead = {};
+        uint32_t drawn = 0;
+        if (next < a.n_items) {
+            ahead = a.items[next];
+            if (lane == 0) drawn = atomicAdd(a.drawn + 32 * list, 1u);
+        }
+        Acc acc;
+        const uint64_t policy = KEEP ? keep_policy(it >= a.keep_from) : 0;
+        if (w.flags & kGradBf16)
+            norm_item<Acc, true, KEEP>(acc, w.src, w.count, lane, policy);
+        else
+            norm_item<Acc, false, KEEP>(acc, w.src, w.count, lane, policy);
+        warp_join(acc);
+        if (lane == 0) a.partials[it] = acc.bits();
+        it = next;
+        w = ahead;
+        next = list + lists * (2 * warps + __shfl_sync(kFull, drawn, 0));
+    }
+}
+
+// The sums of a cluster's CTAs, in their order, through their shared memory:
+// thread 0 of every CTA gets the total.  mine: the CTA's sum, in its thread 0.
+template <class Acc>
+__device__ __forceinline__ Acc cluster_join(const Acc& mine, uint64_t* sums, uint32_t ctas, uint32_t rank) {
+    if (threadIdx.x < 32) {
+        const uint64_t bits = __shfl_sync(kFull, mine.bits(), 0);
+        if (threadIdx.x < ctas) {  // to CTA number `lane`'s shared memory
+            uint32_t to;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(sums + rank)), "r"(threadIdx.x));
+            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(bits) : "memory");
+        }
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    Acc all;
+    if (threadIdx.x == 0)
+        for (uint32_t c = 0; c < ctas; ++c) all.join(sums[c]);
+    return all;
+}
+
+// The items' sums to the record (the first record_ctas CTAs, one cluster) and to
+// the norms of single tensors (a CTA each, after them).
+template <class Acc>
+__global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ uint64_t sm[kFinishThreads / 32], sums[kFinishCtas];
     griddep_wait();
     griddep_launch_dependents();
     Acc acc;
-    if (w.flags & kGradBf16)
-        norm_item<Acc, true, CLIP>(acc, w.src, w.count, lane, policy);
-    else
-        norm_item<Acc, false, CLIP>(acc, w.src, w.count, lane, policy);
-    warp_join(acc);
-    if (lane == 0) {
-        if (a.item_partials && it < a.n_items) a.item_partials[it] = acc.bits();
-        sm[threadIdx.x >> 5] = acc.bits();
+    if (blockIdx.x < a.record_ctas) {
+#pragma unroll 8
+        for (uint32_t i = blockIdx.x * kFinishThreads + threadIdx.x; i < a.n_items; i += kFinishCtas * kFinishThreads)
+            acc.join(a.partials[i]);
+        cta_join<Acc, kFinishThreads / 32>(acc, sm);
+        const Acc all = cluster_join(acc, sums, kFinishCtas, blockIdx.x);
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            store_record(a.result, make_record(all, a.pre_scale, a.max_norm));
+        }
+        if (blockIdx.x == 0 && threadIdx.x < kNormLists) a.drawn[32 * threadIdx.x] = 0;  // for the next call
+        return;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        Acc b;
-#pragma unroll
-        for (int k = 0; k < kGradWarps; ++k) b.join(sm[k]);
-        a.cta_partials[blockIdx.x] = b.bits();
-    }
-    const uint32_t group = blockIdx.x / kNormGroup, groups = (gridDim.x + kNormGroup - 1) / kNormGroup;
-    const uint32_t first = group * kNormGroup, size = min(kNormGroup, gridDim.x - first);
-    if (!last_of(a.counters + group, size, &flag)) return;
-    Acc all;
-#pragma unroll
-    for (uint32_t k = 0; k < kNormGroup; k += kGradThreads)
-        if (k + threadIdx.x < size) all.join(__ldcg(a.cta_partials + first + k + threadIdx.x));
-    cta_join<Acc, kGradWarps>(all, sm);
-    if (groups > 1) {
-        if (threadIdx.x == 0) a.group_partials[group] = all.bits();
-        if (!last_of(a.counters + groups, groups, &flag)) return;
-        all = Acc();
-        for (uint32_t i = threadIdx.x; i < groups; i += kGradThreads) all.join(__ldcg(a.group_partials + i));
-        cta_join<Acc, kGradWarps>(all, sm);
-    }
-    if (threadIdx.x == 0) store_record(a.result, make_record(all, a.pre_scale, a.max_norm));
+    const uint32_t t = blockIdx.x - a.record_ctas;
+    if (t >= a.n_tensors) return;
+#pragma unroll 8
+    for (uint32_t i = a.first[t] + threadIdx.x; i < a.first[t + 1]; i += kFinishThreads) acc.join(a.partials[i]);
+    cta_join<Acc, kFinishThreads / 32>(acc, sm);
+    if (threadIdx.x == 0) a.tensor_norms[t] = make_record(acc, a.pre_scale, 0.0).norm;
 }
 
 // Small sets: one cluster, an item to a warp, the sums exchanged through the
@@ -469,27 +490,17 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
     if (lane < tail) acc.one(edge[1]);
     warp_join(acc);
     if (lane == 0) {
-        if (a.item_partials && it < a.n_items) a.item_partials[it] = acc.bits();
+        if (it < a.n_items) a.partials[it] = acc.bits();
         sm[warp] = acc.bits();
     }
     __syncthreads();
+    Acc cta;
     if (warp == 0) {
-        Acc b;
-        if (lane < kSmallWarps) b.join(sm[lane]);
-        warp_join(b);
-        const uint64_t mine = __shfl_sync(kFull, b.bits(), 0);
-        if (lane < gridDim.x) {  // this CTA's sum to CTA `lane`'s shared memory
-            uint32_t to;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(sums + blockIdx.x)), "r"(lane));
-            asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(mine) : "memory");
-        }
+        if (lane < kSmallWarps) cta.join(sm[lane]);
+        warp_join(cta);
     }
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const Acc all = cluster_join(cta, sums, gridDim.x, blockIdx.x);
     if (threadIdx.x == 0) {
-        Acc all;
-        for (uint32_t c = 0; c < gridDim.x; ++c) all.join(sums[c]);
         const Record r = make_record(all, a.pre_scale, a.max_norm);
         factor = r.scale;
         if (blockIdx.x == 0) store_record(a.result, r);
@@ -530,39 +541,26 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
     if (lane < tail) store_edge(w.count - tail + lane, edge[1]);
 }
 
-// Norms of single tensors: a CTA adds one tensor's item sums.
-template <class Acc>
-__global__ void __launch_bounds__(kTensorNormThreads) tensor_norm_kernel(const __grid_constant__ TensorNormArgs a) {
-    __shared__ uint64_t sm[kTensorNormThreads / 32];
-    griddep_wait();
-    griddep_launch_dependents();
-    const uint32_t lo = a.first[blockIdx.x], hi = a.first[blockIdx.x + 1];
-    Acc acc;
-#pragma unroll 8
-    for (uint32_t i = lo + threadIdx.x; i < hi; i += kTensorNormThreads) acc.join(a.item_partials[i]);
-    cta_join<Acc, kTensorNormThreads / 32>(acc, sm);
-    if (threadIdx.x == 0) a.norms[blockIdx.x] = make_record(acc, a.pre_scale, 0.0).norm;
-}
-
 // ---------------------------------------------------------------- the scaling
 
 // dst = round(f * src) over one item, in quads of four elements.
 template <bool SB, bool DB>
-__device__ __forceinline__ void scale_item(const char* src, char* dst, uint32_t count, float f, uint32_t lane) {
+__device__ __forceinline__ void scale_item(const char* src, char* dst, uint32_t count, float f, uint32_t lane,
+                                           uint32_t lanes) {
     constexpr int U = 8;
     const uint32_t head = min(count, head_elems<SB>(src, SB ? 8 : 16));
     const bool whole = quad_aligned<DB>(dst, head);
     const uint32_t nq = (count - head) / 4;
     const uint32_t done = head + nq * 4;
-    for (uint32_t q = lane; q < nq; q += 32 * U) {
+    for (uint32_t q = lane; q < nq; q += lanes * U) {
         float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (q + 32 * u < nq) x[u] = load_quad<SB, true>(src, head + 4 * (q + 32 * u), true);
+            if (q + lanes * u < nq) x[u] = load_quad<SB, true>(src, head + 4 * (q + lanes * u), true);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (q + 32 * u < nq)
-                store_quad<DB, true>(dst, head + 4 * (q + 32 * u),
+            if (q + lanes * u < nq)
+                store_quad<DB, true>(dst, head + 4 * (q + lanes * u),
                                make_float4(__fmul_rn(x[u].x, f), __fmul_rn(x[u].y, f), __fmul_rn(x[u].z, f),
                                            __fmul_rn(x[u].w, f)),
                                whole);
@@ -577,23 +575,24 @@ __device__ __forceinline__ void scale_item(const char* src, char* dst, uint32_t 
 // results do not push out the gradients that wait there.
 // In place, a factor of exactly 1 leaves nothing to do.
 __global__ void __launch_bounds__(kGradThreads, 4) scale_kernel(const __grid_constant__ ScaleArgs a) {
-    const uint32_t lane = threadIdx.x & 31;
-    const uint32_t w = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    const uint32_t warp = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
+    const uint32_t i = warp / a.item_warps, lanes = 32 * a.item_warps;
+    const uint32_t lane = (warp % a.item_warps) * 32 + (threadIdx.x & 31);
     GradItem it = {};
-    if (w < a.n_items) it = a.items[a.n_items - 1 - w];
+    if (i < a.n_items) it = a.items[a.n_items - 1 - i];
     griddep_wait();
     griddep_launch_dependents();
     const float f = __ldcg(a.result + 1);
     if ((it.flags & kInPlace) && f == 1.f) return;
     const bool sb = it.flags & kGradBf16, db = it.flags & kOutBf16;
     if (sb && db)
-        scale_item<true, true>(it.src, it.dst, it.count, f, lane);
+        scale_item<true, true>(it.src, it.dst, it.count, f, lane, lanes);
     else if (sb)
-        scale_item<true, false>(it.src, it.dst, it.count, f, lane);
+        scale_item<true, false>(it.src, it.dst, it.count, f, lane, lanes);
     else if (db)
-        scale_item<false, true>(it.src, it.dst, it.count, f, lane);
+        scale_item<false, true>(it.src, it.dst, it.count, f, lane, lanes);
     else
-        scale_item<false, false>(it.src, it.dst, it.count, f, lane);
+        scale_item<false, false>(it.src, it.dst, it.count, f, lane, lanes);
 }
 
 // ---------------------------------------------------------------------- AdamW
@@ -755,7 +754,7 @@ cudaError_t make_items(const Tensor* tensors, const uint32_t* first, int n, uint
 }
 
 template <class Args>
-cudaError_t launch(void (*f)(Args), const Args& a, uint32_t grid, int block, cudaStream_t st, bool cluster = false) {
+cudaError_t launch(void (*f)(Args), const Args& a, uint32_t grid, int block, cudaStream_t st, uint32_t cluster = 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(static_cast<unsigned>(block));
@@ -764,7 +763,7 @@ cudaError_t launch(void (*f)(Args), const Args& a, uint32_t grid, int block, cud
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = AR_PDL;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = grid;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
@@ -785,11 +784,12 @@ cudaError_t launch_items(const AdamTensor* tensors, const uint32_t* first, int n
     return make_items(tensors, first, n, n_items, items, st);
 }
 
-cudaError_t launch_norm(const NormArgs& a, bool before_scale, cudaStream_t st) {
+cudaError_t launch_norm(const NormArgs& a, bool keep, int num_sms, cudaStream_t st) {
     const bool max = a.kind == AR_NORM_MAX;
-    return launch(before_scale ? (max ? norm_kernel<MaxAbs, true> : norm_kernel<SumSquares, true>)
-                               : (max ? norm_kernel<MaxAbs, false> : norm_kernel<SumSquares, false>),
-                  a, grad_ctas(a.n_items), kGradThreads, st);
+    const uint32_t wave = static_cast<uint32_t>(num_sms) * kNormCtasPerSm, ctas = grad_ctas(a.n_items);
+    return launch(keep ? (max ? norm_kernel<MaxAbs, true> : norm_kernel<SumSquares, true>)
+                       : (max ? norm_kernel<MaxAbs, false> : norm_kernel<SumSquares, false>),
+                  a, ctas < wave ? ctas : wave, kGradThreads, st);
 }
 
 cudaError_t launch_small(const NormArgs& a, bool scale, cudaStream_t st) {
@@ -797,16 +797,18 @@ cudaError_t launch_small(const NormArgs& a, bool scale, cudaStream_t st) {
     const uint32_t ctas = a.n_items == 0 ? 1 : (a.n_items + kSmallWarps - 1) / kSmallWarps;
     return launch(scale ? (max ? small_kernel<MaxAbs, true> : small_kernel<SumSquares, true>)
                         : (max ? small_kernel<MaxAbs, false> : small_kernel<SumSquares, false>),
-                  a, ctas, kSmallThreads, st, true);
+                  a, ctas, kSmallThreads, st, ctas);
 }
 
-cudaError_t launch_tensor_norms(const TensorNormArgs& a, int n_tensors, cudaStream_t st) {
-    return launch(a.kind == AR_NORM_MAX ? tensor_norm_kernel<MaxAbs> : tensor_norm_kernel<SumSquares>, a,
-                  static_cast<uint32_t>(n_tensors), kTensorNormThreads, st);
+cudaError_t launch_finish(const NormArgs& a, cudaStream_t st) {
+    const uint32_t ctas = a.record_ctas + (a.n_tensors + kFinishCtas - 1) / kFinishCtas * kFinishCtas;
+    return launch(a.kind == AR_NORM_MAX ? finish_kernel<MaxAbs> : finish_kernel<SumSquares>, a, ctas, kFinishThreads,
+                  st, kFinishCtas);
 }
 
 cudaError_t launch_scale(const ScaleArgs& a, cudaStream_t st) {
-    return launch(scale_kernel, a, grad_ctas(a.n_items), kGradThreads, st);
+    const uint32_t warps = a.n_items * a.item_warps;
+    return launch(scale_kernel, a, (warps + kGradWarps - 1) / kGradWarps, kGradThreads, st);
 }
 
 cudaError_t launch_adamw(const AdamArgs& a, bool whole, cudaStream_t st) {

@@ -84,9 +84,10 @@ struct alignas(16) AdamItem {
 
 constexpr int kGradThreads = 256;  // 8 warps, an item each
 constexpr int kGradWarps = kGradThreads / 32;
-constexpr int kTensorNormThreads = 128;
-// CTAs whose sums one CTA adds up (four a thread) on the way to the norm
-constexpr uint32_t kNormGroup = 4 * kGradThreads;
+constexpr int kNormCtasPerSm = 3;
+constexpr uint32_t kNormLists = 8;
+// The cluster that adds up the items' sums
+constexpr uint32_t kFinishThreads = 512, kFinishCtas = 8;
 // Small sets: one cluster, a range of at most kSmallItemElems to each warp
 constexpr int kSmallThreads = 512;
 constexpr int kSmallWarps = kSmallThreads / 32;
@@ -97,32 +98,26 @@ constexpr uint32_t kSmallItemElems = 1024;
 inline uint32_t grad_ctas(uint32_t n_items) {
     return n_items <= kGradWarps ? 1 : (n_items + kGradWarps - 1) / kGradWarps;
 }
-inline uint32_t norm_groups(uint32_t n_items) { return (grad_ctas(n_items) + kNormGroup - 1) / kNormGroup; }
 
 struct NormArgs {
     const GradItem* items;
     uint32_t n_items;
-    uint32_t keep_from;        // before a scaling: items from here on stay in L2 for it
-    int kind;                  // AR_NORM_L2 or AR_NORM_MAX
-    uint64_t* cta_partials;    // one per CTA
-    uint64_t* group_partials;  // one per kNormGroup CTAs
-    uint64_t* item_partials;   // one per item, or null: no norms of single tensors
-    uint32_t* counters;        // CTAs done of each group, then groups done; 0 between calls
+    uint32_t keep_from;     // launch_norm's keep: items from here on stay in L2
+    int kind;               // AR_NORM_L2 or AR_NORM_MAX
+    uint64_t* partials;     // each item's sum
+    uint32_t* drawn;        // items drawn from the counter; 0 between calls
     double pre_scale, max_norm;
-    float* result;             // norm, scale, nonfinite, clipped
-};
-
-struct TensorNormArgs {
-    const uint64_t* item_partials;
-    const uint32_t* first;     // n + 1: each tensor's first item
-    int kind;
-    double pre_scale;
-    float* norms;              // n
+    float* result;          // norm, scale, nonfinite, clipped
+    uint32_t record_ctas;   // finish: CTAs that write the record: 0 or kFinishCtas
+    const uint32_t* first;  // finish: each tensor's first item (n_tensors + 1)
+    float* tensor_norms;    // finish: the norms of single tensors
+    uint32_t n_tensors;     // finish: their number, or 0
 };
 
 struct ScaleArgs {
     const GradItem* items;
     uint32_t n_items;
+    uint32_t item_warps;    // warps that share an item: 1, 2, 4 or 8
     const float* result;
 };
 
@@ -144,10 +139,12 @@ cudaError_t launch_items(const GradTensor* tensors, const uint32_t* first, int n
 cudaError_t launch_items(const AdamTensor* tensors, const uint32_t* first, int n, uint32_t n_items, AdamItem* items,
                          cudaStream_t st);
 
-cudaError_t launch_norm(const NormArgs& a, bool before_scale, cudaStream_t st);
-cudaError_t launch_tensor_norms(const TensorNormArgs& a, int n_tensors, cudaStream_t st);
+// Every item's sum, for launch_finish.  keep: the gradients are read again
+// after it, last items first; num_sms: the device's.
+cudaError_t launch_norm(const NormArgs& a, bool keep, int num_sms, cudaStream_t st);
+cudaError_t launch_finish(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_scale(const ScaleArgs& a, cudaStream_t st);
-// The norm and, with `scale`, the scaling in one launch: at most kSmallItems
+// The sums, the record and, with `scale`, the scaling in one launch: at most kSmallItems
 // items of at most kSmallItemElems elements.
 cudaError_t launch_small(const NormArgs& a, bool scale, cudaStream_t st);
 // whole: every stream of every tensor can be read and written in quads.
