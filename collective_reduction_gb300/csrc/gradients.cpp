@@ -197,7 +197,11 @@ ar_status run_norm(ar_grads_s* h, ar_norm_kind kind, double pre_scale, double ma
     const bool small = h->n_items <= ar::kSmallItems;
     a.record_ctas = small ? 0 : ar::kFinishCtas;
     cudaError_t e = small ? ar::launch_small(a, clip, st) : ar::launch_norm(a, max_norm <= kFloatMax, h->num_sms, st);
-    if (e == cudaSuccess && (!small || norms)) e = ar::launch_finish(a, st);
+    if (e == cudaSuccess && (!small || norms)) {
+        e = ar::launch_finish(a, st);
+        // what would have put the counters back did not start
+        if (e != cudaSuccess) cudaMemsetAsync(h->drawn, 0, sizeof(uint32_t) * 32 * ar::kNormLists, st);
+    }
     if (e == cudaSuccess && clip && !small) {
         ar::ScaleArgs b = {};
         b.items = h->items;

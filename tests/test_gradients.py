@@ -479,6 +479,69 @@ def test_offsets_past_32_bits():
 
 
 @gpu
+@pytest.mark.parametrize("types", ["float32", "bfloat16"])
+def test_sets_around_the_kernels_limits(types):
+    """Ranges on both sides of one cluster (128), of one wave of warps (3648),
+    and enough that warps draw them: the sums, and each tensor's own."""
+    import torch
+    wave = 152 * 3 * 8
+    for n in ([1] * 127, [1] * 128, [1] * 129, [1024] * 128, [1023, 1025] * 64, [5] * wave, [5] * (wave + 1),
+              [3] * (9 * wave), [wave * 1024 - 1], [wave * 1024], [wave * 12288 + 7, 11], [3 * wave * 12288, 1, 70000]):
+        x = torch.empty(sum(n), dtype=tdt(types), device="cuda")
+        x.copy_(torch.randn(x.numel(), generator=torch.Generator(device="cuda").manual_seed(len(n)), device="cuda"))
+        h = ar.Grads(list(x.split(n)))
+        wide = x.double().square_()
+        each = [c.sum() for c in wide.split(n)] if len(n) < 1000 else list(wide.view(len(n), -1).sum(1))
+        per = torch.empty(len(n), device="cuda")
+        for k in range(2):  # the counters are back in place
+            got = h.norm(per_tensor=per)[0].item()
+            assert_close(got, math.sqrt(wide.sum().item()), 10 * U, (len(n), n[0]))
+            want = torch.stack(each).sqrt()
+            assert bool(((per.double() - want).abs() <= 10 * U * want).all())
+        rec = h.clip(0.5 * got).tolist()
+        assert_close(rec[1], 0.5, 12 * U, "scale")
+        h.close()
+
+
+@gpu
+@pytest.mark.parametrize("P,n", [(1, 1000), (3, 100003), (8, 70), (8, 1000001)])
+def test_sharded_training_step(P, n):
+    """reduce-scatter, norm, AdamW, all-gather: the norm is the averaged
+    gradient's, every rank ends with the owners' rounded weights, and the loss
+    falls."""
+    import sys
+    import torch
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import zero_step
+    z = zero_step.ZeroStep(P, n, weight_decay=0.01)
+    chunks = zero_step.owned(P, n)
+    assert sorted(i for a, b in chunks for i in range(a, b)) == list(range(n))
+    losses = []
+    for _ in range(4):
+        losses.append(z.backward().item())
+        mean = sum(g.double() for g in z.grads) / P
+        before = [x.double().cpu() for x in z.master], [x.double().cpu() for x in z.exp_avg], \
+            [x.double().cpu() for x in z.exp_avg_sq]
+        rec = z.step().tolist()
+        # P - 1 float32 additions and a division: P u of the terms' magnitudes, below 2 P u of a norm of this kind
+        assert_close(rec[0], float(mean.norm()), (10 + 2 * P) * U, "norm")
+        for r, (a, b) in enumerate(chunks):
+            g = z.grads[r][a:b].double().cpu()
+            want = adamw_reference(before[0][r], g, before[1][r], before[2][r], rec[1], z.steps, z.lr, 0.9, 0.999,
+                                   1e-8, 0.01)
+            assert bool(((z.master[r].double().cpu() - want[0]).abs() <= want[3]).all())
+            assert all(torch.equal(w[a:b], z.master[r].bfloat16()) for w in z.weights)
+    assert losses == sorted(losses, reverse=True)
+    z.scatter.check()
+    z.gather.check()
+    before = [w.clone() for w in z.weights]
+    z.capture().replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(z.weights[0], w) for w in z.weights)
+    assert not torch.equal(before[0], z.weights[0])
+
+
+@gpu
 def test_refusals():
     import torch
     a, b = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
