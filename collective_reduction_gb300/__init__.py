@@ -142,6 +142,7 @@ _EXPORTS = {
     "ar_adamw_query": (ctypes.c_int, [_VP, ctypes.POINTER(TensorsInfo)]),
     "ar_adamw_destroy": (ctypes.c_int, [_VP]),
     "ar_adamw_step": (ctypes.c_int, [_VP, ctypes.POINTER(AdamWParams), _VP, _VP]),
+    "ar_adamw_step_counted": (ctypes.c_int, [_VP, ctypes.POINTER(AdamWParams), _VP, _VP, _VP, _VP]),
 }
 
 
@@ -452,12 +453,26 @@ class AdamW:
     def step(self, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, clip=None, stream=None):
         """Enqueue update number `step` (from 1).  `clip`: the record of a norm
         of these gradients; its scale multiplies them, and if it says
-        nonfinite nothing changes."""
-        if step < 1:
-            raise ValueError("step counts from 1")
-        p = AdamWParams(int(step), lr, beta1, beta2, eps, weight_decay)
+        nonfinite nothing changes.
+
+        For a CUDA graph, `step` is a CUDA tensor of one int64: the number of
+        updates done, which the call counts up unless the update is skipped;
+        `lr` may then be a float32 CUDA tensor too."""
         record = None if clip is None else _float_out(clip, 4, "clip")
-        _check(lib().ar_adamw_step(self._h, ctypes.byref(p), record, _stream_handle(stream)), "ar_adamw_step")
+        stream = _stream_handle(stream)
+        if not hasattr(step, "data_ptr"):
+            if step < 1:
+                raise ValueError("step counts from 1")
+            p = AdamWParams(int(step), lr, beta1, beta2, eps, weight_decay)
+            _check(lib().ar_adamw_step(self._h, ctypes.byref(p), record, stream), "ar_adamw_step")
+            return
+        if str(step.dtype) != "torch.int64" or not step.is_cuda or step.numel() != 1:
+            raise ValueError("step: expected an int or a CUDA tensor of one int64")
+        on_device = hasattr(lr, "data_ptr")
+        p = AdamWParams(0, 0.0 if on_device else lr, beta1, beta2, eps, weight_decay)
+        _check(lib().ar_adamw_step_counted(self._h, ctypes.byref(p), step.data_ptr(),
+                                           _float_out(lr, 1, "lr") if on_device else None, record, stream),
+               "ar_adamw_step_counted")
 
     def close(self):
         if getattr(self, "_h", None):

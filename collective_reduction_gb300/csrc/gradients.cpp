@@ -42,9 +42,10 @@ uint32_t adam_item_elems(int n, const uint64_t* counts) {
 
 // Gradient bytes at the end of a set that a norm asks L2 to keep (of 129 MB)
 // when it has a bound, for then the scaling or the update reads the gradients
-// next, last ones first.  Measured: clipping 96 MB into other tensors 51.6 us
-// with none, 46.7 with 48 or 64 MB, 48.0 with 100; the norm and AdamW on 244 MB
-// of bf16 gradients 447 us with none, 439 with 64 MB.
+// next, last ones first.  Measured with none and with 64 MB: clipping 96 MB into
+// other tensors 47.0 and 44.5 us (47.3 with 32 MB, 44.0 with 96); the norm and
+// AdamW on 48 MB of float32 gradients 65.5 and 61.3 us, on 244 MB of bf16 441 and
+// 433; clipping 2.7 GB 1137 and 1139.
 constexpr uint64_t kKeepBytes = 64ull << 20;
 
 ar_status cuda_status(cudaError_t e) {
@@ -166,6 +167,7 @@ struct ar_adamw_s {
     bool whole = true;
     DeviceMemory memory;
     const ar::AdamItem* items = nullptr;
+    ar::AdamScalars* scalars = nullptr;
 };
 
 namespace {
@@ -213,6 +215,26 @@ ar_status run_norm(ar_grads_s* h, ar_norm_kind kind, double pre_scale, double ma
         e = ar::launch_scale(b, st);
     }
     return cuda_status(e);
+}
+
+bool float_finite(double x) { return x >= 0.0 && x <= kFloatMax; }
+
+bool adam_params_ok(const ar_adamw_params& p) {
+    return float_finite(p.lr) && float_finite(p.weight_decay) && float_finite(p.lr * p.weight_decay) &&
+           float_normal(p.eps) && p.beta1 >= 0.0 && p.beta1 < 1.0 && p.beta2 >= 0.0 && p.beta2 < 1.0;
+}
+
+ar::AdamArgs adam_args(const ar_adamw_s* h, const ar_adamw_params& p, const float* result) {
+    ar::AdamArgs a = {};
+    a.items = h->items;
+    a.n_items = h->n_items;
+    a.result = result;
+    a.beta1 = static_cast<float>(p.beta1);
+    a.omb1 = static_cast<float>(1.0 - p.beta1);
+    a.beta2 = static_cast<float>(p.beta2);
+    a.omb2 = static_cast<float>(1.0 - p.beta2);
+    a.eps = static_cast<float>(p.eps);
+    return a;
 }
 
 }  // namespace
@@ -427,6 +449,7 @@ ar_status ar_adamw_create(int n_tensors, const uint64_t* counts, const ar_dtype*
         }
         const size_t o_items = h->memory.part(sizeof(ar::AdamItem) * h->n_items);
         const size_t o_first = h->memory.part(sizeof(uint32_t) * first.size());
+        const size_t o_scalars = h->memory.part(sizeof(ar::AdamScalars));
         cudaError_t up = h->memory.allocate();
         if (up == cudaSuccess)
             up = upload_items(tensors, first, h->memory.at<uint32_t>(o_first), h->memory.at<ar::AdamItem>(o_items));
@@ -435,6 +458,7 @@ ar_status ar_adamw_create(int n_tensors, const uint64_t* counts, const ar_dtype*
             return cuda_status(up);
         }
         h->items = h->memory.at<ar::AdamItem>(o_items);
+        h->scalars = h->memory.at<ar::AdamScalars>(o_scalars);
         fill_info(n_tensors, counts, elems, h->n_items, &h->info);
         h->info.table_bytes = h->memory.bytes;
         h->info.tiling_ok = 1;
@@ -461,30 +485,41 @@ ar_status ar_adamw_destroy(ar_adamw_t h) {
 
 ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* p, const float* result, void* stream) {
     ar::TraceRange trace("ar_adamw_step");
-    if (!h || !p) return AR_ERR_INVALID_ARG;
-    const auto finite = [](double x) { return x >= 0.0 && x <= kFloatMax; };
-    if (p->step < 1 || !finite(p->lr) || !finite(p->weight_decay) || !finite(p->lr * p->weight_decay) ||
-        !float_normal(p->eps) || !(p->beta1 >= 0.0 && p->beta1 < 1.0) ||
-        !(p->beta2 >= 0.0 && p->beta2 < 1.0))
-        return AR_ERR_INVALID_ARG;
+    if (!h || !p || p->step < 1 || !adam_params_ok(*p)) return AR_ERR_INVALID_ARG;
     const double t = static_cast<double>(p->step);
     const double bc1 = 1.0 - std::pow(p->beta1, t), bc2 = 1.0 - std::pow(p->beta2, t);
-    if (!finite(p->lr / bc1)) return AR_ERR_INVALID_ARG;
+    if (!float_finite(p->lr / bc1)) return AR_ERR_INVALID_ARG;
     if (!on_device(h->device) || (result && !float_buffer(result, 4, h->device))) return AR_ERR_INVALID_ARG;
     if (h->n_items == 0) return AR_OK;
-    ar::AdamArgs a = {};
-    a.items = h->items;
-    a.n_items = h->n_items;
-    a.result = result;
-    a.beta1 = static_cast<float>(p->beta1);
-    a.omb1 = static_cast<float>(1.0 - p->beta1);
-    a.beta2 = static_cast<float>(p->beta2);
-    a.omb2 = static_cast<float>(1.0 - p->beta2);
-    a.step_size = static_cast<float>(p->lr / bc1);
-    a.inv_bc2 = static_cast<float>(1.0 / std::sqrt(bc2));
-    a.eps = static_cast<float>(p->eps);
-    a.lr_decay = static_cast<float>(p->lr * p->weight_decay);
+    ar::AdamArgs a = adam_args(h, *p, result);
+    a.scalars = {static_cast<float>(p->lr / bc1), static_cast<float>(1.0 / std::sqrt(bc2)),
+                 static_cast<float>(p->lr * p->weight_decay)};
     return cuda_status(ar::launch_adamw(a, h->whole, static_cast<cudaStream_t>(stream)));
+}
+
+ar_status ar_adamw_step_counted(ar_adamw_t h, const ar_adamw_params* p, uint64_t* steps, const float* lr,
+                                const float* result, void* stream) {
+    ar::TraceRange trace("ar_adamw_step_counted");
+    if (!h || !p || !adam_params_ok(*p)) return AR_ERR_INVALID_ARG;
+    if (!on_device(h->device) || !steps || reinterpret_cast<uintptr_t>(steps) % sizeof(uint64_t) != 0 ||
+        !ar::device_resident(steps, sizeof(uint64_t), h->device) || (lr && !float_buffer(lr, 1, h->device)) ||
+        (result && !float_buffer(result, 4, h->device)))
+        return AR_ERR_INVALID_ARG;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    ar::CountArgs c = {};
+    c.steps = steps;
+    c.lr = lr;
+    c.result = result;
+    c.host_lr = p->lr;
+    c.beta1 = p->beta1;
+    c.beta2 = p->beta2;
+    c.weight_decay = p->weight_decay;
+    c.scalars = h->scalars;
+    cudaError_t e = ar::launch_count(c, st);
+    if (e != cudaSuccess || h->n_items == 0) return cuda_status(e);
+    ar::AdamArgs a = adam_args(h, *p, result);
+    a.counted = h->scalars;
+    return cuda_status(ar::launch_adamw(a, h->whole, st));
 }
 
 }  // extern "C"

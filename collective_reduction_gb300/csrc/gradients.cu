@@ -600,32 +600,33 @@ __global__ void __launch_bounds__(kGradThreads, 4) scale_kernel(const __grid_con
 // One element: moments and parameter, in float32.  The decay is subtracted
 // with the update (p - (lr wd p + update)), so its small factor is never
 // rounded against 1.
-__device__ __forceinline__ void adam_one(const AdamArgs& a, float decay, float f, float& p, float g, float& m,
+__device__ __forceinline__ void adam_one(const AdamArgs& a, const AdamScalars& s, float decay, float f, float& p, float g, float& m,
                                          float& v) {
     g = __fmul_rn(g, f);
     m = __fmaf_rn(a.omb1, g, __fmul_rn(a.beta1, m));
     v = __fmaf_rn(__fmul_rn(a.omb2, g), g, __fmul_rn(a.beta2, v));
-    const float den = __fmaf_rn(__fsqrt_rn(v), a.inv_bc2, a.eps);
-    const float upd = __fmul_rn(a.step_size, __fdiv_rn(m, den));
+    const float den = __fmaf_rn(__fsqrt_rn(v), s.inv_bc2, a.eps);
+    const float upd = __fmul_rn(s.step_size, __fdiv_rn(m, den));
     p = __fsub_rn(p, __fmaf_rn(decay, p, upd));
 }
 
-__device__ __forceinline__ void adam_quad(const AdamArgs& a, float decay, float f, float4& p, float4 g, float4& m,
+__device__ __forceinline__ void adam_quad(const AdamArgs& a, const AdamScalars& s, float decay, float f, float4& p, float4 g, float4& m,
                                           float4& v) {
-    adam_one(a, decay, f, p.x, g.x, m.x, v.x);
-    adam_one(a, decay, f, p.y, g.y, m.y, v.y);
-    adam_one(a, decay, f, p.z, g.z, m.z, v.z);
-    adam_one(a, decay, f, p.w, g.w, m.w, v.w);
+    adam_one(a, s, decay, f, p.x, g.x, m.x, v.x);
+    adam_one(a, s, decay, f, p.y, g.y, m.y, v.y);
+    adam_one(a, s, decay, f, p.z, g.z, m.z, v.z);
+    adam_one(a, s, decay, f, p.w, g.w, m.w, v.w);
 }
 
 template <bool PB, bool GB, bool COPY>
-__device__ __forceinline__ void adam_elem(const AdamArgs& a, const AdamItem& it, float decay, float f, uint32_t i) {
+__device__ __forceinline__ void adam_elem(const AdamArgs& a, const AdamScalars& s, const AdamItem& it, float decay, float f,
+                                          uint32_t i) {
     char* mp = reinterpret_cast<char*>(it.m);
     char* vp = reinterpret_cast<char*>(it.v);
     float p = __uint_as_float(load_elem<PB>(it.p, i)), m = __uint_as_float(load_elem<false>(mp, i));
     const float g = __uint_as_float(load_elem<GB>(it.g, i));
     float v = __uint_as_float(load_elem<false>(vp, i));
-    adam_one(a, decay, f, p, g, m, v);
+    adam_one(a, s, decay, f, p, g, m, v);
     store_elem<PB>(it.p, i, p);
     store_elem<false>(mp, i, m);
     store_elem<false>(vp, i, v);
@@ -633,9 +634,10 @@ __device__ __forceinline__ void adam_elem(const AdamArgs& a, const AdamItem& it,
 }
 
 template <bool PB, bool GB, bool COPY, bool WHOLE>
-__device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamItem& it, float f, uint32_t lane) {
+__device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamScalars& s, const AdamItem& it, float f,
+                                          uint32_t lane) {
     constexpr int U = WHOLE ? 2 : 1;
-    const float decay = __fmul_rn(a.lr_decay, it.decay);
+    const float decay = __fmul_rn(s.lr_decay, it.decay);
     char* mp = reinterpret_cast<char*>(it.m);
     char* vp = reinterpret_cast<char*>(it.v);
     const uint32_t head = min(it.count, head_elems<false>(mp, 16));
@@ -659,7 +661,7 @@ __device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamItem& it,
         for (int u = 0; u < U; ++u) {
             const uint32_t i = head + 4 * (q + 32 * u);
             if (q + 32 * u < nq) {
-                adam_quad(a, decay, f, p[u], g[u], m[u], v[u]);
+                adam_quad(a, s, decay, f, p[u], g[u], m[u], v[u]);
                 store_quad<PB>(it.p, i, p[u], pw);
                 store_quad<false>(mp, i, m[u], true);
                 store_quad<false>(vp, i, v[u], vw);
@@ -667,8 +669,8 @@ __device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamItem& it,
             }
         }
     }
-    if (lane < head) adam_elem<PB, GB, COPY>(a, it, decay, f, lane);
-    if (done + lane < it.count) adam_elem<PB, GB, COPY>(a, it, decay, f, done + lane);
+    if (lane < head) adam_elem<PB, GB, COPY>(a, s, it, decay, f, lane);
+    if (done + lane < it.count) adam_elem<PB, GB, COPY>(a, s, it, decay, f, done + lane);
 }
 
 // A warp updates one item; with a record, nothing is touched when the
@@ -693,14 +695,38 @@ __global__ void __launch_bounds__(kGradThreads, WHOLE ? 4 : 6) adamw_kernel(cons
         f = __ldcg(a.result + 1);
         if (__ldcg(a.result + 2) != 0.f) return;
     }
+    AdamScalars s = a.scalars;
+    if (a.counted) s = {__ldcg(&a.counted->step_size), __ldcg(&a.counted->inv_bc2), __ldcg(&a.counted->lr_decay)};
     switch (it.flags & (kGradBf16 | kParamBf16 | kHasCopy)) {
-        case 0: return adam_item<false, false, false, WHOLE>(a, it, f, lane);
-        case kGradBf16: return adam_item<false, true, false, WHOLE>(a, it, f, lane);
-        case kHasCopy: return adam_item<false, false, true, WHOLE>(a, it, f, lane);
-        case kHasCopy | kGradBf16: return adam_item<false, true, true, WHOLE>(a, it, f, lane);
-        case kParamBf16: return adam_item<true, false, false, WHOLE>(a, it, f, lane);
-        default: return adam_item<true, true, false, WHOLE>(a, it, f, lane);
+        case 0: return adam_item<false, false, false, WHOLE>(a, s, it, f, lane);
+        case kGradBf16: return adam_item<false, true, false, WHOLE>(a, s, it, f, lane);
+        case kHasCopy: return adam_item<false, false, true, WHOLE>(a, s, it, f, lane);
+        case kHasCopy | kGradBf16: return adam_item<false, true, true, WHOLE>(a, s, it, f, lane);
+        case kParamBf16: return adam_item<true, false, false, WHOLE>(a, s, it, f, lane);
+        default: return adam_item<true, true, false, WHOLE>(a, s, it, f, lane);
     }
+}
+
+// x^n for n >= 1, by squaring.
+__device__ double power(double x, uint64_t n) {
+    double y = 1.0;
+    for (; n > 0; n >>= 1, x *= x)
+        if (n & 1) y *= x;
+    return y;
+}
+
+// The number of an update, and what follows from it, on the device: a CUDA
+// graph of a training step then counts its replays, and a skipped update is
+// not counted.  One thread; the update's kernel waits for it.
+__global__ void count_kernel(const __grid_constant__ CountArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    if (threadIdx.x != 0 || (a.result && a.result[2] != 0.f)) return;
+    const uint64_t t = *a.steps + 1;
+    const double lr = a.lr ? static_cast<double>(*a.lr) : a.host_lr;
+    *a.scalars = {static_cast<float>(lr / (1.0 - power(a.beta1, t))),
+                  static_cast<float>(1.0 / sqrt(1.0 - power(a.beta2, t))), static_cast<float>(lr * a.weight_decay)};
+    *a.steps = t;
 }
 
 // ------------------------------------------------------------------ the items
@@ -810,6 +836,8 @@ cudaError_t launch_scale(const ScaleArgs& a, cudaStream_t st) {
     const uint32_t warps = a.n_items * a.item_warps;
     return launch(scale_kernel, a, (warps + kGradWarps - 1) / kGradWarps, kGradThreads, st);
 }
+
+cudaError_t launch_count(const CountArgs& a, cudaStream_t st) { return launch(count_kernel, a, 1, 32, st); }
 
 cudaError_t launch_adamw(const AdamArgs& a, bool whole, cudaStream_t st) {
     return launch(whole ? adamw_kernel<true> : adamw_kernel<false>, a, grad_ctas(a.n_items), kGradThreads, st);

@@ -121,16 +121,32 @@ struct ScaleArgs {
     const float* result;
 };
 
+// What of an update depends on its number.
+struct AdamScalars {
+    float step_size;           // lr / (1 - beta1^t)
+    float inv_bc2;             // 1 / sqrt(1 - beta2^t)
+    float lr_decay;            // lr times the weight decay
+};
+
 struct AdamArgs {
     const AdamItem* items;
     uint32_t n_items;
     const float* result;       // the norm's record, or null: factor 1
     float beta1, omb1;         // omb: one minus beta, rounded from 64 bits
     float beta2, omb2;
-    float step_size;           // lr / (1 - beta1^t)
-    float inv_bc2;             // 1 / sqrt(1 - beta2^t)
     float eps;
-    float lr_decay;            // lr times the weight decay
+    AdamScalars scalars;
+    const AdamScalars* counted;  // null, or where launch_count left them
+};
+
+// The scalars of update *steps + 1, and *steps counted up, unless the record
+// says that the update is skipped.
+struct CountArgs {
+    uint64_t* steps;
+    const float* lr;           // null: host_lr
+    const float* result;
+    double host_lr, beta1, beta2, weight_decay;
+    AdamScalars* scalars;
 };
 
 // Writes the items of n tensors; first[t] is tensor t's first item (n + 1).
@@ -147,6 +163,7 @@ cudaError_t launch_scale(const ScaleArgs& a, cudaStream_t st);
 // The sums, the record and, with `scale`, the scaling in one launch: at most kSmallItems
 // items of at most kSmallItemElems elements.
 cudaError_t launch_small(const NormArgs& a, bool scale, cudaStream_t st);
+cudaError_t launch_count(const CountArgs& a, cudaStream_t st);
 // whole: every stream of every tensor can be read and written in quads.
 cudaError_t launch_adamw(const AdamArgs& a, bool whole, cudaStream_t st);
 

@@ -57,7 +57,8 @@ class ZeroStep:
         self.norm = ar.Grads(grad_chunks)
         self.adamw = ar.AdamW(self.master, grad_chunks, self.exp_avg, self.exp_avg_sq,
                               copies=[x[a:b] for x, (a, b) in zip(self.weights, chunks)])
-        self.steps = 0
+        self.steps = torch.zeros(1, dtype=torch.int64, device="cuda")  # on the device, so that a graph counts it
+        self.rate = torch.full((1,), lr, device="cuda")
 
     def backward(self):
         """Every rank's gradient; the mean loss over ranks and elements."""
@@ -69,15 +70,14 @@ class ZeroStep:
 
     def step(self):
         """Enqueue the step on the current stream; returns the norm's record."""
-        self.steps += 1
         self.scatter.execute(self.grads)
         record = self.norm.norm(max_norm=self.max_norm)
-        self.adamw.step(self.steps, lr=self.lr, weight_decay=self.weight_decay, clip=record)
+        self.adamw.step(self.steps, lr=self.rate, weight_decay=self.weight_decay, clip=record)
         self.gather.execute(self.weights)
         return record
 
     def capture(self):
-        """The next step as a CUDA graph (its step number is part of it)."""
+        """The step as a CUDA graph: gradients in, weights out."""
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             self.step()
@@ -91,20 +91,19 @@ def main():
     ap.add_argument("--steps", type=int, default=20)
     a = ap.parse_args()
     z = ZeroStep(a.ranks, a.elements)
+    graph = z.capture()
     for i in range(a.steps):
         loss = z.backward()
-        record = z.step()
+        graph.replay()
         if i % max(1, a.steps // 10) == 0 or i == a.steps - 1:
-            norm, scale, nonfinite, clipped = record.tolist()
-            print(f"step {z.steps:4d}  loss {loss.item():.5f}  norm {norm:10.3f}  scale {scale:.3e}"
+            norm, scale, nonfinite, clipped = z.norm.record.tolist()
+            print(f"step {z.steps.item():4d}  loss {loss.item():.5f}  norm {norm:10.3f}  scale {scale:.3e}"
                   f"{'  clipped' if clipped else ''}{'  skipped: nonfinite' if nonfinite else ''}")
     z.scatter.check()
     z.gather.check()
     same = all(torch.equal(z.weights[0], w) for w in z.weights[1:])
     print(f"weights of all {a.ranks} ranks equal: {same}")
     start, stop = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-    graph = z.capture()
-    graph.replay()
     start.record()
     for _ in range(20):
         graph.replay()

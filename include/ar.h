@@ -474,6 +474,14 @@ typedef struct {
  * After ar_grad_clip the gradients are scaled already: pass NULL, or the
  * record would scale them twice. */
 ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* params, const float* result, void* stream);
+/* The same update with its number and rate on the device, for CUDA graphs,
+ * whose host arguments stay as captured.  *steps (device memory, 8-byte
+ * aligned) counts the updates done: this one is number *steps + 1, and the
+ * call counts it unless it is skipped.  lr: NULL for params->lr, or a device
+ * float read when the kernels run (>= 0 and finite; not checked).
+ * params->step is not looked at.  One more launch than ar_adamw_step. */
+ar_status ar_adamw_step_counted(ar_adamw_t h, const ar_adamw_params* params, uint64_t* steps, const float* lr,
+                                const float* result, void* stream);
 
 /* Static text for a status code (never NULL). */
 const char* ar_status_string(ar_status s);

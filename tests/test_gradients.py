@@ -74,6 +74,7 @@ def test_null_handles_are_refused():
     assert L.ar_grad_norm(None, 0, 1.0, 1.0, None, None, None) == 1
     assert L.ar_grad_clip(None, 0, 1.0, 1.0, None, None, None) == 1
     assert L.ar_adamw_step(None, ctypes.byref(p), None, None) == 1
+    assert L.ar_adamw_step_counted(None, ctypes.byref(p), None, None, None, None) == 1
     assert L.ar_grads_create(1, None, None, None, None, None, ctypes.byref(h)) == 1
     assert L.ar_grads_create(0, None, None, None, None, None, None) == 1
     assert L.ar_adamw_create(1, None, None, None, None, None, None, None, None, None, ctypes.byref(h)) == 1
@@ -399,6 +400,55 @@ def test_adamw_first_steps_and_edges():
 
 
 @gpu
+def test_adamw_counts_its_updates_on_the_device():
+    """The counted form gives what the host's numbers give, in a graph too,
+    reads its rate when it runs, and does not count a skipped update."""
+    import torch
+    n = [4099, 3]
+    g = Tensors(n, "float32", seed=2, sigma=1e-2)
+    a = [Tensors(n, "float32", seed=1) for _ in range(2)]
+    m, v = ([[torch.zeros(k, device="cuda") for k in n] for _ in range(2)] for _ in range(2))
+    host, device = (ar.AdamW(a[i].views, g.views, m[i], v[i]) for i in range(2))
+    steps, lr = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.full((1,), 0.125, device="cuda")
+    record = torch.tensor([1.0, 0.5, 0.0, 1.0], device="cuda")
+    device.step(steps, lr=lr, weight_decay=0.25, clip=record)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        device.step(steps, lr=lr, weight_decay=0.25, clip=record)
+    rates = [0.125, 0.5, 0.25, 0.0625]
+    for t in range(1, 5):
+        if t > 1:
+            lr.fill_(rates[t - 1])
+            graph.replay()
+        host.step(t, lr=rates[t - 1], weight_decay=0.25, clip=record)
+        assert steps.item() == t
+        for i in range(2):
+            assert torch.equal(m[0][i], m[1][i]) and torch.equal(v[0][i], v[1][i])
+            # the two scalars may round apart by one float32 unit: 4 u of an update
+            x, y = a[0].views[i], a[1].views[i]
+            assert bool(((x - y).abs() <= 8 * U * (x.abs() + rates[t - 1] * 10)).all())
+            y.copy_(x)
+    kept = a[1].host()
+    record[2] = 1.0
+    graph.replay()
+    assert steps.item() == 4 and all(torch.equal(x, y) for x, y in zip(kept, a[1].host()))
+    steps.fill_(10 ** 15)
+    record[2] = 0.0
+    device.step(steps, lr=0.0, clip=record)
+    assert steps.item() == 10 ** 15 + 1 and all(torch.equal(x, y) for x, y in zip(kept, a[1].host()))
+    with pytest.raises(ValueError, match="one int64"):
+        device.step(steps.int(), lr=0.1)
+    with pytest.raises(ValueError, match="lr"):
+        device.step(steps, lr=lr.double())
+    with pytest.raises(ar.ArError):
+        device.step(steps, lr=-1.0)
+    L, p = ar.lib(), ar.AdamWParams(0, 0.1, 0.9, 0.99, 1e-8, 0.0)
+    for bad in (None, steps.data_ptr() + 4, torch.zeros(1, dtype=torch.int64).data_ptr()):
+        assert L.ar_adamw_step_counted(device._h, ctypes.byref(p), bad, None, None, None) == 1
+    assert steps.item() == 10 ** 15 + 1
+
+
+@gpu
 def test_dense_tensors_in_another_order():
     import torch
     g = torch.Generator(device="cuda").manual_seed(3)
@@ -527,18 +577,19 @@ def test_sharded_training_step(P, n):
         assert_close(rec[0], float(mean.norm()), (10 + 2 * P) * U, "norm")
         for r, (a, b) in enumerate(chunks):
             g = z.grads[r][a:b].double().cpu()
-            want = adamw_reference(before[0][r], g, before[1][r], before[2][r], rec[1], z.steps, z.lr, 0.9, 0.999,
+            want = adamw_reference(before[0][r], g, before[1][r], before[2][r], rec[1], z.steps.item(), z.lr, 0.9, 0.999,
                                    1e-8, 0.01)
             assert bool(((z.master[r].double().cpu() - want[0]).abs() <= want[3]).all())
             assert all(torch.equal(w[a:b], z.master[r].bfloat16()) for w in z.weights)
     assert losses == sorted(losses, reverse=True)
     z.scatter.check()
     z.gather.check()
-    before = [w.clone() for w in z.weights]
-    z.capture().replay()
-    torch.cuda.synchronize()
-    assert all(torch.equal(z.weights[0], w) for w in z.weights)
-    assert not torch.equal(before[0], z.weights[0])
+    graph = z.capture()
+    for _ in range(3):
+        losses.append(z.backward().item())
+        graph.replay()
+        assert all(torch.equal(z.weights[0], w) for w in z.weights)
+    assert losses == sorted(losses, reverse=True) and z.steps.item() == 7
 
 
 @gpu
