@@ -3,6 +3,7 @@
 // and the calls that launch the kernels on them.
 #include "gradients.hpp"
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -143,7 +144,8 @@ bool on_device(int device) {
 
 // A caller's device float array that a call reads or writes.
 bool float_buffer(const float* p, uint64_t n, int device) {
-    return p && reinterpret_cast<uintptr_t>(p) % sizeof(float) == 0 && ar::device_resident(p, n * sizeof(float), device);
+    return p && reinterpret_cast<uintptr_t>(p) % sizeof(float) == 0 &&
+           ar::device_resident(p, n * sizeof(float), device);
 }
 
 }  // namespace
@@ -153,6 +155,7 @@ struct ar_grads_s {
     ar_tensors_info info = {};
     uint32_t n_items = 0, keep_from = 0;
     uint32_t least_es = 4;  // bytes of the gradients' smallest element type
+    bool in_place = true;   // every tensor is scaled where it is
     DeviceMemory memory;
     const ar::GradItem* items = nullptr;
     const uint32_t* first = nullptr;
@@ -211,6 +214,10 @@ ar_status run_norm(ar_grads_s* h, ar_norm_kind kind, double pre_scale, double ma
         b.item_warps = 1;
         while (b.item_warps < ar::kGradWarps && b.item_warps * 2 * 4096 <= h->info.item_elems * h->least_es)
             b.item_warps *= 2;  // 4 KB of gradients at least to each
+        // in place: several items to a CTA, while 8 waves of CTAs are left
+        const uint32_t ctas = h->n_items / (ar::kGradWarps / b.item_warps);
+        b.rounds = h->in_place ? std::min(8u, std::max(1u, ctas / (8 * 4 * 152))) : 1;
+        b.in_place = h->in_place;
         b.result = result;
         e = ar::launch_scale(b, st);
     }
@@ -306,6 +313,7 @@ ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype*
             const ar_dtype gt = grad_dtypes[t], ot = outs ? out_dtypes[t] : gt;
             void* dst = outs ? outs[t] : grads[t];
             if (gt == AR_BFLOAT16) h->least_es = 2;
+            h->in_place = h->in_place && (dst == grads[t] || counts[t] == 0);
             const uint32_t flags = (gt == AR_BFLOAT16 ? ar::kGradBf16 : 0) | (ot == AR_BFLOAT16 ? ar::kOutBf16 : 0) |
                                    (dst == grads[t] ? ar::kInPlace : 0);
             tensors.push_back({static_cast<const char*>(grads[t]), static_cast<char*>(dst),

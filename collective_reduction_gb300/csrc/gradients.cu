@@ -1,10 +1,19 @@
 // Kernels over many tensors after a gradient allreduce: the global norm, the
 // scaling by the clip factor, and the AdamW update.  All are bound by HBM at
-// size and by launches and one dependent chain when small.
+// size and by launches and one dependent chain when small.  Measured on GB300,
+// TB/s of the bytes each has to move (a copy: 6.77):
 //
-// A handle's tables split every tensor into ranges ("items") of equal element
-// count; a warp works through one item at a time, so items of tiny tensors
-// run beside each other and no barrier stands between items.
+//   norm    4.3 GB of bf16 574 us (7.5), 25 MB of float32 9.9 us, 35 KB 3.7 us
+//   clip    2.7 GB of float32 into other tensors 1137 us (7.1 of its two reads
+//           and one write), 96 MB 44 us, 0.4 MB 5.3 us
+//   AdamW   184M float32 parameters, bf16 gradients and copies 739 us (7.0),
+//           0.4M float32 parameters 3.9 us
+//
+// A handle's tables split every tensor into ranges ("items"); a warp works
+// through one item at a time, so items of tiny tensors run beside each other
+// and no barrier stands between items.  An item's vectors start on whole
+// lines of the leading stream; the elements before and after them, at a
+// tensor's ends, go singly.
 #include "device.cuh"
 #include "gradients.hpp"
 
@@ -168,10 +177,11 @@ __device__ __forceinline__ uint32_t magnitude(const uint4 (&x)[U]) {
 // Range: squares leave float32's range where the values themselves do not
 // (|x| above 1.8e19 or below 1e-19).  A group whose float32 sum is finite and
 // at least 2^-100 lost nothing that counts (a square that fell below the
-// smallest normal is off by 2^-150 at most).  Any other group is summed again
-// from the registers, scaled by the power of two that brings its largest
-// value to [1, 2); the float64 accumulator takes the exact scale back out.
-// All-zero groups end at the look at the largest value.
+// smallest normal is off by 2^-150 at most), and a group of zeros adds none.
+// Any other group is loaded and summed again, scaled by the power of two that
+// brings its largest value to [1, 2), and the exact scale goes back in in
+// float64.  (That path is a function of its own: inlined, it cost the loads
+// their registers.)
 struct SumSquares {
     double s = 0.0;
 
@@ -412,7 +422,9 @@ __device__ __forceinline__ Acc cluster_join(const Acc& mine, uint64_t* sums, uin
         const uint64_t bits = __shfl_sync(kFull, mine.bits(), 0);
         if (threadIdx.x < ctas) {  // to CTA number `lane`'s shared memory
             uint32_t to;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_addr(sums + rank)), "r"(threadIdx.x));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(to)
+                         : "r"(smem_addr(sums + rank)), "r"(threadIdx.x));
             asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(bits) : "memory");
         }
     }
@@ -439,9 +451,7 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
             acc.join(a.partials[i]);
         cta_join<Acc, kFinishThreads / 32>(acc, sm);
         const Acc all = cluster_join(acc, sums, kFinishCtas, blockIdx.x);
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
-            store_record(a.result, make_record(all, a.pre_scale, a.max_norm));
-        }
+        if (blockIdx.x == 0 && threadIdx.x == 0) store_record(a.result, make_record(all, a.pre_scale, a.max_norm));
         if (blockIdx.x == 0 && threadIdx.x < kNormLists) a.drawn[32 * threadIdx.x] = 0;  // for the next call
         return;
     }
@@ -454,9 +464,10 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
 }
 
 // Small sets: one cluster, an item to a warp, the sums exchanged through the
-// CTAs' shared memory.  No counter in global memory, and with SCALE the
-// gradients wait in registers for the factor: one launch and one read where
-// the general path takes two of each.
+// CTAs' shared memory; with SCALE the gradients wait in registers for the
+// factor: one launch and one read where the general path takes three and two.
+// Bound by its chain of latencies: 17 vectors 3.7 us a norm (5.0 with the
+// general kernels), 0.4 MB 5.3 us a clip (7.1).
 template <class Acc, bool SCALE>
 __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ NormArgs a) {
     __shared__ uint64_t sm[kSmallWarps], sums[kSmallCtas];
@@ -543,56 +554,82 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_const
 
 // ---------------------------------------------------------------- the scaling
 
-// dst = round(f * src) over one item, in quads of four elements.
-template <bool SB, bool DB>
-__device__ __forceinline__ void scale_item(const char* src, char* dst, uint32_t count, float f, uint32_t lane,
-                                           uint32_t lanes) {
-    constexpr int U = 8;
-    const uint32_t head = min(count, head_elems<SB>(src, SB ? 8 : 16));
-    const bool whole = quad_aligned<DB>(dst, head);
-    const uint32_t nq = (count - head) / 4;
-    const uint32_t done = head + nq * 4;
-    for (uint32_t q = lane; q < nq; q += lanes * U) {
+// dst = round(f * src) for n quads of four elements, the source on its
+// alignment, the destination too if WHOLE.  (Every x gets a value: one left
+// undefined past the end would hold its register through the caller's loop.)
+template <bool SB, bool DB, bool WHOLE, int U>
+__device__ __forceinline__ void scale_quads(const char* src, char* dst, uint32_t n, float f, uint32_t lane) {
+#pragma unroll 1
+    for (uint32_t q = lane; q < n; q += 32 * U) {
+        const char* from = src + q * (SB ? 8 : 16);
+        char* to = dst + q * (DB ? 8 : 16);
         float4 x[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (q + lanes * u < nq) x[u] = load_quad<SB, true>(src, head + 4 * (q + lanes * u), true);
+            x[u] = q + 32 * u < n ? load_quad<SB, true>(from, 128 * u, true) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (q + lanes * u < nq)
-                store_quad<DB, true>(dst, head + 4 * (q + lanes * u),
-                               make_float4(__fmul_rn(x[u].x, f), __fmul_rn(x[u].y, f), __fmul_rn(x[u].z, f),
-                                           __fmul_rn(x[u].w, f)),
-                               whole);
+            if (q + 32 * u < n)
+                store_quad<DB, true>(to, 128 * u,
+                                     make_float4(__fmul_rn(x[u].x, f), __fmul_rn(x[u].y, f), __fmul_rn(x[u].z, f),
+                                                 __fmul_rn(x[u].w, f)),
+                                     WHOLE);
     }
-    if (lane < head) store_elem<DB>(dst, lane, __fmul_rn(__uint_as_float(load_elem<SB>(src, lane)), f));
-    if (done + lane < count)
-        store_elem<DB>(dst, done + lane, __fmul_rn(__uint_as_float(load_elem<SB>(src, done + lane)), f));
+}
+
+// One of `warps` warps' part of an item; the first also takes the elements
+// before and after the quads.
+template <bool SB, bool DB>
+__device__ __forceinline__ void scale_item(const GradItem& it, float f, uint32_t warp, uint32_t warps, uint32_t lane) {
+    const uint32_t head = min(it.count, head_elems<SB>(it.src, SB ? 8 : 16));
+    const uint32_t nq = (it.count - head) / 4;
+    const uint32_t part = (nq + 32 * warps - 1) / (32 * warps) * 32, at = min(nq, warp * part);
+    const char* from = it.src + (head + 4 * at) * (SB ? 2 : 4);
+    char* to = it.dst + (head + 4 * at) * (DB ? 2 : 4);
+    if (quad_aligned<DB>(to, 0))
+        scale_quads<SB, DB, true, 8>(from, to, min(part, nq - at), f, lane);
+    else
+        scale_quads<SB, DB, false, 4>(from, to, min(part, nq - at), f, lane);
+    if (warp != 0) return;
+    const uint32_t done = head + nq * 4;
+    if (lane < head) store_elem<DB>(it.dst, lane, __fmul_rn(__uint_as_float(load_elem<SB>(it.src, lane)), f));
+    if (done + lane < it.count)
+        store_elem<DB>(it.dst, done + lane, __fmul_rn(__uint_as_float(load_elem<SB>(it.src, done + lane)), f));
 }
 
 // The items in the reverse of the norm's order: the norm leaves its last ones
 // in L2.  Loads and stores are streaming (neither is used again), so the
-// results do not push out the gradients that wait there.
-// In place, a factor of exactly 1 leaves nothing to do.
+// results do not push out the gradients that wait there.  item_warps warps
+// share an item, 4 KB of gradients to each: 2.7 GB of float32 take 1141 us,
+// 1148 with twice that a warp, 1176 with an item a warp.
+// In place, a factor of exactly 1 leaves nothing to do, as for most steps of a
+// training that runs well; then the CTAs' starts are what is left, and a CTA
+// takes several items in turn: 2.7 GB within the bound 370 us, 447 with an item
+// a CTA.  (Into other tensors, where that case writes all the same, an item a
+// CTA is the faster: 1139 us against 1156.)
 __global__ void __launch_bounds__(kGradThreads, 4) scale_kernel(const __grid_constant__ ScaleArgs a) {
-    const uint32_t warp = blockIdx.x * kGradWarps + (threadIdx.x >> 5);
-    const uint32_t i = warp / a.item_warps, lanes = 32 * a.item_warps;
-    const uint32_t lane = (warp % a.item_warps) * 32 + (threadIdx.x & 31);
+    const uint32_t side = kGradWarps / a.item_warps;  // items side by side in a CTA
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % a.item_warps;
+    uint32_t i = blockIdx.x * a.rounds * side + warp / a.item_warps;
     GradItem it = {};
     if (i < a.n_items) it = a.items[a.n_items - 1 - i];
     griddep_wait();
     griddep_launch_dependents();
     const float f = __ldcg(a.result + 1);
-    if ((it.flags & kInPlace) && f == 1.f) return;
-    const bool sb = it.flags & kGradBf16, db = it.flags & kOutBf16;
-    if (sb && db)
-        scale_item<true, true>(it.src, it.dst, it.count, f, lane, lanes);
-    else if (sb)
-        scale_item<true, false>(it.src, it.dst, it.count, f, lane, lanes);
-    else if (db)
-        scale_item<false, true>(it.src, it.dst, it.count, f, lane, lanes);
-    else
-        scale_item<false, false>(it.src, it.dst, it.count, f, lane, lanes);
+    if (a.in_place && f == 1.f) return;
+#pragma unroll 1
+    for (uint32_t r = 0; r < a.rounds && i < a.n_items; ++r) {
+        if (r > 0) it = a.items[a.n_items - 1 - i];
+        if (!(it.flags & kInPlace) || f != 1.f) {
+            switch (it.flags & (kGradBf16 | kOutBf16)) {
+                case 0: scale_item<false, false>(it, f, part, a.item_warps, lane); break;
+                case kGradBf16: scale_item<true, false>(it, f, part, a.item_warps, lane); break;
+                case kOutBf16: scale_item<false, true>(it, f, part, a.item_warps, lane); break;
+                default: scale_item<true, true>(it, f, part, a.item_warps, lane);
+            }
+        }
+        i += side;
+    }
 }
 
 // ---------------------------------------------------------------------- AdamW
@@ -600,8 +637,8 @@ __global__ void __launch_bounds__(kGradThreads, 4) scale_kernel(const __grid_con
 // One element: moments and parameter, in float32.  The decay is subtracted
 // with the update (p - (lr wd p + update)), so its small factor is never
 // rounded against 1.
-__device__ __forceinline__ void adam_one(const AdamArgs& a, const AdamScalars& s, float decay, float f, float& p, float g, float& m,
-                                         float& v) {
+__device__ __forceinline__ void adam_one(const AdamArgs& a, const AdamScalars& s, float decay, float f, float& p,
+                                         float g, float& m, float& v) {
     g = __fmul_rn(g, f);
     m = __fmaf_rn(a.omb1, g, __fmul_rn(a.beta1, m));
     v = __fmaf_rn(__fmul_rn(a.omb2, g), g, __fmul_rn(a.beta2, v));
@@ -610,8 +647,8 @@ __device__ __forceinline__ void adam_one(const AdamArgs& a, const AdamScalars& s
     p = __fsub_rn(p, __fmaf_rn(decay, p, upd));
 }
 
-__device__ __forceinline__ void adam_quad(const AdamArgs& a, const AdamScalars& s, float decay, float f, float4& p, float4 g, float4& m,
-                                          float4& v) {
+__device__ __forceinline__ void adam_quad(const AdamArgs& a, const AdamScalars& s, float decay, float f, float4& p,
+                                          float4 g, float4& m, float4& v) {
     adam_one(a, s, decay, f, p.x, g.x, m.x, v.x);
     adam_one(a, s, decay, f, p.y, g.y, m.y, v.y);
     adam_one(a, s, decay, f, p.z, g.z, m.z, v.z);
@@ -619,8 +656,8 @@ __device__ __forceinline__ void adam_quad(const AdamArgs& a, const AdamScalars& 
 }
 
 template <bool PB, bool GB, bool COPY>
-__device__ __forceinline__ void adam_elem(const AdamArgs& a, const AdamScalars& s, const AdamItem& it, float decay, float f,
-                                          uint32_t i) {
+__device__ __forceinline__ void adam_elem(const AdamArgs& a, const AdamScalars& s, const AdamItem& it, float decay,
+                                          float f, uint32_t i) {
     char* mp = reinterpret_cast<char*>(it.m);
     char* vp = reinterpret_cast<char*>(it.v);
     float p = __uint_as_float(load_elem<PB>(it.p, i)), m = __uint_as_float(load_elem<false>(mp, i));
@@ -678,9 +715,9 @@ __device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamScalars& 
 // order, whose last gradients may still be in L2.  Bound by HBM.
 // WHOLE: every stream moves in quads.  Two quads of each in flight a thread at
 // 4 CTAs an SM; a stream off its alignment takes single elements, which need
-// more warps instead: one quad, 6 CTAs.  (Measured, in us, both ways: a billion
-// float32 parameters 4584 and 4647; bf16 parameters with bf16 gradients packed
-// tight at odd sizes 492 and 455, norm included.)
+// more warps instead: one quad, 6 CTAs.  Measured both ways, norm included: a
+// billion float32 parameters 4584 and 4647 us; 122M bf16 parameters whose bf16
+// gradients are packed tight at odd sizes 492 and 455.
 template <bool WHOLE>
 __global__ void __launch_bounds__(kGradThreads, WHOLE ? 4 : 6) adamw_kernel(const __grid_constant__ AdamArgs a) {
     const uint32_t lane = threadIdx.x & 31;
@@ -717,16 +754,25 @@ __device__ double power(double x, uint64_t n) {
 
 // The number of an update, and what follows from it, on the device: a CUDA
 // graph of a training step then counts its replays, and a skipped update is
-// not counted.  One thread; the update's kernel waits for it.
-__global__ void count_kernel(const __grid_constant__ CountArgs a) {
+// not counted.  A thread of one warp and one of another take a moment each;
+// float32's reciprocals and a Newton step in float64 stand for its divisions
+// and root, whose long chains the update would wait for.
+__global__ void __launch_bounds__(64) count_kernel(const __grid_constant__ CountArgs a) {
     griddep_wait();
     griddep_launch_dependents();
-    if (threadIdx.x != 0 || (a.result && a.result[2] != 0.f)) return;
+    if (a.result && a.result[2] != 0.f) return;
     const uint64_t t = *a.steps + 1;
-    const double lr = a.lr ? static_cast<double>(*a.lr) : a.host_lr;
-    *a.scalars = {static_cast<float>(lr / (1.0 - power(a.beta1, t))),
-                  static_cast<float>(1.0 / sqrt(1.0 - power(a.beta2, t))), static_cast<float>(lr * a.weight_decay)};
-    *a.steps = t;
+    if (threadIdx.x == 0) {
+        const double lr = a.lr ? static_cast<double>(*a.lr) : a.host_lr;
+        const double d = 1.0 - power(a.beta1, t), y = __frcp_rn(static_cast<float>(d));
+        a.scalars->step_size = static_cast<float>(lr * fma(y, fma(-d, y, 1.0), y));
+        a.scalars->lr_decay = static_cast<float>(lr * a.weight_decay);
+    } else if (threadIdx.x == 32) {
+        const double d = 1.0 - power(a.beta2, t), y = rsqrtf(static_cast<float>(d));
+        a.scalars->inv_bc2 = static_cast<float>(fma(y, fma(-0.5 * d * y, y, 0.5), y));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) *a.steps = t;
 }
 
 // ------------------------------------------------------------------ the items
@@ -833,11 +879,11 @@ cudaError_t launch_finish(const NormArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_scale(const ScaleArgs& a, cudaStream_t st) {
-    const uint32_t warps = a.n_items * a.item_warps;
-    return launch(scale_kernel, a, (warps + kGradWarps - 1) / kGradWarps, kGradThreads, st);
+    const uint32_t items = a.rounds * (kGradWarps / a.item_warps);  // of a CTA
+    return launch(scale_kernel, a, (a.n_items + items - 1) / items, kGradThreads, st);
 }
 
-cudaError_t launch_count(const CountArgs& a, cudaStream_t st) { return launch(count_kernel, a, 1, 32, st); }
+cudaError_t launch_count(const CountArgs& a, cudaStream_t st) { return launch(count_kernel, a, 1, 64, st); }
 
 cudaError_t launch_adamw(const AdamArgs& a, bool whole, cudaStream_t st) {
     return launch(whole ? adamw_kernel<true> : adamw_kernel<false>, a, grad_ctas(a.n_items), kGradThreads, st);

@@ -118,6 +118,8 @@ struct ScaleArgs {
     const GradItem* items;
     uint32_t n_items;
     uint32_t item_warps;    // warps that share an item: 1, 2, 4 or 8
+    uint32_t rounds;        // items that a CTA's warps work through in turn
+    bool in_place;          // every item
     const float* result;
 };
 

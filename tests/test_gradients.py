@@ -211,7 +211,7 @@ def test_no_tensors_and_only_empty_ones():
 # Values whose squares leave float32's range, alone and beside ordinary ones.
 @gpu
 @pytest.mark.parametrize("types", ["float32", "bfloat16"])
-@pytest.mark.parametrize("size", [1, 33, 4099, 50021])
+@pytest.mark.parametrize("size", [1, 33, 4099, 50021, 200003])
 @pytest.mark.parametrize("values", ["huge", "top", "small", "subnormal", "zeros", "zeros-and-one", "huge-and-small",
                                     "edge", "steps"])
 def test_norm_over_the_whole_range(values, size, types):
@@ -256,21 +256,23 @@ def test_norm_over_the_whole_range(values, size, types):
 
 @gpu
 @pytest.mark.parametrize("types", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rest", [[], [150001]])
 @pytest.mark.parametrize("where", [0, 1, 20, 4500, 9000])
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
-def test_nonfinite_gradients(bad, where, types):
+def test_nonfinite_gradients(bad, where, rest, types):
     import torch
-    t = Tensors([300, 9001], types, offset=1)
+    sizes = [300, 9001] + rest
+    t = Tensors(sizes, types, offset=1)
     t.views[1][where] = bad
     before = t.host()
     h = ar.Grads(t.views)
-    per = torch.empty(2, device="cuda")
+    per = torch.empty(len(sizes), device="cuda")
     for kind in ("l2", "max"):
         rec = h.norm(max_norm=1.0, kind=kind, pre_scale=0.25, per_tensor=per).tolist()
         assert rec[1:] == [0.25, 1.0, 0.0]
         assert math.isnan(rec[0]) if math.isnan(bad) else rec[0] == math.inf
-        assert math.isfinite(per[0].item()) and not math.isfinite(per[1].item())
-    p, m, v = (Tensors([300, 9001], "float32", seed=k, square=k == 3) for k in (1, 2, 3))
+        assert [math.isfinite(x) for x in per.tolist()] == [True, False, True][:len(sizes)]
+    p, m, v = (Tensors(sizes, "float32", seed=k, square=k == 3) for k in (1, 2, 3))
     kept = [x.host() for x in (p, m, v)]
     opt = ar.AdamW(p.views, t.views, m.views, v.views)
     opt.step(1, lr=1e-2, weight_decay=0.1, clip=h.record)
@@ -334,7 +336,8 @@ def adamw_reference(p, g, m, v, s, step, lr, b1, b2, eps, wd):
 
 
 @gpu
-@pytest.mark.parametrize("offsets", [(0, 0, 0, 0, 0), (0, 1, 0, 0, 0), (1, 1, 1, 1, 1), (2, 1, 0, 3, 5), (4, 4, 4, 4, 4)])
+@pytest.mark.parametrize("offsets", [(0, 0, 0, 0, 0), (0, 1, 0, 0, 0), (1, 1, 1, 1, 1), (2, 1, 0, 3, 5),
+                                     (4, 4, 4, 4, 4)])
 @pytest.mark.parametrize("kinds", [("float32", "float32", False), ("float32", "bfloat16", True),
                                    ("float32", "mixed", False), ("float32", "float32", True),
                                    ("bfloat16", "bfloat16", False), ("bfloat16", "float32", False),
@@ -577,8 +580,8 @@ def test_sharded_training_step(P, n):
         assert_close(rec[0], float(mean.norm()), (10 + 2 * P) * U, "norm")
         for r, (a, b) in enumerate(chunks):
             g = z.grads[r][a:b].double().cpu()
-            want = adamw_reference(before[0][r], g, before[1][r], before[2][r], rec[1], z.steps.item(), z.lr, 0.9, 0.999,
-                                   1e-8, 0.01)
+            want = adamw_reference(before[0][r], g, before[1][r], before[2][r], rec[1], z.steps.item(), z.lr, 0.9,
+                                   0.999, 1e-8, 0.01)
             assert bool(((z.master[r].double().cpu() - want[0]).abs() <= want[3]).all())
             assert all(torch.equal(w[a:b], z.master[r].bfloat16()) for w in z.weights)
     assert losses == sorted(losses, reverse=True)
