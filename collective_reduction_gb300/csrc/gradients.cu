@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_con
 // Small sets: one cluster, an item to a warp, the sums exchanged through the
 // CTAs' shared memory; with SCALE the gradients wait in registers for the
 // factor: one launch and one read where the general path takes three and two.
-// Bound by its chain of latencies: 17 vectors 3.7 us a norm (5.0 with the
-// general kernels), 0.4 MB 5.3 us a clip (7.1).
+// Bound by its chain of latencies: 17 vectors 3.75 us a norm (4.96 with the
+// general kernels), 0.4 MB 5.25 us a clip (6.88).
 template <class Acc, bool SCALE>
 __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ NormArgs a) {
     __shared__ uint64_t sm[kSmallWarps], sums[kSmallCtas];
@@ -716,8 +716,8 @@ __device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamScalars& 
 // WHOLE: every stream moves in quads.  Two quads of each in flight a thread at
 // 4 CTAs an SM; a stream off its alignment takes single elements, which need
 // more warps instead: one quad, 6 CTAs.  Measured both ways, norm included: a
-// billion float32 parameters 4584 and 4647 us; 122M bf16 parameters whose bf16
-// gradients are packed tight at odd sizes 492 and 455.
+// billion float32 parameters 4530 and 4646 us; 122M bf16 parameters whose bf16
+// gradients are packed tight at odd sizes 481 and 431.
 template <bool WHOLE>
 __global__ void __launch_bounds__(kGradThreads, WHOLE ? 4 : 6) adamw_kernel(const __grid_constant__ AdamArgs a) {
     const uint32_t lane = threadIdx.x & 31;
