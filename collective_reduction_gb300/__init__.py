@@ -384,6 +384,7 @@ class Grads:
         self.grads, types = _tensor_list(grads, "grads")
         self.out, out_types = (None, None) if out is None else _tensor_list(out, "out", like=self.grads)
         self.record = torch.zeros(4, dtype=torch.float32, device="cuda")
+        torch.cuda.current_stream().synchronize()  # the calls may run on any stream
         self._record = _VP(self.record.data_ptr())
         h = _VP()
         _check(lib().ar_grads_create(len(self.grads), _counts(self.grads), _dtype_array(types), _ptrs(self.grads),

@@ -381,7 +381,10 @@ __device__ __forceinline__ void norm_item(Acc& acc, const char* src, uint32_t co
 // from one of them, after a first two items each that are fixed: the SMs do
 // not all read at one rate (with equal shares some idled for the last tenth).
 // One list would do but for its counter: an item every 3 ns is what one
-// address gives out.  Item and draw are fetched one item ahead.
+// address gives out (4.3 GB in ranges of 8192 elements: 897 us with one list,
+// 580 with eight).  Fewer items than warps are one list, an item to each of the
+// first warps (25 MB: 9.7 us, 11.6 dealt to eight).  Item and draw are fetched
+// one item ahead.
 // KEEP: a reader of the gradients follows, in the reverse order.
 template <class Acc, bool KEEP>
 __global__ void __launch_bounds__(kGradThreads, kNormCtasPerSm) norm_kernel(const __grid_constant__ NormArgs a) {
