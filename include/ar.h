@@ -403,8 +403,9 @@ typedef struct {
     int tiling_ok;         /* ar_tensors_lowering: the ranges tile every tensor */
 } ar_tensors_info;
 
-/* Host only: the ranges a gradient handle over these sizes would have, checked
- * against the sizes by code apart from the one that makes them.  Errors as
+/* Host only: the ranges a gradient handle over these sizes would have (for
+ * tensors that start on 128-byte boundaries; others may take one range more),
+ * and whether they tile every tensor, on and off a boundary.  Errors as
  * ar_grads_create. */
 ar_status ar_tensors_lowering(int n_tensors, const uint64_t* counts, const ar_dtype* dtypes, ar_tensors_info* out);
 
@@ -425,7 +426,7 @@ ar_status ar_grads_destroy(ar_grads_t h);
 /* The norm of all N tensors as one vector g, times the pre-scale c (one over
  * the loss scale or the rank count; a float32-normal positive number):
  *   AR_NORM_L2   c sqrt(sum g^2)        AR_NORM_MAX   c max |g|
- * written to result, 4 floats of device memory:
+ * written to result, 4 floats of device memory of its own:
  *   [0] norm
  *   [1] scale      c max_norm / norm if clipped, else c
  *   [2] nonfinite  1 if any element is an infinity or NaN, else 0
