@@ -18,21 +18,23 @@ constexpr int kMaxTensors = 1 << 20;
 constexpr uint64_t kMaxElems = uint64_t(1) << 40;
 
 // One wave of warps on GB300's 152 SMs: the norm kernel runs 3 CTAs of 8 warps
-// on each, the AdamW kernel 4.  A set with less than a full range for every
-// warp of a wave is split to fill one wave; beyond that the ranges stay at
-// their full size.  Measured: a norm of 25 MB takes 9.8 us split this way and
-// 15.4 in ranges of 1024 elements; one of 4.2 GB in bf16 583 us in ranges of
-// 12288 elements, 587 and 597 of 8192 and 16384, in float32 1148 us, 1178 and
-// 1167; AdamW on 0.4M elements 3.9 us, 8.4 in ranges of 1024; on a billion,
-// the norm included, 4526 us in ranges of 512, 4545 and 4565 of 768 and 1024.
+// on each, the AdamW kernel 4.  The ranges are the largest, up to a full one,
+// that fill a whole number of waves: a set a little over one wave of full
+// ranges would wait for the few warps with two.  Measured: a norm of 180 MB
+// (1.004 waves of full ranges) 31.6 us in two waves, 39.1 in full ranges; one of
+// 25 MB 9.8 us in one wave, 15.4 in ranges of 1024 elements.  Full: a norm of
+// 4.2 GB takes in bf16 583 us in ranges of 12288 elements, 587 and 597 of 8192
+// and 16384, in float32 1148 us, 1178 and 1167; AdamW on a billion, the norm
+// included, 4526 us in ranges of 512, 4545 and 4565 of 768 and 1024, and on 0.4M
+// 3.9 us in ranges of 256, 8.4 of 1024.
 constexpr uint64_t kNormWave = 152 * ar::kNormCtasPerSm * ar::kGradWarps, kAdamWave = 152 * 4 * ar::kGradWarps;
 constexpr uint32_t kGradItemMax = 12288, kAdamItemStep = 256, kAdamItemMax = 512;
 
 uint32_t item_elems(int n, const uint64_t* counts, uint64_t wave, uint32_t step, uint32_t most) {
     uint64_t total = 0;
     for (int t = 0; t < n; ++t) total += counts[t];
-    const uint64_t e = (total / wave / step + 1) * step;
-    return e < most ? static_cast<uint32_t>(e) : most;
+    const uint64_t waves = total / (wave * most) + 1;
+    return static_cast<uint32_t>((total / (wave * waves) / step + 1) * step);
 }
 uint32_t grad_item_elems(int n, const uint64_t* counts) {
     return item_elems(n, counts, kNormWave, ar::kSmallItemElems, kGradItemMax);
