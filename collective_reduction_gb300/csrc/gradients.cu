@@ -3,10 +3,10 @@
 // size and by launches and one dependent chain when small.  Measured on GB300,
 // TB/s of the bytes each has to move (a copy: 6.77):
 //
-//   norm    4.3 GB of bf16 574 us (7.5), 25 MB of float32 9.9 us, 35 KB 3.7 us
-//   clip    2.7 GB of float32 into other tensors 1137 us (7.1 of its two reads
-//           and one write), 96 MB 44 us, 0.4 MB 5.3 us
-//   AdamW   184M float32 parameters, bf16 gradients and copies 739 us (7.0),
+//   norm    4.3 GB of bf16 580 us (7.4), 25 MB of float32 9.8 us, 35 KB 3.75 us
+//   clip    2.7 GB of float32 into other tensors 1139 us (7.1 of its two reads
+//           and one write), 96 MB 44 us, 0.4 MB 5.25 us
+//   AdamW   184M float32 parameters, bf16 gradients and copies 737 us (7.0),
 //           0.4M float32 parameters 3.9 us
 //
 // A handle's tables split every tensor into ranges ("items"); a warp works
