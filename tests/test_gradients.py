@@ -529,6 +529,15 @@ def test_offsets_past_32_bits():
     for at in (0, (1 << 31) - 4, (1 << 32) - 4, n - 8):
         assert bool((x[at:at + 8] == 0.25).all())
     assert float(x.max()) == 0.25 and float(x.min()) == 0.25
+    h.close()
+    del x, h
+    n = (1 << 31) + 4099
+    p, g = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    m, v = (torch.zeros(n, device="cuda") for _ in range(2))
+    g[n - 1] = -1.0
+    ar.AdamW([p], [g], [m], [v]).step(1, lr=0.5)  # the first update moves by lr, eps and roundings aside
+    assert float(p[:n - 1].max()) == -0.5 and float(p[:n - 1].min()) == -0.5 and p[n - 1].item() == 0.5
+    assert bool((v == v[0]).all()) and bool((m[:n - 1] == m[0]).all()) and m[n - 1].item() == -m[0].item() != 0.0
 
 
 @gpu
