@@ -417,10 +417,21 @@ __global__ void __launch_bounds__(kGradThreads, kNormCtasPerSm) norm_kernel(cons
     }
 }
 
+// A CTA's shared memory may be written by others of its cluster only once it has
+// started, which nothing but a cluster barrier says: every thread arrives at its
+// kernel's start (relaxed: nothing is handed over yet), and cluster_join waits
+// for the others before its first store to them, with the loads in between.
+__device__ __forceinline__ void cluster_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
 // The sums of a cluster's CTAs, in their order, through their shared memory:
 // thread 0 of every CTA gets the total.  mine: the CTA's sum, in its thread 0.
+// Every thread of the cluster has called cluster_started before.
 template <class Acc>
 __device__ __forceinline__ Acc cluster_join(const Acc& mine, uint64_t* sums, uint32_t ctas, uint32_t rank) {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (threadIdx.x < 32) {
         const uint64_t bits = __shfl_sync(kFull, mine.bits(), 0);
         if (threadIdx.x < ctas) {  // to CTA number `lane`'s shared memory
@@ -445,6 +456,7 @@ __device__ __forceinline__ Acc cluster_join(const Acc& mine, uint64_t* sums, uin
 template <class Acc>
 __global__ void __launch_bounds__(kFinishThreads) finish_kernel(const __grid_constant__ NormArgs a) {
     __shared__ uint64_t sm[kFinishThreads / 32], sums[kFinishCtas];
+    if (blockIdx.x < a.record_ctas) cluster_started();
     griddep_wait();
     griddep_launch_dependents();
     Acc acc;
@@ -475,6 +487,7 @@ template <class Acc, bool SCALE>
 __global__ void __launch_bounds__(kSmallThreads) small_kernel(const __grid_constant__ NormArgs a) {
     __shared__ uint64_t sm[kSmallWarps], sums[kSmallCtas];
     __shared__ float factor;
+    cluster_started();
     constexpr int U = kSmallItemElems / 128;  // float32 vectors of a full item, a lane's
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t it = blockIdx.x * kSmallWarps + warp;
