@@ -43,13 +43,13 @@ uint32_t adam_item_elems(int n, const uint64_t* counts) {
     return item_elems(n, counts, kAdamWave, kAdamItemStep, kAdamItemMax);
 }
 
-// Gradient bytes at the end of a set that a norm asks L2 to keep (of 129 MB)
-// when it has a bound, for then the scaling or the update reads the gradients
-// next, last ones first.  Measured with none and with 64 MB: clipping 96 MB into
-// other tensors 47.0 and 44.5 us (47.3 with 32 MB, 44.0 with 96); the norm and
-// AdamW on 48 MB of float32 gradients 65.5 and 61.3 us, on 244 MB of bf16 441 and
-// 433; clipping 2.7 GB 1137 and 1139; a whole sharded step of 8 ranks, 10M
-// elements (reduce-scatter to all-gather), 170 and 166.
+// Gradient bytes at the end of a set that may stay in L2 (of 129 MB) after a norm
+// that has a bound, the ones before them leaving first: the scaling or the update
+// reads the gradients next, last ones first.  Measured without and with, in a
+// graph that writes the gradients first (its time included): clipping into other
+// tensors 80 MB of float32 87.3 and 88.2 us, 640 MB 703 and 695, 600 MB of bf16 665
+// and 654; the norm and AdamW on 160 MB of float32 gradients 296 and 292, on 600 MB of
+// bf16 1609 and 1596.
 constexpr uint64_t kKeepBytes = 64ull << 20;
 
 ar_status cuda_status(cudaError_t e) {

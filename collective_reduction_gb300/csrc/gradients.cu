@@ -22,11 +22,16 @@ namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
-// How long the lines that a load brings in should stay in L2.
+// How soon the lines that a load brings in may leave L2: the last ones read in
+// their usual turn, the others first.  Not evict_last: such lines stay after
+// their reader has gone (reading them again with evict_first or streaming loads
+// does not release them) and take their part of L2 from every kernel that
+// follows.  Measured: four passes over an 80 MB tensor after a clip of 24 MB
+// 60 us, 70 with evict_last (which itself took 0.5 to 5% off norm and AdamW).
 __device__ __forceinline__ uint64_t keep_policy(bool last_out) {
     uint64_t p;
     if (last_out)
-        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
     else
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;

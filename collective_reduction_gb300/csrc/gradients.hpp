@@ -102,7 +102,7 @@ inline uint32_t grad_ctas(uint32_t n_items) {
 struct NormArgs {
     const GradItem* items;
     uint32_t n_items;
-    uint32_t keep_from;     // launch_norm's keep: items from here on stay in L2
+    uint32_t keep_from;     // launch_norm's keep: items before it leave L2 first
     int kind;               // AR_NORM_L2 or AR_NORM_MAX
     uint64_t* partials;     // each item's sum
     uint32_t* drawn;        // items drawn from the counter; 0 between calls

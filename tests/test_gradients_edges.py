@@ -77,3 +77,13 @@ def test_clusters_with_blocks_that_have_nothing_to_read(n, kind):
     assert_close(got[0, 1].item(), 0.5, 11 * U, "scale")
     want = g * got[0, 1]
     assert all(v.item() == w.item() for v, w in zip(h.out, want))
+
+
+# ------------------------------------------------- what a call leaves behind
+
+def test_no_load_pins_lines_in_l2():
+    """Lines of a higher than usual priority outlive the call and take L2 from
+    every kernel that follows."""
+    bodies = function_bodies(os.path.join(ROOT, "collective_reduction_gb300", "csrc", "gradients.cu"))
+    assert "createpolicy" in bodies["keep_policy"]
+    assert not [name for name, body in bodies.items() if "evict_last" in body]
