@@ -54,6 +54,7 @@ constexpr uint64_t kKeepBytes = 64ull << 20;
 
 ar_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
+    cudaGetLastError();  // reported here: not once more by whoever looks at the thread's last error
     return e == cudaErrorMemoryAllocation ? AR_ERR_NOMEM : AR_ERR_CUDA;
 }
 

@@ -842,8 +842,10 @@ __global__ void items_kernel(const Tensor* tensors, const uint32_t* first, int n
 template <class Tensor, class Item>
 cudaError_t make_items(const Tensor* tensors, const uint32_t* first, int n, uint32_t n_items, Item* items,
                        cudaStream_t st) {
-    items_kernel<<<(n_items + 255) / 256, 256, 0, st>>>(tensors, first, n, items);
-    return cudaGetLastError();
+    // (a launch by <<<>>> has its status in the thread's last error, where an earlier call's may still be)
+    void* args[] = {&tensors, &first, &n, &items};
+    return cudaLaunchKernel(reinterpret_cast<const void*>(&items_kernel<Tensor, Item>), dim3((n_items + 255) / 256),
+                            dim3(256), args, 0, st);
 }
 
 template <class Args>

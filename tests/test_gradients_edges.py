@@ -87,3 +87,29 @@ def test_no_load_pins_lines_in_l2():
     bodies = function_bodies(os.path.join(ROOT, "collective_reduction_gb300", "csrc", "gradients.cu"))
     assert "createpolicy" in bodies["keep_policy"]
     assert not [name for name, body in bodies.items() if "evict_last" in body]
+
+
+@gpu
+def test_a_handle_that_found_no_memory_can_be_made_again():
+    """The failure is reported once: with memory free again the same call works."""
+    import torch
+    n = 1 << 28  # a table of 32 MB
+    p, g = (torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    m, v = (torch.zeros(n, device="cuda") for _ in range(2))
+    ar.AdamW([p[:8]], [g[:8]], [m[:8]], [v[:8]]).step(1, lr=0.0)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    filler = torch.empty(free - (20 << 20), dtype=torch.uint8, device="cuda")
+    try:
+        with pytest.raises(ar.ArError) as e:
+            ar.AdamW([p], [g], [m], [v])
+    finally:
+        del filler
+        torch.cuda.empty_cache()
+    assert e.value.name == "AR_ERR_NOMEM"
+    g.fill_(1.0)
+    opt = ar.AdamW([p], [g], [m], [v])
+    assert opt.info()["table_bytes"] > 20 << 20
+    opt.step(1, lr=0.5)
+    assert float(p.max()) == -0.5 and float(p.min()) == -0.5
