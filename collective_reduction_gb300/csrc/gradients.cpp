@@ -120,19 +120,22 @@ uint32_t first_items(const std::vector<Tensor>& tensors, std::vector<uint32_t>& 
     return static_cast<uint32_t>(n);
 }
 
-// Uploads the tensors and has the device write their items.
+// Uploads the tensors and has the device write their items.  All of it is in
+// place on return (a copy from pageable memory alone may return before that, and
+// the calls may be on streams that do not wait for this one).
 template <class Tensor, class Item>
 cudaError_t upload_items(const std::vector<Tensor>& tensors, const std::vector<uint32_t>& first, uint32_t* d_first,
                          Item* d_items) {
     const uint32_t n_items = first.back();
     cudaError_t e = cudaMemcpy(d_first, first.data(), first.size() * sizeof(uint32_t), cudaMemcpyHostToDevice);
-    if (e != cudaSuccess || n_items == 0) return e;
     Tensor* d_tensors = nullptr;
-    e = cudaMalloc(&d_tensors, tensors.size() * sizeof(Tensor));
-    if (e == cudaSuccess)
-        e = cudaMemcpy(d_tensors, tensors.data(), tensors.size() * sizeof(Tensor), cudaMemcpyHostToDevice);
-    if (e == cudaSuccess)
-        e = ar::launch_items(d_tensors, d_first, static_cast<int>(tensors.size()), n_items, d_items, nullptr);
+    if (n_items > 0) {
+        if (e == cudaSuccess) e = cudaMalloc(&d_tensors, tensors.size() * sizeof(Tensor));
+        if (e == cudaSuccess)
+            e = cudaMemcpy(d_tensors, tensors.data(), tensors.size() * sizeof(Tensor), cudaMemcpyHostToDevice);
+        if (e == cudaSuccess)
+            e = ar::launch_items(d_tensors, d_first, static_cast<int>(tensors.size()), n_items, d_items, nullptr);
+    }
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     cudaFree(d_tensors);
     return e;

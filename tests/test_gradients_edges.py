@@ -113,3 +113,28 @@ def test_a_handle_that_found_no_memory_can_be_made_again():
     assert opt.info()["table_bytes"] > 20 << 20
     opt.step(1, lr=0.5)
     assert float(p.max()) == -0.5 and float(p.min()) == -0.5
+
+
+@gpu
+@pytest.mark.parametrize("sizes", [[0], [0] * 3000, [0] * 1000 + [1]])
+def test_a_new_handle_is_complete_for_any_stream(sizes):
+    """Made and used at once on a stream that waits for no other, over memory
+    that held other numbers: every tensor's norm is its own."""
+    import torch
+    s = torch.cuda.Stream()
+    x = torch.ones(1, device="cuda")
+    views = [x[:n] for n in sizes]
+    torch.cuda.synchronize()
+    for k in range(20):
+        with torch.cuda.stream(s):
+            other = ar.Grads([torch.full((4096,), 7.0, device="cuda")])
+            other.norm()
+            other.close()  # its memory is free for the next handle
+            h = ar.Grads(views)
+            per = torch.full((len(sizes),), -7.0, device="cuda")
+            rec = h.norm(max_norm=0.5, per_tensor=per)
+        s.synchronize()
+        total = float(sum(sizes))
+        assert rec.tolist() == [total, 0.5 if total else 1.0, 0.0, total]
+        assert per.tolist() == [float(n) for n in sizes]
+        h.close()
