@@ -5,13 +5,14 @@ handles made and freed at awkward moments, the range splits of large sets.
 Tolerances as derived in test_gradients.py: an L2 norm is off by 10 u of
 itself, u = 2^-24, a max norm by the one product with the pre-scale."""
 
+import math
 import os
 import re
 
 import pytest
 
 import collective_reduction_gb300 as ar
-from test_gradients import U, assert_close
+from test_gradients import U, adamw_reference, assert_close, tdt, types_of
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 gpu = pytest.mark.gpu
@@ -138,3 +139,97 @@ def test_a_new_handle_is_complete_for_any_stream(sizes):
         assert rec.tolist() == [total, 0.5 if total else 1.0, 0.0, total]
         assert per.tolist() == [float(n) for n in sizes]
         h.close()
+
+
+# ------------------------------------------------- the range splits of large sets
+
+class Large:
+    """Views of guarded device buffers as test_gradients.Tensors, filled on the
+    device: tensor i starts `offset` elements past a 256-byte boundary."""
+
+    def __init__(self, sizes, types, offset=0, seed=0, sigma=1.0, square=False):
+        import torch
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.big, self.views = [], []
+        for n, t in zip(sizes, types_of(types, len(sizes))):
+            big = torch.full((256 + offset + n + 256,), -7.0, dtype=tdt(t), device="cuda")
+            x = torch.randn(n, generator=g, device="cuda") * sigma
+            big[256 + offset:256 + offset + n] = x.square_() if square else x
+            self.big.append(big)
+            self.views.append(big[256 + offset:256 + offset + n])
+        self.lead = 256 + offset
+
+    def check_guards(self):
+        for b, v in zip(self.big, self.views):
+            assert bool((b[:self.lead] == -7.0).all()) and bool((b[self.lead + v.numel():] == -7.0).all())
+
+
+# 1, 2, 4 and 8 warps to a range; several ranges to a block in place (above 120M
+# float32 elements, 240M bfloat16)
+LARGE = {
+    "5m": [5000011, 64, 3, 100003],
+    "20m": [33, 7000001, 0, 13000007],
+    "130m": [130000007, 70001],
+    "500m": [12289, 250000003, 251000001],
+}
+
+
+PAIRS = [("float32", None), ("bfloat16", None), ("mixed", None), ("float32", "float32"), ("bfloat16", "float32"),
+         ("float32", "bfloat16"), ("bfloat16", "bfloat16"), ("mixed", "float32")]
+
+
+@gpu
+@pytest.mark.parametrize("sizes,pair,offsets",
+                         [(s, p, o) for s in ("5m", "20m", "130m") for p in PAIRS
+                          for o in ([(0, 0), (1, 1), (0, 1), (3, 2)] if p[1] else [(0, 0), (1, 1)])] +
+                         [("500m", p, (0, 0)) for p in PAIRS[:2]])
+def test_clip_of_large_sets(sizes, pair, offsets):
+    import torch
+    n = LARGE[sizes]
+    g = Large(n, pair[0], offsets[0], seed=3)
+    o = None if pair[1] is None else Large(n, pair[1], offsets[1], seed=4)
+    before = [v.clone() for v in g.views]
+    square = sum(float(v.double().square().sum()) for v in before)
+    h = ar.Grads(g.views, out=None if o is None else o.views)
+    rec = h.clip(0.25 * math.sqrt(square))
+    assert_close(rec[0].item(), math.sqrt(square), 10 * U, "norm")
+    assert_close(rec[1].item(), 0.25, 11 * U, "scale")
+    for b, a in zip(before, (g if o is None else o).views):
+        assert torch.equal(a, (b.float() * rec[1]).to(a.dtype))
+    g.check_guards()
+    if o is not None:
+        assert all(torch.equal(a, b) for a, b in zip(g.views, before))
+        o.check_guards()
+    h.close()
+
+
+@gpu
+@pytest.mark.parametrize("offsets", [(0, 0, 0, 0, 0), (1, 1, 1, 1, 1), (0, 1, 0, 0, 0), (2, 1, 0, 3, 5)])
+@pytest.mark.parametrize("kinds", [("float32", "float32", False), ("float32", "bfloat16", True),
+                                   ("bfloat16", "bfloat16", False), ("mixed", "mixed", False)])
+@pytest.mark.parametrize("sizes", [[1500001, 3, 5000], [5000011, 64], [20000003, 255, 0, 70001]])
+def test_adamw_of_large_sets(sizes, kinds, offsets):
+    import torch
+    k = len(sizes)
+    p = Large(sizes, kinds[0], offsets[0], seed=1, sigma=0.05)
+    g = Large(sizes, kinds[1], offsets[1], seed=2, sigma=1e-2)
+    m = Large(sizes, "float32", offsets[2], seed=3, sigma=3e-3)
+    v = Large(sizes, "float32", offsets[3], seed=4, sigma=1e-2, square=True)
+    w = Large(sizes, "bfloat16", offsets[4], seed=5) if kinds[2] else None
+    before = [[a.double() for a in x.views] for x in (p, g, m, v)]
+    decay = [float(1 + i % 2) for i in range(k)]
+    opt = ar.AdamW(p.views, g.views, m.views, v.views, copies=w.views if w else None, decay=decay)
+    record = ar.Grads(g.views).norm(max_norm=1e-2)
+    opt.step(7, lr=3e-3, beta2=0.95, weight_decay=0.1, clip=record)
+    for i in range(k):
+        want = adamw_reference(*[b[i] for b in before], record[1].item(), 7, 3e-3, 0.9, 0.95, 1e-8, 0.1 * decay[i])
+        for x, value, bound in ((p, want[0], want[3]), (m, want[1], want[4]), (v, want[2], want[5])):
+            if x.views[i].dtype == torch.bfloat16:
+                bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * value.abs()
+            assert bool(((x.views[i].double() - value).abs() <= bound).all()), (i, sizes[i])
+        if w:
+            assert torch.equal(w.views[i], p.views[i].bfloat16())
+        assert torch.equal(g.views[i].double(), before[1][i])
+    for x in (p, g, m, v, w):
+        if x:
+            x.check_guards()
