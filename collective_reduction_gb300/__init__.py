@@ -307,8 +307,9 @@ class Plan:
 # ------------------------------------------- after the allreduce: many tensors
 
 def _layout(t):
-    """The strides a dense tensor's elements lie at in memory, None for a
-    tensor with gaps, repeated elements or another order than dense."""
+    """The strides a dense tensor's elements lie at in memory (0 in dimensions
+    of size 1, where torch leaves them open), None for a tensor with gaps,
+    repeated elements or another order than dense."""
     if t.is_contiguous():
         return "contiguous"
     want = 1
@@ -316,7 +317,7 @@ def _layout(t):
         if stride != want:
             return None
         want *= size
-    return tuple(t.stride())
+    return tuple(0 if n == 1 else s for n, s in zip(t.shape, t.stride()))
 
 
 def _tensor_list(tensors, what, like=None, dtypes=("float32", "bfloat16")):

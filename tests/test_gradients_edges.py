@@ -233,3 +233,32 @@ def test_adamw_of_large_sets(sizes, kinds, offsets):
     for x in (p, g, m, v, w):
         if x:
             x.check_guards()
+
+
+# ------------------------------------------------- what the binding takes
+
+def layout_pairs():
+    """Pairs of tensors whose elements lie in the same order, made in two ways."""
+    import torch
+    a = torch.zeros(4, 1, 3).permute(2, 1, 0)
+    b = torch.zeros(4, 3).t().unsqueeze(1)
+    c = torch.zeros(2, 5, 3, 1).to(memory_format=torch.channels_last)
+    d = torch.zeros(2, 3, 5).permute(0, 2, 1).unsqueeze(3)
+    return [(a, b), (c, d)]
+
+
+@pytest.mark.parametrize("k", [0, 1])
+def test_dimensions_of_size_one_do_not_tell_layouts_apart(k):
+    a, b = layout_pairs()[k]
+    assert a.shape == b.shape and not a.is_contiguous() and a.stride() != b.stride()
+    assert ar._layout(a) == ar._layout(b) is not None
+
+
+@gpu
+def test_binds_equal_layouts_made_in_two_ways():
+    import torch
+    for a, b in layout_pairs():
+        p, g, m, v = a.cuda(), b.cuda(), torch.zeros_like(a).cuda(), torch.zeros_like(b).cuda()
+        g.normal_(0.0, 1.0)
+        ar.AdamW([p], [g], [m], [v]).step(1, lr=0.5, beta1=0.0, beta2=0.0)
+        assert torch.equal(m, g) and torch.equal(v, g * g)
