@@ -361,6 +361,25 @@ def _float_out(t, n, what):
     return _VP(t.data_ptr())
 
 
+def _version_owners(tensors):
+    """One tensor for each version counter of `tensors` (views of one buffer
+    share it; inference tensors have none)."""
+    owners = {}
+    for t in tensors:
+        if not t.is_inference():
+            owners.setdefault(id(t if t._base is None else t._base), t)
+    return list(owners.values())
+
+
+def _version_raiser():
+    """What tells autograd that a call writes a list of tensors: a backward that
+    saved one of them before then raises, as after torch's own in-place
+    operations.  (The function under torch.autograd.graph.increment_version,
+    whose checks of its argument cost a call 0.3 us.)"""
+    import torch
+    return torch._C._increment_version
+
+
 def tensors_lowering(counts, dtypes):
     """Host only: the ranges a Grads handle over tensors of these sizes and
     element types would work through (ar_tensors_lowering)."""
@@ -378,7 +397,8 @@ class Grads:
 
     Both calls return the record, four floats on the device: norm, scale,
     nonfinite, clipped.  Without `result` that is `self.record`, which the
-    next call overwrites."""
+    next call overwrites.  clip() raises the written tensors' autograd versions
+    (a replay of a captured one does not)."""
 
     def __init__(self, grads, out=None):
         import torch
@@ -392,6 +412,8 @@ class Grads:
                                      None if out is None else _dtype_array(out_types),
                                      None if out is None else _ptrs(self.out), ctypes.byref(h)), "ar_grads_create")
         self._h = h
+        self._raise_versions = _version_raiser()
+        self._written = _version_owners(self.grads if out is None else self.out)
 
     def info(self):
         i = TensorsInfo()
@@ -412,7 +434,9 @@ class Grads:
     def clip(self, max_norm, kind="l2", pre_scale=1.0, result=None, per_tensor=None, stream=None):
         """Enqueue the norm, then every gradient times the record's scale, into
         `out` or in place."""
-        return self._run(lib().ar_grad_clip, "ar_grad_clip", max_norm, kind, pre_scale, result, per_tensor, stream)
+        record = self._run(lib().ar_grad_clip, "ar_grad_clip", max_norm, kind, pre_scale, result, per_tensor, stream)
+        self._raise_versions(self._written)
+        return record
 
     def close(self):
         if getattr(self, "_h", None):
@@ -426,7 +450,8 @@ class AdamW:
     """Parameters (float32 or bfloat16) bound with their gradients, float32
     moments and, for float32 parameters, optional bfloat16 copies for the
     forward pass.  `decay`: one factor of the weight decay per tensor (None:
-    1).  The handle keeps references to all tensors."""
+    1).  The handle keeps references to all tensors.  step() raises the autograd
+    versions of parameters and copies (a replay of a captured one does not)."""
 
     def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, decay=None):
         self.params, ptypes = _tensor_list(params, "params")
@@ -446,6 +471,8 @@ class AdamW:
                                      None if decay is None else (ctypes.c_float * n)(*decay), ctypes.byref(h)),
                "ar_adamw_create")
         self._h = h
+        self._raise_versions = _version_raiser()
+        self._written = _version_owners(self.params + (self.copies or []))  # no graph saves the moments
 
     def info(self):
         i = TensorsInfo()
@@ -467,6 +494,7 @@ class AdamW:
                 raise ValueError("step counts from 1")
             p = AdamWParams(int(step), lr, beta1, beta2, eps, weight_decay)
             _check(lib().ar_adamw_step(self._h, ctypes.byref(p), record, stream), "ar_adamw_step")
+            self._raise_versions(self._written)
             return
         if str(step.dtype) != "torch.int64" or not step.is_cuda or step.numel() != 1:
             raise ValueError("step: expected an int or a CUDA tensor of one int64")
@@ -475,6 +503,7 @@ class AdamW:
         _check(lib().ar_adamw_step_counted(self._h, ctypes.byref(p), step.data_ptr(),
                                            _float_out(lr, 1, "lr") if on_device else None, record, stream),
                "ar_adamw_step_counted")
+        self._raise_versions(self._written)
 
     def close(self):
         if getattr(self, "_h", None):

@@ -262,3 +262,62 @@ def test_binds_equal_layouts_made_in_two_ways():
         g.normal_(0.0, 1.0)
         ar.AdamW([p], [g], [m], [v]).step(1, lr=0.5, beta1=0.0, beta2=0.0)
         assert torch.equal(m, g) and torch.equal(v, g * g)
+
+
+# ------------------------------------------------- what autograd sees
+
+@gpu
+def test_backward_over_a_value_from_before_the_update_is_an_error():
+    import torch
+    w, x = torch.randn(8, 8, device="cuda", requires_grad=True), torch.randn(8, 8, device="cuda", requires_grad=True)
+    low = torch.randn(8, 8, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    g, m, v = (torch.ones(8, 8, device="cuda") for _ in range(3))
+    opt = ar.AdamW([w], [g], [m], [v], copies=[low])
+    steps = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for counted in (False, True):
+        saved = (x @ w).sum(), (x.bfloat16() @ low).sum()
+        opt.step(steps if counted else 1, lr=0.1)
+        for loss in saved:
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+        (x @ w).sum().backward()  # a forward after the update is fine
+
+
+@gpu
+@pytest.mark.parametrize("elsewhere", [False, True])
+def test_backward_over_a_gradient_from_before_the_clip_is_an_error(elsewhere):
+    import torch
+    g, x = torch.ones(64, device="cuda"), torch.ones(64, device="cuda", requires_grad=True)
+    out = torch.ones(64, device="cuda") if elsewhere else None
+    h = ar.Grads([g[:32], g[32:]], out=[out[:32], out[32:]] if elsewhere else None)
+    read, written = (x * g).sum(), (x * out).sum() if elsewhere else None
+    h.norm(max_norm=1.0)
+    read.backward(retain_graph=True)  # a norm writes nothing
+    h.clip(1.0)
+    if elsewhere:
+        read.backward()
+        read = written
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        read.backward()
+
+
+@gpu
+def test_tensors_without_versions_are_taken_too():
+    import torch
+    with torch.inference_mode():
+        p, g, m, v = (torch.zeros(8, device="cuda") for _ in range(4))
+    opt = ar.AdamW([p], [g], [m], [v])
+    opt.step(1, lr=0.5, weight_decay=0.5)
+    ar.Grads([g]).clip(1.0)
+    assert not bool(p.any())
+
+
+def test_one_version_counter_is_raised_once():
+    import torch
+    flat, alone = torch.zeros(12), torch.zeros(3)
+    owners = ar._version_owners([flat[:4], flat[4:], flat.view(3, 4), alone, alone])
+    assert len(owners) == 2
+    ar._version_raiser()(owners)
+    assert flat._version == 1 and flat[:4]._version == 1 and alone._version == 1
+    with torch.inference_mode():
+        assert ar._version_owners([torch.zeros(3)]) == []
