@@ -20,6 +20,7 @@ What follows the allreduce in a training step works on lists of tensors:
 
 import ctypes
 import os
+import sys
 
 DTYPES = {"int32": 0, "float32": 1, "bfloat16": 2}
 OPS = {"sum": 0, "prod": 1, "max": 2, "min": 3, "avg": 4}
@@ -203,6 +204,24 @@ def _stream_handle(stream):
     return int(stream)
 
 
+_retired = []
+
+
+def _free(destroy=None, handle=None, keep=None):
+    """Free a device handle, and those that still wait for it.  Freeing
+    synchronises the device, which would end a capture: handles that go while
+    the current stream captures (the collector may come then) wait, with the
+    tensors they `keep`, until a handle is made or freed outside one."""
+    if handle:
+        _retired.append((destroy, handle, keep))
+    torch = sys.modules.get("torch")
+    if torch and torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+        return
+    while _retired:
+        destroy, handle, keep = _retired.pop()
+        destroy(handle)
+
+
 class Schedule:
     """Host-only compiled schedule: counters, per-round traffic, trees."""
 
@@ -262,6 +281,7 @@ class Plan:
         self.P, self.n, self.dtype = P, n, dtype
         p, self._keep = _params(**params)
         h = _VP()
+        _free()
         _check(lib().ar_plan_create(P, n, DTYPES[dtype], OPS[op], ALGOS[algo], ctypes.byref(p),
                                     ctypes.byref(h)), "ar_plan_create")
         self._h = h
@@ -298,8 +318,8 @@ class Plan:
 
     def close(self):
         if getattr(self, "_h", None):
-            lib().ar_plan_destroy(self._h)
-            self._h = None
+            h, self._h = self._h, None
+            _free(lib().ar_plan_destroy, h)
 
     __del__ = close
 
@@ -408,6 +428,7 @@ class Grads:
         torch.cuda.current_stream().synchronize()  # the calls may run on any stream
         self._record = _VP(self.record.data_ptr())
         h = _VP()
+        _free()
         _check(lib().ar_grads_create(len(self.grads), _counts(self.grads), _dtype_array(types), _ptrs(self.grads),
                                      None if out is None else _dtype_array(out_types),
                                      None if out is None else _ptrs(self.out), ctypes.byref(h)), "ar_grads_create")
@@ -440,8 +461,8 @@ class Grads:
 
     def close(self):
         if getattr(self, "_h", None):
-            lib().ar_grads_destroy(self._h)
-            self._h = None
+            h, self._h = self._h, None
+            _free(lib().ar_grads_destroy, h, (self.grads, self.out, self.record))
 
     __del__ = close
 
@@ -465,6 +486,7 @@ class AdamW:
             raise ValueError(f"decay: expected {len(self.params)} factors, got {len(decay)}")
         n = len(self.params)
         h = _VP()
+        _free()
         _check(lib().ar_adamw_create(n, _counts(self.params), _dtype_array(ptypes), _ptrs(self.params),
                                      _dtype_array(gtypes), _ptrs(self.grads), _ptrs(self.exp_avg),
                                      _ptrs(self.exp_avg_sq), None if copies is None else _ptrs(self.copies),
@@ -507,8 +529,8 @@ class AdamW:
 
     def close(self):
         if getattr(self, "_h", None):
-            lib().ar_adamw_destroy(self._h)
-            self._h = None
+            h, self._h = self._h, None
+            _free(lib().ar_adamw_destroy, h, (self.params, self.grads, self.exp_avg, self.exp_avg_sq, self.copies))
 
     __del__ = close
 

@@ -144,6 +144,20 @@ cudaError_t upload_items(const std::vector<Tensor>& tensors, const std::vector<u
 // A positive number that float32 holds without losing digits.
 bool float_normal(double x) { return x >= 1.17549436e-38 && x <= kFloatMax; }
 
+// Frees a handle when its device has done its work, whichever is current.
+template <class Handle>
+ar_status destroy(Handle* h) {
+    if (!h) return AR_ERR_INVALID_ARG;
+    int now = -1;
+    cudaError_t e = cudaGetDevice(&now);
+    const bool other = e == cudaSuccess && now != h->device;
+    if (other) e = cudaSetDevice(h->device);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    delete h;
+    if (other) cudaSetDevice(now);
+    return cuda_status(e);
+}
+
 bool on_device(int device) {
     int now = -1;
     return cudaGetDevice(&now) == cudaSuccess && now == device;
@@ -382,12 +396,7 @@ ar_status ar_grads_query(ar_grads_t h, ar_tensors_info* info) {
     return AR_OK;
 }
 
-ar_status ar_grads_destroy(ar_grads_t h) {
-    if (!h) return AR_ERR_INVALID_ARG;
-    const cudaError_t e = cudaDeviceSynchronize();
-    delete h;
-    return cuda_status(e);
-}
+ar_status ar_grads_destroy(ar_grads_t h) { return destroy(h); }
 
 ar_status ar_grad_norm(ar_grads_t h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
                        float* tensor_norms, void* stream) {
@@ -491,12 +500,7 @@ ar_status ar_adamw_query(ar_adamw_t h, ar_tensors_info* info) {
     return AR_OK;
 }
 
-ar_status ar_adamw_destroy(ar_adamw_t h) {
-    if (!h) return AR_ERR_INVALID_ARG;
-    const cudaError_t e = cudaDeviceSynchronize();
-    delete h;
-    return cuda_status(e);
-}
+ar_status ar_adamw_destroy(ar_adamw_t h) { return destroy(h); }
 
 ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* p, const float* result, void* stream) {
     ar::TraceRange trace("ar_adamw_step");

@@ -420,7 +420,10 @@ ar_status ar_tensors_lowering(int n_tensors, const uint64_t* counts, const ar_dt
 ar_status ar_grads_create(int n_tensors, const uint64_t* counts, const ar_dtype* grad_dtypes, void* const* grads,
                           const ar_dtype* out_dtypes, void* const* outs, ar_grads_t* out);
 ar_status ar_grads_query(ar_grads_t h, ar_tensors_info* info);
-/* Frees the handle, not the tensors.  Synchronises the device first. */
+/* Frees the handle, not the tensors.  Synchronises the handle's device first
+ * (so not while a stream of it captures: that would end the capture).  A graph
+ * that captured calls on the handle uses its memory at every replay: destroy
+ * the handle after the graph. */
 ar_status ar_grads_destroy(ar_grads_t h);
 
 /* The norm of all N tensors as one vector g, times the pre-scale c (one over
@@ -454,7 +457,7 @@ ar_status ar_adamw_create(int n_tensors, const uint64_t* counts, const ar_dtype*
                           const ar_dtype* grad_dtypes, void* const* grads, float* const* exp_avg,
                           float* const* exp_avg_sq, void* const* copies, const float* decay, ar_adamw_t* out);
 ar_status ar_adamw_query(ar_adamw_t h, ar_tensors_info* info);
-ar_status ar_adamw_destroy(ar_adamw_t h);
+ar_status ar_adamw_destroy(ar_adamw_t h);  /* as ar_grads_destroy */
 
 typedef struct {
     uint64_t step;        /* t, from 1: the number of this update          */

@@ -321,3 +321,69 @@ def test_one_version_counter_is_raised_once():
     assert flat._version == 1 and flat[:4]._version == 1 and alone._version == 1
     with torch.inference_mode():
         assert ar._version_owners([torch.zeros(3)]) == []
+
+
+# ------------------------------------------------- freeing handles
+
+def test_handles_wait_for_the_end_of_a_capture(monkeypatch):
+    """_free against a stand-in for torch: nothing is freed while the current
+    stream captures, everything with the next handle after it."""
+    class Cuda:
+        capturing = False
+
+        def is_initialized(self):
+            return True
+
+        def is_current_stream_capturing(self):
+            return self.capturing
+
+    class Torch:
+        cuda = Cuda()
+    monkeypatch.setitem(ar.sys.modules, "torch", Torch)
+    freed = []
+    ar._free(freed.append, 1)
+    assert freed == [1]
+    Torch.cuda.capturing = True
+    ar._free(freed.append, 2, keep="tensors")
+    ar._free(freed.append, 3)
+    ar._free()
+    assert freed == [1] and [h for _, h, _ in ar._retired] == [2, 3]
+    Torch.cuda.capturing = False
+    ar._free()
+    assert sorted(freed) == [1, 2, 3] and not ar._retired
+
+
+@gpu
+def test_handles_dropped_during_a_capture_do_not_end_it():
+    import torch
+    g = [torch.full((1000,), 2.0, device="cuda")]
+    lasting, dropped = ar.Grads(g), [ar.Grads(g)]
+    p, m, v = ([torch.zeros(1000, device="cuda")] for _ in range(3))
+    dropped.append(ar.AdamW(p, g, m, v))
+    dropped.append(ar.Plan(2, 64, "float32", "sum", "ring"))
+    lasting.clip(1e9)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lasting.clip(1e9, pre_scale=0.5)
+        dropped.clear()
+        assert len(ar._retired) == 3
+        lasting.norm()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert bool((g[0] == 1.0).all())
+    ar.Grads(g).close()
+    assert not ar._retired
+    graph.replay()
+    assert bool((g[0] == 0.5).all())
+
+
+@gpu
+def test_closing_twice_and_calls_after_it():
+    import torch
+    g = [torch.ones(8, device="cuda")]
+    h = ar.Grads(g)
+    h.close()
+    h.close()
+    with pytest.raises(ar.ArError):
+        h.norm()
