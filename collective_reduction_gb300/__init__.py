@@ -16,6 +16,7 @@ What follows the allreduce in a training step works on lists of tensors:
     record = grads.norm(max_norm=1.0)        # [norm, scale, nonfinite, clipped], on the device
     opt = ar.AdamW(params, [p.grad for p in params], exp_avg, exp_avg_sq)
     opt.step(1, lr=3e-4, clip=record)        # reads the scale on the device: no pass of its own, no sync
+    # or grads.clip(1.0), which scales the gradients, and then opt.step without clip
 """
 
 import ctypes
@@ -413,7 +414,10 @@ def tensors_lowering(counts, dtypes):
 class Grads:
     """Gradient tensors bound for norms and clipping (float32 or bfloat16,
     each its own; dense).  `out`: the tensors that clip() writes, of the same
-    sizes (None: in place).  The handle keeps references to all of them.
+    sizes (None: in place).  The handle keeps references to all of them, and
+    goes on with them when a parameter's .grad has become another tensor: zero
+    gradients in place (zero_grad(set_to_none=False)) or make a new handle.  A
+    CUDA graph that captured calls does not keep the handle: do, while it lives.
 
     Both calls return the record, four floats on the device: norm, scale,
     nonfinite, clipped.  Without `result` that is `self.record`, which the
@@ -471,7 +475,8 @@ class AdamW:
     """Parameters (float32 or bfloat16) bound with their gradients, float32
     moments and, for float32 parameters, optional bfloat16 copies for the
     forward pass.  `decay`: one factor of the weight decay per tensor (None:
-    1).  The handle keeps references to all tensors.  step() raises the autograd
+    1).  The handle keeps references to all tensors and goes on with these, as
+    Grads does; a CUDA graph that captured calls does not keep it.  step() raises the autograd
     versions of parameters and copies (a replay of a captured one does not)."""
 
     def __init__(self, params, grads, exp_avg, exp_avg_sq, copies=None, decay=None):

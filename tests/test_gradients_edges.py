@@ -387,3 +387,41 @@ def test_closing_twice_and_calls_after_it():
     h.close()
     with pytest.raises(ar.ArError):
         h.norm()
+
+
+# ------------------------------------------------- the example in the README
+
+def readme_alternatives():
+    """The lines of README's example of a training step, once for each of its
+    alternatives ("# either ...", "# or ...")."""
+    with open(os.path.join(ROOT, "README.md")) as f:
+        text = f.read().split("After the allreduce, over lists of tensors", 1)[1].split("\n\n", 1)[1]
+    lines = [x[4:] for x in re.match(r"(?:    .*\n|\n)+", text).group(0).splitlines()]
+    parts = re.split(r"(?m)^# (?:either|or)\b.*$", "\n".join(x for x in lines if not x.startswith("python ")))
+    return [parts[0] + p for p in parts[1:]] or parts
+
+
+@gpu
+def test_the_readme_example_scales_the_gradients_once():
+    import torch
+    assert len(readme_alternatives()) == 2
+    for code in readme_alternatives():
+        gen = torch.Generator(device="cuda").manual_seed(1)
+        params = [torch.zeros(n, device="cuda") for n in (1000, 77)]
+        for p in params:
+            p.grad = torch.randn(p.shape, generator=gen, device="cuda")
+        masters = [torch.randn(p.shape, generator=gen, device="cuda") for p in params]
+        exp_avg = [torch.randn(p.shape, generator=gen, device="cuda") for p in params]
+        exp_avg_sq = [torch.rand(p.shape, generator=gen, device="cuda") for p in params]
+        before = [[x.double() for x in xs] for xs in (masters, [p.grad for p in params], exp_avg, exp_avg_sq)]
+        names = {"ar": ar, "params": params, "masters": masters, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq,
+                 "bf16_weights": [p.bfloat16() for p in params], "step": 3}
+        exec(code, names)
+        norm = math.sqrt(sum(float(g.square().sum()) for g in before[1]))
+        for i in range(2):
+            want = adamw_reference(*[x[i] for x in before], 1.0 / norm, 3, 3e-4, 0.9, 0.999, 1e-8, 0.1)
+            # the scale is off by 11 u, a gradient clipped in place by one more: 12 u on m (6 u by itself), 24 u on v
+            # (8 u) and so 24 u on the update (16 u): within 4 times the bounds
+            for got, value, bound in ((masters, want[0], want[3]), (exp_avg, want[1], want[4]),
+                                      (exp_avg_sq, want[2], want[5])):
+                assert bool(((got[i].double() - value).abs() <= 4 * bound).all())
