@@ -18,15 +18,22 @@ constexpr int kMaxTensors = 1 << 20;
 constexpr uint64_t kMaxElems = uint64_t(1) << 40;
 
 // One wave of warps on GB300's 152 SMs: the norm kernel runs 3 CTAs of 8 warps
-// on each, the AdamW kernel 4.  The ranges are the largest, up to a full one,
-// that fill a whole number of waves: a set a little over one wave of full
-// ranges would wait for the few warps with two.  Measured: a norm of 180 MB
-// (1.004 waves of full ranges) 31.6 us in two waves, 39.1 in full ranges; one of
-// 25 MB 9.8 us in one wave, 15.4 in ranges of 1024 elements.  Full: a norm of
-// 4.2 GB takes in bf16 583 us in ranges of 12288 elements, 587 and 597 of 8192
+// on each, the AdamW kernel 4 (off alignment 6: its ranges are sized for 4 all the
+// same).  Constants, as a set's ranges follow from its sizes alone, also where no
+// device is asked (ar_tensors_lowering).
+//
+// A set takes as many waves of ranges as full ones would need, and the range is
+// what each warp gets then, rounded up to a multiple of the step that is larger.
+// The rounding counts where a warp gets one or a few steps: 15 MB of float32
+// (one step each) are split into ranges of two, which half of a wave takes, 25 MB
+// into 0.83 of a wave, 180 MB (1.004 waves of full ranges) into 1.7.  Measured in a
+// graph: a norm of 180 MB 31.9 us, 39.1 in full ranges, where a few warps have two
+// and the others wait; one of 25 MB 9.8 us, 15.4 in ranges of one step.  Full: a norm
+// of 4.2 GB takes in bf16 583 us in ranges of 12288 elements, 587 and 597 of 8192
 // and 16384, in float32 1148 us, 1178 and 1167; AdamW on a billion, the norm
-// included, 4526 us in ranges of 512, 4545 and 4565 of 768 and 1024, and on 0.4M
-// 3.9 us in ranges of 256, 8.4 of 1024.
+// included, 4541 us in ranges of 512, 4559 and 4575 of 768 and 1024, and on 0.4M
+// 3.85 us in ranges of 256, 8.4 of 1024.  An AdamW range is 64 bytes of table: an
+// eighth of a byte a parameter.
 constexpr uint64_t kNormWave = 152 * ar::kNormCtasPerSm * ar::kGradWarps, kAdamWave = 152 * 4 * ar::kGradWarps;
 constexpr uint32_t kGradItemMax = 12288, kAdamItemStep = 256, kAdamItemMax = 512;
 

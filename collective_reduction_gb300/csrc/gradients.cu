@@ -1,13 +1,16 @@
 // Kernels over many tensors after a gradient allreduce: the global norm, the
 // scaling by the clip factor, and the AdamW update.  All are bound by HBM at
-// size and by launches and one dependent chain when small.  Measured on GB300,
-// TB/s of the bytes each has to move (a copy: 6.77):
+// size and by launches and one dependent chain when small.  Measured on GB300 in
+// a CUDA graph, sets rotating beyond L2; TB/s of the bytes each has to move (a
+// copy: 6.77):
 //
-//   norm    4.3 GB of bf16 580 us (7.4), 25 MB of float32 9.8 us, 35 KB 3.75 us
-//   clip    2.7 GB of float32 into other tensors 1139 us (7.1 of its two reads
-//           and one write), 96 MB 44 us, 0.4 MB 5.25 us
+//   norm    4.3 GB of bf16 581 us (7.4), 25 MB of float32 9.8 us, 35 KB 3.75 us
+//   clip    2.7 GB of float32 into other tensors 1144 us (7.0 of its two reads
+//           and one write), in place 1154 us, 96 MB 44.8 us, 0.4 MB 5.25 us
 //   AdamW   184M float32 parameters, bf16 gradients and copies 737 us (7.0),
-//           0.4M float32 parameters 3.9 us
+//           0.4M float32 parameters 3.85 us
+//
+// (Called from Python in a loop, where launches overlap, 25 MB takes 8.3 us.)
 //
 // A handle's tables split every tensor into ranges ("items"); a warp works
 // through one item at a time, so items of tiny tensors run beside each other
@@ -388,7 +391,7 @@ __device__ __forceinline__ void norm_item(Acc& acc, const char* src, uint32_t co
 // One list would do but for its counter: an item every 3 ns is what one
 // address gives out (4.3 GB in ranges of 8192 elements: 897 us with one list,
 // 580 with eight).  Fewer items than warps are one list, an item to each of the
-// first warps (25 MB: 9.7 us, 11.6 dealt to eight).  Item and draw are fetched
+// first warps (25 MB in a graph: 9.8 us, 11.6 dealt to eight).  Item and draw are fetched
 // one item ahead.
 // KEEP: a reader of the gradients follows, in the reverse order.
 template <class Acc, bool KEEP>
@@ -621,13 +624,13 @@ __device__ __forceinline__ void scale_item(const GradItem& it, float f, uint32_t
 // The items in the reverse of the norm's order: the norm leaves its last ones
 // in L2.  Loads and stores are streaming (neither is used again), so the
 // results do not push out the gradients that wait there.  item_warps warps
-// share an item, 4 KB of gradients to each: 2.7 GB of float32 take 1141 us,
-// 1148 with twice that a warp, 1176 with an item a warp.
+// share an item, 4 KB of gradients to each: a clip of 2.7 GB of float32 takes
+// 1144 us, 1155 with twice that a warp, 1164 with an item a warp.
 // In place, a factor of exactly 1 leaves nothing to do, as for most steps of a
 // training that runs well; then the CTAs' starts are what is left, and a CTA
-// takes several items in turn: 2.7 GB within the bound 370 us, 447 with an item
-// a CTA.  (Into other tensors, where that case writes all the same, an item a
-// CTA is the faster: 1139 us against 1156.)
+// takes several items in turn: 2.7 GB within the bound 377 us, 451 with an item
+// a CTA; scaled it is the slower, 1154 us against 1133.  Into other tensors,
+// which are written either way, it is an item a CTA: 1144 us against 1164.
 __global__ void __launch_bounds__(kGradThreads, 4) scale_kernel(const __grid_constant__ ScaleArgs a) {
     const uint32_t side = kGradWarps / a.item_warps;  // items side by side in a CTA
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % a.item_warps;
@@ -736,9 +739,10 @@ __device__ __forceinline__ void adam_item(const AdamArgs& a, const AdamScalars& 
 // order, whose last gradients may still be in L2.  Bound by HBM.
 // WHOLE: every stream moves in quads.  Two quads of each in flight a thread at
 // 4 CTAs an SM; a stream off its alignment takes single elements, which need
-// more warps instead: one quad, 6 CTAs.  Measured both ways, norm included: a
-// billion float32 parameters 4530 and 4646 us; 122M bf16 parameters whose bf16
-// gradients are packed tight at odd sizes 481 and 431.
+// more warps instead: one quad, 6 CTAs (whose 40 registers a thread spill a
+// few: 16 bytes stored, 104 read).  Measured both ways, norm included: a billion
+// float32 parameters 4541 and 4653 us; 122M bf16 parameters whose bf16 gradients
+// are packed tight at odd sizes 501 and 440 (457 with 5 CTAs).
 template <bool WHOLE>
 __global__ void __launch_bounds__(kGradThreads, WHOLE ? 4 : 6) adamw_kernel(const __grid_constant__ AdamArgs a) {
     const uint32_t lane = threadIdx.x & 31;

@@ -398,8 +398,10 @@ typedef struct {
     int n_tensors;
     uint64_t elems;        /* over all tensors                                  */
     uint64_t n_items;      /* ranges the kernels work through, one warp each    */
-    uint64_t item_elems;   /* elements of every range but a tensor's last       */
-    uint64_t table_bytes;  /* device memory the handle owns (0 without one)     */
+    uint64_t item_elems;   /* elements of a range; a tensor's first and last may
+                            * be shorter                                        */
+    uint64_t table_bytes;  /* device memory the handle owns (0 without one): 64
+                            * bytes a range of an AdamW handle, 40 of gradients */
     int tiling_ok;         /* ar_tensors_lowering: the ranges tile every tensor */
 } ar_tensors_info;
 
@@ -442,7 +444,7 @@ ar_status ar_grads_destroy(ar_grads_t h);
 ar_status ar_grad_norm(ar_grads_t h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
                        float* tensor_norms, void* stream);
 /* ar_grad_norm, then every element times result[1], rounded to nearest even
- * in its output's type: global-norm clipping.  With a nonfinite element the
+ * in float32 and from there in its output's type: global-norm clipping.  With a nonfinite element the
  * factor is c: infinities and NaN stay where they are for whoever looks for
  * them.  In place a factor of exactly 1 writes nothing. */
 ar_status ar_grad_clip(ar_grads_t h, ar_norm_kind kind, double pre_scale, double max_norm, float* result,
