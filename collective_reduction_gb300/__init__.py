@@ -17,6 +17,12 @@ What follows the allreduce in a training step works on lists of tensors:
     opt = ar.AdamW(params, [p.grad for p in params], exp_avg, exp_avg_sq)
     opt.step(1, lr=3e-4, clip=record)        # reads the scale on the device: no pass of its own, no sync
     # or grads.clip(1.0), which scales the gradients, and then opt.step without clip
+
+and what comes before it, a rank's loss and the gradients of its output layer:
+
+    loss = ar.OutputLoss(tokens=4096, hidden=2048, vocab=50001)
+    record = loss.cross_entropy(hidden, weight, targets, grad_hidden=dh, grad_weight=dw)
+    # [loss, counted, nonfinite, factor]; or loss.distill(hidden, weight, teacher_ids, teacher_logits, ...)
 """
 
 import ctypes
@@ -32,6 +38,7 @@ GROUPS = {"cyclic": 0, "xor": 1}
 PHASES = {"allreduce": 0, "reduce_scatter": 1, "all_gather": 2}
 JIT = {"auto": 0, "on": 1, "off": -1}
 NORMS = {"l2": 0, "max": 1}
+REDUCTIONS = {"mean": 0, "sum": 1}
 ESIZE = {"int32": 4, "float32": 4, "bfloat16": 2}
 KERNEL_STREAM, KERNEL_STAGED, KERNEL_ELEMENTWISE, KERNEL_DAG_JIT, KERNEL_WORD_JIT, KERNEL_CHAIN_WORD = 1, 2, 4, 8, 16, 32
 KERNEL_COPY, KERNEL_FEW = 64, 128
@@ -103,6 +110,25 @@ class AdamWParams(ctypes.Structure):
                 ("beta2", ctypes.c_double), ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
 
 
+class OutputLossInfo(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_uint64), ("hidden", ctypes.c_uint64), ("vocab", ctypes.c_uint64),
+                ("top", ctypes.c_int), ("piece", ctypes.c_uint64), ("pieces", ctypes.c_int),
+                ("workspace_bytes", ctypes.c_uint64), ("tiling_ok", ctypes.c_int)]
+
+    def as_dict(self):
+        return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+class OutputLossArgs(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_uint64), ("hidden", ctypes.c_void_p), ("hidden_stride", ctypes.c_uint64),
+                ("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_uint64),
+                ("grad_hidden", ctypes.c_void_p), ("grad_hidden_stride", ctypes.c_uint64),
+                ("grad_hidden_dtype", ctypes.c_int),
+                ("grad_weight", ctypes.c_void_p), ("grad_weight_stride", ctypes.c_uint64),
+                ("grad_weight_dtype", ctypes.c_int), ("accumulate", ctypes.c_int), ("reduction", ctypes.c_int),
+                ("scale", ctypes.c_double), ("losses", ctypes.c_void_p), ("result", ctypes.c_void_p)]
+
+
 _lib = None
 _VP = ctypes.c_void_p
 _U64P, _INTP, _VPP = ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_void_p)
@@ -145,6 +171,18 @@ _EXPORTS = {
     "ar_adamw_destroy": (ctypes.c_int, [_VP]),
     "ar_adamw_step": (ctypes.c_int, [_VP, ctypes.POINTER(AdamWParams), _VP, _VP]),
     "ar_adamw_step_counted": (ctypes.c_int, [_VP, ctypes.POINTER(AdamWParams), _VP, _VP, _VP, _VP]),
+    "ar_output_loss_layout": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_int,
+                                             ctypes.c_int, ctypes.c_uint64, ctypes.c_int,
+                                             ctypes.POINTER(OutputLossInfo)]),
+    "ar_output_loss_create": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint64, ctypes.c_uint64, ctypes.c_int,
+                                             ctypes.c_int, ctypes.c_uint64, ctypes.c_int, _VPP]),
+    "ar_output_loss_query": (ctypes.c_int, [_VP, ctypes.POINTER(OutputLossInfo)]),
+    "ar_output_loss_destroy": (ctypes.c_int, [_VP]),
+    "ar_output_loss_check": (ctypes.c_int, [_VP]),
+    "ar_output_cross_entropy": (ctypes.c_int, [_VP, ctypes.POINTER(OutputLossArgs), _VP, ctypes.c_int,
+                                               ctypes.c_int64, _VP]),
+    "ar_output_distill": (ctypes.c_int, [_VP, ctypes.POINTER(OutputLossArgs), _VP, ctypes.c_int, ctypes.c_uint64,
+                                         _VP, ctypes.c_int, ctypes.c_uint64, ctypes.c_int, ctypes.c_double, _VP]),
 }
 
 
@@ -536,6 +574,132 @@ class AdamW:
         if getattr(self, "_h", None):
             h, self._h = self._h, None
             _free(lib().ar_adamw_destroy, h, (self.params, self.grads, self.exp_avg, self.exp_avg_sq, self.copies))
+
+    __del__ = close
+
+
+# ---------------------------------- before the allreduce: the output layer
+
+def output_loss_layout(tokens, hidden, vocab, dtype="bfloat16", top=0, piece=0, grads=True):
+    """Host only: the sizes an OutputLoss of these arguments would have
+    (ar_output_loss_layout)."""
+    info = OutputLossInfo()
+    _check(lib().ar_output_loss_layout(tokens, hidden, vocab, DTYPES[dtype], top, piece, int(grads),
+                                       ctypes.byref(info)), "ar_output_loss_layout")
+    return info.as_dict()
+
+
+def _rows_of(t, what, rows, width, dtypes):
+    """Address, row stride and element type of a CUDA matrix whose rows are dense."""
+    name = str(t.dtype).replace("torch.", "")
+    if name not in dtypes:
+        raise ValueError(f"{what}: element type {name}, expected {' or '.join(dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: not a CUDA tensor")
+    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{what}: expected shape ({'n' if rows is None else rows}, {width}), got {tuple(t.shape)}")
+    if (width > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < width):
+        raise ValueError(f"{what}: its rows are not dense and apart (strides {t.stride()})")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else width), name
+
+
+class OutputLoss:
+    """The losses of an output layer, logits = hidden @ weight.T, for up to
+    `tokens` tokens, without an array of tokens x vocab; with the gradients of
+    hidden states and weights.  hidden and weight are bfloat16 or float32
+    (`dtype`), as (n, hidden) and (vocab, hidden) tensors with any row stride.
+    `top`: entries of a teacher's list at most; `piece`: vocabulary entries worked
+    on at a time (0: chosen); `grads=False`: losses alone, little workspace.
+
+    Both calls return the record, four floats on the device: loss, tokens
+    counted, nonfinite, factor.  Without `result` that is `self.record`, which
+    the next call overwrites.  loss = factor * sum of the counted tokens' losses,
+    factor = scale / counted (reduction "mean") or scale ("sum"); the gradients are
+    the loss's, in the dtype or float32, written or (accumulate) added to what is
+    there.  `losses` (float32, n) takes every token's loss, 0 for tokens that do
+    not count.  The written gradients' autograd versions are raised (a replay of
+    a captured call does not).  Calls on one handle share its workspace: order
+    them on one stream.  A CUDA graph that captured calls does not keep the
+    handle: do, while it lives."""
+
+    def __init__(self, tokens, hidden, vocab, dtype="bfloat16", top=0, piece=0, grads=True):
+        import torch
+        self.tokens, self.hidden, self.vocab, self.dtype, self.top = tokens, hidden, vocab, dtype, top
+        h = _VP()
+        _free()
+        _check(lib().ar_output_loss_create(tokens, hidden, vocab, DTYPES[dtype], top, piece, int(grads),
+                                           ctypes.byref(h)), "ar_output_loss_create")
+        self._h = h
+        self.record = torch.zeros(4, dtype=torch.float32, device="cuda")
+        torch.cuda.current_stream().synchronize()  # the calls may run on any stream
+        self._raise_versions = _version_raiser()
+
+    def info(self):
+        i = OutputLossInfo()
+        _check(lib().ar_output_loss_query(self._h, ctypes.byref(i)), "ar_output_loss_query")
+        return i.as_dict()
+
+    def _args(self, hidden, weight, reduction, scale, grad_hidden, grad_weight, accumulate, losses, result):
+        a = OutputLossArgs()
+        a.hidden, a.hidden_stride, _ = _rows_of(hidden, "hidden", None, self.hidden, (self.dtype,))
+        n = a.tokens = hidden.shape[0]
+        if n > self.tokens:
+            raise ValueError(f"hidden: {n} tokens, the handle is for {self.tokens}")
+        a.weight, a.weight_stride, _ = _rows_of(weight, "weight", self.vocab, self.hidden, (self.dtype,))
+        types = (self.dtype, "float32")
+        if grad_hidden is not None:
+            a.grad_hidden, a.grad_hidden_stride, name = _rows_of(grad_hidden, "grad_hidden", n, self.hidden, types)
+            a.grad_hidden_dtype = DTYPES[name]
+        if grad_weight is not None:
+            a.grad_weight, a.grad_weight_stride, name = _rows_of(grad_weight, "grad_weight", self.vocab, self.hidden,
+                                                                 types)
+            a.grad_weight_dtype = DTYPES[name]
+        a.accumulate, a.reduction, a.scale = int(bool(accumulate)), REDUCTIONS[reduction], scale
+        if losses is not None:
+            a.losses = _float_out(losses, n, "losses").value
+        a.result = _float_out(self.record if result is None else result, 4, "result").value
+        return a
+
+    def _done(self, grad_hidden, grad_weight, result):
+        self._raise_versions([t for t in (grad_hidden, grad_weight) if t is not None and not t.is_inference()])
+        return self.record if result is None else result
+
+    def cross_entropy(self, hidden, weight, targets, ignore_index=-100, reduction="mean", scale=1.0,
+                      grad_hidden=None, grad_weight=None, accumulate=False, losses=None, result=None, stream=None):
+        """Enqueue the softmax cross entropy of every token against its target
+        (int64 or int32, n; `ignore_index`: the token does not count)."""
+        a = self._args(hidden, weight, reduction, scale, grad_hidden, grad_weight, accumulate, losses, result)
+        size = {"torch.int64": 8, "torch.int32": 4}.get(str(targets.dtype))
+        if size is None or not targets.is_cuda or not targets.is_contiguous() or targets.shape != (a.tokens,):
+            raise ValueError(f"targets: expected {a.tokens} contiguous int64 or int32 on the device")
+        _check(lib().ar_output_cross_entropy(self._h, ctypes.byref(a), targets.data_ptr(), size, ignore_index,
+                                             _stream_handle(stream)), "ar_output_cross_entropy")
+        return self._done(grad_hidden, grad_weight, result)
+
+    def distill(self, hidden, weight, ids, logits, temperature=1.0, reduction="mean", scale=1.0,
+                grad_hidden=None, grad_weight=None, accumulate=False, losses=None, result=None, stream=None):
+        """Enqueue the distillation from each token's k teacher logits (bfloat16 or
+        float32, (n, k)) at `ids` (int64 or int32, (n, k); negative: no entry, as
+        a logit of -infinity): temperature^2 times the Kullback-Leibler divergence
+        of the student's softmax over the vocabulary from the teacher's over its
+        list, both at the temperature.  A token without entries does not count."""
+        a = self._args(hidden, weight, reduction, scale, grad_hidden, grad_weight, accumulate, losses, result)
+        k = ids.shape[1] if ids.dim() == 2 else -1
+        at, stride, name = _rows_of(ids, "ids", a.tokens, k, ("int64", "int32"))
+        t_at, t_stride, t_name = _rows_of(logits, "logits", a.tokens, k, ("bfloat16", "float32"))
+        _check(lib().ar_output_distill(self._h, ctypes.byref(a), at, 8 if name == "int64" else 4, stride, t_at,
+                                       DTYPES[t_name], t_stride, k, temperature, _stream_handle(stream)),
+               "ar_output_distill")
+        return self._done(grad_hidden, grad_weight, result)
+
+    def check(self):
+        """Synchronise; raise ArError(AR_ERR_TIMEOUT) if a kernel gave up a wait."""
+        _check(lib().ar_output_loss_check(self._h), "ar_output_loss_check")
+
+    def close(self):
+        if getattr(self, "_h", None):
+            h, self._h = self._h, None
+            _free(lib().ar_output_loss_destroy, h, self.record)
 
     __del__ = close
 

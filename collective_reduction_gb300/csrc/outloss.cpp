@@ -1,0 +1,484 @@
+// C ABI of the output layer's losses: handles that hold the sizes and the
+// workspace, and the calls that check their arguments and launch the kernels.
+#include "outloss.hpp"
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "bufcheck.hpp"
+
+namespace {
+
+constexpr double kFloatMax = 3.4028234e38;
+constexpr uint64_t kMaxTokens = 1ull << 22, kMaxHidden = 1ull << 16, kMaxVocab = 1ull << 24;
+constexpr int kMaxTop = 1024;
+
+// Logits of a piece of the vocabulary that the caller leaves to the handle: in
+// bf16 0.5 GB of gradients.
+constexpr uint64_t kPieceLogits = 1ull << 28;
+
+ar_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return AR_OK;
+    cudaGetLastError();  // reported here: not once more by whoever looks at the thread's last error
+    return e == cudaErrorMemoryAllocation ? AR_ERR_NOMEM : AR_ERR_CUDA;
+}
+
+bool float_normal(double x) { return x >= 1.17549436e-38 && x <= kFloatMax; }
+bool float_dtype(ar_dtype d) { return d == AR_FLOAT32 || d == AR_BFLOAT16; }
+int esize(ar_dtype d) { return d == AR_BFLOAT16 ? 2 : 4; }
+uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
+
+// The workspace's parts: offsets of each in one allocation.
+struct Layout {
+    uint64_t rows = 0, pitch = 0, piece = 0, pieces = 0, parts = 0;  // padded tokens, padded D, ..., floats
+    int planes = 1, list = 1;
+    size_t status = 0, count = 0, factor = 0, row = 0, counted = 0, ids = 0, shares = 0, entropy = 0, logits = 0;
+    size_t stats = 0, stat = 0, gain = 0, loss = 0, hidden = 0, weight = 0, grad = 0, part = 0;
+    size_t bytes = 0;
+    size_t add(uint64_t n) {
+        const size_t at = bytes;
+        bytes += up(n, 256);
+        return at;
+    }
+};
+
+ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype dtype, int top, uint64_t piece,
+                      int gradients, Layout& l) {
+    if (hidden < 1 || vocab < 1 || top < 0 || (dtype != AR_INT32 && !float_dtype(dtype))) return AR_ERR_INVALID_ARG;
+    if (!float_dtype(dtype) || tokens > kMaxTokens || hidden > kMaxHidden || vocab > kMaxVocab || top > kMaxTop ||
+        tokens * static_cast<uint64_t>(std::max(1, top)) > (1ull << 31))
+        return AR_ERR_UNSUPPORTED;
+    const uint64_t tile = ar::kLossTile;
+    l.planes = dtype == AR_BFLOAT16 ? 1 : ar::kMaxPlanes;
+    l.list = std::max(1, top);
+    l.rows = std::max(tile, up(tokens, tile));
+    l.pitch = up(hidden, 8);
+    if (piece == 0) piece = std::max(tile, kPieceLogits / l.rows);
+    piece = std::min(up(piece, tile), up(vocab, tile));
+    l.pieces = (vocab + piece - 1) / piece;
+    l.piece = up((vocab + l.pieces - 1) / l.pieces, tile);  // as even as whole tiles allow
+    l.pieces = (vocab + l.piece - 1) / l.piece;
+    const uint64_t n = l.rows, k = n * l.list;
+    l.status = l.add(4);
+    l.count = l.add(4);
+    l.factor = l.add(4);
+    l.row = l.add(4 * n);
+    l.counted = l.add(4 * n);
+    l.entropy = l.add(4 * n);
+    l.ids = l.add(4 * k);
+    l.shares = l.add(4 * k);
+    l.logits = l.add(4 * k);
+    l.stats = l.add(8 * n * (up(vocab, tile) / tile));
+    l.stat = l.add(8 * n);
+    l.gain = l.add(4 * n);
+    l.loss = l.add(4 * n);
+    l.hidden = l.add(2 * l.planes * n * l.pitch);
+    l.weight = l.add(2 * l.planes * l.piece * l.pitch);
+    if (gradients) {
+        l.grad = l.add(2 * l.planes * n * l.piece);
+        l.parts = std::max(n * up(hidden, tile), ar::kLossSms * tile * tile);
+        l.part = l.add(4 * l.parts);
+    }
+    return AR_OK;
+}
+
+}  // namespace
+
+struct ar_output_loss_s {
+    int device = 0;
+    uint64_t tokens = 0, hidden = 0, vocab = 0;
+    ar_dtype dtype = AR_BFLOAT16;
+    int top = 0;
+    bool gradients = false;
+    Layout l;
+    char* dev = nullptr;
+    template <class T>
+    T* at(size_t offset) const {
+        return reinterpret_cast<T*>(dev + offset);
+    }
+    ~ar_output_loss_s() {
+        if (dev) cudaFree(dev);
+    }
+};
+
+namespace {
+
+// A caller's matrix of `rows` rows.
+struct Matrix {
+    const void* p;
+    uint64_t rows, width, stride;
+    int es;
+    uint64_t bytes() const { return rows == 0 || width == 0 ? 0 : ((rows - 1) * stride + width) * es; }
+};
+
+bool on_device(int device) {
+    int now = -1;
+    return cudaGetDevice(&now) == cudaSuccess && now == device;
+}
+
+// Inputs, which may overlap one another, and outputs, which may overlap nothing.
+ar_status check_matrices(const std::vector<Matrix>& in, const std::vector<Matrix>& out, int device) {
+    std::vector<Matrix> all(out);
+    all.insert(all.end(), in.begin(), in.end());
+    for (size_t i = 0; i < all.size(); ++i) {
+        const Matrix& m = all[i];
+        if (m.stride < m.width || m.stride > (1ull << 40)) return AR_ERR_INVALID_ARG;
+        if (m.bytes() == 0) continue;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(m.p);
+        if (!a || a % m.es || a + m.bytes() < a) return AR_ERR_INVALID_ARG;
+        for (size_t j = 0; j < i && j < out.size(); ++j) {
+            const uintptr_t b = reinterpret_cast<uintptr_t>(all[j].p);
+            if (all[j].bytes() && a < b + all[j].bytes() && b < a + m.bytes()) return AR_ERR_INVALID_ARG;
+        }
+    }
+    for (const Matrix& m : all)
+        if (m.bytes() && !ar::device_resident(m.p, m.bytes(), device)) return AR_ERR_INVALID_ARG;
+    return AR_OK;
+}
+
+// One call: what it was given, and its launches.
+struct Call {
+    const ar_output_loss_s* h;
+    const ar_output_loss_args* a;
+    cudaStream_t st;
+    uint32_t n;
+    ar::Lists lists = {};
+    ar::Counted rows = {};
+    cudaError_t e = cudaSuccess;
+
+    Call(const ar_output_loss_s* h_, const ar_output_loss_args* a_, cudaStream_t st_)
+        : h(h_), a(a_), st(st_), n(static_cast<uint32_t>(a_->tokens)) {
+        lists.ids = h->at<int32_t>(h->l.ids);
+        lists.entropy = h->at<float>(h->l.entropy);
+        lists.counted = h->at<uint32_t>(h->l.counted);
+        lists.logits = h->at<float>(h->l.logits);
+        lists.top = 1;
+        rows.count = h->at<uint32_t>(h->l.count);
+        rows.row = h->at<int32_t>(h->l.row);
+        rows.factor = h->at<float>(h->l.factor);
+    }
+
+    ar::Planes hidden() const {
+        return {h->at<uint16_t>(h->l.hidden), h->l.rows * h->l.pitch, h->l.pitch, h->l.planes};
+    }
+    ar::Planes grad() const {
+        return {h->at<uint16_t>(h->l.grad), h->l.rows * h->l.piece, h->l.piece, h->l.planes};
+    }
+    bool weight_as_is() const { return h->dtype == AR_BFLOAT16; }
+    const char* weight_row(uint64_t v) const {
+        return static_cast<const char*>(a->weight) + v * a->weight_stride * esize(h->dtype);
+    }
+    // Rows [v0, v1) of the weights as planes: where they are, or packed.
+    ar::Planes weight(uint64_t v0, uint64_t v1) {
+        if (weight_as_is())
+            return {reinterpret_cast<uint16_t*>(const_cast<char*>(weight_row(v0))), 0, a->weight_stride, 1};
+        ar::PackArgs p = {};
+        p.src = weight_row(v0);
+        p.stride = a->weight_stride;
+        p.bf16 = h->dtype == AR_BFLOAT16;
+        p.n = static_cast<uint32_t>(v1 - v0);
+        p.width = static_cast<uint32_t>(h->hidden);
+        p.out = {h->at<uint16_t>(h->l.weight), h->l.piece * h->l.pitch, h->l.pitch, h->l.planes};
+        run(ar::launch_pack(p, st));
+        return p.out;
+    }
+    void run(cudaError_t next) {
+        if (e == cudaSuccess) e = next;
+    }
+
+    ar::ProductArgs product() const {
+        ar::ProductArgs p = {};
+        p.count = rows.count;
+        p.splits = 1;
+        p.status = h->at<uint32_t>(h->l.status);
+        return p;
+    }
+
+    // The logits of [v0, v1): their statistics, or their gradient into grad().
+    void logits(uint64_t v0, uint64_t v1, const ar::Planes& w, ar::LossEpilogue epilogue, float c) {
+        ar::ProductArgs p = product();
+        p.a = {hidden(), false, n, h->hidden};
+        p.b = {w, false, v1 - v0, h->hidden};
+        p.m = n;
+        p.count_m = 1;
+        p.n = static_cast<uint32_t>(v1 - v0);
+        p.k = static_cast<uint32_t>(h->hidden);
+        p.epilogue = epilogue;
+        p.logit = {static_cast<uint32_t>(v0), static_cast<uint32_t>(v1), c, lists, h->at<float2>(h->l.stats),
+                   h->l.rows, h->at<ar::RowStat>(h->l.stat), h->at<float>(h->l.gain), {}};
+        if (epilogue == ar::kLossGrad) p.logit.g = grad();
+        p.out.row = rows.row;
+        run(ar::launch_product(p, st));
+    }
+
+    void grad_weight(uint64_t v0, uint64_t v1) {
+        ar::ProductArgs p = product();
+        p.a = {grad(), true, n, v1 - v0};
+        p.b = {hidden(), true, n, h->hidden};
+        p.m = static_cast<uint32_t>(v1 - v0);
+        p.n = static_cast<uint32_t>(h->hidden);
+        p.k = n;
+        p.count_k = 1;
+        p.epilogue = ar::kLossOut;
+        p.out.out = static_cast<char*>(a->grad_weight) + v0 * a->grad_weight_stride * esize(a->grad_weight_dtype);
+        p.out.stride = a->grad_weight_stride;
+        p.out.bf16 = a->grad_weight_dtype == AR_BFLOAT16;
+        p.out.accumulate = a->accumulate;
+        run(ar::launch_product(p, st));
+    }
+
+    void grad_hidden(uint64_t v0, uint64_t v1, const ar::Planes& w) {
+        ar::ProductArgs p = product();
+        p.a = {grad(), false, n, v1 - v0};
+        p.b = {w, true, v1 - v0, h->hidden};
+        p.m = n;
+        p.count_m = 1;
+        p.n = static_cast<uint32_t>(h->hidden);
+        p.k = static_cast<uint32_t>(v1 - v0);
+        p.epilogue = ar::kLossOut;
+        const bool parts = h->l.pieces > 1;
+        if (parts) {
+            p.out.parts = h->at<float>(h->l.part);
+            p.out.part_pitch = up(h->hidden, ar::kLossTile);
+            p.out.part_stride = up(n, ar::kLossTile) * p.out.part_pitch;
+            p.out.add_parts = v0 > 0;
+        } else {
+            p.out.out = a->grad_hidden;
+            p.out.stride = a->grad_hidden_stride;
+            p.out.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
+            p.out.accumulate = a->accumulate;
+            p.out.row = rows.row;
+        }
+        run(ar::launch_product(p, st));
+        if (!parts || v1 < h->vocab) return;
+        ar::FinishArgs f = {};
+        f.parts = p.out.parts;
+        f.part_stride = p.out.part_stride;
+        f.part_pitch = p.out.part_pitch;
+        f.splits = p.splits;
+        f.n = n;
+        f.width = p.n;
+        f.rows = rows;
+        f.by_count = 1;
+        f.out = a->grad_hidden;
+        f.stride = a->grad_hidden_stride;
+        f.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
+        f.accumulate = a->accumulate;
+        run(ar::launch_finish_parts(f, st));
+    }
+
+    // Everything after the lists: `rows` with its targets, the passes over the
+    // vocabulary, the record.
+    ar_status finish(ar::RowsArgs r, double t) {
+        r.n = n;
+        r.vocab = static_cast<uint32_t>(h->vocab);
+        r.scale = a->scale;
+        r.mean = a->reduction == AR_LOSS_MEAN;
+        r.lists = lists;
+        r.rows = rows;
+        run(ar::launch_rows(r, st));
+        const float c = static_cast<float>(1.4426950408889634 / t);
+        const uint64_t step = weight_as_is() ? h->vocab : h->l.piece;
+        if (n > 0) {
+            ar::ClearArgs z = {lists.counted, n, static_cast<uint32_t>(h->hidden), a->losses,
+                               a->accumulate ? nullptr : a->grad_hidden, a->grad_hidden_stride,
+                               a->grad_hidden_dtype == AR_BFLOAT16};
+            if (z.losses || z.grad_hidden) run(ar::launch_clear(z, st));
+            ar::PackArgs p = {};
+            p.src = a->hidden;
+            p.stride = a->hidden_stride;
+            p.bf16 = h->dtype == AR_BFLOAT16;
+            p.n = n;
+            p.width = static_cast<uint32_t>(h->hidden);
+            p.rows = rows;
+            p.out = hidden();
+            run(ar::launch_pack(p, st));
+            for (uint64_t v = 0; v < h->vocab; v += step) {
+                const uint64_t end = std::min(h->vocab, v + step);
+                logits(v, end, weight(v, end), ar::kLossStats, c);
+            }
+            ar::JoinArgs j = {};
+            j.stats = h->at<float2>(h->l.stats);
+            j.pitch = h->l.rows;
+            j.tiles = static_cast<uint32_t>(up(h->vocab, ar::kLossTile) / ar::kLossTile);
+            j.n = n;
+            j.c = c;
+            j.t = t;
+            j.lists = lists;
+            j.rows = rows;
+            j.stat = h->at<ar::RowStat>(h->l.stat);
+            j.gain = h->at<float>(h->l.gain);
+            j.loss = h->at<float>(h->l.loss);
+            j.losses = a->losses;
+            run(ar::launch_join(j, st));
+        }
+        run(ar::launch_record({h->at<float>(h->l.loss), rows, a->result}, st));
+        if (a->grad_weight || (a->grad_hidden && n > 0)) {
+            for (uint64_t v = 0; v < h->vocab; v += h->l.piece) {
+                const uint64_t end = std::min(h->vocab, v + h->l.piece);
+                const ar::Planes w = n > 0 ? weight(v, end) : ar::Planes{};
+                if (n > 0) logits(v, end, w, ar::kLossGrad, c);
+                if (a->grad_weight) grad_weight(v, end);
+                if (a->grad_hidden && n > 0) grad_hidden(v, end, w);
+            }
+        }
+        return cuda_status(e);
+    }
+};
+
+// What both losses' arguments have to be; `more`: the call's own inputs.
+ar_status check_args(const ar_output_loss_s* h, const ar_output_loss_args* a, std::vector<Matrix> more) {
+    if (!h || !a || a->tokens > h->tokens || !on_device(h->device)) return AR_ERR_INVALID_ARG;
+    if (!float_normal(a->scale) || (a->reduction != AR_LOSS_MEAN && a->reduction != AR_LOSS_SUM)) return AR_ERR_INVALID_ARG;
+    if (!h->gradients && (a->grad_hidden || a->grad_weight)) return AR_ERR_INVALID_ARG;
+    if (a->grad_hidden && a->grad_hidden_dtype != h->dtype && a->grad_hidden_dtype != AR_FLOAT32) return AR_ERR_INVALID_ARG;
+    if (a->grad_weight && a->grad_weight_dtype != h->dtype && a->grad_weight_dtype != AR_FLOAT32) return AR_ERR_INVALID_ARG;
+    const int es = esize(h->dtype);
+    more.push_back({a->hidden, a->tokens, h->hidden, a->hidden_stride, es});
+    more.push_back({a->weight, h->vocab, h->hidden, a->weight_stride, es});
+    std::vector<Matrix> out = {{a->result, 1, 4, 4, 4}};
+    if (a->losses) out.push_back({a->losses, 1, a->tokens, a->tokens, 4});
+    if (a->grad_hidden)
+        out.push_back({a->grad_hidden, a->tokens, h->hidden, a->grad_hidden_stride, esize(a->grad_hidden_dtype)});
+    if (a->grad_weight)
+        out.push_back({a->grad_weight, h->vocab, h->hidden, a->grad_weight_stride, esize(a->grad_weight_dtype)});
+    return check_matrices(more, out, h->device);
+}
+
+}  // namespace
+
+extern "C" {
+
+ar_status ar_output_loss_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype dtype, int top,
+                                uint64_t piece, int gradients, ar_output_loss_info* info) {
+    if (!info) return AR_ERR_INVALID_ARG;
+    std::memset(info, 0, sizeof(*info));
+    Layout l;
+    const ar_status s = make_layout(tokens, hidden, vocab, dtype, top, piece, gradients, l);
+    if (s != AR_OK) return s;
+    info->tokens = tokens;
+    info->hidden = hidden;
+    info->vocab = vocab;
+    info->top = top;
+    info->piece = l.piece;
+    info->pieces = static_cast<int>(l.pieces);
+    info->workspace_bytes = l.bytes;
+    info->tiling_ok = l.piece % ar::kLossTile == 0 && l.piece * l.pieces >= vocab && l.piece * (l.pieces - 1) < vocab;
+    return AR_OK;
+}
+
+ar_status ar_output_loss_create(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype dtype, int top,
+                                uint64_t piece, int gradients, ar_output_loss_t* out) {
+    ar::TraceRange trace("ar_output_loss_create");
+    if (!out) return AR_ERR_INVALID_ARG;
+    *out = nullptr;
+    Layout l;
+    const ar_status s = make_layout(tokens, hidden, vocab, dtype, top, piece, gradients, l);
+    if (s != AR_OK) return s;
+    ar_output_loss_s* h = new (std::nothrow) ar_output_loss_s();
+    if (!h) return AR_ERR_NOMEM;
+    h->tokens = tokens;
+    h->hidden = hidden;
+    h->vocab = vocab;
+    h->dtype = dtype;
+    h->top = top;
+    h->gradients = gradients != 0;
+    h->l = l;
+    cudaError_t e = cudaGetDevice(&h->device);
+    if (e == cudaSuccess) e = cudaMalloc(&h->dev, l.bytes);
+    // in place on return: the calls may run on streams that do not wait for this one
+    if (e == cudaSuccess) e = cudaMemset(h->dev, 0, l.row);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) {
+        delete h;
+        return cuda_status(e);
+    }
+    *out = h;
+    return AR_OK;
+}
+
+ar_status ar_output_loss_query(ar_output_loss_t h, ar_output_loss_info* info) {
+    if (!h || !info) return AR_ERR_INVALID_ARG;
+    return ar_output_loss_layout(h->tokens, h->hidden, h->vocab, h->dtype, h->top, h->l.piece, h->gradients, info);
+}
+
+ar_status ar_output_loss_destroy(ar_output_loss_t h) {
+    if (!h) return AR_ERR_INVALID_ARG;
+    int now = -1;
+    cudaError_t e = cudaGetDevice(&now);
+    const bool other = e == cudaSuccess && now != h->device;
+    if (other) e = cudaSetDevice(h->device);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    delete h;
+    if (other) cudaSetDevice(now);
+    return cuda_status(e);
+}
+
+ar_status ar_output_loss_check(ar_output_loss_t h) {
+    if (!h || !on_device(h->device)) return AR_ERR_INVALID_ARG;
+    uint32_t word = 0;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess) e = cudaMemcpy(&word, h->at<uint32_t>(h->l.status), 4, cudaMemcpyDeviceToHost);
+    if (e == cudaSuccess && word) e = cudaMemset(h->at<uint32_t>(h->l.status), 0, 4);
+    if (e == cudaSuccess && word) e = cudaStreamSynchronize(nullptr);
+    if (e != cudaSuccess) return cuda_status(e);
+    return word ? AR_ERR_TIMEOUT : AR_OK;
+}
+
+ar_status ar_output_cross_entropy(ar_output_loss_t h, const ar_output_loss_args* args, const void* targets,
+                                  int target_bytes, int64_t ignore_index, void* stream) {
+    ar::TraceRange trace("ar_output_cross_entropy");
+    if (!h || !args || (target_bytes != 4 && target_bytes != 8)) return AR_ERR_INVALID_ARG;
+    try {
+        const ar_status s = check_args(h, args, {{targets, 1, args->tokens, args->tokens, target_bytes}});
+        if (s != AR_OK) return s;
+        Call call(h, args, static_cast<cudaStream_t>(stream));
+        ar::RowsArgs r = {};
+        r.targets = targets;
+        r.target_bytes = target_bytes;
+        r.ignore = ignore_index;
+        return call.finish(r, 1.0);
+    } catch (const std::bad_alloc&) {
+        return AR_ERR_NOMEM;
+    }
+}
+
+ar_status ar_output_distill(ar_output_loss_t h, const ar_output_loss_args* args, const void* ids, int id_bytes,
+                            uint64_t ids_stride, const void* logits, ar_dtype logit_dtype, uint64_t logits_stride,
+                            int k, double temperature, void* stream) {
+    ar::TraceRange trace("ar_output_distill");
+    if (!h || !args || (id_bytes != 4 && id_bytes != 8) || !float_dtype(logit_dtype)) return AR_ERR_INVALID_ARG;
+    if (k < 1 || k > h->top || !float_normal(temperature) || !float_normal(1.0 / temperature)) return AR_ERR_INVALID_ARG;
+    try {
+        const uint64_t width = static_cast<uint64_t>(k);
+        const ar_status s = check_args(h, args, {{ids, args->tokens, width, ids_stride, id_bytes},
+                                                 {logits, args->tokens, width, logits_stride, esize(logit_dtype)}});
+        if (s != AR_OK) return s;
+        Call call(h, args, static_cast<cudaStream_t>(stream));
+        call.lists.top = k;
+        call.lists.shares = h->at<float>(h->l.shares);
+        if (args->tokens > 0) {
+            ar::TeacherArgs t = {};
+            t.ids = ids;
+            t.logits = logits;
+            t.ids_stride = ids_stride;
+            t.logits_stride = logits_stride;
+            t.id_bytes = id_bytes;
+            t.logits_bf16 = logit_dtype == AR_BFLOAT16;
+            t.k = k;
+            t.inv_t = static_cast<float>(1.0 / temperature);
+            t.n = call.n;
+            t.vocab = static_cast<uint32_t>(h->vocab);
+            t.lists = call.lists;
+            call.run(ar::launch_teacher(t, call.st));
+        }
+        return call.finish({}, temperature);
+    } catch (const std::bad_alloc&) {
+        return AR_ERR_NOMEM;
+    }
+}
+
+}  // extern "C"

@@ -489,6 +489,109 @@ ar_status ar_adamw_step(ar_adamw_t h, const ar_adamw_params* params, const float
 ar_status ar_adamw_step_counted(ar_adamw_t h, const ar_adamw_params* params, uint64_t* steps, const float* lr,
                                 const float* result, void* stream);
 
+/* ---- before the allreduce: the output layer's losses and gradients ---------
+ * What a language model's ranks reduce begins here: logits z = X W^T of n
+ * tokens' hidden states X (n x D) and an output layer's weights W (V x D), a loss
+ * of each token's softmax over the V logits, and the gradients of X and W.  The
+ * pages take gradients as given; these calls have no counterpart on them.
+ *
+ * No n x V array is made: logits and their gradients are worked on in pieces
+ * of the vocabulary that fit the handle's workspace.  Both losses are, for a
+ * token with teacher shares p over a short list of ids at temperature t,
+ *   loss = t^2 [ sum_k p_k log p_k - sum_k p_k z_k / t + log sum_v exp(z_v / t) ]
+ * whose gradient by z is t (softmax(z / t) - p); cross entropy has one id of
+ * share 1 and t = 1.
+ *
+ * A handle holds the sizes and the workspace.  Calls launch kernels only
+ * (capturable in a CUDA graph once the handle exists), never synchronise and keep
+ * nothing between calls.  Calls on one handle must be ordered on one stream, a
+ * replayed graph's among them: they share the workspace.  The handle's device
+ * must be current (AR_ERR_INVALID_ARG otherwise).  Repeated calls on equal inputs
+ * give equal bits.
+ *
+ * Tokens that do not count (a target of ignore_index, a teacher list without
+ * entries) have loss 0 and gradient 0, and their hidden states are not read:
+ * products run over the tokens that count alone.  A target or id outside the
+ * vocabulary makes its token's loss and the gradients it enters NaN, and the
+ * record says nonfinite. */
+typedef struct ar_output_loss_s* ar_output_loss_t;
+typedef enum { AR_LOSS_MEAN = 0, AR_LOSS_SUM = 1 } ar_loss_reduction;
+
+typedef struct {
+    uint64_t tokens, hidden, vocab;  /* n at most, D, V                          */
+    int top;                         /* entries of a teacher's list at most      */
+    uint64_t piece;                  /* vocabulary entries worked on at a time   */
+    int pieces;
+    uint64_t workspace_bytes;        /* device memory the handle owns            */
+    int tiling_ok;                   /* the pieces tile the vocabulary           */
+} ar_output_loss_info;
+
+/* Host only: the sizes a handle would have (ar_output_loss_create, same
+ * arguments and errors). */
+ar_status ar_output_loss_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype dtype, int top,
+                                uint64_t piece, int gradients, ar_output_loss_info* info);
+/* A handle for up to `tokens` tokens of hidden size D over V vocabulary entries,
+ * X and W of `dtype`.  top: entries of a teacher's list at most (0: cross entropy
+ * alone).  piece: vocabulary entries at a time (rounded up to 256; 0: as many as
+ * make 2^28 logits).  gradients: 0 for losses alone, with a small workspace.
+ * AR_ERR_INVALID_ARG: null out, D or V of 0, top < 0, unknown types.
+ * AR_ERR_UNSUPPORTED: AR_INT32, more than 2^22 tokens, D > 2^16, V > 2^24, top >
+ * 1024, more than 2^31 list entries.  AR_ERR_NOMEM, AR_ERR_CUDA. */
+ar_status ar_output_loss_create(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype dtype, int top,
+                                uint64_t piece, int gradients, ar_output_loss_t* out);
+ar_status ar_output_loss_query(ar_output_loss_t h, ar_output_loss_info* info);
+ar_status ar_output_loss_destroy(ar_output_loss_t h);  /* as ar_grads_destroy */
+/* Synchronises the device and reads the handle's status word: AR_OK, or
+ * AR_ERR_TIMEOUT if a bounded wait in a kernel gave up (and clears it). */
+ar_status ar_output_loss_check(ar_output_loss_t h);
+
+typedef struct {
+    uint64_t tokens;           /* n <= the handle's; 0 is valid                   */
+    const void* hidden;        /* X, n rows                                       */
+    uint64_t hidden_stride;    /* elements between rows, >= D, here and below     */
+    const void* weight;        /* W, V rows                                       */
+    uint64_t weight_stride;
+    void* grad_hidden;         /* NULL, or n rows that take the gradient of X     */
+    uint64_t grad_hidden_stride;
+    ar_dtype grad_hidden_dtype;  /* the handle's, or AR_FLOAT32                   */
+    void* grad_weight;         /* NULL, or V rows that take the gradient of W     */
+    uint64_t grad_weight_stride;
+    ar_dtype grad_weight_dtype;
+    int accumulate;            /* 1: gradients are added to what is there         */
+    ar_loss_reduction reduction;
+    double scale;              /* of loss and gradients; a float32-normal number > 0 */
+    float* losses;             /* NULL, or n floats: each token's loss, unscaled  */
+    float* result;             /* the record, 4 floats                            */
+} ar_output_loss_args;
+
+/* Softmax cross entropy of n tokens against targets (n integers of
+ * target_bytes 4 or 8, contiguous): loss_i = log sum_v exp(z_iv) - z_i,target.
+ * The record, in device memory:
+ *   [0] loss       factor times the sum of the counted tokens' losses
+ *   [1] counted    tokens that count
+ *   [2] nonfinite  1 if a counted token's loss is an infinity or NaN, else 0
+ *   [3] factor     scale / max(1, counted) (AR_LOSS_MEAN), scale (AR_LOSS_SUM)
+ * The gradients are the loss's.  They are computed from bf16 inputs with the
+ * logits' gradient rounded to bf16 once (float32 inputs: in float32), summed in
+ * float32 and rounded to their type once.  Outputs may overlap neither each
+ * other nor the inputs.  Errors: AR_ERR_INVALID_ARG for null or misaligned (to
+ * their element) pointers, memory that is not the handle's device's or ends too
+ * early, overlaps, strides below D, a gradient type that is neither, a scale
+ * that is not a float32-normal positive number, gradients of a handle without. */
+ar_status ar_output_cross_entropy(ar_output_loss_t h, const ar_output_loss_args* args, const void* targets,
+                                  int target_bytes, int64_t ignore_index, void* stream);
+/* Distillation from each token's k <= top largest teacher logits: the teacher's
+ * shares p are their softmax at temperature t (a float32-normal number > 0), and
+ * the loss is t^2 times the Kullback-Leibler divergence of the student's softmax
+ * over the whole vocabulary from p.  ids: n x k integers of id_bytes 4 or 8,
+ * negative for no entry; logits: n x k of logit_dtype, -infinity for no entry (with
+ * an entry absent, its logit is not looked at); strides in elements between
+ * rows.  Entries of one id add their shares.  Record, gradients and errors as
+ * ar_output_cross_entropy; k < 1 or k > top: AR_ERR_INVALID_ARG. */
+ar_status ar_output_distill(ar_output_loss_t h, const ar_output_loss_args* args, const void* ids, int id_bytes,
+                            uint64_t ids_stride, const void* logits, ar_dtype logit_dtype, uint64_t logits_stride,
+                            int k, double temperature, void* stream);
+
 /* Static text for a status code (never NULL). */
 const char* ar_status_string(ar_status s);
 
