@@ -167,7 +167,11 @@ struct Call {
     ar::Planes grad() const {
         return {h->at<uint16_t>(h->l.grad), h->l.rows * h->l.piece, h->l.piece, h->l.planes};
     }
-    bool weight_as_is() const { return h->dtype == AR_BFLOAT16; }
+    // TMA reads rows that start on 16-byte boundaries
+    bool weight_as_is() const {
+        return h->dtype == AR_BFLOAT16 && reinterpret_cast<uintptr_t>(a->weight) % 16 == 0 &&
+               a->weight_stride % 8 == 0 && a->weight_stride < (1ull << 38);
+    }
     const char* weight_row(uint64_t v) const {
         return static_cast<const char*>(a->weight) + v * a->weight_stride * esize(h->dtype);
     }
@@ -388,6 +392,7 @@ ar_status ar_output_loss_create(uint64_t tokens, uint64_t hidden, uint64_t vocab
     h->gradients = gradients != 0;
     h->l = l;
     cudaError_t e = cudaGetDevice(&h->device);
+    if (e == cudaSuccess) e = ar::prepare_products();
     if (e == cudaSuccess) e = cudaMalloc(&h->dev, l.bytes);
     // in place on return: the calls may run on streams that do not wait for this one
     if (e == cudaSuccess) e = cudaMemset(h->dev, 0, l.row);

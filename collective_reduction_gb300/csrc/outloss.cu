@@ -6,6 +6,10 @@
 // of ids, the loss is t^2 (sum p log p - sum p z / t + log sum exp(z / t)) and
 // its gradient by z, with the factor f of the record,
 //   g = f t (2^(y - top) / sum 2^(y - top) - p),   dX = g W,   dW = g^T X.
+#include <cuda.h>  // the tensor map's types only: the driver call is resolved at run time
+
+#include <algorithm>
+
 #include "device.cuh"
 #include "outloss.hpp"
 
@@ -13,6 +17,7 @@ namespace ar {
 namespace {
 
 constexpr uint32_t kFull = 0xFFFFFFFFu;
+constexpr float kInf = __builtin_huge_valf();
 constexpr double kLn2 = 0.69314718055994530942;
 
 __device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
@@ -26,7 +31,7 @@ __device__ __forceinline__ float load_value(const void* p, uint64_t i, int bf16)
 // an infinity: towards zero); x keeps what is left, exactly.
 __device__ __forceinline__ uint16_t split_plane(float& x) {
     uint16_t b = bf16_of(x);
-    if ((b & 0x7FFFu) == 0x7F80u && fabsf(x) < __int_as_float(0x7F800000)) b -= 1;
+    if ((b & 0x7FFFu) == 0x7F80u && fabsf(x) < kInf) b -= 1;
     const float v = bf16_value(b);
     x = (b & 0x7F80u) == 0x7F80u ? 0.f : __fsub_rn(x, v);  // an infinity or NaN leaves nothing
     return b;
@@ -53,15 +58,15 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const __gri
     griddep_wait();
     if (i >= a.n) return;
     bool bad = false;
-    float top = -__int_as_float(0x7F800000);
+    float top = -kInf;
     for (int j = lane; j < a.k; j += 32) {
         const uint64_t at = i * a.ids_stride + j;
         const int64_t v = a.id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[at] : static_cast<const int32_t*>(a.ids)[at];
-        float u = -__int_as_float(0x7F800000);
+        float u = -kInf;
         int32_t x = kNoId;
         if (v >= 0) {
             u = load_value(a.logits, i * a.logits_stride + j, a.logits_bf16);
-            if (u != -__int_as_float(0x7F800000)) {  // NaN stays in
+            if (u != -kInf) {  // NaN stays in
                 if (v >= a.vocab) bad = true;
                 else x = static_cast<int32_t>(v);
                 if (u != u) bad = true;
@@ -72,7 +77,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const __gri
         if (x != kNoId) top = fmaxf(top, u);
     }
     for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-    bad = __any_sync(kFull, bad) || top == __int_as_float(0x7F800000);
+    bad = __any_sync(kFull, bad) || top == kInf;
     float sum = 0.f;
     for (int j = lane; j < a.k; j += 32) {
         const bool in = id[j] != kNoId && !bad;
@@ -81,7 +86,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const __gri
         sum = __fadd_rn(sum, e);
     }
     for (int o = 16; o > 0; o /= 2) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
-    const bool any = __any_sync(kFull, top != -__int_as_float(0x7F800000));
+    const bool any = __any_sync(kFull, top != -kInf);
     __syncwarp();
     // entries of one id: the first takes the sum, the others go
     for (int b = 0; b < a.k; b += 32) {
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(256) clear_kernel(const __grid_constant__ Clea
 // nothing, +infinity or NaN make the sum NaN.
 __device__ __forceinline__ void join_stat(float& top, float& sum, float top2, float sum2) {
     const float m = fmaxf(top, top2);
-    const float low = -__int_as_float(0x7F800000);
+    const float low = -kInf;
     const float a = top == low ? 0.f : __fmul_rn(sum, exp2_fast(__fsub_rn(top, m)));
     const float b = top2 == low ? 0.f : __fmul_rn(sum2, exp2_fast(__fsub_rn(top2, m)));
     top = m;
@@ -234,7 +239,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     griddep_wait();
     if (r >= *a.rows.count) return;
     const uint64_t i = a.rows.row[r];
-    float top = -__int_as_float(0x7F800000), sum = 0.f;
+    float top = -kInf, sum = 0.f;
     for (uint32_t q = lane; q < a.tiles; q += 32) {
         const float2 s = a.stats[q * a.pitch + r];
         join_stat(top, sum, s.x, s.y);
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kRecordThreads) record_kernel(const __grid_con
     bool bad = false;
     for (uint32_t r = threadIdx.x; r < n; r += kRecordThreads) {
         const float x = a.loss[r];
-        bad = bad || !(fabsf(x) < __int_as_float(0x7F800000));
+        bad = bad || !(fabsf(x) < kInf);
         sum += x;
     }
     bad = __any_sync(kFull, bad);
@@ -316,96 +321,511 @@ __global__ void __launch_bounds__(256) finish_parts_kernel(const __grid_constant
 }
 
 // ---------------------------------------------------------------- products
+//
+// C = A B^T on the tensor cores: a pair of CTAs (a cluster of two) works on one
+// tile of 256 x 256, each holding 128 rows of A and of B in shared memory and 128
+// rows of C in its tensor memory, twice (the epilogue of one tile runs beside the
+// products of the next).  Persistent: pairs take tiles in turn.  Warp 0 loads (TMA,
+// a ring of kStages blocks of 64 products), warp 1 of the pair's first CTA issues
+// the products, warps 4 to 7 are the epilogue, a thread a row.
 
-constexpr int kSide = 64, kDeep = 16;
+constexpr int kSide = 256;             // rows and columns of a pair's tile
+constexpr int kHalf = kSide / 2;       // ... of A and of B in one CTA
+constexpr int kDeep = 64;              // products of a block: 128 bytes of bf16
+constexpr int kStages = 6;
+constexpr uint32_t kOperandBytes = kHalf * kDeep * 2, kStageBytes = 2 * kOperandBytes;
+constexpr int kProductThreads = 256, kEpilogueWarp = 4, kEpilogueWarps = 4;
+constexpr int kTmemColumns = 512;
 
-__device__ __forceinline__ float operand_value(const Operand& o, uint64_t row, uint64_t k) {
-    const uint64_t at = o.turned ? k * o.m.pitch + row : row * o.m.pitch + k;
-    float x = 0.f;
-    for (int q = o.m.planes - 1; q >= 0; --q) x = __fadd_rn(x, bf16_value(o.m.p[q * o.m.plane + at]));
-    return x;
+static_assert(kSide == static_cast<int>(kLossTile), "statistics are of one tile's columns");
+
+// Barriers, in 8-byte words of shared memory.
+enum : uint32_t {
+    kFullBar = 0,                      // a stage's blocks are there (the pair's; in its first CTA)
+    kEmptyBar = kFullBar + kStages,    // ... have been read
+    kReadyBar = kEmptyBar + kStages,   // an accumulator is complete
+    kFreeBar = kReadyBar + 2,          // ... has been read (in the pair's first CTA)
+    kDoneBar = kFreeBar + 2,           // the products issued are complete
+    kTmemWord = kDoneBar + 1,
+    kBarWords = kTmemWord + 1
+};
+constexpr uint32_t kProductSmem = kStages * kStageBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
+
+struct ProductParams {
+    CUtensorMap a, b;
+    ProductArgs args;
+    uint32_t m_group;  // rows of tiles that are worked on side by side
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
 
-template <int EPI>
-__global__ void __launch_bounds__(256) product_kernel(const __grid_constant__ ProductArgs a) {
-    __shared__ float as[kDeep][kSide + 1], bs[kDeep][kSide + 1], cs[kSide][kSide + 1];
-    const uint32_t tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-    griddep_wait();
-    const uint32_t count = *a.count;
-    const uint32_t m = a.count_m ? min(a.m, count) : a.m, k_all = a.count_k ? min(a.k, count) : a.k;
-    const uint32_t wide = (a.n + kLossTile - 1) / kLossTile;
-    const uint64_t tall = (static_cast<uint64_t>(a.m) + kLossTile - 1) / kLossTile * (kLossTile / kSide);
-    uint64_t b = blockIdx.x;
-    const uint64_t m0 = b % tall * kSide;
-    b /= tall;
-    const uint32_t tile = static_cast<uint32_t>(b % wide), split = static_cast<uint32_t>(b / wide);
-    const uint32_t per = (k_all + a.splits - 1) / a.splits;
-    const uint32_t k_lo = min(k_all, split * per), k_hi = min(k_all, k_lo + per);
-    if (m0 >= (static_cast<uint64_t>(m) + kLossTile - 1) / kLossTile * kLossTile) return;
-    float top = -__int_as_float(0x7F800000), sum = 0.f;
-    for (uint32_t n0 = tile * kLossTile; n0 < (tile + 1) * kLossTile && n0 < a.n; n0 += kSide) {
-        float acc[4][4] = {};
-        for (uint32_t k0 = k_lo; k0 < k_hi; k0 += kDeep) {
-            for (int q = tid; q < kSide * kDeep; q += 256) {
-                const uint32_t ra = a.a.turned ? q % kSide : q / kDeep, ka = a.a.turned ? q / kSide : q % kDeep;
-                const uint32_t rb = a.b.turned ? q % kSide : q / kDeep, kb = a.b.turned ? q / kSide : q % kDeep;
-                as[ka][ra] = m0 + ra < m && k0 + ka < k_hi ? operand_value(a.a, m0 + ra, k0 + ka) : 0.f;
-                bs[kb][rb] = n0 + rb < a.n && k0 + kb < k_hi ? operand_value(a.b, n0 + rb, k0 + kb) : 0.f;
-            }
-            __syncthreads();
-            for (int k = 0; k < kDeep; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __fmaf_rn(as[k][ty * 4 + i], bs[k][tx * 4 + j], acc[i][j]);
-            __syncthreads();
-        }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) cs[ty * 4 + i][tx * 4 + j] = acc[i][j];
-        __syncthreads();
-        if (tid < kSide) {
-            const uint64_t r = m0 + tid;
-            const LogitArgs& g = a.logit;
-            if (EPI != kLossOut) {
-                const uint64_t at = r < m ? static_cast<uint64_t>(a.logit.lists.top) * a.out.row[r] : 0;
-                const RowStat st = EPI == kLossGrad && r < m ? g.stat[r] : RowStat{0.f, 0.f};
-                for (uint32_t j = 0; j < kSide; ++j) {
-                    const uint32_t v = g.v0 + n0 + j;
-                    const bool in = r < m && n0 + j < a.n;
-                    const float z = cs[tid][j];
-                    float share = 0.f;
-                    if (in)
-                        for (int k = 0; k < g.lists.top; ++k)
-                            if (g.lists.ids[at + k] == static_cast<int32_t>(v)) {
-                                share = g.lists.shares ? g.lists.shares[at + k] : 1.f;
-                                if (EPI == kLossStats) g.lists.logits[at + k] = z;
-                            }
-                    if (EPI == kLossStats) {
-                        if (in) join_stat(top, sum, __fmul_rn(z, g.c), 1.f);
-                    } else {
-                        float x = 0.f;
-                        if (in)
-                            x = __fsub_rn(__fmul_rn(exp2_fast(__fmaf_rn(z, g.c, -st.top)), st.inv),
-                                          __fmul_rn(share, g.gain[r]));
-                        for (int q = 0; q < g.g.planes; ++q)
-                            g.g.p[q * g.g.plane + r * g.g.pitch + n0 + j] = split_plane(x);
-                    }
-                }
-            } else if (r < m) {
-                for (uint32_t j = 0; j < kSide && n0 + j < a.n; ++j) {
-                    if (a.out.parts) {
-                        float* p = a.out.parts + split * a.out.part_stride + r * a.out.part_pitch + n0 + j;
-                        *p = a.out.add_parts ? __fadd_rn(*p, cs[tid][j]) : cs[tid][j];
-                    } else {
-                        const uint64_t to = (a.out.row ? static_cast<uint64_t>(a.out.row[r]) : r) * a.out.stride;
-                        store_out(a.out.out, to + n0 + j, a.out.bf16, a.out.accumulate, cs[tid][j]);
-                    }
-                }
-            }
-        }
-        __syncthreads();
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address of the pair's first CTA's copy of a shared variable.
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(addr));
+    return a;
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// A block of 64 x rows x 1 of a tensor into this CTA's shared memory; its bytes
+// count for a barrier of the pair's first CTA.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Shared memory descriptor of a bf16 operand in 128-byte swizzled rows of 64
+// values.  Rows along k: eight rows are 1024 bytes.  Turned (rows along the other
+// axis): eight values of k are 1024 bytes, the next 64 of the other axis start
+// kDeep rows on.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool turned) {
+    const uint64_t lead = turned ? kDeep * 128 : 16, stride = 1024;
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | ((lead >> 4) << 16) | ((stride >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// float32 accumulators of bf16 products, M = N = 256 over the pair.
+__host__ __device__ constexpr uint32_t mma_desc(bool a_turned, bool b_turned) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_turned ? 1u << 15 : 0u) | (b_turned ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(kSide >> 3) << 17) | (static_cast<uint32_t>(kSide >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem),
+        "l"(a), "l"(b), "r"(desc), "r"(add)
+        : "memory");
+}
+
+// Arrives at the barrier in both CTAs once the products issued so far are complete.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_read32(uint32_t taddr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The tiles of a product and the blocks of each, alike in every role.
+struct Tiles {
+    uint32_t m, blocks, per, passes;  // rows of A, blocks of k, ... of a split, passes of planes
+    uint32_t tall, wide, group;
+    uint64_t total;
+    __device__ explicit Tiles(const ProductParams& p) {
+        const ProductArgs& a = p.args;
+        const uint32_t count = *a.count;
+        m = a.count_m ? min(a.m, count) : a.m;
+        blocks = ((a.count_k ? min(a.k, count) : a.k) + kDeep - 1) / kDeep;
+        per = (blocks + a.splits - 1) / a.splits;
+        passes = a.a.m.planes == 1 ? 1 : 6;
+        tall = (m + kSide - 1) / kSide;
+        wide = (a.n + kSide - 1) / kSide;
+        group = p.m_group;
+        total = static_cast<uint64_t>(tall) * wide * a.splits;
     }
-    if (EPI == kLossStats && tid < kSide && m0 + tid < m)
-        a.logit.stats[(a.logit.v0 / kLossTile + tile) * a.logit.stats_pitch + m0 + tid] = make_float2(top, sum);
+    // Tile t: in each split, groups of `group` rows of tiles, column by column.
+    __device__ void at(uint64_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
+        const uint64_t each = static_cast<uint64_t>(tall) * wide;
+        split = static_cast<uint32_t>(t / each);
+        const uint32_t r = static_cast<uint32_t>(t - split * each);
+        const uint32_t g = r / (group * wide), rest = r - g * group * wide;
+        const uint32_t rows = min(group, tall - g * group);
+        nt = rest / rows;
+        mt = g * group + rest - nt * rows;
+        lo = min(blocks, split * per);
+        n = (min(blocks, lo + per) - lo) * passes;
+    }
+};
+
+// The planes of pass q of float32 operands, small products first.
+__device__ __forceinline__ int plane_a(uint32_t q) { return (0x001012 >> (4 * q)) & 3; }
+__device__ __forceinline__ int plane_b(uint32_t q) { return (0x010210 >> (4 * q)) & 3; }
+
+// A row's next id at or behind column v, as its place in the list.
+__device__ __forceinline__ int first_id(const int32_t* ids, int top, int32_t v) {
+    int lo = 0, hi = top;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (ids[mid] < v) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// One thread's row of a tile: columns c0 to c0 + 31 of the tile at a time.
+template <int EPI>
+struct Epilogue {
+    const ProductArgs& a;
+    uint64_t row;
+    uint32_t n0, cols, split;
+    bool in;
+    // lists
+    uint64_t list = 0;
+    int next = 0;
+    int32_t next_id = kNoId;
+    // statistics
+    float top = -kInf, sum = 0.f;
+    // gradient
+    float inv = 0.f, gain = 0.f;
+
+    __device__ Epilogue(const ProductArgs& a_, uint32_t m, uint64_t row_, uint32_t nt, uint32_t split_)
+        : a(a_), row(row_), n0(nt * kSide), cols(min(static_cast<uint32_t>(kSide), a_.n - nt * kSide)), split(split_),
+          in(row_ < m) {
+        if (EPI == kLossOut || !in) return;
+        const LogitArgs& g = a.logit;
+        list = static_cast<uint64_t>(a.out.row[row]) * g.lists.top;
+        next = first_id(g.lists.ids + list, g.lists.top, static_cast<int32_t>(g.v0 + n0));
+        if (next < g.lists.top) next_id = g.lists.ids[list + next];
+        if (EPI == kLossGrad) {
+            const RowStat s = g.stat[row];
+            top = s.top;
+            inv = s.inv;
+            gain = g.gain[row];
+        }
+    }
+
+    __device__ __forceinline__ void chunk(uint32_t c0, float (&z)[32]) {
+        if constexpr (EPI == kLossOut) out(c0, z);
+        else logit(c0, z);
+    }
+
+    __device__ __forceinline__ void logit(uint32_t c0, float (&z)[32]) {
+        const LogitArgs& g = a.logit;
+        const int32_t v = static_cast<int32_t>(g.v0 + n0 + c0);
+        if (c0 + 32 > cols) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c0 + j >= cols) z[j] = -kInf;
+        }
+        if (EPI == kLossStats) {
+            while (next_id < v + 32) {  // ids end at kNoId, or before the list does
+                const int at = next_id - v;
+                float x = 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j == at) x = z[j];
+                g.lists.logits[list + next] = x;
+                step();
+            }
+            float m = top;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m = fmaxf(m, __fmul_rn(z[j], g.c));
+            const float base = m == -kInf ? 0.f : m;
+            sum = __fmul_rn(sum, exp2_fast(__fsub_rn(top, base)));
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) part[j % 4] = __fadd_rn(part[j % 4], exp2_fast(__fmaf_rn(z[j], g.c, -base)));
+            sum = __fadd_rn(sum, __fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])));
+            top = m;
+        } else {
+            if (in) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z[j] = __fmul_rn(exp2_fast(__fmaf_rn(z[j], g.c, -top)), inv);
+                if (c0 + 32 > cols) {  // a row of NaN leaves the columns behind the last at 0
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j >= cols) z[j] = 0.f;
+                }
+                while (next_id < v + 32) {
+                    const int at = next_id - v;
+                    const float share = g.lists.shares ? g.lists.shares[list + next] : 1.f;
+                    const float x = __fmul_rn(share, gain);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j == at) z[j] = __fsub_rn(z[j], x);
+                    step();
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z[j] = 0.f;
+            }
+            if (g.g.planes == 1) {
+                uint4* p = reinterpret_cast<uint4*>(g.g.p + row * g.g.pitch + n0 + c0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    p[j] = make_uint4(pack_bf16x2(z[8 * j], z[8 * j + 1]), pack_bf16x2(z[8 * j + 2], z[8 * j + 3]),
+                                      pack_bf16x2(z[8 * j + 4], z[8 * j + 5]), pack_bf16x2(z[8 * j + 6], z[8 * j + 7]));
+            } else {
+                for (int q = 0; q < g.g.planes; ++q) {
+                    uint4* p = reinterpret_cast<uint4*>(g.g.p + q * g.g.plane + row * g.g.pitch + n0 + c0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t lo = split_plane(z[8 * j + 2 * i]), hi = split_plane(z[8 * j + 2 * i + 1]);
+                            w[i] = lo | (hi << 16);
+                        }
+                        p[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void step() {
+        const Lists& l = a.logit.lists;
+        ++next;
+        next_id = next < l.top ? l.ids[list + next] : kNoId;
+    }
+
+    __device__ __forceinline__ void out(uint32_t c0, float (&z)[32]) {
+        if (!in || c0 >= cols) return;
+        const OutArgs& o = a.out;
+        if (o.parts) {
+            float4* p = reinterpret_cast<float4*>(o.parts + split * o.part_stride + row * o.part_pitch + n0 + c0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float4 x = make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
+                if (o.add_parts) {
+                    const float4 y = p[j];
+                    x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+                }
+                p[j] = x;
+            }
+            return;
+        }
+        const uint64_t at = (o.row ? static_cast<uint64_t>(o.row[row]) : row) * o.stride + n0 + c0;
+        if (c0 + 32 <= cols && !o.accumulate) {
+            if (o.bf16) {
+                uint16_t* p = static_cast<uint16_t*>(o.out) + at;
+                if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        reinterpret_cast<uint4*>(p)[j] =
+                            make_uint4(pack_bf16x2(z[8 * j], z[8 * j + 1]), pack_bf16x2(z[8 * j + 2], z[8 * j + 3]),
+                                       pack_bf16x2(z[8 * j + 4], z[8 * j + 5]), pack_bf16x2(z[8 * j + 6], z[8 * j + 7]));
+                    return;
+                }
+            } else {
+                float* p = static_cast<float*>(o.out) + at;
+                if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        reinterpret_cast<float4*>(p)[j] = make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
+                    return;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (c0 + j < cols) store_out(o.out, at + j, o.bf16, o.accumulate, z[j]);
+    }
+
+    __device__ __forceinline__ void end(uint32_t nt) {
+        if (EPI == kLossStats && in)
+            a.logit.stats[(a.logit.v0 / kLossTile + nt) * a.logit.stats_pitch + row] = make_float2(top, sum);
+    }
+};
+
+template <int EPI, bool AT, bool BT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+    product_kernel(const __grid_constant__ ProductParams p) {
+    extern __shared__ char raw[];
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;  // the same in both CTAs
+    const uint32_t bars = base + kStages * kStageBytes;
+    auto bar = [bars](uint32_t i) { return bars + 8 * i; };
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < kStages; ++s) {
+            mbar_init(bar(kFullBar + s), 1);
+            mbar_init(bar(kEmptyBar + s), 1);
+        }
+        for (uint32_t b = 0; b < 2; ++b) {
+            mbar_init(bar(kReadyBar + b), 1);
+            mbar_init(bar(kFreeBar + b), 2 * kEpilogueWarps);
+        }
+        mbar_init(bar(kDoneBar), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.a) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.b) : "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar(kTmemWord)),
+                     "r"(kTmemColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        tmem_fence_before();
+    }
+    __syncthreads();
+    cluster_sync();
+    tmem_fence_after();
+    const uint32_t tmem = lds32(bar(kTmemWord));
+    griddep_wait();
+    const ProductArgs& a = p.args;
+    const Tiles tiles(p);
+    const uint64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+    uint32_t mt, nt, split, lo, n;
+    bool ok = true;
+    if (warp == 0 && lane == 0) {
+        uint32_t it = 0;
+        for (uint64_t t = first; t < tiles.total && ok; t += step) {
+            tiles.at(t, mt, nt, split, lo, n);
+            const int m0 = static_cast<int>(mt * kSide + rank * kHalf), n0 = static_cast<int>(nt * kSide + rank * kHalf);
+            const uint32_t each = tiles.passes == 1 ? n : n / tiles.passes;
+            for (uint32_t i = 0; i < n; ++i, ++it) {
+                const uint32_t s = it % kStages, round = it / kStages;
+                if (round > 0 && !(ok = mbar_wait(bar(kEmptyBar + s), (round - 1) & 1))) break;
+                const uint32_t q = tiles.passes == 1 ? 0 : i / each;
+                const int k0 = static_cast<int>((lo + i - q * each) * kDeep);
+                const int za = tiles.passes == 1 ? 0 : plane_a(q), zb = tiles.passes == 1 ? 0 : plane_b(q);
+                const uint32_t to = base + s * kStageBytes, full = in_first(bar(kFullBar + s));
+                if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
+                if (AT) {
+                    tma_load(to, &p.a, m0, k0, za, full);
+                    tma_load(to + kOperandBytes / 2, &p.a, m0 + 64, k0, za, full);
+                } else {
+                    tma_load(to, &p.a, k0, m0, za, full);
+                }
+                if (BT) {
+                    tma_load(to + kOperandBytes, &p.b, n0, k0, zb, full);
+                    tma_load(to + kOperandBytes + kOperandBytes / 2, &p.b, n0 + 64, k0, zb, full);
+                } else {
+                    tma_load(to + kOperandBytes, &p.b, k0, n0, zb, full);
+                }
+            }
+        }
+        // the last blocks have been read before the pair's memory goes
+        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+            if (!mbar_wait(bar(kEmptyBar + i % kStages), (i / kStages) & 1)) ok = false;
+        if (rank == 1 && !mbar_wait(bar(kDoneBar), 0)) ok = false;
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        uint32_t it = 0, done = 0;
+        for (uint64_t t = first; t < tiles.total && ok; t += step) {
+            tiles.at(t, mt, nt, split, lo, n);
+            if (n == 0) continue;
+            const uint32_t b = done & 1, acc = tmem + b * kSide;
+            if (done >= 2 && !(ok = mbar_wait(bar(kFreeBar + b), (done / 2 - 1) & 1))) break;
+            tmem_fence_after();
+            for (uint32_t i = 0; i < n; ++i, ++it) {
+                const uint32_t s = it % kStages;
+                if (!(ok = mbar_wait(bar(kFullBar + s), (it / kStages) & 1))) break;
+                tmem_fence_after();
+                const uint32_t at = base + s * kStageBytes;
+#pragma unroll
+                for (uint32_t k = 0; k < kDeep / 16; ++k)
+                    mma(acc, operand_desc(at + k * (AT ? 2048 : 32), AT),
+                        operand_desc(at + kOperandBytes + k * (BT ? 2048 : 32), BT), mma_desc(AT, BT), i > 0 || k > 0);
+                mma_commit(bar(kEmptyBar + s));
+            }
+            if (!ok) break;
+            mma_commit(bar(kReadyBar + b));
+            ++done;
+        }
+        mma_commit(bar(kDoneBar));
+        if (!mbar_wait(bar(kDoneBar), 0)) ok = false;
+    } else if (warp >= kEpilogueWarp) {
+        const uint32_t quarter = warp % 4;
+        uint32_t done = 0;
+        for (uint64_t t = first; t < tiles.total; t += step) {
+            tiles.at(t, mt, nt, split, lo, n);
+            Epilogue<EPI> e(a, tiles.m, static_cast<uint64_t>(mt) * kSide + rank * kHalf + quarter * 32 + lane, nt, split);
+            const uint32_t b = done & 1;
+            if (n > 0) {
+                ok = mbar_wait(bar(kReadyBar + b), (done / 2) & 1);
+                if (!__all_sync(kFull, ok)) break;
+                tmem_fence_after();
+            }
+            const uint32_t acc = tmem + b * kSide + ((quarter * 32) << 16);
+#pragma unroll 1
+            for (uint32_t c0 = 0; c0 < kSide; c0 += 32) {
+                float z[32];
+                if (n > 0) {
+                    tmem_read32(acc + c0, z);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[j] = 0.f;
+                }
+                e.chunk(c0, z);
+            }
+            e.end(nt);
+            if (n > 0) {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_first(bar(kFreeBar + b)));
+                ++done;
+            }
+        }
+    }
+    if (!ok) atomicOr(a.status, 1u);
+    __syncwarp();
+    tmem_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tmem_fence_after();
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+}
+
+using ProductKernel = void (*)(ProductParams);
+
+ProductKernel product_of(const ProductArgs& a) {
+    if (a.epilogue == kLossStats) return product_kernel<kLossStats, false, false>;
+    if (a.epilogue == kLossGrad) return product_kernel<kLossGrad, false, false>;
+    return a.a.turned ? product_kernel<kLossOut, true, true> : product_kernel<kLossOut, false, true>;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the runtime's driver entry-point query (the
+// library links only the static runtime); null if the driver has none.
+EncodeFn encode_tiled() {
+    static const EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return static_cast<EncodeFn>(nullptr);
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// Blocks of 64 columns x 128 rows (turned: 64 rows) of one plane; zeros outside.
+cudaError_t make_map(const Operand& o, CUtensorMap* map) {
+    const EncodeFn encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t row = 2 * o.m.pitch, plane = o.m.planes > 1 ? 2 * o.m.plane : row;
+    const cuuint64_t dims[3] = {o.cols, std::max<uint64_t>(1, o.rows), static_cast<cuuint64_t>(o.m.planes)};
+    const cuuint64_t strides[2] = {row, plane};
+    const cuuint32_t box[3] = {kDeep, static_cast<cuuint32_t>(o.turned ? kDeep : kHalf), 1}, steps[3] = {1, 1, 1};
+    static_assert(kDeep == 64, "a block's rows are one swizzle wide, turned or not");
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.m.p, dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
 }
 
 template <class Args>
@@ -445,12 +865,27 @@ cudaError_t launch_record(const RecordArgs& a, cudaStream_t st) {
     return launch(record_kernel, a, 1, kRecordThreads, st);
 }
 
+cudaError_t prepare_products() {
+    for (ProductKernel f : {product_kernel<kLossStats, false, false>, product_kernel<kLossGrad, false, false>,
+                            product_kernel<kLossOut, true, true>, product_kernel<kLossOut, false, true>}) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t st) {
-    const uint64_t tall = (static_cast<uint64_t>(a.m) + kLossTile - 1) / kLossTile * (kLossTile / kSide);
-    const uint64_t grid = tall * ((a.n + kLossTile - 1) / kLossTile) * a.splits;
-    return launch(a.epilogue == kLossStats ? product_kernel<kLossStats>
-                                           : (a.epilogue == kLossGrad ? product_kernel<kLossGrad> : product_kernel<kLossOut>),
-                  a, grid, 256, st);
+    ProductParams p;
+    p.args = a;
+    cudaError_t e = make_map(a.a, &p.a);
+    if (e == cudaSuccess) e = make_map(a.b, &p.b);
+    if (e != cudaSuccess) return e;
+    const uint64_t tall = (static_cast<uint64_t>(a.m) + kSide - 1) / kSide, wide = (static_cast<uint64_t>(a.n) + kSide - 1) / kSide;
+    p.m_group = static_cast<uint32_t>(std::max<uint64_t>(1, tall));
+    if (tall * kSide * a.k * 2 > (64ull << 20)) p.m_group = 8;
+    const uint64_t pairs = std::min<uint64_t>(std::max<uint64_t>(1, tall * wide * a.splits), kLossSms / 2);
+    return launch(product_of(a), p, 2 * pairs, kProductThreads, st, kProductSmem);
 }
 
 cudaError_t launch_finish_parts(const FinishArgs& a, cudaStream_t st) {

@@ -182,6 +182,8 @@ cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
 cudaError_t launch_clear(const ClearArgs& a, cudaStream_t st);
 cudaError_t launch_join(const JoinArgs& a, cudaStream_t st);
 cudaError_t launch_record(const RecordArgs& a, cudaStream_t st);
+// What the products' kernels need once on a device before their first launch.
+cudaError_t prepare_products();
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t st);
 cudaError_t launch_finish_parts(const FinishArgs& a, cudaStream_t st);
 
