@@ -608,7 +608,7 @@ class OutputLoss:
     `tokens` tokens, without an array of tokens x vocab; with the gradients of
     hidden states and weights.  hidden and weight are bfloat16 or float32
     (`dtype`), as (n, hidden) and (vocab, hidden) tensors with any row stride.
-    `top`: entries of a teacher's list at most; `piece`: vocabulary entries worked
+    `top`: entries of a teacher's list at most; `piece`: tokens worked
     on at a time (0: chosen); `grads=False`: losses alone, little workspace.
 
     Both calls return the record, four floats on the device: loss, tokens

@@ -16,9 +16,17 @@ constexpr double kFloatMax = 3.4028234e38;
 constexpr uint64_t kMaxTokens = 1ull << 22, kMaxHidden = 1ull << 16, kMaxVocab = 1ull << 24;
 constexpr int kMaxTop = 1024;
 
-// Logits of a piece of the vocabulary that the caller leaves to the handle: in
-// bf16 0.5 GB of gradients.
+// Logits of a piece of the tokens that the caller leaves to the handle: 1 GB of
+// them and in bf16 0.5 GB of their gradients.
 constexpr uint64_t kPieceLogits = 1ull << 28;
+
+// Vocabulary entries that are packed at a time where the weights are not read as they are.
+constexpr uint64_t kPackEntries = 1ull << 15;
+
+// Blocks of 64 products that are summed in the tensor cores before float32 sums
+// take over: for logits and float32 results, and for bf16 ones (whose rounding
+// is 2^-8).
+constexpr uint32_t kExactRun = 8, kLongRun = 1u << 30;
 
 ar_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
@@ -33,10 +41,12 @@ uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
 // The workspace's parts: offsets of each in one allocation.
 struct Layout {
-    uint64_t rows = 0, pitch = 0, piece = 0, pieces = 0, parts = 0;  // padded tokens, padded D, ..., floats
+    uint64_t rows = 0, pitch = 0;    // padded tokens, padded D
+    uint64_t piece = 0, pieces = 0;  // tokens at a time
+    uint64_t pack = 0, part_room = 0, wide = 0, sum_pitch = 0;  // entries packed at a time, floats, padded V, ... D
     int planes = 1, list = 1;
     size_t status = 0, count = 0, factor = 0, row = 0, counted = 0, ids = 0, shares = 0, entropy = 0, logits = 0;
-    size_t stats = 0, stat = 0, gain = 0, loss = 0, hidden = 0, weight = 0, grad = 0, part = 0;
+    size_t stats = 0, stat = 0, gain = 0, loss = 0, hidden = 0, weight = 0, z = 0, grad = 0, part = 0, sum = 0;
     size_t bytes = 0;
     size_t add(uint64_t n) {
         const size_t at = bytes;
@@ -56,11 +66,15 @@ ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype
     l.list = std::max(1, top);
     l.rows = std::max(tile, up(tokens, tile));
     l.pitch = up(hidden, 8);
-    if (piece == 0) piece = std::max(tile, kPieceLogits / l.rows);
-    piece = std::min(up(piece, tile), up(vocab, tile));
-    l.pieces = (vocab + piece - 1) / piece;
-    l.piece = up((vocab + l.pieces - 1) / l.pieces, tile);  // as even as whole tiles allow
-    l.pieces = (vocab + l.piece - 1) / l.piece;
+    l.wide = up(vocab, tile);
+    l.sum_pitch = up(hidden, tile);
+    if (!gradients) piece = l.rows;  // no logits are stored
+    if (piece == 0) piece = std::max(tile, kPieceLogits / l.wide / tile * tile);
+    piece = std::min(up(std::min(piece, l.rows), tile), l.rows);
+    l.pieces = (l.rows + piece - 1) / piece;
+    l.piece = up((l.rows + l.pieces - 1) / l.pieces, tile);  // as even as whole tiles allow
+    l.pieces = (l.rows + l.piece - 1) / l.piece;
+    l.pack = std::min(l.wide, kPackEntries);
     const uint64_t n = l.rows, k = n * l.list;
     l.status = l.add(4);
     l.count = l.add(4);
@@ -71,16 +85,19 @@ ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype
     l.ids = l.add(4 * k);
     l.shares = l.add(4 * k);
     l.logits = l.add(4 * k);
-    l.stats = l.add(8 * n * (up(vocab, tile) / tile));
+    l.stats = l.add(8 * l.piece * (l.wide / ar::kStatColumns));
     l.stat = l.add(8 * n);
     l.gain = l.add(4 * n);
     l.loss = l.add(4 * n);
     l.hidden = l.add(2 * l.planes * n * l.pitch);
-    l.weight = l.add(2 * l.planes * l.piece * l.pitch);
+    l.weight = l.add(2 * l.planes * l.pack * l.pitch);
     if (gradients) {
-        l.grad = l.add(2 * l.planes * n * l.piece);
-        l.parts = std::max(n * up(hidden, tile), ar::kLossSms * tile * tile);
-        l.part = l.add(4 * l.parts);
+        l.z = l.add(4 * l.piece * l.wide);
+        l.grad = l.add(2 * l.planes * l.piece * l.wide);
+        // four parts of a piece's gradient by the hidden states, a tile for every SM pair of small ones
+        l.part_room = std::max(4 * l.piece * l.sum_pitch, ar::kLossSms / 2 * tile * l.sum_pitch);
+        l.part = l.add(4 * l.part_room);
+        if (l.pieces > 1) l.sum = l.add(4 * std::max(l.wide, l.piece) * l.sum_pitch);
     }
     return AR_OK;
 }
@@ -144,13 +161,17 @@ struct Call {
     const ar_output_loss_s* h;
     const ar_output_loss_args* a;
     cudaStream_t st;
-    uint32_t n;
+    uint32_t n, width, vocab;
+    bool grads;
+    float c = 0.f;
+    double t = 1.0;
     ar::Lists lists = {};
     ar::Counted rows = {};
     cudaError_t e = cudaSuccess;
 
     Call(const ar_output_loss_s* h_, const ar_output_loss_args* a_, cudaStream_t st_)
-        : h(h_), a(a_), st(st_), n(static_cast<uint32_t>(a_->tokens)) {
+        : h(h_), a(a_), st(st_), n(static_cast<uint32_t>(a_->tokens)), width(static_cast<uint32_t>(h_->hidden)),
+          vocab(static_cast<uint32_t>(h_->vocab)), grads(a_->grad_weight || a_->grad_hidden) {
         lists.ids = h->at<int32_t>(h->l.ids);
         lists.entropy = h->at<float>(h->l.entropy);
         lists.counted = h->at<uint32_t>(h->l.counted);
@@ -161,31 +182,30 @@ struct Call {
         rows.factor = h->at<float>(h->l.factor);
     }
 
-    ar::Planes hidden() const {
-        return {h->at<uint16_t>(h->l.hidden), h->l.rows * h->l.pitch, h->l.pitch, h->l.planes};
+    // Places [r, ...) of the counted tokens' hidden states.
+    ar::Planes hidden(uint64_t r) const {
+        return {h->at<uint16_t>(h->l.hidden) + r * h->l.pitch, h->l.rows * h->l.pitch, h->l.pitch, h->l.planes};
     }
     ar::Planes grad() const {
-        return {h->at<uint16_t>(h->l.grad), h->l.rows * h->l.piece, h->l.piece, h->l.planes};
+        return {h->at<uint16_t>(h->l.grad), h->l.piece * h->l.wide, h->l.wide, h->l.planes};
     }
     // TMA reads rows that start on 16-byte boundaries
     bool weight_as_is() const {
         return h->dtype == AR_BFLOAT16 && reinterpret_cast<uintptr_t>(a->weight) % 16 == 0 &&
                a->weight_stride % 8 == 0 && a->weight_stride < (1ull << 38);
     }
-    const char* weight_row(uint64_t v) const {
-        return static_cast<const char*>(a->weight) + v * a->weight_stride * esize(h->dtype);
-    }
-    // Rows [v0, v1) of the weights as planes: where they are, or packed.
+    // Vocabulary entries that are at hand at a time, [v0, v1) as planes: where they are, or packed.
+    uint64_t entries() const { return weight_as_is() ? h->vocab : h->l.pack; }
     ar::Planes weight(uint64_t v0, uint64_t v1) {
-        if (weight_as_is())
-            return {reinterpret_cast<uint16_t*>(const_cast<char*>(weight_row(v0))), 0, a->weight_stride, 1};
+        const char* from = static_cast<const char*>(a->weight) + v0 * a->weight_stride * esize(h->dtype);
+        if (weight_as_is()) return {reinterpret_cast<uint16_t*>(const_cast<char*>(from)), 0, a->weight_stride, 1};
         ar::PackArgs p = {};
-        p.src = weight_row(v0);
+        p.src = from;
         p.stride = a->weight_stride;
         p.bf16 = h->dtype == AR_BFLOAT16;
         p.n = static_cast<uint32_t>(v1 - v0);
-        p.width = static_cast<uint32_t>(h->hidden);
-        p.out = {h->at<uint16_t>(h->l.weight), h->l.piece * h->l.pitch, h->l.pitch, h->l.planes};
+        p.width = width;
+        p.out = {h->at<uint16_t>(h->l.weight), h->l.pack * h->l.pitch, h->l.pitch, h->l.planes};
         run(ar::launch_pack(p, st));
         return p.out;
     }
@@ -193,142 +213,158 @@ struct Call {
         if (e == cudaSuccess) e = next;
     }
 
-    ar::ProductArgs product() const {
+    // Of the counted tokens at places [r, r + m).
+    ar::ProductArgs product(uint64_t r) const {
         ar::ProductArgs p = {};
         p.count = rows.count;
-        p.splits = 1;
+        p.base = static_cast<uint32_t>(r);
         p.status = h->at<uint32_t>(h->l.status);
         return p;
     }
 
-    // The logits of [v0, v1): their statistics, or their gradient into grad().
-    void logits(uint64_t v0, uint64_t v1, const ar::Planes& w, ar::LossEpilogue epilogue, float c) {
-        ar::ProductArgs p = product();
-        p.a = {hidden(), false, n, h->hidden};
-        p.b = {w, false, v1 - v0, h->hidden};
-        p.m = n;
-        p.count_m = 1;
-        p.n = static_cast<uint32_t>(v1 - v0);
-        p.k = static_cast<uint32_t>(h->hidden);
-        p.epilogue = epilogue;
-        p.logit = {static_cast<uint32_t>(v0), static_cast<uint32_t>(v1), c, lists, h->at<float2>(h->l.stats),
-                   h->l.rows, h->at<ar::RowStat>(h->l.stat), h->at<float>(h->l.gain), {}};
-        if (epilogue == ar::kLossGrad) p.logit.g = grad();
-        p.out.row = rows.row;
-        run(ar::launch_product(p, st));
+    void logits(uint64_t r, uint32_t m) {
+        for (uint64_t v = 0; v < h->vocab; v += entries()) {
+            const uint64_t end = std::min(h->vocab, v + entries());
+            ar::ProductArgs p = product(r);
+            p.a = {hidden(r), false, m, h->hidden};
+            p.b = {weight(v, end), false, end - v, h->hidden};
+            p.m = m;
+            p.count_m = 1;
+            p.n = static_cast<uint32_t>(end - v);
+            p.k = width;
+            p.run = kExactRun;
+            p.logits = 1;
+            p.logit.c = c;
+            p.logit.v0 = static_cast<uint32_t>(v);
+            p.logit.lists = lists;
+            p.logit.row = rows.row + r;
+            p.logit.stats = h->at<float2>(h->l.stats) + v / ar::kStatColumns * h->l.piece;
+            p.logit.stats_pitch = h->l.piece;
+            if (grads) p.logit.z = h->at<float>(h->l.z) + v;
+            p.logit.z_pitch = h->l.wide;
+            run(ar::launch_product(p, st));
+        }
+        ar::JoinArgs j = {};
+        j.stats = h->at<float2>(h->l.stats);
+        j.pitch = h->l.piece;
+        j.parts = static_cast<uint32_t>(up(h->vocab, ar::kStatColumns) / ar::kStatColumns);
+        j.base = static_cast<uint32_t>(r);
+        j.n = m;
+        j.c = c;
+        j.t = t;
+        j.lists = lists;
+        j.rows = rows;
+        j.stat = h->at<ar::RowStat>(h->l.stat) + r;
+        j.gain = h->at<float>(h->l.gain) + r;
+        j.loss = h->at<float>(h->l.loss) + r;
+        j.losses = a->losses;
+        run(ar::launch_join(j, st));
     }
 
-    void grad_weight(uint64_t v0, uint64_t v1) {
-        ar::ProductArgs p = product();
-        p.a = {grad(), true, n, v1 - v0};
-        p.b = {hidden(), true, n, h->hidden};
-        p.m = static_cast<uint32_t>(v1 - v0);
-        p.n = static_cast<uint32_t>(h->hidden);
-        p.k = n;
+    void grad_logits(uint64_t r, uint32_t m) {
+        ar::GradArgs g = {};
+        g.z = h->at<float>(h->l.z);
+        g.pitch = h->l.wide;
+        g.base = static_cast<uint32_t>(r);
+        g.n = m;
+        g.vocab = vocab;
+        g.c = c;
+        g.lists = lists;
+        g.rows = rows;
+        g.stat = h->at<ar::RowStat>(h->l.stat) + r;
+        g.gain = h->at<float>(h->l.gain) + r;
+        g.g = grad();
+        run(ar::launch_grad(g, st));
+    }
+
+    // The last piece's product goes to the caller, with the sum of those before.
+    void grad_weight(uint64_t r, uint32_t m, bool last) {
+        ar::ProductArgs p = product(r);
+        p.a = {grad(), true, m, h->vocab};
+        p.b = {hidden(r), true, m, h->hidden};
+        p.m = vocab;
+        p.n = width;
+        p.k = m;
         p.count_k = 1;
-        p.epilogue = ar::kLossOut;
-        p.out.out = static_cast<char*>(a->grad_weight) + v0 * a->grad_weight_stride * esize(a->grad_weight_dtype);
+        p.run = a->grad_weight_dtype == AR_BFLOAT16 ? kLongRun : kExactRun;
+        p.out.out = a->grad_weight;
         p.out.stride = a->grad_weight_stride;
         p.out.bf16 = a->grad_weight_dtype == AR_BFLOAT16;
         p.out.accumulate = a->accumulate;
+        p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
+        p.out.part_room = h->l.part_room;
+        if (r > 0) p.out.add = h->at<float>(h->l.sum);
+        if (!last) p.out.sum = h->at<float>(h->l.sum);
+        if (r == 0 && last) p.out.parts = h->at<float>(h->l.part);
         run(ar::launch_product(p, st));
+        if (p.out.parts) run(ar::launch_finish(p, st));
     }
 
-    void grad_hidden(uint64_t v0, uint64_t v1, const ar::Planes& w) {
-        ar::ProductArgs p = product();
-        p.a = {grad(), false, n, v1 - v0};
-        p.b = {w, true, v1 - v0, h->hidden};
-        p.m = n;
-        p.count_m = 1;
-        p.n = static_cast<uint32_t>(h->hidden);
-        p.k = static_cast<uint32_t>(v1 - v0);
-        p.epilogue = ar::kLossOut;
-        const bool parts = h->l.pieces > 1;
-        if (parts) {
-            p.out.parts = h->at<float>(h->l.part);
-            p.out.part_pitch = up(h->hidden, ar::kLossTile);
-            p.out.part_stride = up(n, ar::kLossTile) * p.out.part_pitch;
-            p.out.add_parts = v0 > 0;
-        } else {
+    void grad_hidden(uint64_t r, uint32_t m) {
+        for (uint64_t v = 0; v < h->vocab; v += entries()) {
+            const uint64_t end = std::min(h->vocab, v + entries());
+            ar::ProductArgs p = product(r);
+            ar::Planes g = grad();
+            g.p += v;
+            p.a = {g, false, m, end - v};
+            p.b = {weight(v, end), true, end - v, h->hidden};
+            p.m = m;
+            p.count_m = 1;
+            p.n = width;
+            p.k = static_cast<uint32_t>(end - v);
+            p.run = a->grad_hidden_dtype == AR_BFLOAT16 ? kLongRun : kExactRun;
             p.out.out = a->grad_hidden;
             p.out.stride = a->grad_hidden_stride;
             p.out.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
             p.out.accumulate = a->accumulate;
-            p.out.row = rows.row;
+            p.out.row = rows.row + r;
+            p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
+            p.out.part_room = h->l.part_room;
+            const bool whole = v == 0 && end == h->vocab;
+            if (whole) p.out.parts = h->at<float>(h->l.part);
+            // entries packed at a time: sums in the parts' memory
+            if (v > 0) p.out.add = h->at<float>(h->l.part);
+            if (end < h->vocab) p.out.sum = h->at<float>(h->l.part);
+            run(ar::launch_product(p, st));
+            if (whole) run(ar::launch_finish(p, st));
         }
-        run(ar::launch_product(p, st));
-        if (!parts || v1 < h->vocab) return;
-        ar::FinishArgs f = {};
-        f.parts = p.out.parts;
-        f.part_stride = p.out.part_stride;
-        f.part_pitch = p.out.part_pitch;
-        f.splits = p.splits;
-        f.n = n;
-        f.width = p.n;
-        f.rows = rows;
-        f.by_count = 1;
-        f.out = a->grad_hidden;
-        f.stride = a->grad_hidden_stride;
-        f.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
-        f.accumulate = a->accumulate;
-        run(ar::launch_finish_parts(f, st));
     }
 
-    // Everything after the lists: `rows` with its targets, the passes over the
-    // vocabulary, the record.
-    ar_status finish(ar::RowsArgs r, double t) {
+    // Everything after the lists: the tokens that count, then in pieces of them
+    // logits, losses and gradients, and the record.
+    ar_status finish(ar::RowsArgs r, double temperature) {
+        t = temperature;
+        c = static_cast<float>(1.4426950408889634 / t);
         r.n = n;
-        r.vocab = static_cast<uint32_t>(h->vocab);
+        r.vocab = vocab;
         r.scale = a->scale;
         r.mean = a->reduction == AR_LOSS_MEAN;
         r.lists = lists;
         r.rows = rows;
         run(ar::launch_rows(r, st));
-        const float c = static_cast<float>(1.4426950408889634 / t);
-        const uint64_t step = weight_as_is() ? h->vocab : h->l.piece;
         if (n > 0) {
-            ar::ClearArgs z = {lists.counted, n, static_cast<uint32_t>(h->hidden), a->losses,
-                               a->accumulate ? nullptr : a->grad_hidden, a->grad_hidden_stride,
-                               a->grad_hidden_dtype == AR_BFLOAT16};
+            ar::ClearArgs z = {lists.counted, n, width, a->losses, a->accumulate ? nullptr : a->grad_hidden,
+                               a->grad_hidden_stride, a->grad_hidden_dtype == AR_BFLOAT16};
             if (z.losses || z.grad_hidden) run(ar::launch_clear(z, st));
             ar::PackArgs p = {};
             p.src = a->hidden;
             p.stride = a->hidden_stride;
             p.bf16 = h->dtype == AR_BFLOAT16;
             p.n = n;
-            p.width = static_cast<uint32_t>(h->hidden);
+            p.width = width;
             p.rows = rows;
-            p.out = hidden();
+            p.out = hidden(0);
             run(ar::launch_pack(p, st));
-            for (uint64_t v = 0; v < h->vocab; v += step) {
-                const uint64_t end = std::min(h->vocab, v + step);
-                logits(v, end, weight(v, end), ar::kLossStats, c);
-            }
-            ar::JoinArgs j = {};
-            j.stats = h->at<float2>(h->l.stats);
-            j.pitch = h->l.rows;
-            j.tiles = static_cast<uint32_t>(up(h->vocab, ar::kLossTile) / ar::kLossTile);
-            j.n = n;
-            j.c = c;
-            j.t = t;
-            j.lists = lists;
-            j.rows = rows;
-            j.stat = h->at<ar::RowStat>(h->l.stat);
-            j.gain = h->at<float>(h->l.gain);
-            j.loss = h->at<float>(h->l.loss);
-            j.losses = a->losses;
-            run(ar::launch_join(j, st));
+        }
+        for (uint64_t at = 0; at < n || at == 0; at += h->l.piece) {
+            const uint32_t m = static_cast<uint32_t>(std::min<uint64_t>(n - at, h->l.piece));
+            const bool last = at + h->l.piece >= n;
+            if (m > 0) logits(at, m);
+            if (m > 0 && grads) grad_logits(at, m);
+            if (a->grad_weight) grad_weight(at, m, last);
+            if (m > 0 && a->grad_hidden) grad_hidden(at, m);
         }
         run(ar::launch_record({h->at<float>(h->l.loss), rows, a->result}, st));
-        if (a->grad_weight || (a->grad_hidden && n > 0)) {
-            for (uint64_t v = 0; v < h->vocab; v += h->l.piece) {
-                const uint64_t end = std::min(h->vocab, v + h->l.piece);
-                const ar::Planes w = n > 0 ? weight(v, end) : ar::Planes{};
-                if (n > 0) logits(v, end, w, ar::kLossGrad, c);
-                if (a->grad_weight) grad_weight(v, end);
-                if (a->grad_hidden && n > 0) grad_hidden(v, end, w);
-            }
-        }
         return cuda_status(e);
     }
 };
@@ -370,7 +406,7 @@ ar_status ar_output_loss_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab
     info->piece = l.piece;
     info->pieces = static_cast<int>(l.pieces);
     info->workspace_bytes = l.bytes;
-    info->tiling_ok = l.piece % ar::kLossTile == 0 && l.piece * l.pieces >= vocab && l.piece * (l.pieces - 1) < vocab;
+    info->tiling_ok = l.piece % ar::kLossTile == 0 && l.piece * l.pieces >= tokens && l.piece * (l.pieces - 1) < l.rows;
     return AR_OK;
 }
 

@@ -9,6 +9,7 @@
 #include <cuda.h>  // the tensor map's types only: the driver call is resolved at run time
 
 #include <algorithm>
+#include <type_traits>
 
 #include "device.cuh"
 #include "outloss.hpp"
@@ -232,15 +233,15 @@ __device__ __forceinline__ void join_stat(float& top, float& sum, float top2, fl
     sum = __fadd_rn(a, b);
 }
 
-// A warp a place: the tiles' statistics in a fixed order, the loss.
+// A warp a place: the parts' statistics in a fixed order, the loss.
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
     const uint32_t lane = threadIdx.x % 32;
-    const uint64_t r = blockIdx.x * 8ull + threadIdx.x / 32;
+    const uint32_t r = blockIdx.x * 8 + threadIdx.x / 32;
     griddep_wait();
-    if (r >= *a.rows.count) return;
-    const uint64_t i = a.rows.row[r];
+    if (r >= a.n || a.base + r >= *a.rows.count) return;
+    const uint64_t i = a.rows.row[a.base + r];
     float top = -kInf, sum = 0.f;
-    for (uint32_t q = lane; q < a.tiles; q += 32) {
+    for (uint32_t q = lane; q < a.parts; q += 32) {
         const float2 s = a.stats[q * a.pitch + r];
         join_stat(top, sum, s.x, s.y);
     }
@@ -306,17 +307,52 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int 
     else static_cast<float*>(out)[at] = x;
 }
 
-// The parts of a product, added in their order.
-__global__ void __launch_bounds__(256) finish_parts_kernel(const __grid_constant__ FinishArgs a) {
-    const uint32_t lane = threadIdx.x % 32;
-    const uint64_t r = blockIdx.x * 8ull + threadIdx.x / 32;
+constexpr int kGradThreads = 256, kGradColumns = 8192;  // of a CTA: one row's
+
+// g = 2^(y - top) factor t / sum - share factor t, from the logits of a row's
+// columns; then the few columns of the row's list.
+__global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ GradArgs a) {
+    const uint32_t tid = threadIdx.x;
+    const uint32_t lo = blockIdx.x * kGradColumns, hi = min(a.vocab, lo + kGradColumns);
     griddep_wait();
-    if (r >= (a.by_count ? *a.rows.count : a.n)) return;
-    const uint64_t to = (a.rows.row ? static_cast<uint64_t>(a.rows.row[r]) : r) * a.stride;
-    for (uint32_t c = lane; c < a.width; c += 32) {
-        float x = 0.f;
-        for (int s = 0; s < a.splits; ++s) x = __fadd_rn(x, a.parts[s * a.part_stride + r * a.part_pitch + c]);
-        store_out(a.out, to + c, a.bf16, a.accumulate, x);
+    const uint32_t count = *a.rows.count, m = count > a.base ? min(a.n, count - a.base) : 0;
+    for (uint64_t r = blockIdx.y; r < (m + 63) / 64 * 64; r += gridDim.y) {
+        const bool in = r < m;
+        const RowStat st = in ? a.stat[r] : RowStat{0.f, 0.f};
+        const float* z = a.z + r * a.pitch;
+        uint16_t* g = a.g.p + r * a.g.pitch;
+        auto value = [&](float x) { return __fmul_rn(exp2_fast(__fmaf_rn(x, a.c, -st.top)), st.inv); };
+        for (uint32_t v = lo + 8 * tid; v < hi; v += 8 * kGradThreads) {  // the pitch is of whole tiles
+            float x[8] = {};
+            if (in) {
+                const float4 p = *reinterpret_cast<const float4*>(z + v), q = *reinterpret_cast<const float4*>(z + v + 4);
+                x[0] = value(p.x), x[1] = value(p.y), x[2] = value(p.z), x[3] = value(p.w);
+                x[4] = value(q.x), x[5] = value(q.y), x[6] = value(q.z), x[7] = value(q.w);
+            }
+            for (int q = 0; q < a.g.planes; ++q) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (a.g.planes == 1) {
+                        w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                    } else {
+                        const uint32_t low = split_plane(x[2 * i]), high = split_plane(x[2 * i + 1]);
+                        w[i] = low | (high << 16);
+                    }
+                }
+                *reinterpret_cast<uint4*>(g + q * a.g.plane + v) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        if (!in) continue;  // the whole CTA
+        __syncthreads();
+        const uint64_t list = static_cast<uint64_t>(a.rows.row[a.base + r]) * a.lists.top;
+        for (int k = tid; k < a.lists.top; k += kGradThreads) {
+            const uint32_t v = static_cast<uint32_t>(a.lists.ids[list + k]);
+            if (v < lo || v >= hi) continue;
+            const float share = a.lists.shares ? a.lists.shares[list + k] : 1.f;
+            float x = __fsub_rn(value(a.lists.logits[list + k]), __fmul_rn(share, a.gain[r]));
+            for (int q = 0; q < a.g.planes; ++q) g[q * a.g.plane + v] = split_plane(x);
+        }
     }
 }
 
@@ -327,17 +363,22 @@ __global__ void __launch_bounds__(256) finish_parts_kernel(const __grid_constant
 // rows of C in its tensor memory, twice (the epilogue of one tile runs beside the
 // products of the next).  Persistent: pairs take tiles in turn.  Warp 0 loads (TMA,
 // a ring of kStages blocks of 64 products), warp 1 of the pair's first CTA issues
-// the products, warps 4 to 7 are the epilogue, a thread a row.
+// the products, warps 4 to 11 are the epilogue: a thread half a row.
+//
+// The tensor cores cut sums off where float32 would round them.  Products whose
+// result is float32 are therefore summed there for a run of blocks only, and runs
+// are added up in the epilogue's registers.
 
 constexpr int kSide = 256;             // rows and columns of a pair's tile
 constexpr int kHalf = kSide / 2;       // ... of A and of B in one CTA
 constexpr int kDeep = 64;              // products of a block: 128 bytes of bf16
 constexpr int kStages = 6;
 constexpr uint32_t kOperandBytes = kHalf * kDeep * 2, kStageBytes = 2 * kOperandBytes;
-constexpr int kProductThreads = 256, kEpilogueWarp = 4, kEpilogueWarps = 4;
+constexpr int kProductThreads = 384, kEpilogueWarp = 4, kEpilogueWarps = 8;
+constexpr uint32_t kStagedBytes = 32 * 128;  // of an epilogue warp: 32 rows' part of a result on its way out
 constexpr int kTmemColumns = 512;
 
-static_assert(kSide == static_cast<int>(kLossTile), "statistics are of one tile's columns");
+static_assert(kSide == static_cast<int>(kLossTile) && kHalf == static_cast<int>(kStatColumns), "statistics are of an epilogue thread's columns");
 
 // Barriers, in 8-byte words of shared memory.
 enum : uint32_t {
@@ -349,13 +390,22 @@ enum : uint32_t {
     kTmemWord = kDoneBar + 1,
     kBarWords = kTmemWord + 1
 };
-constexpr uint32_t kProductSmem = kStages * kStageBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
+constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
 
 struct ProductParams {
     CUtensorMap a, b;
     ProductArgs args;
     uint32_t m_group;  // rows of tiles that are worked on side by side
 };
+
+// As mbar_wait, without a call: accumulators live in registers across it.
+__device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer() - t0 > kWaitNs) return false;
+    return true;
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -420,35 +470,53 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_read32(uint32_t taddr, float (&v)[32]) {
+// 16 columns of the warp's lanes; tmem_wait_ld before their use.
+__device__ __forceinline__ void tmem_read16(uint32_t taddr, float* v) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
         : "r"(taddr)
         : "memory");
 }
 
-// The tiles of a product and the blocks of each, alike in every role.
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// The tiles of a product and the blocks of each, alike in every role and kernel.
 struct Tiles {
-    uint32_t m, blocks, per, passes;  // rows of A, blocks of k, ... of a split, passes of planes
-    uint32_t tall, wide, group;
+    uint32_t m, blocks, splits, per;  // rows of A, blocks of k times passes, ... of a split
+    uint32_t k_blocks, tall, wide, group;
     uint64_t total;
-    __device__ explicit Tiles(const ProductParams& p) {
-        const ProductArgs& a = p.args;
-        const uint32_t count = *a.count;
-        m = a.count_m ? min(a.m, count) : a.m;
-        blocks = ((a.count_k ? min(a.k, count) : a.k) + kDeep - 1) / kDeep;
-        per = (blocks + a.splits - 1) / a.splits;
-        passes = a.a.m.planes == 1 ? 1 : 6;
+    __device__ Tiles(const ProductArgs& a, uint32_t m_group) {
+        const uint32_t count = *a.count, left = count > a.base ? count - a.base : 0;
+        m = a.count_m ? min(a.m, left) : a.m;
+        k_blocks = ((a.count_k ? min(a.k, left) : a.k) + kDeep - 1) / kDeep;
+        blocks = k_blocks * (a.a.m.planes == 1 ? 1 : 6);
         tall = (m + kSide - 1) / kSide;
         wide = (a.n + kSide - 1) / kSide;
-        group = p.m_group;
-        total = static_cast<uint64_t>(tall) * wide * a.splits;
+        group = m_group;
+        splits = 1;
+        if (a.out.parts) {
+            const uint64_t rows = static_cast<uint64_t>(tall) * kSide;
+            choose(rows ? static_cast<uint32_t>(min(static_cast<uint64_t>(blocks / 4), a.out.part_room / (rows * a.out.part_pitch))) : 1);
+        }
+        per = (blocks + splits - 1) / splits;
+        total = static_cast<uint64_t>(tall) * wide * splits;
+    }
+    // How many parts of k: what the fullest pair of SMs has to do, in blocks, with
+    // what the parts cost (about 8 blocks' time for their launch and 1 for 4 parts).
+    __device__ void choose(uint32_t most) {
+        const uint32_t pairs = kLossSms / 2, tiles = tall * wide;
+        if (tiles == 0 || tiles >= 8 * pairs) return;
+        uint32_t best = (tiles + pairs - 1) / pairs * blocks;
+        auto look = [&](uint32_t s) {
+            if (s < 2 || s > most) return;
+            const uint32_t cost = (tiles * s + pairs - 1) / pairs * ((blocks + s - 1) / s) + 8 + tiles * s / 4;
+            if (cost < best) best = cost, splits = s;
+        };
+        for (uint32_t s = 2; s <= 8; ++s) look(s);
+        if (pairs / tiles > 8) look(min(most, pairs / tiles));
     }
     // Tile t: in each split, groups of `group` rows of tiles, column by column.
     __device__ void at(uint64_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
@@ -460,7 +528,7 @@ struct Tiles {
         nt = rest / rows;
         mt = g * group + rest - nt * rows;
         lo = min(blocks, split * per);
-        n = (min(blocks, lo + per) - lo) * passes;
+        n = min(blocks, lo + per) - lo;
     }
 };
 
@@ -479,178 +547,186 @@ __device__ __forceinline__ int first_id(const int32_t* ids, int top, int32_t v) 
     return lo;
 }
 
-// One thread's row of a tile: columns c0 to c0 + 31 of the tile at a time.
-template <int EPI>
-struct Epilogue {
-    const ProductArgs& a;
-    uint64_t row;
-    uint32_t n0, cols, split;
+// One thread's half row of a tile.
+struct Place {
+    uint64_t row;   // of C
+    uint32_t n0;    // first column, and how many there are
+    uint32_t cols;
     bool in;
-    // lists
+    uint32_t staged;  // the warp's shared memory
+    uint32_t lane;
+};
+
+// The warp's 32 rows' 128 bytes each, word(0..31) this lane's, to shared memory; use() is
+// then given every row's 16 bytes by eight lanes a row: whole lines for memory.
+template <class Word, class Use>
+__device__ __forceinline__ void transposed(const Place& p, Word word, Use use) {
+    __syncwarp();
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j)
+        sts128(p.staged + p.lane * 128 + ((j ^ (p.lane & 7)) << 4),
+               make_uint4(word(4 * j), word(4 * j + 1), word(4 * j + 2), word(4 * j + 3)));
+    __syncwarp();
+#pragma unroll 2
+    for (uint32_t i = 0; i < 8; ++i) {
+        const uint32_t r = 4 * i + p.lane / 8, j = p.lane % 8;
+        use(r, j, lds128(p.staged + r * 128 + ((j ^ (r & 7)) << 4)));
+    }
+}
+
+__device__ __forceinline__ float4 floats(uint4 v) {
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+// Logits: the largest and the sum of a thread's 128 columns, the logits at its
+// row's ids, and the logits.
+struct LogitTile {
+    const LogitArgs& g;
     uint64_t list = 0;
     int next = 0;
     int32_t next_id = kNoId;
-    // statistics
-    float top = -kInf, sum = 0.f;
-    // gradient
-    float inv = 0.f, gain = 0.f;
+    float top, sum;
 
-    __device__ Epilogue(const ProductArgs& a_, uint32_t m, uint64_t row_, uint32_t nt, uint32_t split_)
-        : a(a_), row(row_), n0(nt * kSide), cols(min(static_cast<uint32_t>(kSide), a_.n - nt * kSide)), split(split_),
-          in(row_ < m) {
-        if (EPI == kLossOut || !in) return;
-        const LogitArgs& g = a.logit;
-        list = static_cast<uint64_t>(a.out.row[row]) * g.lists.top;
-        next = first_id(g.lists.ids + list, g.lists.top, static_cast<int32_t>(g.v0 + n0));
+    // Before the products are complete: the row's place in its list.
+    __device__ __forceinline__ LogitTile(const ProductArgs& a, const Place& p) : g(a.logit) {
+        top = -kInf;
+        sum = 0.f;
+        if (!p.in) return;
+        list = static_cast<uint64_t>(g.row[p.row]) * g.lists.top;
+        next = first_id(g.lists.ids + list, g.lists.top, static_cast<int32_t>(g.v0 + p.n0));
         if (next < g.lists.top) next_id = g.lists.ids[list + next];
-        if (EPI == kLossGrad) {
-            const RowStat s = g.stat[row];
-            top = s.top;
-            inv = s.inv;
-            gain = g.gain[row];
+    }
+
+    template <int C>
+    __device__ __forceinline__ void chunk(const Place& p, float (&z)[32]) {
+        const uint32_t c0 = 32 * C;
+        const int32_t v = static_cast<int32_t>(g.v0 + p.n0 + c0);
+        if (g.z) {
+            float* to = g.z + (p.row - p.lane) * g.z_pitch + p.n0 + c0;  // rows behind the last are the workspace's too
+            transposed(p, [&](uint32_t j) { return __float_as_uint(z[j]); }, [&](uint32_t r, uint32_t j, uint4 x) {
+                *reinterpret_cast<uint4*>(to + r * g.z_pitch + 4 * j) = x;
+            });
         }
-    }
-
-    __device__ __forceinline__ void chunk(uint32_t c0, float (&z)[32]) {
-        if constexpr (EPI == kLossOut) out(c0, z);
-        else logit(c0, z);
-    }
-
-    __device__ __forceinline__ void logit(uint32_t c0, float (&z)[32]) {
-        const LogitArgs& g = a.logit;
-        const int32_t v = static_cast<int32_t>(g.v0 + n0 + c0);
-        if (c0 + 32 > cols) {
+        if (c0 + 32 > p.cols) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (c0 + j >= cols) z[j] = -kInf;
+                if (c0 + j >= p.cols) z[j] = -kInf;
         }
-        if (EPI == kLossStats) {
-            while (next_id < v + 32) {  // ids end at kNoId, or before the list does
-                const int at = next_id - v;
-                float x = 0.f;
+        while (next_id < v + 32) {  // a list ends at kNoId, or with its places
+            const int at = next_id - v;
+            float x = 0.f;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    if (j == at) x = z[j];
-                g.lists.logits[list + next] = x;
-                step();
-            }
-            float m = top;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) m = fmaxf(m, __fmul_rn(z[j], g.c));
-            const float base = m == -kInf ? 0.f : m;
-            sum = __fmul_rn(sum, exp2_fast(__fsub_rn(top, base)));
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int j = 0; j < 32; ++j) part[j % 4] = __fadd_rn(part[j % 4], exp2_fast(__fmaf_rn(z[j], g.c, -base)));
-            sum = __fadd_rn(sum, __fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])));
-            top = m;
-        } else {
-            if (in) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) z[j] = __fmul_rn(exp2_fast(__fmaf_rn(z[j], g.c, -top)), inv);
-                if (c0 + 32 > cols) {  // a row of NaN leaves the columns behind the last at 0
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c0 + j >= cols) z[j] = 0.f;
-                }
-                while (next_id < v + 32) {
-                    const int at = next_id - v;
-                    const float share = g.lists.shares ? g.lists.shares[list + next] : 1.f;
-                    const float x = __fmul_rn(share, gain);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j == at) z[j] = __fsub_rn(z[j], x);
-                    step();
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) z[j] = 0.f;
-            }
-            if (g.g.planes == 1) {
-                uint4* p = reinterpret_cast<uint4*>(g.g.p + row * g.g.pitch + n0 + c0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    p[j] = make_uint4(pack_bf16x2(z[8 * j], z[8 * j + 1]), pack_bf16x2(z[8 * j + 2], z[8 * j + 3]),
-                                      pack_bf16x2(z[8 * j + 4], z[8 * j + 5]), pack_bf16x2(z[8 * j + 6], z[8 * j + 7]));
-            } else {
-                for (int q = 0; q < g.g.planes; ++q) {
-                    uint4* p = reinterpret_cast<uint4*>(g.g.p + q * g.g.plane + row * g.g.pitch + n0 + c0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t lo = split_plane(z[8 * j + 2 * i]), hi = split_plane(z[8 * j + 2 * i + 1]);
-                            w[i] = lo | (hi << 16);
-                        }
-                        p[j] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-            }
+            for (int j = 0; j < 32; ++j)
+                if (j == at) x = z[j];
+            g.lists.logits[list + next] = x;
+            ++next;
+            next_id = next < g.lists.top ? g.lists.ids[list + next] : kNoId;
         }
+        float m = top;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) m = fmaxf(m, __fmul_rn(z[j], g.c));
+        const float base = m == -kInf ? 0.f : m;
+        sum = __fmul_rn(sum, exp2_fast(__fsub_rn(top, base)));
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 32; ++j) part[j % 4] = __fadd_rn(part[j % 4], exp2_fast(__fmaf_rn(z[j], g.c, -base)));
+        sum = __fadd_rn(sum, __fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])));
+        top = m;
     }
 
-    __device__ __forceinline__ void step() {
-        const Lists& l = a.logit.lists;
-        ++next;
-        next_id = next < l.top ? l.ids[list + next] : kNoId;
-    }
-
-    __device__ __forceinline__ void out(uint32_t c0, float (&z)[32]) {
-        if (!in || c0 >= cols) return;
-        const OutArgs& o = a.out;
-        if (o.parts) {
-            float4* p = reinterpret_cast<float4*>(o.parts + split * o.part_stride + row * o.part_pitch + n0 + c0);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float4 x = make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
-                if (o.add_parts) {
-                    const float4 y = p[j];
-                    x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
-                }
-                p[j] = x;
-            }
-            return;
-        }
-        const uint64_t at = (o.row ? static_cast<uint64_t>(o.row[row]) : row) * o.stride + n0 + c0;
-        if (c0 + 32 <= cols && !o.accumulate) {
-            if (o.bf16) {
-                uint16_t* p = static_cast<uint16_t*>(o.out) + at;
-                if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        reinterpret_cast<uint4*>(p)[j] =
-                            make_uint4(pack_bf16x2(z[8 * j], z[8 * j + 1]), pack_bf16x2(z[8 * j + 2], z[8 * j + 3]),
-                                       pack_bf16x2(z[8 * j + 4], z[8 * j + 5]), pack_bf16x2(z[8 * j + 6], z[8 * j + 7]));
-                    return;
-                }
-            } else {
-                float* p = static_cast<float*>(o.out) + at;
-                if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        reinterpret_cast<float4*>(p)[j] = make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
-                    return;
-                }
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (c0 + j < cols) store_out(o.out, at + j, o.bf16, o.accumulate, z[j]);
-    }
-
-    __device__ __forceinline__ void end(uint32_t nt) {
-        if (EPI == kLossStats && in)
-            a.logit.stats[(a.logit.v0 / kLossTile + nt) * a.logit.stats_pitch + row] = make_float2(top, sum);
+    __device__ __forceinline__ void finish(const Place& p, float (&z)[4][32]) {
+        chunk<0>(p, z[0]);
+        chunk<1>(p, z[1]);
+        chunk<2>(p, z[2]);
+        chunk<3>(p, z[3]);
+        if (p.in && p.cols) g.stats[p.n0 / kStatColumns * g.stats_pitch + p.row] = make_float2(top, sum);
     }
 };
 
-template <int EPI, bool AT, bool BT>
+// Four columns of a row of the caller's matrix.
+__device__ __forceinline__ void store_four(const OutArgs& o, uint64_t at, uint32_t cols, float4 x) {
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    if (cols >= 4 && !o.accumulate) {
+        if (o.bf16) {
+            uint16_t* p = static_cast<uint16_t*>(o.out) + at;
+            if ((reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+                *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+                return;
+            }
+        } else {
+            float* p = static_cast<float*>(o.out) + at;
+            if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+                *reinterpret_cast<float4*>(p) = x;
+                return;
+            }
+        }
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j)
+        if (j < cols) store_out(o.out, at + j, o.bf16, o.accumulate, v[j]);
+}
+
+struct OutTile {
+    const OutArgs& o;
+    uint64_t to = 0;  // this lane's row in the caller's matrix
+
+    __device__ __forceinline__ OutTile(const ProductArgs& a, const Place& p) : o(a.out) {
+        if (p.in) to = (o.row ? static_cast<uint64_t>(o.row[p.row]) : p.row) * o.stride;
+    }
+
+    __device__ __forceinline__ void finish(const Place& p, float (&z)[4][32], float* part) const {
+        if (p.cols == 0) return;
+        const uint32_t rows = __popc(__ballot_sync(kFull, p.in));  // the warp's first ones
+        const uint64_t row0 = p.row - p.lane;
+        float* sum = part ? part : o.sum;
+        const uint64_t pitch = part ? o.part_pitch : o.sum_pitch;
+        if (!sum && !o.add && o.bf16 && !o.accumulate) {
+            // two values a word: 64 columns at a time; off alignment or at the edge by pieces
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                auto word = [&](uint32_t j) {
+                    return pack_bf16x2(z[2 * h + j / 16][2 * j % 32], z[2 * h + j / 16][2 * j % 32 + 1]);
+                };
+                transposed(p, word, [&](uint32_t r, uint32_t j, uint4 x) {
+                    const uint32_t c = 64 * h + 8 * j;
+                    uint16_t* q = static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, r) + p.n0 + c;
+                    if (r >= rows || c >= p.cols) return;
+                    if (c + 8 <= p.cols && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
+                        *reinterpret_cast<uint4*>(q) = x;
+                        return;
+                    }
+                    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (uint32_t i = 0; i < 8; ++i)
+                        if (c + i < p.cols) q[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
+                });
+            }
+            return;
+        }
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            transposed(p, [&](uint32_t j) { return __float_as_uint(z[h][j]); }, [&](uint32_t r, uint32_t j, uint4 bits) {
+                const uint32_t c = 32 * h + 4 * j;
+                const uint64_t at = __shfl_sync(kFull, to, r) + p.n0 + c;
+                if (r >= rows || c >= p.cols) return;
+                float4 x = floats(bits);
+                if (o.add) {
+                    const float4 y = *reinterpret_cast<const float4*>(o.add + (row0 + r) * o.sum_pitch + p.n0 + c);
+                    x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+                }
+                if (sum) *reinterpret_cast<float4*>(sum + (row0 + r) * pitch + p.n0 + c) = x;
+                else store_four(o, at, p.cols - c, x);
+            });
+        }
+    }
+};
+
+template <bool LOGITS, bool AT, bool BT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p) {
     extern __shared__ char raw[];
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;  // the same in both CTAs
-    const uint32_t bars = base + kStages * kStageBytes;
+    const uint32_t staged = base + kStages * kStageBytes, bars = staged + kEpilogueWarps * kStagedBytes;
     auto bar = [bars](uint32_t i) { return bars + 8 * i; };
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, rank = cluster_rank();
     if (threadIdx.x == 0) {
@@ -680,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const uint32_t tmem = lds32(bar(kTmemWord));
     griddep_wait();
     const ProductArgs& a = p.args;
-    const Tiles tiles(p);
+    const Tiles tiles(a, p.m_group);
     const uint64_t first = blockIdx.x / 2, step = gridDim.x / 2;
     uint32_t mt, nt, split, lo, n;
     bool ok = true;
@@ -689,13 +765,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         for (uint64_t t = first; t < tiles.total && ok; t += step) {
             tiles.at(t, mt, nt, split, lo, n);
             const int m0 = static_cast<int>(mt * kSide + rank * kHalf), n0 = static_cast<int>(nt * kSide + rank * kHalf);
-            const uint32_t each = tiles.passes == 1 ? n : n / tiles.passes;
+            uint32_t q = lo / max(1u, tiles.k_blocks), k = lo - q * tiles.k_blocks;
             for (uint32_t i = 0; i < n; ++i, ++it) {
                 const uint32_t s = it % kStages, round = it / kStages;
-                if (round > 0 && !(ok = mbar_wait(bar(kEmptyBar + s), (round - 1) & 1))) break;
-                const uint32_t q = tiles.passes == 1 ? 0 : i / each;
-                const int k0 = static_cast<int>((lo + i - q * each) * kDeep);
-                const int za = tiles.passes == 1 ? 0 : plane_a(q), zb = tiles.passes == 1 ? 0 : plane_b(q);
+                if (round > 0 && !(ok = mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1))) break;
+                const int k0 = static_cast<int>(k * kDeep);
+                const int za = a.a.m.planes == 1 ? 0 : plane_a(q), zb = a.a.m.planes == 1 ? 0 : plane_b(q);
                 const uint32_t to = base + s * kStageBytes, full = in_first(bar(kFullBar + s));
                 if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
                 if (AT) {
@@ -710,68 +785,84 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 } else {
                     tma_load(to + kOperandBytes, &p.b, k0, n0, zb, full);
                 }
+                if (++k == tiles.k_blocks) k = 0, ++q;
             }
         }
         // the last blocks have been read before the pair's memory goes
         for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-            if (!mbar_wait(bar(kEmptyBar + i % kStages), (i / kStages) & 1)) ok = false;
-        if (rank == 1 && !mbar_wait(bar(kDoneBar), 0)) ok = false;
+            if (!mbar_wait_here(bar(kEmptyBar + i % kStages), (i / kStages) & 1)) ok = false;
+        if (rank == 1 && !mbar_wait_here(bar(kDoneBar), 0)) ok = false;
     } else if (warp == 1 && lane == 0 && rank == 0) {
         uint32_t it = 0, done = 0;
         for (uint64_t t = first; t < tiles.total && ok; t += step) {
             tiles.at(t, mt, nt, split, lo, n);
-            if (n == 0) continue;
-            const uint32_t b = done & 1, acc = tmem + b * kSide;
-            if (done >= 2 && !(ok = mbar_wait(bar(kFreeBar + b), (done / 2 - 1) & 1))) break;
-            tmem_fence_after();
-            for (uint32_t i = 0; i < n; ++i, ++it) {
-                const uint32_t s = it % kStages;
-                if (!(ok = mbar_wait(bar(kFullBar + s), (it / kStages) & 1))) break;
+            for (uint32_t i = 0; i < n && ok; ++done) {
+                const uint32_t b = done & 1, acc = tmem + b * kSide;
+                if (done >= 2 && !(ok = mbar_wait_here(bar(kFreeBar + b), (done / 2 - 1) & 1))) break;
                 tmem_fence_after();
-                const uint32_t at = base + s * kStageBytes;
+                const uint32_t end = n - i > a.run ? i + a.run : n;
+                for (uint32_t j = i; j < end; ++j, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!(ok = mbar_wait_here(bar(kFullBar + s), (it / kStages) & 1))) break;
+                    tmem_fence_after();
+                    const uint32_t at = base + s * kStageBytes;
 #pragma unroll
-                for (uint32_t k = 0; k < kDeep / 16; ++k)
-                    mma(acc, operand_desc(at + k * (AT ? 2048 : 32), AT),
-                        operand_desc(at + kOperandBytes + k * (BT ? 2048 : 32), BT), mma_desc(AT, BT), i > 0 || k > 0);
-                mma_commit(bar(kEmptyBar + s));
+                    for (uint32_t k = 0; k < kDeep / 16; ++k)
+                        mma(acc, operand_desc(at + k * (AT ? 2048 : 32), AT),
+                            operand_desc(at + kOperandBytes + k * (BT ? 2048 : 32), BT), mma_desc(AT, BT), j > i || k > 0);
+                    mma_commit(bar(kEmptyBar + s));
+                }
+                if (!ok) break;
+                mma_commit(bar(kReadyBar + b));
+                i = end;
             }
-            if (!ok) break;
-            mma_commit(bar(kReadyBar + b));
-            ++done;
         }
         mma_commit(bar(kDoneBar));
-        if (!mbar_wait(bar(kDoneBar), 0)) ok = false;
+        if (!mbar_wait_here(bar(kDoneBar), 0)) ok = false;
     } else if (warp >= kEpilogueWarp) {
-        const uint32_t quarter = warp % 4;
+        const uint32_t quarter = warp % 4, half = (warp - kEpilogueWarp) / 4;
+        const uint32_t lanes = tmem + ((quarter * 32) << 16) + half * kHalf;
         uint32_t done = 0;
+        Place at;
+        at.staged = staged + (warp - kEpilogueWarp) * kStagedBytes;
+        at.lane = lane;
         for (uint64_t t = first; t < tiles.total; t += step) {
             tiles.at(t, mt, nt, split, lo, n);
-            Epilogue<EPI> e(a, tiles.m, static_cast<uint64_t>(mt) * kSide + rank * kHalf + quarter * 32 + lane, nt, split);
-            const uint32_t b = done & 1;
-            if (n > 0) {
-                ok = mbar_wait(bar(kReadyBar + b), (done / 2) & 1);
-                if (!__all_sync(kFull, ok)) break;
-                tmem_fence_after();
-            }
-            const uint32_t acc = tmem + b * kSide + ((quarter * 32) << 16);
-#pragma unroll 1
-            for (uint32_t c0 = 0; c0 < kSide; c0 += 32) {
-                float z[32];
-                if (n > 0) {
-                    tmem_read32(acc + c0, z);
-                } else {
+            at.row = static_cast<uint64_t>(mt) * kSide + rank * kHalf + quarter * 32 + lane;
+            at.in = at.row < tiles.m;
+            at.n0 = nt * kSide + half * kHalf;
+            at.cols = a.n > at.n0 ? min(static_cast<uint32_t>(kHalf), a.n - at.n0) : 0;
+            std::conditional_t<LOGITS, LogitTile, OutTile> tile(a, at);
+            float z[4][32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) z[j] = 0.f;
+            for (int h = 0; h < 4; ++h)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) z[h][j] = 0.f;
+            for (uint32_t i = 0; i < n;) {
+                const uint32_t b = done & 1;
+                ok = __all_sync(kFull, mbar_wait_here(bar(kReadyBar + b), (done / 2) & 1));
+                if (!ok) break;
+                tmem_fence_after();
+#pragma unroll
+                for (int h = 0; h < 8; ++h) {
+                    float x[16];
+                    tmem_read16(lanes + b * kSide + 16 * h, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        z[h / 2][16 * (h & 1) + j] = __fadd_rn(z[h / 2][16 * (h & 1) + j], x[j]);
                 }
-                e.chunk(c0, z);
-            }
-            e.end(nt);
-            if (n > 0) {
                 tmem_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(in_first(bar(kFreeBar + b)));
                 ++done;
+                i = n - i > a.run ? i + a.run : n;
             }
+            if (!ok) break;
+            if constexpr (LOGITS)
+                tile.finish(at, z);
+            else
+                tile.finish(at, z, tiles.splits > 1 ? a.out.parts + split * (static_cast<uint64_t>(tiles.tall) * kSide * a.out.part_pitch) : nullptr);
         }
     }
     if (!ok) atomicOr(a.status, 1u);
@@ -784,12 +875,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
 }
 
+// A split product's parts, added in their order: four columns a thread.
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ ProductParams p) {
+    griddep_wait();
+    const ProductArgs& a = p.args;
+    const Tiles tiles(a, p.m_group);
+    if (tiles.splits == 1) return;
+    const OutArgs& o = a.out;
+    const uint64_t stride = static_cast<uint64_t>(tiles.tall) * kSide * o.part_pitch;
+    const uint32_t quads = (a.n + 3) / 4;
+    const uint64_t all = static_cast<uint64_t>(tiles.m) * quads;
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < all; i += gridDim.x * 256ull) {
+        const uint64_t r = i / quads;
+        const uint32_t c = 4 * static_cast<uint32_t>(i - r * quads);
+        const float* from = o.parts + r * o.part_pitch + c;
+        float4 x = *reinterpret_cast<const float4*>(from);
+        for (uint32_t s = 1; s < tiles.splits; ++s) {
+            const float4 y = *reinterpret_cast<const float4*>(from + s * stride);
+            x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+        }
+        store_four(o, (o.row ? static_cast<uint64_t>(o.row[r]) : r) * o.stride + c, a.n - c, x);
+    }
+}
+
 using ProductKernel = void (*)(ProductParams);
 
 ProductKernel product_of(const ProductArgs& a) {
-    if (a.epilogue == kLossStats) return product_kernel<kLossStats, false, false>;
-    if (a.epilogue == kLossGrad) return product_kernel<kLossGrad, false, false>;
-    return a.a.turned ? product_kernel<kLossOut, true, true> : product_kernel<kLossOut, false, true>;
+    if (a.logits) return product_kernel<true, false, false>;
+    return a.a.turned ? product_kernel<false, true, true> : product_kernel<false, false, true>;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -866,8 +979,8 @@ cudaError_t launch_record(const RecordArgs& a, cudaStream_t st) {
 }
 
 cudaError_t prepare_products() {
-    for (ProductKernel f : {product_kernel<kLossStats, false, false>, product_kernel<kLossGrad, false, false>,
-                            product_kernel<kLossOut, true, true>, product_kernel<kLossOut, false, true>}) {
+    for (ProductKernel f : {product_kernel<true, false, false>, product_kernel<false, true, true>,
+                            product_kernel<false, false, true>}) {
         const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
         if (e != cudaSuccess) return e;
@@ -875,21 +988,51 @@ cudaError_t prepare_products() {
     return cudaSuccess;
 }
 
+namespace {
+
+uint64_t tiles_of(uint64_t x) { return (x + kSide - 1) / kSide; }
+
+// Rows of tiles worked on side by side: all of them while A's rows stay in L2,
+// then eight.
+uint32_t group_of(const ProductArgs& a) {
+    const uint64_t tall = std::max<uint64_t>(1, tiles_of(a.m));
+    return tall * kSide * a.k * 2 * a.a.m.planes > (64ull << 20) ? 8 : static_cast<uint32_t>(tall);
+}
+
+}  // namespace
+
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t st) {
     ProductParams p;
     p.args = a;
+    p.m_group = group_of(a);
     cudaError_t e = make_map(a.a, &p.a);
     if (e == cudaSuccess) e = make_map(a.b, &p.b);
     if (e != cudaSuccess) return e;
-    const uint64_t tall = (static_cast<uint64_t>(a.m) + kSide - 1) / kSide, wide = (static_cast<uint64_t>(a.n) + kSide - 1) / kSide;
-    p.m_group = static_cast<uint32_t>(std::max<uint64_t>(1, tall));
-    if (tall * kSide * a.k * 2 > (64ull << 20)) p.m_group = 8;
-    const uint64_t pairs = std::min<uint64_t>(std::max<uint64_t>(1, tall * wide * a.splits), kLossSms / 2);
+    const uint64_t most = a.out.parts ? kLossSms / 2 : 1;  // parts of a tile
+    const uint64_t pairs = std::min<uint64_t>(std::max<uint64_t>(1, tiles_of(a.m) * tiles_of(a.n) * most), kLossSms / 2);
     return launch(product_of(a), p, 2 * pairs, kProductThreads, st, kProductSmem);
 }
 
-cudaError_t launch_finish_parts(const FinishArgs& a, cudaStream_t st) {
-    return launch(finish_parts_kernel, a, (a.n + 7) / 8, 256, st);
+cudaError_t launch_finish(const ProductArgs& a, cudaStream_t st) {
+    ProductParams p = {};
+    p.args = a;
+    p.m_group = group_of(a);
+    const uint64_t ctas = (static_cast<uint64_t>(a.m) * ((a.n + 3) / 4) + 255) / 256;
+    return launch(finish_kernel, p, std::min<uint64_t>(std::max<uint64_t>(1, ctas), 8 * kLossSms), 256, st);
+}
+
+cudaError_t launch_grad(const GradArgs& a, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.vocab + kGradColumns - 1) / kGradColumns, std::min((a.n + 63) / 64 * 64, 32768u));
+    cfg.blockDim = dim3(kGradThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = AR_PDL;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[] = {const_cast<GradArgs*>(&a)};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(grad_kernel), args);
 }
 
 }  // namespace ar

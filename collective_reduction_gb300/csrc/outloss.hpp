@@ -12,7 +12,7 @@ namespace ar {
 
 // Rows and columns that the workspace's arrays are padded to, and the columns
 // of one partial softmax statistic.
-constexpr uint32_t kLossTile = 256;
+constexpr uint32_t kLossTile = 256, kStatColumns = 128;
 constexpr int kMaxPlanes = 3;
 constexpr int32_t kNoId = 0x7FFFFFFF;  // behind the last entry of a sorted list
 
@@ -95,18 +95,34 @@ struct RowStat {
     float top, inv;
 };
 
+// The counted tokens at places [base, base + n) are a piece; arrays by place
+// start at the piece's first.
 struct JoinArgs {
-    const float2* stats;  // [tiles][pitch]: largest y, sum 2^(y - largest)
+    const float2* stats;  // [parts][pitch]: largest y, sum 2^(y - largest)
     uint64_t pitch;
-    uint32_t tiles, n;
+    uint32_t parts, base, n;
     float c;              // log2(e) / t
     double t;
     Lists lists;
     Counted rows;
-    RowStat* stat;        // by place
-    float* gain;          // by place: what the shares are multiplied by, factor t
-    float* loss;          // by place
+    RowStat* stat;
+    float* gain;          // what the shares are multiplied by, factor t
+    float* loss;
     float* losses;        // by token; null: none
+};
+
+// The logits' gradient of a piece from its logits, zeros in the rows behind the
+// last up to a block of products.
+struct GradArgs {
+    const float* z;
+    uint64_t pitch;
+    uint32_t base, n, vocab;
+    float c;
+    Lists lists;
+    Counted rows;
+    const RowStat* stat;
+    const float* gain;
+    Planes g;
 };
 
 struct RecordArgs {
@@ -123,27 +139,28 @@ struct Operand {
     uint64_t rows, cols;  // of the array in memory
 };
 
-enum LossEpilogue { kLossStats, kLossGrad, kLossOut };
-
-// Columns [v0, v1) of the logits or of their gradient; columns of a piece
-// start at 0.
+// Logits of a piece: their statistics and, if z is not null, the logits.
 struct LogitArgs {
-    uint32_t v0, v1;
     float c;
+    uint32_t v0;         // the first column's vocabulary entry (stats and z start there)
     Lists lists;
+    const int32_t* row;  // the token at each place
     float2* stats;
     uint64_t stats_pitch;
-    const RowStat* stat;
-    const float* gain;
-    Planes g;
+    float* z;
+    uint64_t z_pitch;
 };
 
-// Where a product goes: parts (float32, one of `splits` each, added to if
-// `add_parts`), or the caller's rows (row i into row[i] if row is not null).
+// Where a product goes: `add` (float32, null: nothing) is added to it, and it is
+// stored in `sum` (float32), or if that is null in the caller's rows (row i into
+// row[i] if row is not null).  Split products go to parts[split] and are finished
+// by launch_finish; they have no add and sum.
 struct OutArgs {
+    const float* add;
+    float* sum;
+    uint64_t sum_pitch;
     float* parts;
-    uint64_t part_stride, part_pitch;
-    int add_parts;
+    uint64_t part_pitch, part_room;  // ..., floats there
     void* out;
     uint64_t stride;
     int bf16;
@@ -153,27 +170,15 @@ struct OutArgs {
 
 struct ProductArgs {
     Operand a, b;
-    uint32_t m, n, k;       // rows of A, rows of B, products of a sum
-    int count_m, count_k;   // m, k: no more than the tokens that count
-    int splits;             // parts of k
+    uint32_t m, n, k;      // rows of A, rows of B, products of a sum
+    int count_m, count_k;  // m, k: no more than the counted tokens behind base
+    uint32_t base;
+    uint32_t run;          // blocks of 64 products that are summed in the tensor cores
     const uint32_t* count;
-    LossEpilogue epilogue;
+    int logits;            // which of the two follows
     LogitArgs logit;
     OutArgs out;
     uint32_t* status;
-};
-
-struct FinishArgs {
-    const float* parts;
-    uint64_t part_stride, part_pitch;
-    int splits;
-    uint32_t n, width;
-    Counted rows;
-    int by_count;  // n: the tokens that count
-    void* out;
-    uint64_t stride;
-    int bf16;
-    int accumulate;
 };
 
 cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st);
@@ -185,6 +190,8 @@ cudaError_t launch_record(const RecordArgs& a, cudaStream_t st);
 // What the products' kernels need once on a device before their first launch.
 cudaError_t prepare_products();
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t st);
-cudaError_t launch_finish_parts(const FinishArgs& a, cudaStream_t st);
+// Adds a split product's parts (nothing where it was not split).
+cudaError_t launch_finish(const ProductArgs& a, cudaStream_t st);
+cudaError_t launch_grad(const GradArgs& a, cudaStream_t st);
 
 }  // namespace ar

@@ -496,7 +496,7 @@ ar_status ar_adamw_step_counted(ar_adamw_t h, const ar_adamw_params* params, uin
  * pages take gradients as given; these calls have no counterpart on them.
  *
  * No n x V array is made: logits and their gradients are worked on in pieces
- * of the vocabulary that fit the handle's workspace.  Both losses are, for a
+ * of the tokens that fit the handle's workspace (losses alone store no logits).  Both losses are, for a
  * token with teacher shares p over a short list of ids at temperature t,
  *   loss = t^2 [ sum_k p_k log p_k - sum_k p_k z_k / t + log sum_v exp(z_v / t) ]
  * whose gradient by z is t (softmax(z / t) - p); cross entropy has one id of
@@ -520,10 +520,10 @@ typedef enum { AR_LOSS_MEAN = 0, AR_LOSS_SUM = 1 } ar_loss_reduction;
 typedef struct {
     uint64_t tokens, hidden, vocab;  /* n at most, D, V                          */
     int top;                         /* entries of a teacher's list at most      */
-    uint64_t piece;                  /* vocabulary entries worked on at a time   */
+    uint64_t piece;                  /* tokens worked on at a time               */
     int pieces;
     uint64_t workspace_bytes;        /* device memory the handle owns            */
-    int tiling_ok;                   /* the pieces tile the vocabulary           */
+    int tiling_ok;                   /* the pieces tile the tokens               */
 } ar_output_loss_info;
 
 /* Host only: the sizes a handle would have (ar_output_loss_create, same
@@ -532,8 +532,9 @@ ar_status ar_output_loss_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab
                                 uint64_t piece, int gradients, ar_output_loss_info* info);
 /* A handle for up to `tokens` tokens of hidden size D over V vocabulary entries,
  * X and W of `dtype`.  top: entries of a teacher's list at most (0: cross entropy
- * alone).  piece: vocabulary entries at a time (rounded up to 256; 0: as many as
- * make 2^28 logits).  gradients: 0 for losses alone, with a small workspace.
+ * alone).  piece: tokens at a time (rounded up to 256; 0: as many as make 2^28
+ * logits, 256 at least): the workspace is mostly 6 bytes for each of their logits
+ * (float32: 10).  gradients: 0 for losses alone, with a small workspace.
  * AR_ERR_INVALID_ARG: null out, D or V of 0, top < 0, unknown types.
  * AR_ERR_UNSUPPORTED: AR_INT32, more than 2^22 tokens, D > 2^16, V > 2^24, top >
  * 1024, more than 2^31 list entries.  AR_ERR_NOMEM, AR_ERR_CUDA. */

@@ -40,20 +40,19 @@ def built():
 
 # ------------------------------------------------------------------ host only
 
-@pytest.mark.parametrize("tokens, vocab, piece", [(0, 1, 0), (1, 255, 0), (1, 256, 0), (7, 257, 256), (300, 1003, 300),
-                                                  (8192, 128000, 0), (1 << 22, 1 << 24, 0), (1 << 20, 1000003, 0)])
-def test_pieces_tile_the_vocabulary(tokens, vocab, piece):
+@pytest.mark.parametrize("tokens, vocab, piece", [(0, 1, 0), (1, 255, 0), (256, 256, 0), (257, 7, 256), (1003, 300, 300),
+                                                  (8192, 128000, 0), (1 << 22, 1 << 20, 0), (1 << 20, 1000003, 0)])
+def test_pieces_tile_the_tokens(tokens, vocab, piece):
     info = ar.output_loss_layout(tokens, 64, vocab, piece=piece)
+    rows, wide = max(256, -(-tokens // 256) * 256), -(-vocab // 256) * 256
     assert info["tiling_ok"] == 1 and info["piece"] % 256 == 0
-    assert info["piece"] * info["pieces"] >= vocab > info["piece"] * (info["pieces"] - 1)
-    rows = max(256, -(-tokens // 256) * 256)
-    if piece:
-        assert info["piece"] <= -(-piece // 256) * 256
-    else:
-        assert info["piece"] <= max(256, (1 << 28) // rows + 255)
-    assert info["workspace_bytes"] >= 2 * rows * info["piece"]
+    assert info["piece"] * info["pieces"] >= rows > info["piece"] * (info["pieces"] - 1)
+    assert info["piece"] <= (-(-piece // 256) * 256 if piece else max(256, (1 << 28) // wide))
+    assert info["workspace_bytes"] >= 6 * info["piece"] * wide
     less = ar.output_loss_layout(tokens, 64, vocab, piece=piece, grads=False)
-    assert less["workspace_bytes"] <= info["workspace_bytes"] - 2 * rows * info["piece"]
+    assert less["pieces"] == 1
+    if info["pieces"] == 1:
+        assert less["workspace_bytes"] <= info["workspace_bytes"] - 6 * info["piece"] * wide
 
 
 def test_layout_refusals():
@@ -218,7 +217,7 @@ def test_cross_entropy(n, d, v, dtype, keep):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-@pytest.mark.parametrize("n, d, v, piece", [(70, 40, 1003, 256), (300, 136, 1500, 512), (5, 1000, 777, 256)])
+@pytest.mark.parametrize("n, d, v, piece", [(700, 40, 303, 256), (1100, 136, 500, 512), (257, 1000, 77, 256)])
 def test_pieces(n, d, v, piece, dtype):
     x, w, g = make(n, d, v, dtype, seed=3)
     t = targets_of(n, v, g, 0.8)
@@ -232,18 +231,18 @@ def test_pieces(n, d, v, piece, dtype):
 @pytest.mark.parametrize("grads", [(), ("hidden",), ("weight",)])
 @pytest.mark.parametrize("piece", [0, 256])
 def test_one_gradient_or_none(grads, piece):
-    x, w, g = make(90, 72, 600, "bfloat16", seed=4)
-    t = targets_of(90, 600, g, 0.7)
-    h = ar.OutputLoss(90, 72, 600, piece=piece, grads=bool(grads))
+    x, w, g = make(390, 72, 600, "bfloat16", seed=4)
+    t = targets_of(390, 600, g, 0.7)
+    h = ar.OutputLoss(390, 72, 600, piece=piece, grads=bool(grads))
     Expected(x, w, *one_hot_lists(t)).check(*run_ce(h, x, w, t, "bfloat16", grads))
 
 
 @gpu
 def test_gradients_in_float32_of_bf16_inputs():
-    x, w, g = make(130, 72, 700, "bfloat16", seed=5)
-    t = targets_of(130, 700, g, 0.9)
+    x, w, g = make(530, 72, 700, "bfloat16", seed=5)
+    t = targets_of(530, 700, g, 0.9)
     for piece in (0, 256):
-        h = ar.OutputLoss(130, 72, 700, piece=piece)
+        h = ar.OutputLoss(530, 72, 700, piece=piece)
         Expected(x, w, *one_hot_lists(t)).check(*run_ce(h, x, w, t, "bfloat16", gtype="float32"))
 
 
@@ -252,9 +251,9 @@ def test_gradients_in_float32_of_bf16_inputs():
 @pytest.mark.parametrize("piece", [0, 256])
 def test_gradients_are_added(gtype, piece):
     import torch
-    x, w, g = make(130, 72, 700, "bfloat16", seed=6)
-    t = targets_of(130, 700, g, 0.5)
-    h = ar.OutputLoss(130, 72, 700, piece=piece)
+    x, w, g = make(630, 72, 300, "bfloat16", seed=6)
+    t = targets_of(630, 300, g, 0.5)
+    h = ar.OutputLoss(630, 72, 300, piece=piece)
     dx = (0.01 * torch.randn(x.shape, generator=g)).to(tdt(gtype)).cuda()
     dw = (0.01 * torch.randn(w.shape, generator=g)).to(tdt(gtype)).cuda()
     x0, w0 = dx.clone(), dw.clone()
@@ -320,7 +319,7 @@ def test_distillation(n, d, v, k, t, dtype, absent):
 def test_entries_of_one_id_add_up(k):
     x, w, g = make(50, 40, 600, "bfloat16", seed=8)
     ids, logits = teacher(50, k, 600, g, "float32", 0.2, twice=True)
-    h = ar.OutputLoss(60, 40, 600, top=80, piece=256)
+    h = ar.OutputLoss(600, 40, 600, top=80, piece=256)
     lists, shares, spread = teacher_lists(ids, logits, 2.0)
     want = Expected(x, w, lists, shares, 2.0, spread=spread, reduction="sum", scale=3.0)
     want.check(*run_distill(h, x, w, ids.int(), logits, "bfloat16", temperature=2.0, reduction="sum", scale=3.0))
@@ -360,12 +359,12 @@ def test_hidden_states_of_tokens_that_do_not_count_are_not_read(n, d, v, dtype):
 @pytest.mark.parametrize("piece", [0, 256])
 def test_nothing_counts(piece):
     import torch
-    x, w, _ = make(65, 40, 600, "bfloat16")
-    h = ar.OutputLoss(65, 40, 600, top=3, piece=piece)
-    rec, losses, dx, dw = run_ce(h, x, w, torch.full((65,), -100), "bfloat16", scale=2.0)
+    x, w, _ = make(265, 40, 600, "bfloat16")
+    h = ar.OutputLoss(265, 40, 600, top=3, piece=piece)
+    rec, losses, dx, dw = run_ce(h, x, w, torch.full((265,), -100), "bfloat16", scale=2.0)
     assert rec.tolist() == [0.0, 0.0, 0.0, 2.0]
     assert all(bool((y == 0).all()) for y in (losses, dx, dw))
-    rec, losses, dx, dw = run_distill(h, x, w, torch.full((65, 3), -1), torch.zeros(65, 3), "bfloat16")
+    rec, losses, dx, dw = run_distill(h, x, w, torch.full((265, 3), -1), torch.zeros(265, 3), "bfloat16")
     assert rec.tolist() == [0.0, 0.0, 0.0, 1.0]
     assert all(bool((y == 0).all()) for y in (losses, dx, dw))
 
@@ -411,9 +410,9 @@ def test_targets_outside_the_vocabulary(dtype):
 @pytest.mark.parametrize("gain", [20.0, 60.0])
 def test_steep_logits(dtype, gain):
     """Logits of tens to hundreds: shares that are 0 or 1 in float32."""
-    x, w, g = make(100, 64, 900, dtype, seed=12, gain=gain)
-    t = targets_of(100, 900, g, 0.9)
-    h = ar.OutputLoss(100, 64, 900, dtype, piece=512)
+    x, w, g = make(300, 64, 900, dtype, seed=12, gain=gain)
+    t = targets_of(300, 900, g, 0.9)
+    h = ar.OutputLoss(300, 64, 900, dtype, piece=256)
     Expected(x, w, *one_hot_lists(t), dtype=dtype).check(*run_ce(h, x, w, t, dtype))
 
 
@@ -463,13 +462,13 @@ def test_strided_rows(d, lead, pad, dtype):
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 def test_fewer_tokens_than_the_handle_is_for(dtype):
     """Stale rows of a larger call before do not show."""
-    x, w, g = make(600, 64, 700, dtype, seed=15)
-    t = targets_of(600, 700, g)
-    h = ar.OutputLoss(600, 64, 700, dtype, top=5, piece=512)
+    x, w, g = make(900, 64, 700, dtype, seed=15)
+    t = targets_of(900, 700, g)
+    h = ar.OutputLoss(900, 64, 700, dtype, top=5, piece=512)
     big = x.clone()
     big[:] = math.nan
     run_ce(h, big, w, t, dtype)
-    for n in (1, 255, 300):
+    for n in (1, 255, 600):
         Expected(x[:n], w, *one_hot_lists(t[:n]), dtype=dtype).check(*run_ce(h, x[:n], w, t[:n], dtype))
         ids, logits = teacher(n, 2, 700, g, "float32")
         lists, shares, spread = teacher_lists(ids, logits, 1.0)
@@ -506,7 +505,7 @@ def test_gradients_against_differences():
 @gpu
 def test_in_a_graph_on_its_stream_with_new_inputs():
     import torch
-    n, d, v = 140, 72, 900
+    n, d, v = 640, 72, 500
     x, w, g = make(n, d, v, "bfloat16", seed=17)
     t = targets_of(n, v, g, 0.8).cuda()
     h = ar.OutputLoss(n, d, v, top=4, piece=512)
