@@ -17,16 +17,22 @@ constexpr uint64_t kMaxTokens = 1ull << 22, kMaxHidden = 1ull << 16, kMaxVocab =
 constexpr int kMaxTop = 1024;
 
 // Logits of a piece of the tokens that the caller leaves to the handle: 1 GB of
-// them and in bf16 0.5 GB of their gradients.
+// them.  Their gradients (2 bytes each in bf16) are kept for up to kPiecesKept
+// pieces before the products with them, whose float32 sums over more than that go
+// through memory: 8192 x 128000 logits of hidden size 4096 in four pieces took
+// 20.7 ms with every piece's product added to a sum in memory.
 constexpr uint64_t kPieceLogits = 1ull << 28;
+constexpr uint64_t kPiecesKept = 4;
 
-// Vocabulary entries that are packed at a time where the weights are not read as they are.
-constexpr uint64_t kPackEntries = 1ull << 15;
+// Bytes of weights that are packed at a time where they are not read as they are.
+constexpr uint64_t kPackBytes = 1ull << 30;
 
 // Blocks of 64 products that are summed in the tensor cores before float32 sums
-// take over: for logits and float32 results, and for bf16 ones (whose rounding
-// is 2^-8).
-constexpr uint32_t kExactRun = 8, kLongRun = 1u << 30;
+// take over: for float32 inputs (six blocks for one) and results, for logits of
+// bf16 inputs, and for bf16 results (whose rounding is 2^-8).  Logits of 4096
+// tokens, hidden size 2048 and 50001 entries: 605 us in runs of 4, 520 of 8, 506
+// of 16, 507 in one.
+constexpr uint32_t kExactRun = 8, kLogitRun = 16, kLongRun = 1u << 30;
 
 ar_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
@@ -43,10 +49,11 @@ uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 struct Layout {
     uint64_t rows = 0, pitch = 0;    // padded tokens, padded D
     uint64_t piece = 0, pieces = 0;  // tokens at a time
+    uint64_t kept = 0;               // tokens whose logits' gradients are kept
     uint64_t pack = 0, part_room = 0, wide = 0, sum_pitch = 0;  // entries packed at a time, floats, padded V, ... D
     int planes = 1, list = 1;
     size_t status = 0, count = 0, factor = 0, row = 0, counted = 0, ids = 0, shares = 0, entropy = 0, logits = 0;
-    size_t stats = 0, stat = 0, gain = 0, loss = 0, hidden = 0, weight = 0, z = 0, grad = 0, part = 0, sum = 0;
+    size_t ticket = 0, sums = 0, bad = 0, stats = 0, stat = 0, gain = 0, hidden = 0, weight = 0, z = 0, grad = 0, part = 0, sum = 0;
     size_t bytes = 0;
     size_t add(uint64_t n) {
         const size_t at = bytes;
@@ -74,10 +81,14 @@ ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype
     l.pieces = (l.rows + piece - 1) / piece;
     l.piece = up((l.rows + l.pieces - 1) / l.pieces, tile);  // as even as whole tiles allow
     l.pieces = (l.rows + l.piece - 1) / l.piece;
-    l.pack = std::min(l.wide, kPackEntries);
+    l.kept = std::min(l.pieces, kPiecesKept) * l.piece;
+    l.pack = std::min(l.wide, std::max(tile, kPackBytes / (2 * l.planes * l.pitch) / tile * tile));
     const uint64_t n = l.rows, k = n * l.list;
     l.status = l.add(4);
     l.count = l.add(4);
+    l.ticket = l.add(4);
+    l.sums = l.add(8 * (n / ar::kJoinRows));
+    l.bad = l.add(4 * (n / ar::kJoinRows));
     l.factor = l.add(4);
     l.row = l.add(4 * n);
     l.counted = l.add(4 * n);
@@ -88,16 +99,16 @@ ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype
     l.stats = l.add(8 * l.piece * (l.wide / ar::kStatColumns));
     l.stat = l.add(8 * n);
     l.gain = l.add(4 * n);
-    l.loss = l.add(4 * n);
     l.hidden = l.add(2 * l.planes * n * l.pitch);
     l.weight = l.add(2 * l.planes * l.pack * l.pitch);
     if (gradients) {
         l.z = l.add(4 * l.piece * l.wide);
-        l.grad = l.add(2 * l.planes * l.piece * l.wide);
-        // four parts of a piece's gradient by the hidden states, a tile for every SM pair of small ones
-        l.part_room = std::max(4 * l.piece * l.sum_pitch, ar::kLossSms / 2 * tile * l.sum_pitch);
+        l.grad = l.add(2 * l.planes * l.kept * l.wide);
+        // the kept tokens' gradient once (packed weights are summed up there), and several
+        // parts for each pair of SMs
+        l.part_room = std::max(l.kept * l.sum_pitch, 8 * ar::kLossSms / 2 * tile * tile);
         l.part = l.add(4 * l.part_room);
-        if (l.pieces > 1) l.sum = l.add(4 * std::max(l.wide, l.piece) * l.sum_pitch);
+        if (l.kept < l.rows) l.sum = l.add(4 * l.wide * l.sum_pitch);
     }
     return AR_OK;
 }
@@ -162,7 +173,7 @@ struct Call {
     const ar_output_loss_args* a;
     cudaStream_t st;
     uint32_t n, width, vocab;
-    bool grads;
+    bool grads, packed = false;
     float c = 0.f;
     double t = 1.0;
     ar::Lists lists = {};
@@ -182,12 +193,12 @@ struct Call {
         rows.factor = h->at<float>(h->l.factor);
     }
 
-    // Places [r, ...) of the counted tokens' hidden states.
+    // Places [r, ...) of the counted tokens' hidden states; of the kept logits' gradients.
     ar::Planes hidden(uint64_t r) const {
         return {h->at<uint16_t>(h->l.hidden) + r * h->l.pitch, h->l.rows * h->l.pitch, h->l.pitch, h->l.planes};
     }
-    ar::Planes grad() const {
-        return {h->at<uint16_t>(h->l.grad), h->l.piece * h->l.wide, h->l.wide, h->l.planes};
+    ar::Planes grad(uint64_t r) const {
+        return {h->at<uint16_t>(h->l.grad) + r % h->l.kept * h->l.wide, h->l.kept * h->l.wide, h->l.wide, h->l.planes};
     }
     // TMA reads rows that start on 16-byte boundaries
     bool weight_as_is() const {
@@ -196,6 +207,7 @@ struct Call {
     }
     // Vocabulary entries that are at hand at a time, [v0, v1) as planes: where they are, or packed.
     uint64_t entries() const { return weight_as_is() ? h->vocab : h->l.pack; }
+    // All of them stay packed for the call.
     ar::Planes weight(uint64_t v0, uint64_t v1) {
         const char* from = static_cast<const char*>(a->weight) + v0 * a->weight_stride * esize(h->dtype);
         if (weight_as_is()) return {reinterpret_cast<uint16_t*>(const_cast<char*>(from)), 0, a->weight_stride, 1};
@@ -206,7 +218,8 @@ struct Call {
         p.n = static_cast<uint32_t>(v1 - v0);
         p.width = width;
         p.out = {h->at<uint16_t>(h->l.weight), h->l.pack * h->l.pitch, h->l.pitch, h->l.planes};
-        run(ar::launch_pack(p, st));
+        if (!packed) run(ar::launch_pack(p, st));
+        packed = v0 == 0 && v1 == h->vocab;
         return p.out;
     }
     void run(cudaError_t next) {
@@ -218,6 +231,7 @@ struct Call {
         ar::ProductArgs p = {};
         p.count = rows.count;
         p.base = static_cast<uint32_t>(r);
+        p.splits = 1;
         p.status = h->at<uint32_t>(h->l.status);
         return p;
     }
@@ -232,7 +246,7 @@ struct Call {
             p.count_m = 1;
             p.n = static_cast<uint32_t>(end - v);
             p.k = width;
-            p.run = kExactRun;
+            p.run = h->dtype == AR_BFLOAT16 ? kLogitRun : kExactRun;
             p.logits = 1;
             p.logit.c = c;
             p.logit.v0 = static_cast<uint32_t>(v);
@@ -251,13 +265,18 @@ struct Call {
         j.base = static_cast<uint32_t>(r);
         j.n = m;
         j.c = c;
-        j.t = t;
+        j.t = static_cast<float>(t);
+        j.t2 = static_cast<float>(t * t);
         j.lists = lists;
         j.rows = rows;
         j.stat = h->at<ar::RowStat>(h->l.stat) + r;
         j.gain = h->at<float>(h->l.gain) + r;
-        j.loss = h->at<float>(h->l.loss) + r;
         j.losses = a->losses;
+        j.sums = h->at<double>(h->l.sums);
+        j.bad = h->at<uint32_t>(h->l.bad);
+        j.ticket = h->at<uint32_t>(h->l.ticket);
+        j.tickets = (n + ar::kJoinRows - 1) / ar::kJoinRows;
+        j.result = a->result;
         run(ar::launch_join(j, st));
     }
 
@@ -273,14 +292,14 @@ struct Call {
         g.rows = rows;
         g.stat = h->at<ar::RowStat>(h->l.stat) + r;
         g.gain = h->at<float>(h->l.gain) + r;
-        g.g = grad();
+        g.g = grad(r);
         run(ar::launch_grad(g, st));
     }
 
     // The last piece's product goes to the caller, with the sum of those before.
     void grad_weight(uint64_t r, uint32_t m, bool last) {
         ar::ProductArgs p = product(r);
-        p.a = {grad(), true, m, h->vocab};
+        p.a = {grad(r), true, m, h->vocab};
         p.b = {hidden(r), true, m, h->hidden};
         p.m = vocab;
         p.n = width;
@@ -292,19 +311,19 @@ struct Call {
         p.out.bf16 = a->grad_weight_dtype == AR_BFLOAT16;
         p.out.accumulate = a->accumulate;
         p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
-        p.out.part_room = h->l.part_room;
         if (r > 0) p.out.add = h->at<float>(h->l.sum);
         if (!last) p.out.sum = h->at<float>(h->l.sum);
-        if (r == 0 && last) p.out.parts = h->at<float>(h->l.part);
+        if (r == 0 && last) p.splits = ar::splits_of(vocab, width, m, h->l.planes, h->l.part_room);
+        p.out.parts = h->at<float>(h->l.part);
         run(ar::launch_product(p, st));
-        if (p.out.parts) run(ar::launch_finish(p, st));
+        if (p.splits > 1) run(ar::launch_finish(p, st));
     }
 
     void grad_hidden(uint64_t r, uint32_t m) {
         for (uint64_t v = 0; v < h->vocab; v += entries()) {
             const uint64_t end = std::min(h->vocab, v + entries());
             ar::ProductArgs p = product(r);
-            ar::Planes g = grad();
+            ar::Planes g = grad(r);
             g.p += v;
             p.a = {g, false, m, end - v};
             p.b = {weight(v, end), true, end - v, h->hidden};
@@ -319,14 +338,13 @@ struct Call {
             p.out.accumulate = a->accumulate;
             p.out.row = rows.row + r;
             p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
-            p.out.part_room = h->l.part_room;
-            const bool whole = v == 0 && end == h->vocab;
-            if (whole) p.out.parts = h->at<float>(h->l.part);
+            p.out.parts = h->at<float>(h->l.part);
+            if (v == 0 && end == h->vocab) p.splits = ar::splits_of(m, width, vocab, h->l.planes, h->l.part_room);
             // entries packed at a time: sums in the parts' memory
             if (v > 0) p.out.add = h->at<float>(h->l.part);
             if (end < h->vocab) p.out.sum = h->at<float>(h->l.part);
             run(ar::launch_product(p, st));
-            if (whole) run(ar::launch_finish(p, st));
+            if (p.splits > 1) run(ar::launch_finish(p, st));
         }
     }
 
@@ -341,11 +359,10 @@ struct Call {
         r.mean = a->reduction == AR_LOSS_MEAN;
         r.lists = lists;
         r.rows = rows;
+        r.result = a->result;
+        r.ticket = h->at<uint32_t>(h->l.ticket);
         run(ar::launch_rows(r, st));
         if (n > 0) {
-            ar::ClearArgs z = {lists.counted, n, width, a->losses, a->accumulate ? nullptr : a->grad_hidden,
-                               a->grad_hidden_stride, a->grad_hidden_dtype == AR_BFLOAT16};
-            if (z.losses || z.grad_hidden) run(ar::launch_clear(z, st));
             ar::PackArgs p = {};
             p.src = a->hidden;
             p.stride = a->hidden_stride;
@@ -354,17 +371,23 @@ struct Call {
             p.width = width;
             p.rows = rows;
             p.out = hidden(0);
+            p.counted = lists.counted;
+            p.losses = a->losses;
+            p.grad = a->accumulate ? nullptr : a->grad_hidden;
+            p.grad_stride = a->grad_hidden_stride;
+            p.grad_bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
             run(ar::launch_pack(p, st));
         }
-        for (uint64_t at = 0; at < n || at == 0; at += h->l.piece) {
-            const uint32_t m = static_cast<uint32_t>(std::min<uint64_t>(n - at, h->l.piece));
-            const bool last = at + h->l.piece >= n;
-            if (m > 0) logits(at, m);
-            if (m > 0 && grads) grad_logits(at, m);
-            if (a->grad_weight) grad_weight(at, m, last);
-            if (m > 0 && a->grad_hidden) grad_hidden(at, m);
+        for (uint64_t first = 0; first < n || first == 0; first += h->l.kept) {
+            const uint32_t all = static_cast<uint32_t>(std::min<uint64_t>(n - first, h->l.kept));
+            for (uint64_t at = first; at < first + all; at += h->l.piece) {
+                const uint32_t m = static_cast<uint32_t>(std::min<uint64_t>(first + all - at, h->l.piece));
+                logits(at, m);
+                if (grads) grad_logits(at, m);
+            }
+            if (a->grad_weight) grad_weight(first, all, first + h->l.kept >= n);
+            if (all > 0 && a->grad_hidden) grad_hidden(first, all);
         }
-        run(ar::launch_record({h->at<float>(h->l.loss), rows, a->result}, st));
         return cuda_status(e);
     }
 };
@@ -431,7 +454,7 @@ ar_status ar_output_loss_create(uint64_t tokens, uint64_t hidden, uint64_t vocab
     if (e == cudaSuccess) e = ar::prepare_products();
     if (e == cudaSuccess) e = cudaMalloc(&h->dev, l.bytes);
     // in place on return: the calls may run on streams that do not wait for this one
-    if (e == cudaSuccess) e = cudaMemset(h->dev, 0, l.row);
+    if (e == cudaSuccess) e = cudaMemset(h->dev, 0, l.sums);
     if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
     if (e != cudaSuccess) {
         delete h;

@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const __gri
     const uint32_t i = blockIdx.x * kTeacherWarps + warp;
     int32_t* id = reinterpret_cast<int32_t*>(smem) + warp * 2 * a.k;
     float* share = reinterpret_cast<float*>(id + a.k);
+    griddep_launch_dependents();
     griddep_wait();
     if (i >= a.n) return;
     bool bad = false;
@@ -143,35 +144,34 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const __gri
 constexpr int kRowThreads = 1024;
 
 // One CTA: targets into lists of one id, and the tokens that count in their
-// order; every thread has a run of tokens.
+// order; every warp has a run of tokens, 32 at a time.
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowsArgs a) {
     __shared__ uint32_t sums[32];
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const uint32_t run = (a.n + kRowThreads - 1) / kRowThreads;
-    const uint32_t lo = min(a.n, tid * run), hi = min(a.n, lo + run);
+    const uint32_t run = (a.n + kRowThreads - 1) / kRowThreads * 32;
+    const uint32_t lo = min(a.n, warp * run), hi = min(a.n, lo + run);
+    griddep_launch_dependents();
     griddep_wait();
     uint32_t mine = 0;
-    for (uint32_t i = lo; i < hi; ++i) {
-        uint32_t counts = 0;
-        if (a.targets) {
-            const int64_t v = a.target_bytes == 8 ? static_cast<const int64_t*>(a.targets)[i]
-                                                  : static_cast<const int32_t*>(a.targets)[i];
-            counts = v != a.ignore;
-            const bool in = v >= 0 && v < a.vocab;
-            a.lists.ids[static_cast<uint64_t>(i) * a.lists.top] = counts && in ? static_cast<int32_t>(v) : kNoId;
-            a.lists.entropy[i] = counts && !in ? __int_as_float(0x7FC00000) : 0.f;
-            a.lists.counted[i] = counts;
-        } else {
-            counts = a.lists.counted[i];
+#pragma unroll 4
+    for (uint32_t i = lo + lane; i - lane < hi; i += 32) {
+        bool counts = false;
+        if (i < hi) {
+            if (a.targets) {
+                const int64_t v = a.target_bytes == 8 ? static_cast<const int64_t*>(a.targets)[i]
+                                                      : static_cast<const int32_t*>(a.targets)[i];
+                counts = v != a.ignore;
+                const bool in = v >= 0 && v < a.vocab;
+                a.lists.ids[static_cast<uint64_t>(i) * a.lists.top] = counts && in ? static_cast<int32_t>(v) : kNoId;
+                a.lists.entropy[i] = counts && !in ? __int_as_float(0x7FC00000) : 0.f;
+                a.lists.counted[i] = counts;
+            } else {
+                counts = a.lists.counted[i];
+            }
         }
-        mine += counts;
+        mine += __popc(__ballot_sync(kFull, counts));
     }
-    uint32_t before = mine;
-    for (int o = 1; o < 32; o *= 2) {
-        const uint32_t x = __shfl_up_sync(kFull, before, o);
-        if (lane >= static_cast<uint32_t>(o)) before += x;
-    }
-    if (lane == 31) sums[warp] = before;
+    if (lane == 0) sums[warp] = mine;
     __syncthreads();
     if (warp == 0) {
         uint32_t s = sums[lane];
@@ -182,42 +182,95 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         sums[lane] = s;
     }
     __syncthreads();
-    uint32_t place = before - mine + (warp ? sums[warp - 1] : 0);
-    for (uint32_t i = lo; i < hi; ++i)
-        if (a.lists.counted[i]) a.rows.row[place++] = static_cast<int32_t>(i);
+    uint32_t place = warp ? sums[warp - 1] : 0;
+#pragma unroll 4
+    for (uint32_t i = lo + lane; i - lane < hi; i += 32) {
+        const bool counts = i < hi && a.lists.counted[i];
+        const uint32_t who = __ballot_sync(kFull, counts);
+        if (counts) a.rows.row[place + __popc(who & ((1u << lane) - 1))] = static_cast<int32_t>(i);
+        place += __popc(who);
+    }
     if (tid == 0) {
         const uint32_t n = sums[31];
+        const float factor = static_cast<float>(a.mean ? a.scale / (n ? n : 1u) : a.scale);
         *a.rows.count = n;
-        *a.rows.factor = static_cast<float>(a.mean ? a.scale / (n ? n : 1u) : a.scale);
+        *a.rows.factor = factor;
+        *a.ticket = 0;
+        if (n == 0) {
+            a.result[0] = a.result[1] = a.result[2] = 0.f;
+            a.result[3] = factor;
+        }
     }
 }
 
-// A warp a row, over the rows up to a tile's end.
+// Eight values of a row of src, zeros behind its width.
+__device__ __forceinline__ void load_eight(const PackArgs& a, uint64_t from, uint32_t c, float (&x)[8]) {
+    if (a.bf16) {
+        const uint16_t* p = static_cast<const uint16_t*>(a.src) + from + c;
+        if (c + 8 <= a.width && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
+            x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
+            return;
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) x[j] = c + j < a.width ? bf16_value(p[j]) : 0.f;
+        return;
+    }
+    const float* p = static_cast<const float*>(a.src) + from + c;
+    if (c + 8 <= a.width && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const float4 u = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + 4);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+        return;
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) x[j] = c + j < a.width ? p[j] : 0.f;
+}
+
+// Eight values' next plane.
+__device__ __forceinline__ uint4 split_eight(float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t low = split_plane(x[2 * i]), high = split_plane(x[2 * i + 1]);
+        w[i] = low | (high << 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 pack_eight(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+// A warp a row (and a token), over the rows up to a tile's end.
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
     const uint32_t lane = threadIdx.x % 32;
     const uint64_t r = blockIdx.x * 8ull + threadIdx.x / 32;
+    griddep_launch_dependents();
     griddep_wait();
+    if (a.counted && r < a.n && !a.counted[r]) {
+        if (a.losses && lane == 0) a.losses[r] = 0.f;
+        if (a.grad)
+            for (uint32_t c = lane; c < a.width; c += 32) {
+                if (a.grad_bf16) static_cast<uint16_t*>(a.grad)[r * a.grad_stride + c] = 0;
+                else static_cast<float*>(a.grad)[r * a.grad_stride + c] = 0.f;
+            }
+    }
     const uint32_t n = a.rows.row ? *a.rows.count : a.n;
     if (r >= (static_cast<uint64_t>(n) + kLossTile - 1) / kLossTile * kLossTile) return;
     const bool there = r < n;
     const uint64_t from = there ? (a.rows.row ? static_cast<uint64_t>(a.rows.row[r]) : r) * a.stride : 0;
-    for (uint64_t c = lane; c < a.out.pitch; c += 32) {
-        float x = there && c < a.width ? load_value(a.src, from + c, a.bf16) : 0.f;
-        for (int q = 0; q < a.out.planes; ++q) a.out.p[q * a.out.plane + r * a.out.pitch + c] = split_plane(x);
-    }
-}
-
-__global__ void __launch_bounds__(256) clear_kernel(const __grid_constant__ ClearArgs a) {
-    const uint32_t lane = threadIdx.x % 32;
-    const uint64_t i = blockIdx.x * 8ull + threadIdx.x / 32;
-    griddep_wait();
-    if (i >= a.n || a.counted[i]) return;
-    if (a.losses && lane == 0) a.losses[i] = 0.f;
-    if (a.grad_hidden)
-        for (uint32_t c = lane; c < a.width; c += 32) {
-            if (a.bf16) static_cast<uint16_t*>(a.grad_hidden)[i * a.stride + c] = 0;
-            else static_cast<float*>(a.grad_hidden)[i * a.stride + c] = 0.f;
+    uint16_t* out = a.out.p + r * a.out.pitch;
+#pragma unroll 2
+    for (uint32_t c = 8 * lane; c < a.out.pitch; c += 256) {
+        float x[8] = {};
+        if (there) load_eight(a, from, c, x);
+        if (a.out.planes == 1) {
+            *reinterpret_cast<uint4*>(out + c) = pack_eight(x);
+        } else {
+            for (int q = 0; q < a.out.planes; ++q) *reinterpret_cast<uint4*>(out + q * a.out.plane + c) = split_eight(x);
         }
+    }
 }
 
 // ------------------------------------------------------------------- joins
@@ -233,72 +286,112 @@ __device__ __forceinline__ void join_stat(float& top, float& sum, float top2, fl
     sum = __fadd_rn(a, b);
 }
 
-// A warp a place: the parts' statistics in a fixed order, the loss.
+// 32 places a CTA: a lane a place over the parts of each warp, then eight lanes a
+// place for the parts' join and the list.  With y = z c and shares that add up to 1
+//   log sum exp(z / t) - sum p z / t = ln 2 (log2 sum 2^(y - top) + sum p (top - y)),
+// whose terms do not cancel, so float32 does.  Every sum has a fixed order; the
+// call's last CTA adds up the CTAs' and writes the record.
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
-    const uint32_t lane = threadIdx.x % 32;
-    const uint32_t r = blockIdx.x * 8 + threadIdx.x / 32;
+    __shared__ float2 part[8][kJoinRows];
+    __shared__ float losses[kJoinRows];
+    __shared__ uint32_t flag[8];
+    __shared__ double total[8];
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const uint32_t r0 = blockIdx.x * kJoinRows;
+    griddep_launch_dependents();
     griddep_wait();
-    if (r >= a.n || a.base + r >= *a.rows.count) return;
-    const uint64_t i = a.rows.row[a.base + r];
+    const uint32_t count = *a.rows.count, m = count > a.base ? min(a.n, count - a.base) : 0;
+    const float factor = *a.rows.factor;
     float top = -kInf, sum = 0.f;
-    for (uint32_t q = lane; q < a.parts; q += 32) {
-        const float2 s = a.stats[q * a.pitch + r];
-        join_stat(top, sum, s.x, s.y);
+    if (r0 + lane < m) {
+        const float2* at = a.stats + r0 + lane;
+#pragma unroll 8
+        for (uint32_t q = warp; q < a.parts; q += 8) {
+            const float2 s = at[q * a.pitch];
+            join_stat(top, sum, s.x, s.y);
+        }
     }
-    for (int o = 16; o > 0; o /= 2) {
-        const float t2 = __shfl_down_sync(kFull, top, o), s2 = __shfl_down_sync(kFull, sum, o);
-        join_stat(top, sum, t2, s2);
+    part[warp][lane] = make_float2(top, sum);
+    __syncthreads();
+    const uint32_t row = tid / 8, eighth = tid % 8, r = r0 + row;
+    const bool in = r < m;
+    const float2 s = part[eighth][row];
+    top = s.x;
+    sum = s.y;
+    for (int o = 4; o > 0; o /= 2) {  // alike in all eight lanes: each step's operands in the lower lane's order
+        const float t2 = __shfl_xor_sync(kFull, top, o), s2 = __shfl_xor_sync(kFull, sum, o);
+        if (eighth & o) {
+            float t1 = t2, s1 = s2;
+            join_stat(t1, s1, top, sum);
+            top = t1, sum = s1;
+        } else {
+            join_stat(top, sum, t2, s2);
+        }
     }
-    double dot = 0.0;  // sum p z
-    const uint64_t at = i * a.lists.top;
-    for (int k = lane; k < a.lists.top; k += 32) {
-        if (a.lists.ids[at + k] == kNoId) continue;
-        dot += (a.lists.shares ? static_cast<double>(a.lists.shares[at + k]) : 1.0) * a.lists.logits[at + k];
+    const uint64_t i = in ? a.rows.row[a.base + r] : 0, at = i * a.lists.top;
+    float dot = 0.f;  // sum p (top - y)
+    for (int j = eighth; in && j < a.lists.top; j += 8) {
+        if (a.lists.ids[at + j] == kNoId) break;  // nothing behind it
+        const float d = -__fmaf_rn(a.lists.logits[at + j], a.c, -top);
+        dot = a.lists.shares ? __fmaf_rn(a.lists.shares[at + j], d, dot) : d;
     }
-    for (int o = 16; o > 0; o /= 2) dot += __shfl_down_sync(kFull, dot, o);
-    if (lane != 0) return;
-    const double lse = (static_cast<double>(top) + log2(static_cast<double>(sum))) * kLn2;
-    const float loss = static_cast<float>(a.t * a.t * (static_cast<double>(a.lists.entropy[i]) - dot / a.t + lse));
-    const float f = loss == loss ? static_cast<float>(*a.rows.factor * a.t) : loss;  // NaN: the whole row
-    a.loss[r] = loss;
-    a.gain[r] = f;
-    a.stat[r] = {top, __fdiv_rn(f, sum)};
-    if (a.losses) a.losses[i] = loss;
-}
-
-constexpr int kRecordThreads = 1024;
-
-__global__ void __launch_bounds__(kRecordThreads) record_kernel(const __grid_constant__ RecordArgs a) {
-    __shared__ double sums[32];
-    __shared__ uint32_t bads[32];
-    const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    griddep_wait();
-    const uint32_t n = *a.rows.count;
-    double sum = 0.0;
+    for (int o = 4; o > 0; o /= 2) dot = __fadd_rn(dot, __shfl_xor_sync(kFull, dot, o));
     bool bad = false;
-    for (uint32_t r = threadIdx.x; r < n; r += kRecordThreads) {
-        const float x = a.loss[r];
-        bad = bad || !(fabsf(x) < kInf);
-        sum += x;
+    if (eighth == 0) {
+        float loss = 0.f;
+        if (in) {
+            loss = __fmul_rn(a.t2, __fmaf_rn(static_cast<float>(kLn2), __fadd_rn(log2f(sum), dot), a.lists.entropy[i]));
+            const float f = loss == loss ? __fmul_rn(factor, a.t) : loss;  // NaN: the whole row
+            a.gain[r] = f;
+            a.stat[r] = {top, __fdiv_rn(f, sum)};
+            if (a.losses) a.losses[i] = loss;
+            bad = !(fabsf(loss) < kInf);
+        }
+        losses[row] = loss;
     }
     bad = __any_sync(kFull, bad);
-    for (int o = 16; o > 0; o /= 2) sum += __shfl_down_sync(kFull, sum, o);
-    if (lane == 0) {
-        sums[warp] = sum;
-        bads[warp] = bad;
+    if (lane == 0) flag[warp] = bad;
+    __syncthreads();
+    if (warp == 0) {
+        float x = losses[lane];
+        for (int o = 16; o > 0; o /= 2) x = __fadd_rn(x, __shfl_down_sync(kFull, x, o));
+        const uint32_t any = __any_sync(kFull, lane < 8 && flag[lane % 8]);
+        if (lane == 0) {
+            const uint32_t cta = a.base / kJoinRows + blockIdx.x;
+            a.sums[cta] = x;
+            a.bad[cta] = any;
+            __threadfence();
+            flag[0] = atomicAdd(a.ticket, 1u) == a.tickets - 1;
+        }
     }
     __syncthreads();
-    if (threadIdx.x != 0) return;
-    uint32_t any = 0;
-    sum = 0.0;
-    for (int w = 0; w < 32; ++w) {
-        sum += sums[w];
-        any |= bads[w];
+    if (!flag[0] || count == 0) return;
+    __threadfence();
+    double all = 0.0;
+    bad = false;
+    for (uint32_t k = tid; k < (count + kJoinRows - 1) / kJoinRows; k += 256) {
+        all += __ldcg(a.sums + k);
+        bad = bad || __ldcg(a.bad + k);
     }
-    a.result[0] = static_cast<float>(sum * *a.rows.factor);
-    a.result[1] = static_cast<float>(n);
+    for (int o = 16; o > 0; o /= 2) all += __shfl_down_sync(kFull, all, o);
+    bad = __any_sync(kFull, bad);
+    __syncthreads();
+    if (lane == 0) {
+        total[warp] = all;
+        flag[warp] = bad;
+    }
+    __syncthreads();
+    if (tid != 0) return;
+    all = 0.0;
+    uint32_t any = 0;
+    for (int w = 0; w < 8; ++w) {
+        all += total[w];
+        any |= flag[w];
+    }
+    a.result[0] = static_cast<float>(all * factor);
+    a.result[1] = static_cast<float>(count);
     a.result[2] = any ? 1.f : 0.f;
-    a.result[3] = *a.rows.factor;
+    a.result[3] = factor;
 }
 
 __device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int accumulate, float x) {
@@ -314,6 +407,7 @@ constexpr int kGradThreads = 256, kGradColumns = 8192;  // of a CTA: one row's
 __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ GradArgs a) {
     const uint32_t tid = threadIdx.x;
     const uint32_t lo = blockIdx.x * kGradColumns, hi = min(a.vocab, lo + kGradColumns);
+    griddep_launch_dependents();
     griddep_wait();
     const uint32_t count = *a.rows.count, m = count > a.base ? min(a.n, count - a.base) : 0;
     for (uint64_t r = blockIdx.y; r < (m + 63) / 64 * 64; r += gridDim.y) {
@@ -329,18 +423,10 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
                 x[0] = value(p.x), x[1] = value(p.y), x[2] = value(p.z), x[3] = value(p.w);
                 x[4] = value(q.x), x[5] = value(q.y), x[6] = value(q.z), x[7] = value(q.w);
             }
-            for (int q = 0; q < a.g.planes; ++q) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (a.g.planes == 1) {
-                        w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-                    } else {
-                        const uint32_t low = split_plane(x[2 * i]), high = split_plane(x[2 * i + 1]);
-                        w[i] = low | (high << 16);
-                    }
-                }
-                *reinterpret_cast<uint4*>(g + q * a.g.plane + v) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (a.g.planes == 1) {
+                *reinterpret_cast<uint4*>(g + v) = pack_eight(x);
+            } else {
+                for (int q = 0; q < a.g.planes; ++q) *reinterpret_cast<uint4*>(g + q * a.g.plane + v) = split_eight(x);
             }
         }
         if (!in) continue;  // the whole CTA
@@ -496,27 +582,9 @@ struct Tiles {
         tall = (m + kSide - 1) / kSide;
         wide = (a.n + kSide - 1) / kSide;
         group = m_group;
-        splits = 1;
-        if (a.out.parts) {
-            const uint64_t rows = static_cast<uint64_t>(tall) * kSide;
-            choose(rows ? static_cast<uint32_t>(min(static_cast<uint64_t>(blocks / 4), a.out.part_room / (rows * a.out.part_pitch))) : 1);
-        }
+        splits = a.splits;
         per = (blocks + splits - 1) / splits;
         total = static_cast<uint64_t>(tall) * wide * splits;
-    }
-    // How many parts of k: what the fullest pair of SMs has to do, in blocks, with
-    // what the parts cost (about 8 blocks' time for their launch and 1 for 4 parts).
-    __device__ void choose(uint32_t most) {
-        const uint32_t pairs = kLossSms / 2, tiles = tall * wide;
-        if (tiles == 0 || tiles >= 8 * pairs) return;
-        uint32_t best = (tiles + pairs - 1) / pairs * blocks;
-        auto look = [&](uint32_t s) {
-            if (s < 2 || s > most) return;
-            const uint32_t cost = (tiles * s + pairs - 1) / pairs * ((blocks + s - 1) / s) + 8 + tiles * s / 4;
-            if (cost < best) best = cost, splits = s;
-        };
-        for (uint32_t s = 2; s <= 8; ++s) look(s);
-        if (pairs / tiles > 8) look(min(most, pairs / tiles));
     }
     // Tile t: in each split, groups of `group` rows of tiles, column by column.
     __device__ void at(uint64_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
@@ -567,7 +635,7 @@ __device__ __forceinline__ void transposed(const Place& p, Word word, Use use) {
         sts128(p.staged + p.lane * 128 + ((j ^ (p.lane & 7)) << 4),
                make_uint4(word(4 * j), word(4 * j + 1), word(4 * j + 2), word(4 * j + 3)));
     __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
     for (uint32_t i = 0; i < 8; ++i) {
         const uint32_t r = 4 * i + p.lane / 8, j = p.lane % 8;
         use(r, j, lds128(p.staged + r * 128 + ((j ^ (r & 7)) << 4)));
@@ -728,6 +796,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;  // the same in both CTAs
     const uint32_t staged = base + kStages * kStageBytes, bars = staged + kEpilogueWarps * kStagedBytes;
     auto bar = [bars](uint32_t i) { return bars + 8 * i; };
+    griddep_launch_dependents();
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32, rank = cluster_rank();
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < kStages; ++s) {
@@ -877,10 +946,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 
 // A split product's parts, added in their order: four columns a thread.
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ ProductParams p) {
+    griddep_launch_dependents();
     griddep_wait();
     const ProductArgs& a = p.args;
     const Tiles tiles(a, p.m_group);
-    if (tiles.splits == 1) return;
     const OutArgs& o = a.out;
     const uint64_t stride = static_cast<uint64_t>(tiles.tall) * kSide * o.part_pitch;
     const uint32_t quads = (a.n + 3) / 4;
@@ -890,6 +959,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Pro
         const uint32_t c = 4 * static_cast<uint32_t>(i - r * quads);
         const float* from = o.parts + r * o.part_pitch + c;
         float4 x = *reinterpret_cast<const float4*>(from);
+#pragma unroll 8
         for (uint32_t s = 1; s < tiles.splits; ++s) {
             const float4 y = *reinterpret_cast<const float4*>(from + s * stride);
             x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
@@ -970,12 +1040,8 @@ cudaError_t launch_pack(const PackArgs& a, cudaStream_t st) {
     return launch(pack_kernel, a, (a.n + kLossTile - 1) / kLossTile * (kLossTile / 8), 256, st);
 }
 
-cudaError_t launch_clear(const ClearArgs& a, cudaStream_t st) { return launch(clear_kernel, a, (a.n + 7) / 8, 256, st); }
-
-cudaError_t launch_join(const JoinArgs& a, cudaStream_t st) { return launch(join_kernel, a, (a.n + 7) / 8, 256, st); }
-
-cudaError_t launch_record(const RecordArgs& a, cudaStream_t st) {
-    return launch(record_kernel, a, 1, kRecordThreads, st);
+cudaError_t launch_join(const JoinArgs& a, cudaStream_t st) {
+    return launch(join_kernel, a, (a.n + kJoinRows - 1) / kJoinRows, 256, st);
 }
 
 cudaError_t prepare_products() {
@@ -1001,6 +1067,29 @@ uint32_t group_of(const ProductArgs& a) {
 
 }  // namespace
 
+// The number that leaves the fullest pair of SMs the least to do, in blocks of
+// products, with what the parts cost (8 blocks' time for their launch, one for
+// four parts of a tile).
+uint32_t splits_of(uint64_t m, uint64_t n, uint64_t k, int planes, uint64_t room) {
+    const uint64_t pairs = kLossSms / 2, tiles = tiles_of(m) * tiles_of(n);
+    const uint64_t blocks = (k + kDeep - 1) / kDeep * (planes == 1 ? 1 : 6);
+    if (tiles == 0 || tiles >= 8 * pairs) return 1;
+    const uint64_t most = std::min(blocks / 4, room / (tiles * kSide * kSide));
+    uint64_t best = (tiles + pairs - 1) / pairs * blocks;
+    uint32_t splits = 1;
+    auto look = [&](uint64_t s) {
+        if (s < 2 || s > most) return;
+        const uint64_t cost = (tiles * s + pairs - 1) / pairs * ((blocks + s - 1) / s) + 8 + tiles * s / 4;
+        if (cost < best) {
+            best = cost;
+            splits = static_cast<uint32_t>(s);
+        }
+    };
+    for (uint64_t s = 2; s <= 8; ++s) look(s);
+    if (pairs / tiles > 8) look(std::min(most, pairs / tiles));
+    return splits;
+}
+
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t st) {
     ProductParams p;
     p.args = a;
@@ -1008,8 +1097,7 @@ cudaError_t launch_product(const ProductArgs& a, cudaStream_t st) {
     cudaError_t e = make_map(a.a, &p.a);
     if (e == cudaSuccess) e = make_map(a.b, &p.b);
     if (e != cudaSuccess) return e;
-    const uint64_t most = a.out.parts ? kLossSms / 2 : 1;  // parts of a tile
-    const uint64_t pairs = std::min<uint64_t>(std::max<uint64_t>(1, tiles_of(a.m) * tiles_of(a.n) * most), kLossSms / 2);
+    const uint64_t pairs = std::min<uint64_t>(std::max<uint64_t>(1, tiles_of(a.m) * tiles_of(a.n) * a.splits), kLossSms / 2);
     return launch(product_of(a), p, 2 * pairs, kProductThreads, st, kProductSmem);
 }
 

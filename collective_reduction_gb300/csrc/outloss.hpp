@@ -67,10 +67,13 @@ struct RowsArgs {
     int mean;
     Lists lists;
     Counted rows;
+    float* result;     // written here where nothing counts
+    uint32_t* ticket;  // of the joins of this call
 };
 
 // Rows of a caller's matrix into planes: row i from row rows.row[i] of src
-// (rows.row null: row i), zeros behind the last one up to a tile's end.
+// (rows.row null: row i), zeros behind the last one up to a tile's end.  Of the n
+// tokens those that do not count are given a loss and a gradient of 0.
 struct PackArgs {
     const void* src;
     uint64_t stride;
@@ -78,16 +81,11 @@ struct PackArgs {
     uint32_t n, width;  // rows, columns of src; planes have `pitch` columns, zero behind width
     Counted rows;
     Planes out;
-};
-
-// What the tokens that do not count are given.
-struct ClearArgs {
-    const uint32_t* counted;
-    uint32_t n, width;
-    float* losses;       // null: none
-    void* grad_hidden;   // null: none
-    uint64_t stride;
-    int bf16;
+    const uint32_t* counted;  // null: no tokens
+    float* losses;            // null: none, as below
+    void* grad;
+    uint64_t grad_stride;
+    int grad_bf16;
 };
 
 // A token's place's softmax: largest y = z c, and factor / sum 2^(y - max).
@@ -102,14 +100,20 @@ struct JoinArgs {
     uint64_t pitch;
     uint32_t parts, base, n;
     float c;              // log2(e) / t
-    double t;
+    float t, t2;          // t, t^2
     Lists lists;
     Counted rows;
     RowStat* stat;
     float* gain;          // what the shares are multiplied by, factor t
     float* loss;
     float* losses;        // by token; null: none
+    double* sums;         // of 32 places each, from the first of the call on
+    uint32_t* bad;
+    uint32_t *ticket, tickets;  // the last of `tickets` CTAs writes the record
+    float* result;
 };
+
+constexpr uint32_t kJoinRows = 32;  // of a CTA
 
 // The logits' gradient of a piece from its logits, zeros in the rows behind the
 // last up to a block of products.
@@ -123,12 +127,6 @@ struct GradArgs {
     const RowStat* stat;
     const float* gain;
     Planes g;
-};
-
-struct RecordArgs {
-    const float* loss;
-    Counted rows;
-    float* result;
 };
 
 // C = A B^T over k, A's rows and B's rows as planes; a matrix of which k runs
@@ -153,14 +151,14 @@ struct LogitArgs {
 
 // Where a product goes: `add` (float32, null: nothing) is added to it, and it is
 // stored in `sum` (float32), or if that is null in the caller's rows (row i into
-// row[i] if row is not null).  Split products go to parts[split] and are finished
-// by launch_finish; they have no add and sum.
+// row[i] if row is not null).  Products of several splits go to parts, a matrix of
+// whole tiles each, and are finished by launch_finish; they have no add and sum.
 struct OutArgs {
     const float* add;
     float* sum;
     uint64_t sum_pitch;
     float* parts;
-    uint64_t part_pitch, part_room;  // ..., floats there
+    uint64_t part_pitch;
     void* out;
     uint64_t stride;
     int bf16;
@@ -174,6 +172,7 @@ struct ProductArgs {
     int count_m, count_k;  // m, k: no more than the counted tokens behind base
     uint32_t base;
     uint32_t run;          // blocks of 64 products that are summed in the tensor cores
+    uint32_t splits;       // parts of k
     const uint32_t* count;
     int logits;            // which of the two follows
     LogitArgs logit;
@@ -184,13 +183,14 @@ struct ProductArgs {
 cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
 cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
-cudaError_t launch_clear(const ClearArgs& a, cudaStream_t st);
 cudaError_t launch_join(const JoinArgs& a, cudaStream_t st);
-cudaError_t launch_record(const RecordArgs& a, cudaStream_t st);
 // What the products' kernels need once on a device before their first launch.
 cudaError_t prepare_products();
 cudaError_t launch_product(const ProductArgs& a, cudaStream_t st);
-// Adds a split product's parts (nothing where it was not split).
+// How many parts of k suit a product of m x n values whose parts have room for
+// `room` values (m: of whole tiles).
+uint32_t splits_of(uint64_t m, uint64_t n, uint64_t k, int planes, uint64_t room);
+// Adds a split product's parts.
 cudaError_t launch_finish(const ProductArgs& a, cudaStream_t st);
 cudaError_t launch_grad(const GradArgs& a, cudaStream_t st);
 
