@@ -53,7 +53,7 @@ struct Layout {
     uint64_t pack = 0, part_room = 0, wide = 0, sum_pitch = 0;  // entries packed at a time, floats, padded V, ... D
     int planes = 1, list = 1;
     size_t status = 0, count = 0, factor = 0, row = 0, counted = 0, ids = 0, shares = 0, entropy = 0, logits = 0;
-    size_t ticket = 0, sums = 0, bad = 0, stats = 0, stat = 0, gain = 0, hidden = 0, weight = 0, z = 0, grad = 0, part = 0, sum = 0;
+    size_t ticket = 0, sums = 0, bad = 0, stats = 0, loss = 0, hidden = 0, weight = 0, z = 0, grad = 0, part = 0, sum = 0;
     size_t bytes = 0;
     size_t add(uint64_t n) {
         const size_t at = bytes;
@@ -97,8 +97,7 @@ ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype
     l.shares = l.add(4 * k);
     l.logits = l.add(4 * k);
     l.stats = l.add(8 * l.piece * (l.wide / ar::kStatColumns));
-    l.stat = l.add(8 * n);
-    l.gain = l.add(4 * n);
+    l.loss = l.add(4 * n);
     l.hidden = l.add(2 * l.planes * n * l.pitch);
     l.weight = l.add(2 * l.planes * l.pack * l.pitch);
     if (gradients) {
@@ -236,7 +235,9 @@ struct Call {
         return p;
     }
 
-    void logits(uint64_t r, uint32_t m) {
+    // Logits and losses of a piece, and the logits' gradients.
+    void losses(uint64_t r, uint32_t m) {
+        const uint64_t pitch = h->l.wide / ar::kStatColumns;
         for (uint64_t v = 0; v < h->vocab; v += entries()) {
             const uint64_t end = std::min(h->vocab, v + entries());
             ar::ProductArgs p = product(r);
@@ -247,20 +248,19 @@ struct Call {
             p.n = static_cast<uint32_t>(end - v);
             p.k = width;
             p.run = h->dtype == AR_BFLOAT16 ? kLogitRun : kExactRun;
-            p.logits = 1;
             p.logit.c = c;
             p.logit.v0 = static_cast<uint32_t>(v);
             p.logit.lists = lists;
             p.logit.row = rows.row + r;
-            p.logit.stats = h->at<float2>(h->l.stats) + v / ar::kStatColumns * h->l.piece;
-            p.logit.stats_pitch = h->l.piece;
+            p.logit.stats = h->at<float2>(h->l.stats) + v / ar::kStatColumns;
+            p.logit.stats_pitch = pitch;
             if (grads) p.logit.z = h->at<float>(h->l.z) + v;
             p.logit.z_pitch = h->l.wide;
-            run(ar::launch_product(p, st));
+            run(ar::launch_logits(p, st));
         }
         ar::JoinArgs j = {};
         j.stats = h->at<float2>(h->l.stats);
-        j.pitch = h->l.piece;
+        j.pitch = pitch;
         j.parts = static_cast<uint32_t>(up(h->vocab, ar::kStatColumns) / ar::kStatColumns);
         j.base = static_cast<uint32_t>(r);
         j.n = m;
@@ -269,35 +269,26 @@ struct Call {
         j.t2 = static_cast<float>(t * t);
         j.lists = lists;
         j.rows = rows;
-        j.stat = h->at<ar::RowStat>(h->l.stat) + r;
-        j.gain = h->at<float>(h->l.gain) + r;
         j.losses = a->losses;
-        j.sums = h->at<double>(h->l.sums);
-        j.bad = h->at<uint32_t>(h->l.bad);
-        j.ticket = h->at<uint32_t>(h->l.ticket);
-        j.tickets = (n + ar::kJoinRows - 1) / ar::kJoinRows;
-        j.result = a->result;
-        run(ar::launch_join(j, st));
+        if (grads) {
+            j.z = h->at<float>(h->l.z);
+            j.z_pitch = h->l.wide;
+            j.vocab = vocab;
+            j.loss = h->at<float>(h->l.loss) + r;
+            j.g = grad(r);
+            run(ar::launch_grad(j, st));
+        } else {
+            j.sums = h->at<double>(h->l.sums);
+            j.bad = h->at<uint32_t>(h->l.bad);
+            j.ticket = h->at<uint32_t>(h->l.ticket);
+            j.tickets = (n + ar::kJoinRows - 1) / ar::kJoinRows;
+            j.result = a->result;
+            run(ar::launch_join(j, st));
+        }
     }
 
-    void grad_logits(uint64_t r, uint32_t m) {
-        ar::GradArgs g = {};
-        g.z = h->at<float>(h->l.z);
-        g.pitch = h->l.wide;
-        g.base = static_cast<uint32_t>(r);
-        g.n = m;
-        g.vocab = vocab;
-        g.c = c;
-        g.lists = lists;
-        g.rows = rows;
-        g.stat = h->at<ar::RowStat>(h->l.stat) + r;
-        g.gain = h->at<float>(h->l.gain) + r;
-        g.g = grad(r);
-        run(ar::launch_grad(g, st));
-    }
-
-    // The last piece's product goes to the caller, with the sum of those before.
-    void grad_weight(uint64_t r, uint32_t m, bool last) {
+    // The last tokens' product goes to the caller, with the sum of those before.
+    ar::ProductArgs grad_weight(uint64_t r, uint32_t m, bool last) const {
         ar::ProductArgs p = product(r);
         p.a = {grad(r), true, m, h->vocab};
         p.b = {hidden(r), true, m, h->hidden};
@@ -313,39 +304,50 @@ struct Call {
         p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
         if (r > 0) p.out.add = h->at<float>(h->l.sum);
         if (!last) p.out.sum = h->at<float>(h->l.sum);
-        if (r == 0 && last) p.splits = ar::splits_of(vocab, width, m, h->l.planes, h->l.part_room);
-        p.out.parts = h->at<float>(h->l.part);
-        run(ar::launch_product(p, st));
-        if (p.splits > 1) run(ar::launch_finish(p, st));
+        if (!p.out.add && !p.out.sum) p.out.parts = h->at<float>(h->l.part);
+        return p;
     }
 
-    void grad_hidden(uint64_t r, uint32_t m) {
-        for (uint64_t v = 0; v < h->vocab; v += entries()) {
-            const uint64_t end = std::min(h->vocab, v + entries());
-            ar::ProductArgs p = product(r);
-            ar::Planes g = grad(r);
-            g.p += v;
-            p.a = {g, false, m, end - v};
-            p.b = {weight(v, end), true, end - v, h->hidden};
-            p.m = m;
-            p.count_m = 1;
-            p.n = width;
-            p.k = static_cast<uint32_t>(end - v);
-            p.run = a->grad_hidden_dtype == AR_BFLOAT16 ? kLongRun : kExactRun;
-            p.out.out = a->grad_hidden;
-            p.out.stride = a->grad_hidden_stride;
-            p.out.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
-            p.out.accumulate = a->accumulate;
-            p.out.row = rows.row + r;
-            p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
-            p.out.parts = h->at<float>(h->l.part);
-            if (v == 0 && end == h->vocab) p.splits = ar::splits_of(m, width, vocab, h->l.planes, h->l.part_room);
-            // entries packed at a time: sums in the parts' memory
-            if (v > 0) p.out.add = h->at<float>(h->l.part);
-            if (end < h->vocab) p.out.sum = h->at<float>(h->l.part);
-            run(ar::launch_product(p, st));
-            if (p.splits > 1) run(ar::launch_finish(p, st));
+    // By vocabulary entries [v, end), which are all of them, or packed in turn and
+    // summed up in the parts' memory.
+    ar::ProductArgs grad_hidden(uint64_t r, uint32_t m, uint64_t v, uint64_t end) {
+        ar::ProductArgs p = product(r);
+        ar::Planes g = grad(r);
+        g.p += v;
+        p.a = {g, false, m, end - v};
+        p.b = {weight(v, end), true, end - v, h->hidden};
+        p.m = m;
+        p.count_m = 1;
+        p.n = width;
+        p.k = static_cast<uint32_t>(end - v);
+        p.run = a->grad_hidden_dtype == AR_BFLOAT16 ? kLongRun : kExactRun;
+        p.out.out = a->grad_hidden;
+        p.out.stride = a->grad_hidden_stride;
+        p.out.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
+        p.out.accumulate = a->accumulate;
+        p.out.row = rows.row + r;
+        p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
+        if (v > 0) p.out.add = h->at<float>(h->l.part);
+        if (end < h->vocab) p.out.sum = h->at<float>(h->l.part);
+        if (!p.out.add && !p.out.sum) p.out.parts = h->at<float>(h->l.part);
+        return p;
+    }
+
+    // Both gradients of the kept tokens, in one launch but for packed weights.
+    void gradients(uint64_t r, uint32_t m, bool last) {
+        ar::RecordArgs record = {h->at<float>(h->l.loss), rows, last && m > 0 ? a->result : nullptr};
+        ar::ProductArgs p[2];
+        int k = 0;
+        if (a->grad_hidden && m > 0) {
+            uint64_t v = 0;
+            for (; v + entries() < h->vocab; v += entries()) {
+                const ar::ProductArgs q = grad_hidden(r, m, v, v + entries());
+                run(ar::launch_products(&q, 1, h->l.part_room, {}, st));
+            }
+            p[k++] = grad_hidden(r, m, v, h->vocab);
         }
+        if (a->grad_weight) p[k++] = grad_weight(r, m, last);
+        run(ar::launch_products(p, k, h->l.part_room, record, st));
     }
 
     // Everything after the lists: the tokens that count, then in pieces of them
@@ -380,13 +382,9 @@ struct Call {
         }
         for (uint64_t first = 0; first < n || first == 0; first += h->l.kept) {
             const uint32_t all = static_cast<uint32_t>(std::min<uint64_t>(n - first, h->l.kept));
-            for (uint64_t at = first; at < first + all; at += h->l.piece) {
-                const uint32_t m = static_cast<uint32_t>(std::min<uint64_t>(first + all - at, h->l.piece));
-                logits(at, m);
-                if (grads) grad_logits(at, m);
-            }
-            if (a->grad_weight) grad_weight(first, all, first + h->l.kept >= n);
-            if (all > 0 && a->grad_hidden) grad_hidden(first, all);
+            for (uint64_t at = first; at < first + all; at += h->l.piece)
+                losses(at, static_cast<uint32_t>(std::min<uint64_t>(first + all - at, h->l.piece)));
+            if (a->grad_weight || (a->grad_hidden && all > 0)) gradients(first, all, first + h->l.kept >= n);
         }
         return cuda_status(e);
     }

@@ -286,90 +286,84 @@ __device__ __forceinline__ void join_stat(float& top, float& sum, float top2, fl
     sum = __fadd_rn(a, b);
 }
 
-// 32 places a CTA: a lane a place over the parts of each warp, then eight lanes a
-// place for the parts' join and the list.  With y = z c and shares that add up to 1
+// The loss of a place from its softmax statistics, by the lanes of a warp, alike in
+// all of them.  With y = z c and shares that add up to 1
 //   log sum exp(z / t) - sum p z / t = ln 2 (log2 sum 2^(y - top) + sum p (top - y)),
-// whose terms do not cancel, so float32 does.  Every sum has a fixed order; the
-// call's last CTA adds up the CTAs' and writes the record.
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs a) {
-    __shared__ float2 part[8][kJoinRows];
-    __shared__ float losses[kJoinRows];
-    __shared__ uint32_t flag[8];
-    __shared__ double total[8];
+// whose terms do not cancel, so float32 does.
+__device__ __forceinline__ float row_loss(const JoinArgs& a, uint64_t token, float top, float sum, uint32_t lane) {
+    const uint64_t at = token * a.lists.top;
+    float dot = 0.f;  // sum p (top - y)
+    for (int j = lane; j < a.lists.top; j += 32) {
+        if (a.lists.ids[at + j] == kNoId) break;  // nothing behind it
+        const float d = -__fmaf_rn(a.lists.logits[at + j], a.c, -top);
+        const float share = a.lists.shares ? a.lists.shares[at + j] : 1.f;
+        if (share != 0.f) dot = __fmaf_rn(share, d, dot);
+    }
+    for (int o = 16; o > 0; o /= 2) dot = __fadd_rn(dot, __shfl_xor_sync(kFull, dot, o));
+    return __fmul_rn(a.t2, __fmaf_rn(static_cast<float>(kLn2), __fadd_rn(log2f(sum), dot), a.lists.entropy[token]));
+}
+
+// The statistics of a place by the lanes of a warp, from part `first` on in steps of `step`.
+__device__ __forceinline__ void row_stat(const JoinArgs& a, uint64_t r, uint32_t first, uint32_t step, float& top, float& sum) {
+    const float2* at = a.stats + r * a.pitch;
+    top = -kInf;
+    sum = 0.f;
+#pragma unroll 4
+    for (uint32_t q = first; q < a.parts; q += step) {
+        const float2 s = at[q];
+        join_stat(top, sum, s.x, s.y);
+    }
+    for (int o = 16; o > 0; o /= 2) {
+        const float t2 = __shfl_xor_sync(kFull, top, o), s2 = __shfl_xor_sync(kFull, sum, o);
+        join_stat(top, sum, t2, s2);  // either order gives the same bits
+    }
+}
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < kInf; }
+
+// A warp a place.  Every sum has a fixed order; the call's last CTA adds up the
+// CTAs' and writes the record.
+__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_constant__ JoinArgs a) {
+    __shared__ double total[kJoinRows];
+    __shared__ uint32_t flag[kJoinRows];
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const uint32_t r0 = blockIdx.x * kJoinRows;
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t count = *a.rows.count, m = count > a.base ? min(a.n, count - a.base) : 0;
     const float factor = *a.rows.factor;
-    float top = -kInf, sum = 0.f;
-    if (r0 + lane < m) {
-        const float2* at = a.stats + r0 + lane;
-#pragma unroll 8
-        for (uint32_t q = warp; q < a.parts; q += 8) {
-            const float2 s = at[q * a.pitch];
-            join_stat(top, sum, s.x, s.y);
-        }
+    const uint32_t r = blockIdx.x * kJoinRows + warp;
+    float loss = 0.f;
+    if (r < m) {
+        float top, sum;
+        row_stat(a, r, lane, 32, top, sum);
+        const uint64_t token = a.rows.row[a.base + r];
+        loss = row_loss(a, token, top, sum, lane);
+        if (a.losses && lane == 0) a.losses[token] = loss;
     }
-    part[warp][lane] = make_float2(top, sum);
+    if (lane == 0) {
+        total[warp] = loss;
+        flag[warp] = !finite(loss);
+    }
     __syncthreads();
-    const uint32_t row = tid / 8, eighth = tid % 8, r = r0 + row;
-    const bool in = r < m;
-    const float2 s = part[eighth][row];
-    top = s.x;
-    sum = s.y;
-    for (int o = 4; o > 0; o /= 2) {  // alike in all eight lanes: each step's operands in the lower lane's order
-        const float t2 = __shfl_xor_sync(kFull, top, o), s2 = __shfl_xor_sync(kFull, sum, o);
-        if (eighth & o) {
-            float t1 = t2, s1 = s2;
-            join_stat(t1, s1, top, sum);
-            top = t1, sum = s1;
-        } else {
-            join_stat(top, sum, t2, s2);
+    if (tid == 0) {
+        double all = 0.0;
+        uint32_t any = 0;
+        for (uint32_t w = 0; w < kJoinRows; ++w) {
+            all += total[w];
+            any |= flag[w];
         }
-    }
-    const uint64_t i = in ? a.rows.row[a.base + r] : 0, at = i * a.lists.top;
-    float dot = 0.f;  // sum p (top - y)
-    for (int j = eighth; in && j < a.lists.top; j += 8) {
-        if (a.lists.ids[at + j] == kNoId) break;  // nothing behind it
-        const float d = -__fmaf_rn(a.lists.logits[at + j], a.c, -top);
-        dot = a.lists.shares ? __fmaf_rn(a.lists.shares[at + j], d, dot) : d;
-    }
-    for (int o = 4; o > 0; o /= 2) dot = __fadd_rn(dot, __shfl_xor_sync(kFull, dot, o));
-    bool bad = false;
-    if (eighth == 0) {
-        float loss = 0.f;
-        if (in) {
-            loss = __fmul_rn(a.t2, __fmaf_rn(static_cast<float>(kLn2), __fadd_rn(log2f(sum), dot), a.lists.entropy[i]));
-            const float f = loss == loss ? __fmul_rn(factor, a.t) : loss;  // NaN: the whole row
-            a.gain[r] = f;
-            a.stat[r] = {top, __fdiv_rn(f, sum)};
-            if (a.losses) a.losses[i] = loss;
-            bad = !(fabsf(loss) < kInf);
-        }
-        losses[row] = loss;
-    }
-    bad = __any_sync(kFull, bad);
-    if (lane == 0) flag[warp] = bad;
-    __syncthreads();
-    if (warp == 0) {
-        float x = losses[lane];
-        for (int o = 16; o > 0; o /= 2) x = __fadd_rn(x, __shfl_down_sync(kFull, x, o));
-        const uint32_t any = __any_sync(kFull, lane < 8 && flag[lane % 8]);
-        if (lane == 0) {
-            const uint32_t cta = a.base / kJoinRows + blockIdx.x;
-            a.sums[cta] = x;
-            a.bad[cta] = any;
-            __threadfence();
-            flag[0] = atomicAdd(a.ticket, 1u) == a.tickets - 1;
-        }
+        const uint32_t cta = a.base / kJoinRows + blockIdx.x;
+        a.sums[cta] = all;
+        a.bad[cta] = any;
+        __threadfence();
+        flag[0] = atomicAdd(a.ticket, 1u) == a.tickets - 1;
     }
     __syncthreads();
     if (!flag[0] || count == 0) return;
     __threadfence();
     double all = 0.0;
-    bad = false;
-    for (uint32_t k = tid; k < (count + kJoinRows - 1) / kJoinRows; k += 256) {
+    bool bad = false;
+    for (uint32_t k = tid; k < (count + kJoinRows - 1) / kJoinRows; k += 32 * kJoinRows) {
         all += __ldcg(a.sums + k);
         bad = bad || __ldcg(a.bad + k);
     }
@@ -384,7 +378,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     if (tid != 0) return;
     all = 0.0;
     uint32_t any = 0;
-    for (int w = 0; w < 8; ++w) {
+    for (uint32_t w = 0; w < kJoinRows; ++w) {
         all += total[w];
         any |= flag[w];
     }
@@ -394,28 +388,49 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
     a.result[3] = factor;
 }
 
-__device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int accumulate, float x) {
-    if (accumulate) x = __fadd_rn(x, load_value(out, at, bf16));
-    if (bf16) static_cast<uint16_t*>(out)[at] = bf16_of(x);
-    else static_cast<float*>(out)[at] = x;
-}
+constexpr int kGradThreads = 256;
 
-constexpr int kGradThreads = 256, kGradColumns = 8192;  // of a CTA: one row's
-
-// g = 2^(y - top) factor t / sum - share factor t, from the logits of a row's
-// columns; then the few columns of the row's list.
-__global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ GradArgs a) {
-    const uint32_t tid = threadIdx.x;
-    const uint32_t lo = blockIdx.x * kGradColumns, hi = min(a.vocab, lo + kGradColumns);
+// A CTA a place's `columns` columns: the statistics (of the whole row, in every
+// one of its CTAs), then
+//   g = 2^(y - top) factor t / sum - share factor t
+// from the logits, then the few columns of the row's list.  Bound by HBM: a logit's
+// 4 bytes in and its gradient's 2 (float32: 6) out.
+__global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ JoinArgs a) {
+    __shared__ float2 part[kGradThreads / 32];
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const uint32_t lo = blockIdx.x * a.columns, hi = min(a.vocab, lo + a.columns);
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t count = *a.rows.count, m = count > a.base ? min(a.n, count - a.base) : 0;
     for (uint64_t r = blockIdx.y; r < (m + 63) / 64 * 64; r += gridDim.y) {
         const bool in = r < m;
-        const RowStat st = in ? a.stat[r] : RowStat{0.f, 0.f};
-        const float* z = a.z + r * a.pitch;
+        float top = 0.f, inv = 0.f, gain = 0.f;
+        uint64_t token = 0;
+        if (in) {
+            float sum;
+            row_stat(a, r, tid, kGradThreads, top, sum);
+            __syncthreads();  // the row before has been read
+            if (lane == 0) part[warp] = make_float2(top, sum);
+            __syncthreads();
+            top = part[0].x;
+            sum = part[0].y;
+            for (int w = 1; w < kGradThreads / 32; ++w) join_stat(top, sum, part[w].x, part[w].y);
+            token = a.rows.row[a.base + r];
+            const float entropy = a.lists.entropy[token];  // NaN: a list that is not valid
+            gain = entropy == entropy && sum > 0.f ? __fmul_rn(*a.rows.factor, a.t) : __int_as_float(0x7FC00000);
+            inv = __fdiv_rn(gain, sum);
+            if (blockIdx.x == 0 && warp == 0) {
+                const float loss = row_loss(a, token, top, sum, lane);
+                if (lane == 0) {
+                    a.loss[r] = loss;
+                    if (a.losses) a.losses[token] = loss;
+                }
+            }
+        }
+        const float* z = a.z + r * a.z_pitch;
         uint16_t* g = a.g.p + r * a.g.pitch;
-        auto value = [&](float x) { return __fmul_rn(exp2_fast(__fmaf_rn(x, a.c, -st.top)), st.inv); };
+        auto value = [&](float x) { return __fmul_rn(exp2_fast(__fmaf_rn(x, a.c, -top)), inv); };
+#pragma unroll 2
         for (uint32_t v = lo + 8 * tid; v < hi; v += 8 * kGradThreads) {  // the pitch is of whole tiles
             float x[8] = {};
             if (in) {
@@ -431,15 +446,21 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
         }
         if (!in) continue;  // the whole CTA
         __syncthreads();
-        const uint64_t list = static_cast<uint64_t>(a.rows.row[a.base + r]) * a.lists.top;
+        const uint64_t list = token * a.lists.top;
         for (int k = tid; k < a.lists.top; k += kGradThreads) {
             const uint32_t v = static_cast<uint32_t>(a.lists.ids[list + k]);
             if (v < lo || v >= hi) continue;
             const float share = a.lists.shares ? a.lists.shares[list + k] : 1.f;
-            float x = __fsub_rn(value(a.lists.logits[list + k]), __fmul_rn(share, a.gain[r]));
+            float x = __fsub_rn(value(a.lists.logits[list + k]), __fmul_rn(share, gain));
             for (int q = 0; q < a.g.planes; ++q) g[q * a.g.plane + v] = split_plane(x);
         }
     }
+}
+
+__device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int accumulate, float x) {
+    if (accumulate) x = __fadd_rn(x, load_value(out, at, bf16));
+    if (bf16) static_cast<uint16_t*>(out)[at] = bf16_of(x);
+    else static_cast<float*>(out)[at] = x;
 }
 
 // ---------------------------------------------------------------- products
@@ -478,10 +499,11 @@ enum : uint32_t {
 };
 constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
 
+// One or two products in one launch.
 struct ProductParams {
-    CUtensorMap a, b;
-    ProductArgs args;
-    uint32_t m_group;  // rows of tiles that are worked on side by side
+    CUtensorMap a[2], b[2];
+    ProductArgs args[2];
+    RecordArgs record;
 };
 
 // As mbar_wait, without a call: accumulators live in registers across it.
@@ -534,10 +556,10 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool turned) {
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
-// float32 accumulators of bf16 products, M = N = 256 over the pair.
-__host__ __device__ constexpr uint32_t mma_desc(bool a_turned, bool b_turned) {
+// float32 accumulators of bf16 products, M = 256 and N = width over the pair.
+__device__ __forceinline__ uint32_t mma_desc(bool a_turned, bool b_turned, uint32_t width) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_turned ? 1u << 15 : 0u) | (b_turned ? 1u << 16 : 0u) |
-           (static_cast<uint32_t>(kSide >> 3) << 17) | (static_cast<uint32_t>(kSide >> 4) << 24);
+           ((width >> 3) << 17) | (static_cast<uint32_t>(kSide >> 4) << 24);
 }
 
 __device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t desc, uint32_t add) {
@@ -569,25 +591,25 @@ __device__ __forceinline__ void tmem_read16(uint32_t taddr, float* v) {
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// The tiles of a product and the blocks of each, alike in every role and kernel.
+// The tiles of a product and the blocks of each.
 struct Tiles {
     uint32_t m, blocks, splits, per;  // rows of A, blocks of k times passes, ... of a split
     uint32_t k_blocks, tall, wide, group;
     uint64_t total;
-    __device__ Tiles(const ProductArgs& a, uint32_t m_group) {
+    __device__ __forceinline__ void set(const ProductArgs& a) {
         const uint32_t count = *a.count, left = count > a.base ? count - a.base : 0;
         m = a.count_m ? min(a.m, left) : a.m;
         k_blocks = ((a.count_k ? min(a.k, left) : a.k) + kDeep - 1) / kDeep;
         blocks = k_blocks * (a.a.m.planes == 1 ? 1 : 6);
         tall = (m + kSide - 1) / kSide;
-        wide = (a.n + kSide - 1) / kSide;
-        group = m_group;
+        wide = (a.n + a.width - 1) / a.width;
+        group = a.group;
         splits = a.splits;
         per = (blocks + splits - 1) / splits;
         total = static_cast<uint64_t>(tall) * wide * splits;
     }
     // Tile t: in each split, groups of `group` rows of tiles, column by column.
-    __device__ void at(uint64_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
+    __device__ __forceinline__ void at(uint64_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
         const uint64_t each = static_cast<uint64_t>(tall) * wide;
         split = static_cast<uint32_t>(t / each);
         const uint32_t r = static_cast<uint32_t>(t - split * each);
@@ -597,6 +619,42 @@ struct Tiles {
         mt = g * group + rest - nt * rows;
         lo = min(blocks, split * per);
         n = min(blocks, lo + per) - lo;
+    }
+};
+
+// What each pair works on, alike in every role: the tiles of the first product in
+// turn; then the second's, of which the pairs with fewer of the first's take as
+// many more as take the same time.
+struct Work {
+    Tiles tiles[2];
+    uint64_t first;
+    uint32_t pairs, over, early;
+    __device__ __forceinline__ void set(const ProductArgs* a, int n, uint32_t pairs_) {
+        pairs = pairs_;
+        tiles[0].set(a[0]);
+        if (n > 1) tiles[1].set(a[1]);
+        else tiles[1].total = 0;
+        first = tiles[0].total / pairs;
+        over = static_cast<uint32_t>(tiles[0].total - first * pairs);
+        early = 0;
+        const uint64_t cost = n > 1 ? static_cast<uint64_t>(tiles[1].blocks) * a[1].width : 0;
+        if (over && cost)
+            early = static_cast<uint32_t>(min(static_cast<uint64_t>(tiles[0].per) * a[0].width / cost, tiles[1].total / (pairs - over)));
+    }
+    // The pair's i-th tile: of which product, which.
+    __device__ __forceinline__ bool pick(uint32_t i, uint32_t pair, uint32_t& which, uint64_t& t) const {
+        const uint64_t mine = first + (pair < over);
+        which = i >= mine;
+        if (!which) {
+            t = pair + static_cast<uint64_t>(i) * pairs;
+            return true;
+        }
+        const uint64_t j = i - mine;
+        const uint32_t others = pairs - over;  // pairs with fewer of the first product's tiles
+        if (pair < over) t = static_cast<uint64_t>(early) * others + j * pairs + others + pair;
+        else if (j < early) t = j * others + (pair - over);
+        else t = static_cast<uint64_t>(early) * others + (j - early) * pairs + (pair - over);
+        return t < tiles[1].total;
     }
 };
 
@@ -707,7 +765,7 @@ struct LogitTile {
         chunk<1>(p, z[1]);
         chunk<2>(p, z[2]);
         chunk<3>(p, z[3]);
-        if (p.in && p.cols) g.stats[p.n0 / kStatColumns * g.stats_pitch + p.row] = make_float2(top, sum);
+        if (p.in && p.cols) g.stats[p.row * g.stats_pitch + p.n0 / kStatColumns] = make_float2(top, sum);
     }
 };
 
@@ -789,10 +847,36 @@ struct OutTile {
     }
 };
 
-template <bool LOGITS, bool AT, bool BT>
+// The record, by a warp that has nothing else to do.
+__device__ void write_record(const RecordArgs& a, uint32_t lane) {
+    const uint32_t count = *a.rows.count;
+    if (count == 0) return;  // written when the rows were
+    double sum = 0.0;
+    bool bad = false;
+#pragma unroll 4
+    for (uint32_t r = lane; r < count; r += 32) {
+        const float x = a.loss[r];
+        sum += x;
+        bad = bad || !finite(x);
+    }
+    for (int o = 16; o > 0; o /= 2) sum += __shfl_down_sync(kFull, sum, o);
+    bad = __any_sync(kFull, bad);
+    if (lane != 0) return;
+    const float factor = *a.rows.factor;
+    a.result[0] = static_cast<float>(sum * factor);
+    a.result[1] = static_cast<float>(count);
+    a.result[2] = bad ? 1.f : 0.f;
+    a.result[3] = factor;
+}
+
+// LOGITS: one product of two matrices along k, the softmax's statistics in its
+// epilogue.  Otherwise one or two with B turned, into the caller's memory.
+template <bool LOGITS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
-    product_kernel(const __grid_constant__ ProductParams p) {
+    product_kernel(const __grid_constant__ ProductParams p, int products) {
     extern __shared__ char raw[];
+    __shared__ Work work;
+    constexpr bool BT = !LOGITS;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;  // the same in both CTAs
     const uint32_t staged = base + kStages * kStageBytes, bars = staged + kEpilogueWarps * kStagedBytes;
     auto bar = [bars](uint32_t i) { return bars + 8 * i; };
@@ -809,8 +893,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
         mbar_init(bar(kDoneBar), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.a) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.b) : "memory");
+        for (int i = 0; i < products; ++i) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&p.a[i]) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&p.b[i]) : "memory");
+        }
+        griddep_wait();
+        work.set(p.args, products, gridDim.x / 2);
     }
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(bar(kTmemWord)),
@@ -819,42 +907,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         tmem_fence_before();
     }
+    __syncwarp();
     __syncthreads();
     cluster_sync();
     tmem_fence_after();
     const uint32_t tmem = lds32(bar(kTmemWord));
     griddep_wait();
-    const ProductArgs& a = p.args;
-    const Tiles tiles(a, p.m_group);
-    const uint64_t first = blockIdx.x / 2, step = gridDim.x / 2;
-    uint32_t mt, nt, split, lo, n;
+    const uint32_t pair = blockIdx.x / 2;
+    uint32_t mt, nt, split, lo, n, which;
+    uint64_t t;
     bool ok = true;
     if (warp == 0 && lane == 0) {
         uint32_t it = 0;
-        for (uint64_t t = first; t < tiles.total && ok; t += step) {
+        for (uint32_t j = 0; ok && work.pick(j, pair, which, t); ++j) {
+            const Tiles& tiles = work.tiles[which];
+            const ProductArgs& a = p.args[which];
+            const CUtensorMap *ma = &p.a[which], *mb = &p.b[which];
             tiles.at(t, mt, nt, split, lo, n);
-            const int m0 = static_cast<int>(mt * kSide + rank * kHalf), n0 = static_cast<int>(nt * kSide + rank * kHalf);
-            uint32_t q = lo / max(1u, tiles.k_blocks), k = lo - q * tiles.k_blocks;
+            const bool planes = a.a.m.planes > 1, at = !LOGITS && a.a.turned;
+            const int m0 = static_cast<int>(mt * kSide + rank * kHalf);
+            const int n0 = static_cast<int>(nt * a.width + rank * (a.width / 2));
+            const uint32_t k_blocks = tiles.k_blocks;
+            uint32_t q = lo / max(1u, k_blocks), k = lo - q * k_blocks;
             for (uint32_t i = 0; i < n; ++i, ++it) {
                 const uint32_t s = it % kStages, round = it / kStages;
                 if (round > 0 && !(ok = mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1))) break;
                 const int k0 = static_cast<int>(k * kDeep);
-                const int za = a.a.m.planes == 1 ? 0 : plane_a(q), zb = a.a.m.planes == 1 ? 0 : plane_b(q);
+                const int za = planes ? plane_a(q) : 0, zb = planes ? plane_b(q) : 0;
                 const uint32_t to = base + s * kStageBytes, full = in_first(bar(kFullBar + s));
                 if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
-                if (AT) {
-                    tma_load(to, &p.a, m0, k0, za, full);
-                    tma_load(to + kOperandBytes / 2, &p.a, m0 + 64, k0, za, full);
+                if (at) {
+                    tma_load(to, ma, m0, k0, za, full);
+                    tma_load(to + kOperandBytes / 2, ma, m0 + 64, k0, za, full);
                 } else {
-                    tma_load(to, &p.a, k0, m0, za, full);
+                    tma_load(to, ma, k0, m0, za, full);
                 }
                 if (BT) {
-                    tma_load(to + kOperandBytes, &p.b, n0, k0, zb, full);
-                    tma_load(to + kOperandBytes + kOperandBytes / 2, &p.b, n0 + 64, k0, zb, full);
+                    tma_load(to + kOperandBytes, mb, n0, k0, zb, full);
+                    tma_load(to + kOperandBytes + kOperandBytes / 2, mb, n0 + 64, k0, zb, full);
                 } else {
-                    tma_load(to + kOperandBytes, &p.b, k0, n0, zb, full);
+                    tma_load(to + kOperandBytes, mb, k0, n0, zb, full);
                 }
-                if (++k == tiles.k_blocks) k = 0, ++q;
+                if (++k == k_blocks) k = 0, ++q;
             }
         }
         // the last blocks have been read before the pair's memory goes
@@ -863,13 +957,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         if (rank == 1 && !mbar_wait_here(bar(kDoneBar), 0)) ok = false;
     } else if (warp == 1 && lane == 0 && rank == 0) {
         uint32_t it = 0, done = 0;
-        for (uint64_t t = first; t < tiles.total && ok; t += step) {
-            tiles.at(t, mt, nt, split, lo, n);
+        for (uint32_t i0 = 0; ok && work.pick(i0, pair, which, t); ++i0) {
+            const ProductArgs& a = p.args[which];
+            work.tiles[which].at(t, mt, nt, split, lo, n);
+            const bool turned = !LOGITS && a.a.turned;
+            const uint32_t desc = mma_desc(turned, BT, a.width), a_step = turned ? 2048 : 32, run = a.run;
             for (uint32_t i = 0; i < n && ok; ++done) {
                 const uint32_t b = done & 1, acc = tmem + b * kSide;
                 if (done >= 2 && !(ok = mbar_wait_here(bar(kFreeBar + b), (done / 2 - 1) & 1))) break;
                 tmem_fence_after();
-                const uint32_t end = n - i > a.run ? i + a.run : n;
+                const uint32_t end = n - i > run ? i + run : n;
                 for (uint32_t j = i; j < end; ++j, ++it) {
                     const uint32_t s = it % kStages;
                     if (!(ok = mbar_wait_here(bar(kFullBar + s), (it / kStages) & 1))) break;
@@ -877,8 +974,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     const uint32_t at = base + s * kStageBytes;
 #pragma unroll
                     for (uint32_t k = 0; k < kDeep / 16; ++k)
-                        mma(acc, operand_desc(at + k * (AT ? 2048 : 32), AT),
-                            operand_desc(at + kOperandBytes + k * (BT ? 2048 : 32), BT), mma_desc(AT, BT), j > i || k > 0);
+                        mma(acc, operand_desc(at + k * a_step, turned),
+                            operand_desc(at + kOperandBytes + k * (BT ? 2048 : 32), BT), desc, j > i || k > 0);
                     mma_commit(bar(kEmptyBar + s));
                 }
                 if (!ok) break;
@@ -888,6 +985,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         }
         mma_commit(bar(kDoneBar));
         if (!mbar_wait_here(bar(kDoneBar), 0)) ok = false;
+    } else if (!LOGITS && warp == 3 && blockIdx.x == 0) {
+        if (p.record.result) write_record(p.record, lane);
     } else if (warp >= kEpilogueWarp) {
         const uint32_t quarter = warp % 4, half = (warp - kEpilogueWarp) / 4;
         const uint32_t lanes = tmem + ((quarter * 32) << 16) + half * kHalf;
@@ -895,12 +994,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
         Place at;
         at.staged = staged + (warp - kEpilogueWarp) * kStagedBytes;
         at.lane = lane;
-        for (uint64_t t = first; t < tiles.total; t += step) {
-            tiles.at(t, mt, nt, split, lo, n);
+        for (uint32_t i0 = 0; work.pick(i0, pair, which, t); ++i0) {
+            const ProductArgs& a = p.args[LOGITS ? 0 : which];
+            work.tiles[which].at(t, mt, nt, split, lo, n);
             at.row = static_cast<uint64_t>(mt) * kSide + rank * kHalf + quarter * 32 + lane;
-            at.in = at.row < tiles.m;
-            at.n0 = nt * kSide + half * kHalf;
-            at.cols = a.n > at.n0 ? min(static_cast<uint32_t>(kHalf), a.n - at.n0) : 0;
+            at.in = at.row < work.tiles[which].m;
+            at.n0 = nt * a.width + half * kHalf;
+            const uint32_t end = min(a.n, (nt + 1) * a.width);
+            at.cols = end > at.n0 ? min(static_cast<uint32_t>(kHalf), end - at.n0) : 0;
             std::conditional_t<LOGITS, LogitTile, OutTile> tile(a, at);
             float z[4][32];
 #pragma unroll
@@ -928,13 +1029,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 i = n - i > a.run ? i + a.run : n;
             }
             if (!ok) break;
-            if constexpr (LOGITS)
+            if constexpr (LOGITS) {
                 tile.finish(at, z);
-            else
+            } else {
+                const Tiles& tiles = work.tiles[which];
                 tile.finish(at, z, tiles.splits > 1 ? a.out.parts + split * (static_cast<uint64_t>(tiles.tall) * kSide * a.out.part_pitch) : nullptr);
+            }
         }
     }
-    if (!ok) atomicOr(a.status, 1u);
+    if (!ok) atomicOr(p.args[0].status, 1u);
     __syncwarp();
     tmem_fence_before();
     __syncthreads();
@@ -945,11 +1048,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 }
 
 // A split product's parts, added in their order: four columns a thread.
-__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ ProductParams p) {
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ ProductArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    const ProductArgs& a = p.args;
-    const Tiles tiles(a, p.m_group);
+    Tiles tiles;
+    tiles.set(a);
     const OutArgs& o = a.out;
     const uint64_t stride = static_cast<uint64_t>(tiles.tall) * kSide * o.part_pitch;
     const uint32_t quads = (a.n + 3) / 4;
@@ -966,13 +1069,6 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Pro
         }
         store_four(o, (o.row ? static_cast<uint64_t>(o.row[r]) : r) * o.stride + c, a.n - c, x);
     }
-}
-
-using ProductKernel = void (*)(ProductParams);
-
-ProductKernel product_of(const ProductArgs& a) {
-    if (a.logits) return product_kernel<true, false, false>;
-    return a.a.turned ? product_kernel<false, true, true> : product_kernel<false, false, true>;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -996,6 +1092,7 @@ EncodeFn encode_tiled() {
 }
 
 // Blocks of 64 columns x 128 rows (turned: 64 rows) of one plane; zeros outside.
+// A tile narrower than 256 loads as much and multiplies less.
 cudaError_t make_map(const Operand& o, CUtensorMap* map) {
     const EncodeFn encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
@@ -1011,10 +1108,10 @@ cudaError_t make_map(const Operand& o, CUtensorMap* map) {
                : cudaErrorInvalidValue;
 }
 
-template <class Args>
-cudaError_t launch(void (*f)(Args), const Args& a, uint64_t grid, int block, cudaStream_t st, size_t smem = 0) {
+template <class... Args>
+cudaError_t launch(void (*f)(Args...), dim3 grid, int block, size_t smem, cudaStream_t st, const Args&... a) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -1023,104 +1120,122 @@ cudaError_t launch(void (*f)(Args), const Args& a, uint64_t grid, int block, cud
     attr[0].val.programmaticStreamSerializationAllowed = AR_PDL;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void* args[] = {const_cast<Args*>(&a)};
+    void* args[] = {const_cast<Args*>(&a)...};
     return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(f), args);
+}
+
+uint32_t ctas(uint64_t n, uint64_t each) { return static_cast<uint32_t>((n + each - 1) / each); }
+
+uint64_t tall_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.m) + kSide - 1) / kSide; }
+uint64_t wide_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.n) + a.width - 1) / a.width; }
+uint64_t blocks_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.k) + kDeep - 1) / kDeep * (a.a.m.planes == 1 ? 1 : 6); }
+
+// Tiles as wide as they divide the columns evenly; rows of tiles side by side: all
+// of them while A's rows stay in L2, then eight.
+void set_shape(ProductArgs& a) {
+    const uint32_t wide = ctas(a.n, kSide);
+    a.width = (ctas(a.n, wide) + 31) / 32 * 32;
+    const uint64_t tall = std::max<uint64_t>(1, tall_of(a));
+    a.group = tall * kSide * a.k * 2 * a.a.m.planes > (64ull << 20) ? 8 : static_cast<uint32_t>(tall);
+    a.splits = 1;
+}
+
+// Parts of the first product's k: the number that leaves the fullest pair the least
+// to do, in columns of blocks, with what the parts cost (8 blocks' time for their
+// launch, one for four parts of a tile).
+uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t room) {
+    const uint64_t pairs = kLossSms / 2, tiles = tall_of(a) * wide_of(a), blocks = blocks_of(a);
+    if (tiles == 0 || tiles >= 8 * pairs) return 1;
+    const uint64_t most = std::min(blocks / 4, room / (tall_of(a) * kSide * a.out.part_pitch));
+    const uint64_t other = second ? blocks_of(*second) * second->width : 0;
+    const uint64_t others = second ? tall_of(*second) * wide_of(*second) * other : 0;
+    uint64_t best = 0;
+    uint32_t splits = 0;
+    auto look = [&](uint64_t s) {
+        if (s > std::max<uint64_t>(1, most)) return;
+        const uint64_t each = (blocks + s - 1) / s * a.width;
+        const uint64_t fullest = std::max((tiles * s + pairs - 1) / pairs * each, (tiles * s * each + others) / pairs + other / 2);
+        const uint64_t cost = fullest + (s > 1 ? (8 + tiles * s / 4) * kSide : 0);
+        if (splits == 0 || cost < best) {
+            best = cost;
+            splits = static_cast<uint32_t>(s);
+        }
+    };
+    for (uint64_t s = 1; s <= 8; ++s) look(s);
+    for (uint64_t s = 12; s <= pairs / tiles; s += 4) look(s);
+    return splits;
 }
 
 }  // namespace
 
 cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st) {
-    return launch(teacher_kernel, a, (a.n + kTeacherWarps - 1) / kTeacherWarps, 32 * kTeacherWarps, st,
-                  static_cast<size_t>(kTeacherWarps) * 2 * a.k * 4);
+    return launch(teacher_kernel, ctas(a.n, kTeacherWarps), 32 * kTeacherWarps, static_cast<size_t>(kTeacherWarps) * 2 * a.k * 4, st, a);
 }
 
-cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) { return launch(rows_kernel, a, 1, kRowThreads, st); }
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) { return launch(rows_kernel, 1, kRowThreads, 0, st, a); }
 
 cudaError_t launch_pack(const PackArgs& a, cudaStream_t st) {
-    return launch(pack_kernel, a, (a.n + kLossTile - 1) / kLossTile * (kLossTile / 8), 256, st);
+    return launch(pack_kernel, ctas(a.n, kLossTile) * (kLossTile / 8), 256, 0, st, a);
 }
 
 cudaError_t launch_join(const JoinArgs& a, cudaStream_t st) {
-    return launch(join_kernel, a, (a.n + kJoinRows - 1) / kJoinRows, 256, st);
+    return launch(join_kernel, ctas(a.n, kJoinRows), 32 * kJoinRows, 0, st, a);
+}
+
+cudaError_t launch_grad(const JoinArgs& a0, cudaStream_t st) {
+    JoinArgs a = a0;
+    const uint32_t rows = ctas(a.n, 64) * 64;
+    a.columns = 32 * kGradThreads;  // less while a wave of CTAs is not full
+    while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 8 * kLossSms) a.columns /= 2;
+    return launch(grad_kernel, dim3(ctas(a.vocab, a.columns), std::min(rows, 32768u)), kGradThreads, 0, st, a);
 }
 
 cudaError_t prepare_products() {
-    for (ProductKernel f : {product_kernel<true, false, false>, product_kernel<false, true, true>,
-                            product_kernel<false, false, true>}) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&product_kernel<true>),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&product_kernel<false>),
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+    return e;
 }
 
 namespace {
 
-uint64_t tiles_of(uint64_t x) { return (x + kSide - 1) / kSide; }
-
-// Rows of tiles worked on side by side: all of them while A's rows stay in L2,
-// then eight.
-uint32_t group_of(const ProductArgs& a) {
-    const uint64_t tall = std::max<uint64_t>(1, tiles_of(a.m));
-    return tall * kSide * a.k * 2 * a.a.m.planes > (64ull << 20) ? 8 : static_cast<uint32_t>(tall);
+cudaError_t launch_tiles(ProductParams& p, int n, bool logits, cudaStream_t st) {
+    uint64_t tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        const ProductArgs& a = p.args[i];
+        cudaError_t e = make_map(a.a, &p.a[i]);
+        if (e == cudaSuccess) e = make_map(a.b, &p.b[i]);
+        if (e != cudaSuccess) return e;
+        tiles += tall_of(a) * wide_of(a) * a.splits;
+    }
+    const uint32_t pairs = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(1, tiles), kLossSms / 2));
+    return launch(logits ? product_kernel<true> : product_kernel<false>, 2 * pairs, kProductThreads, kProductSmem, st, p, n);
 }
 
 }  // namespace
 
-// The number that leaves the fullest pair of SMs the least to do, in blocks of
-// products, with what the parts cost (8 blocks' time for their launch, one for
-// four parts of a tile).
-uint32_t splits_of(uint64_t m, uint64_t n, uint64_t k, int planes, uint64_t room) {
-    const uint64_t pairs = kLossSms / 2, tiles = tiles_of(m) * tiles_of(n);
-    const uint64_t blocks = (k + kDeep - 1) / kDeep * (planes == 1 ? 1 : 6);
-    if (tiles == 0 || tiles >= 8 * pairs) return 1;
-    const uint64_t most = std::min(blocks / 4, room / (tiles * kSide * kSide));
-    uint64_t best = (tiles + pairs - 1) / pairs * blocks;
-    uint32_t splits = 1;
-    auto look = [&](uint64_t s) {
-        if (s < 2 || s > most) return;
-        const uint64_t cost = (tiles * s + pairs - 1) / pairs * ((blocks + s - 1) / s) + 8 + tiles * s / 4;
-        if (cost < best) {
-            best = cost;
-            splits = static_cast<uint32_t>(s);
-        }
-    };
-    for (uint64_t s = 2; s <= 8; ++s) look(s);
-    if (pairs / tiles > 8) look(std::min(most, pairs / tiles));
-    return splits;
-}
-
-cudaError_t launch_product(const ProductArgs& a, cudaStream_t st) {
-    ProductParams p;
-    p.args = a;
-    p.m_group = group_of(a);
-    cudaError_t e = make_map(a.a, &p.a);
-    if (e == cudaSuccess) e = make_map(a.b, &p.b);
-    if (e != cudaSuccess) return e;
-    const uint64_t pairs = std::min<uint64_t>(std::max<uint64_t>(1, tiles_of(a.m) * tiles_of(a.n) * a.splits), kLossSms / 2);
-    return launch(product_of(a), p, 2 * pairs, kProductThreads, st, kProductSmem);
-}
-
-cudaError_t launch_finish(const ProductArgs& a, cudaStream_t st) {
+cudaError_t launch_logits(ProductArgs a, cudaStream_t st) {
     ProductParams p = {};
-    p.args = a;
-    p.m_group = group_of(a);
-    const uint64_t ctas = (static_cast<uint64_t>(a.m) * ((a.n + 3) / 4) + 255) / 256;
-    return launch(finish_kernel, p, std::min<uint64_t>(std::max<uint64_t>(1, ctas), 8 * kLossSms), 256, st);
+    set_shape(a);
+    a.width = std::min<uint32_t>(kSide, ctas(a.n, 32) * 32);  // statistics are of whole tiles' halves
+    p.args[0] = a;
+    return launch_tiles(p, 1, true, st);
 }
 
-cudaError_t launch_grad(const GradArgs& a, cudaStream_t st) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.vocab + kGradColumns - 1) / kGradColumns, std::min((a.n + 63) / 64 * 64, 32768u));
-    cfg.blockDim = dim3(kGradThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = AR_PDL;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void* args[] = {const_cast<GradArgs*>(&a)};
-    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(grad_kernel), args);
+cudaError_t launch_products(const ProductArgs* a, int n, uint64_t room, const RecordArgs& r, cudaStream_t st) {
+    ProductParams p = {};
+    p.record = r;
+    for (int i = 0; i < n; ++i) {
+        p.args[i] = a[i];
+        set_shape(p.args[i]);
+    }
+    if (p.args[0].out.parts) p.args[0].splits = splits_of(p.args[0], n > 1 ? &p.args[1] : nullptr, room);
+    const cudaError_t e = launch_tiles(p, n, false, st);
+    if (e != cudaSuccess || p.args[0].splits == 1) return e;
+    return launch(finish_kernel, std::min<uint32_t>(std::max<uint32_t>(1, ctas(static_cast<uint64_t>(a[0].m) * ctas(a[0].n, 4), 256)), 8 * kLossSms),
+                  256, 0, st, p.args[0]);
 }
 
 }  // namespace ar

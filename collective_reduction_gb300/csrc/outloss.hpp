@@ -88,46 +88,33 @@ struct PackArgs {
     int grad_bf16;
 };
 
-// A token's place's softmax: largest y = z c, and factor / sum 2^(y - max).
-struct RowStat {
-    float top, inv;
-};
-
 // The counted tokens at places [base, base + n) are a piece; arrays by place
-// start at the piece's first.
+// start at the piece's first.  stats: a place's largest y = z log2(e) / t and sum
+// 2^(y - largest) of every kStatColumns columns, `pitch` of them a place.
 struct JoinArgs {
-    const float2* stats;  // [parts][pitch]: largest y, sum 2^(y - largest)
+    const float2* stats;
     uint64_t pitch;
     uint32_t parts, base, n;
-    float c;              // log2(e) / t
-    float t, t2;          // t, t^2
+    float c;               // log2(e) / t
+    float t, t2;           // t, t^2
     Lists lists;
     Counted rows;
-    RowStat* stat;
-    float* gain;          // what the shares are multiplied by, factor t
-    float* loss;
-    float* losses;        // by token; null: none
-    double* sums;         // of 32 places each, from the first of the call on
+    float* losses;         // by token; null: none
+    // losses alone: the record, by the last of the CTAs, of kJoinRows places each
+    double* sums;
     uint32_t* bad;
-    uint32_t *ticket, tickets;  // the last of `tickets` CTAs writes the record
+    uint32_t *ticket, tickets;
     float* result;
-};
-
-constexpr uint32_t kJoinRows = 32;  // of a CTA
-
-// The logits' gradient of a piece from its logits, zeros in the rows behind the
-// last up to a block of products.
-struct GradArgs {
+    // with gradients: the piece's logits and the place of every loss and logit gradient;
+    // zeros in the rows behind the last up to a block of products
     const float* z;
-    uint64_t pitch;
-    uint32_t base, n, vocab;
-    float c;
-    Lists lists;
-    Counted rows;
-    const RowStat* stat;
-    const float* gain;
+    uint64_t z_pitch;
+    uint32_t vocab, columns;  // ..., of a CTA
+    float* loss;
     Planes g;
 };
+
+constexpr uint32_t kJoinRows = 8;
 
 // C = A B^T over k, A's rows and B's rows as planes; a matrix of which k runs
 // along the rows of memory is `turned`: element (row, k) lies at [k][row].
@@ -173,25 +160,31 @@ struct ProductArgs {
     uint32_t base;
     uint32_t run;          // blocks of 64 products that are summed in the tensor cores
     uint32_t splits;       // parts of k
+    uint32_t width;        // columns of a tile: a multiple of 32 up to 256
+    uint32_t group;        // rows of tiles that are worked on side by side
     const uint32_t* count;
-    int logits;            // which of the two follows
     LogitArgs logit;
     OutArgs out;
     uint32_t* status;
 };
 
+// The record of a call with gradients, written beside its last products.
+struct RecordArgs {
+    const float* loss;  // by place
+    Counted rows;
+    float* result;      // null: none
+};
+
 cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
 cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
-cudaError_t launch_join(const JoinArgs& a, cudaStream_t st);
+cudaError_t launch_join(const JoinArgs& a, cudaStream_t st);  // losses alone
+cudaError_t launch_grad(const JoinArgs& a, cudaStream_t st);  // losses and the logits' gradients
 // What the products' kernels need once on a device before their first launch.
 cudaError_t prepare_products();
-cudaError_t launch_product(const ProductArgs& a, cudaStream_t st);
-// How many parts of k suit a product of m x n values whose parts have room for
-// `room` values (m: of whole tiles).
-uint32_t splits_of(uint64_t m, uint64_t n, uint64_t k, int planes, uint64_t room);
-// Adds a split product's parts.
-cudaError_t launch_finish(const ProductArgs& a, cudaStream_t st);
-cudaError_t launch_grad(const GradArgs& a, cudaStream_t st);
+cudaError_t launch_logits(ProductArgs a, cudaStream_t st);
+// One or two products in one launch (and the finish of the first, if it is worth
+// splitting: its parts have room for `room` values).
+cudaError_t launch_products(const ProductArgs* a, int n, uint64_t room, const RecordArgs& r, cudaStream_t st);
 
 }  // namespace ar
