@@ -594,8 +594,7 @@ __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.
 // The tiles of a product and the blocks of each.
 struct Tiles {
     uint32_t m, blocks, splits, per;  // rows of A, blocks of k times passes, ... of a split
-    uint32_t k_blocks, tall, wide, group;
-    uint64_t total;
+    uint32_t k_blocks, tall, wide, group, total;  // the launch makes sure that total fits
     __device__ __forceinline__ void set(const ProductArgs& a) {
         const uint32_t count = *a.count, left = count > a.base ? count - a.base : 0;
         m = a.count_m ? min(a.m, left) : a.m;
@@ -606,13 +605,13 @@ struct Tiles {
         group = a.group;
         splits = a.splits;
         per = (blocks + splits - 1) / splits;
-        total = static_cast<uint64_t>(tall) * wide * splits;
+        total = tall * wide * splits;
     }
     // Tile t: in each split, groups of `group` rows of tiles, column by column.
-    __device__ __forceinline__ void at(uint64_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
-        const uint64_t each = static_cast<uint64_t>(tall) * wide;
-        split = static_cast<uint32_t>(t / each);
-        const uint32_t r = static_cast<uint32_t>(t - split * each);
+    __device__ __forceinline__ void at(uint32_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
+        const uint32_t each = tall * wide;
+        split = splits == 1 ? 0 : t / each;
+        const uint32_t r = t - split * each;
         const uint32_t g = r / (group * wide), rest = r - g * group * wide;
         const uint32_t rows = min(group, tall - g * group);
         nt = rest / rows;
@@ -627,33 +626,32 @@ struct Tiles {
 // many more as take the same time.
 struct Work {
     Tiles tiles[2];
-    uint64_t first;
-    uint32_t pairs, over, early;
+    uint32_t first, pairs, over, early;
     __device__ __forceinline__ void set(const ProductArgs* a, int n, uint32_t pairs_) {
         pairs = pairs_;
         tiles[0].set(a[0]);
         if (n > 1) tiles[1].set(a[1]);
         else tiles[1].total = 0;
         first = tiles[0].total / pairs;
-        over = static_cast<uint32_t>(tiles[0].total - first * pairs);
+        over = tiles[0].total - first * pairs;
         early = 0;
         const uint64_t cost = n > 1 ? static_cast<uint64_t>(tiles[1].blocks) * a[1].width : 0;
         if (over && cost)
-            early = static_cast<uint32_t>(min(static_cast<uint64_t>(tiles[0].per) * a[0].width / cost, tiles[1].total / (pairs - over)));
+            early = static_cast<uint32_t>(min(static_cast<uint64_t>(tiles[0].per) * a[0].width / cost,
+                                              static_cast<uint64_t>(tiles[1].total / (pairs - over))));
     }
     // The pair's i-th tile: of which product, which.
-    __device__ __forceinline__ bool pick(uint32_t i, uint32_t pair, uint32_t& which, uint64_t& t) const {
-        const uint64_t mine = first + (pair < over);
+    __device__ __forceinline__ bool pick(uint32_t i, uint32_t pair, uint32_t& which, uint32_t& t) const {
+        const uint32_t mine = first + (pair < over);
         which = i >= mine;
         if (!which) {
-            t = pair + static_cast<uint64_t>(i) * pairs;
+            t = pair + i * pairs;
             return true;
         }
-        const uint64_t j = i - mine;
-        const uint32_t others = pairs - over;  // pairs with fewer of the first product's tiles
-        if (pair < over) t = static_cast<uint64_t>(early) * others + j * pairs + others + pair;
+        const uint32_t j = i - mine, others = pairs - over;  // pairs with fewer of the first product's tiles
+        if (pair < over) t = early * others + j * pairs + others + pair;
         else if (j < early) t = j * others + (pair - over);
-        else t = static_cast<uint64_t>(early) * others + (j - early) * pairs + (pair - over);
+        else t = early * others + (j - early) * pairs + (pair - over);
         return t < tiles[1].total;
     }
 };
@@ -914,11 +912,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     const uint32_t tmem = lds32(bar(kTmemWord));
     griddep_wait();
     const uint32_t pair = blockIdx.x / 2;
-    uint32_t mt, nt, split, lo, n, which;
-    uint64_t t;
+    uint32_t mt, nt, split, lo, n, which, t;
     bool ok = true;
     if (warp == 0 && lane == 0) {
         uint32_t it = 0;
+        const uint32_t full0 = in_first(bar(kFullBar));
         for (uint32_t j = 0; ok && work.pick(j, pair, which, t); ++j) {
             const Tiles& tiles = work.tiles[which];
             const ProductArgs& a = p.args[which];
@@ -934,7 +932,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 if (round > 0 && !(ok = mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1))) break;
                 const int k0 = static_cast<int>(k * kDeep);
                 const int za = planes ? plane_a(q) : 0, zb = planes ? plane_b(q) : 0;
-                const uint32_t to = base + s * kStageBytes, full = in_first(bar(kFullBar + s));
+                const uint32_t to = base + s * kStageBytes, full = full0 + 8 * s;
                 if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
                 if (at) {
                     tma_load(to, ma, m0, k0, za, full);
@@ -961,7 +959,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             const ProductArgs& a = p.args[which];
             work.tiles[which].at(t, mt, nt, split, lo, n);
             const bool turned = !LOGITS && a.a.turned;
-            const uint32_t desc = mma_desc(turned, BT, a.width), a_step = turned ? 2048 : 32, run = a.run;
+            // a descriptor's address is its low bits, in units of 16 bytes
+            const uint64_t a0 = operand_desc(base, turned), b0 = operand_desc(base + kOperandBytes, BT);
+            const uint32_t desc = mma_desc(turned, BT, a.width), a_step = turned ? 2048 / 16 : 32 / 16, run = a.run;
             for (uint32_t i = 0; i < n && ok; ++done) {
                 const uint32_t b = done & 1, acc = tmem + b * kSide;
                 if (done >= 2 && !(ok = mbar_wait_here(bar(kFreeBar + b), (done / 2 - 1) & 1))) break;
@@ -971,11 +971,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                     const uint32_t s = it % kStages;
                     if (!(ok = mbar_wait_here(bar(kFullBar + s), (it / kStages) & 1))) break;
                     tmem_fence_after();
-                    const uint32_t at = base + s * kStageBytes;
+                    const uint32_t at = s * (kStageBytes / 16);
 #pragma unroll
                     for (uint32_t k = 0; k < kDeep / 16; ++k)
-                        mma(acc, operand_desc(at + k * a_step, turned),
-                            operand_desc(at + kOperandBytes + k * (BT ? 2048 : 32), BT), desc, j > i || k > 0);
+                        mma(acc, a0 + (at + k * a_step), b0 + (at + k * (BT ? 2048 / 16 : 32 / 16)), desc, j > i || k > 0);
                     mma_commit(bar(kEmptyBar + s));
                 }
                 if (!ok) break;
@@ -1185,8 +1184,8 @@ cudaError_t launch_join(const JoinArgs& a, cudaStream_t st) {
 cudaError_t launch_grad(const JoinArgs& a0, cudaStream_t st) {
     JoinArgs a = a0;
     const uint32_t rows = ctas(a.n, 64) * 64;
-    a.columns = 32 * kGradThreads;  // less while a wave of CTAs is not full
-    while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 8 * kLossSms) a.columns /= 2;
+    a.columns = 128 * kGradThreads;  // less while a few waves of CTAs are not full
+    while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 40 * kLossSms) a.columns /= 2;
     return launch(grad_kernel, dim3(ctas(a.vocab, a.columns), std::min(rows, 32768u)), kGradThreads, 0, st, a);
 }
 
@@ -1210,6 +1209,7 @@ cudaError_t launch_tiles(ProductParams& p, int n, bool logits, cudaStream_t st) 
         if (e != cudaSuccess) return e;
         tiles += tall_of(a) * wide_of(a) * a.splits;
     }
+    if (tiles > 0x7FFFFFFFu) return cudaErrorInvalidValue;  // 2^22 tokens and 2^24 entries make 2^30
     const uint32_t pairs = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(1, tiles), kLossSms / 2));
     return launch(logits ? product_kernel<true> : product_kernel<false>, 2 * pairs, kProductThreads, kProductSmem, st, p, n);
 }
