@@ -28,11 +28,11 @@ constexpr uint64_t kPiecesKept = 4;
 constexpr uint64_t kPackBytes = 1ull << 30;
 
 // Blocks of 64 products that are summed in the tensor cores before float32 sums
-// take over: for float32 inputs (six blocks for one) and results, for logits of
-// bf16 inputs, and for bf16 results (whose rounding is 2^-8).  Logits of 4096
-// tokens, hidden size 2048 and 50001 entries: 605 us in runs of 4, 520 of 8, 506
-// of 16, 507 in one.
-constexpr uint32_t kExactRun = 8, kLogitRun = 16, kLongRun = 1u << 30;
+// take over: of float32 inputs (six products a block), of bf16 inputs for logits
+// and for float32 results, and for bf16 results (whose rounding is 2^-8).  Logits
+// of 4096 tokens, hidden size 2048 and 50001 entries: 605 us in runs of 4, 520 of
+// 8, 506 of 16, 507 in one.
+constexpr uint32_t kFloatRun = 2, kLogitRun = 16, kExactRun = 8, kLongRun = 1u << 30;
 
 ar_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
@@ -96,7 +96,7 @@ ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype
     l.ids = l.add(4 * k);
     l.shares = l.add(4 * k);
     l.logits = l.add(4 * k);
-    l.stats = l.add(8 * l.piece * (l.wide / ar::kStatColumns));
+    l.stats = l.add(8 * std::max(l.piece * (l.wide / ar::kStatColumns), ar::kFewTokens * (l.wide / ar::kFewColumns)));
     l.loss = l.add(4 * n);
     l.hidden = l.add(2 * l.planes * n * l.pitch);
     l.weight = l.add(2 * l.planes * l.pack * l.pitch);
@@ -225,14 +225,85 @@ struct Call {
         if (e == cudaSuccess) e = next;
     }
 
+    uint32_t run_of(ar_dtype result) const {
+        return h->dtype == AR_FLOAT32 ? kFloatRun : result == AR_FLOAT32 ? kExactRun : kLongRun;
+    }
+
     // Of the counted tokens at places [r, r + m).
     ar::ProductArgs product(uint64_t r) const {
         ar::ProductArgs p = {};
         p.count = rows.count;
         p.base = static_cast<uint32_t>(r);
-        p.splits = 1;
+        p.out.factor = rows.factor;
+        p.out.t = static_cast<float>(t);
         p.status = h->at<uint32_t>(h->l.status);
         return p;
+    }
+
+    // Whether the call is on few enough tokens for the kernels that read the weights
+    // as they are, of eight tokens at a time.  Losses alone / with gradients, us, those
+    // kernels against tiles:
+    //                       float32 W   n = 8             bf16 W   n = 2           n = 4            n = 8
+    //   4096 x 128000       2097 MB   658 1513 : 1798 6272   257 720 : 287 1843   291 913 : 225 1789   569 1328 : 229 1783
+    //   1023 x 32003         131 MB    64  214 :  142  656    27 120 :  66  363    39 150 :  65  357    50  174 :  64  356
+    //   640 x 10007           26 MB    23   62 :   49  156    17  43 :  23   53    17  51 :  22   51    31   70 :  21   51
+    //   192 x 4001             3 MB    16   34 :   25   49    15  25 :  17   33    14  27 :  17   33    16   35 :  17   33
+    // The tiles' float32 pays for packing the weights in planes, their odd bf16 rows for
+    // packing them at all.  More than eight tokens of float32 are taken in groups.
+    bool few() const {
+        const uint64_t bytes = static_cast<uint64_t>(vocab) * width * esize(h->dtype), mb = 1u << 20;
+        if (n == 0) return false;
+        if (h->dtype == AR_FLOAT32) return n <= 8 || (n <= 16 && bytes >= 8 * mb) || (n <= 24 && grads && bytes >= 64 * mb);
+        if (!weight_as_is()) return n <= 8;
+        return n <= 2 || (n <= 4 && (grads || bytes < 64 * mb)) || (n <= 8 && grads && bytes >= 64 * mb);
+    }
+
+    ar::FewArgs few_args(uint64_t r) const {
+        ar::FewArgs f = {};
+        f.x = a->hidden;
+        f.w = a->weight;
+        f.x_stride = a->hidden_stride;
+        f.w_stride = a->weight_stride;
+        f.bf16 = h->dtype == AR_BFLOAT16;
+        f.base = static_cast<uint32_t>(r);
+        f.n = static_cast<uint32_t>(std::min<uint64_t>(n - r, ar::kFewTokens));
+        f.width = width;
+        f.vocab = vocab;
+        f.rows = rows;
+        f.c = c;
+        f.lists = lists;
+        f.stats = h->at<float2>(h->l.stats);
+        f.stats_pitch = h->l.wide / ar::kFewColumns;
+        if (grads) f.z = h->at<float>(h->l.z);
+        f.z_pitch = h->l.wide;
+        return f;
+    }
+
+    ar::FewArgs few_gradients(ar::FewArgs f) const {
+        f.g = grad(0);
+        f.t = static_cast<float>(t);
+        f.grad_x = a->grad_hidden;
+        f.grad_w = a->grad_weight;
+        f.grad_x_stride = a->grad_hidden_stride;
+        f.grad_w_stride = a->grad_weight_stride;
+        f.grad_x_bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
+        f.grad_w_bf16 = a->grad_weight_dtype == AR_BFLOAT16;
+        f.accumulate = a->accumulate;
+        f.parts = h->at<float>(h->l.part);
+        f.room = h->l.part_room;
+        return f;
+    }
+
+    // Logits, losses and gradients of a few tokens; the last group's CTAs write the record.
+    void few_tokens() {
+        for (uint64_t r = 0; r < n; r += ar::kFewTokens) {
+            const ar::FewArgs f = few_args(r);
+            run(ar::launch_few_logits(f, st));
+            join(r, f.n, f.stats_pitch, ar::kFewColumns, 1);
+            if (!grads) continue;
+            const bool last = r + f.n >= n;
+            run(ar::launch_few_gradients(few_gradients(f), {h->at<float>(h->l.loss), rows, last ? a->result : nullptr}, st));
+        }
     }
 
     // Logits and losses of a piece, and the logits' gradients.
@@ -247,7 +318,7 @@ struct Call {
             p.count_m = 1;
             p.n = static_cast<uint32_t>(end - v);
             p.k = width;
-            p.run = h->dtype == AR_BFLOAT16 ? kLogitRun : kExactRun;
+            p.run = h->dtype == AR_BFLOAT16 ? kLogitRun : kFloatRun;
             p.logit.c = c;
             p.logit.v0 = static_cast<uint32_t>(v);
             p.logit.lists = lists;
@@ -258,14 +329,18 @@ struct Call {
             p.logit.z_pitch = h->l.wide;
             run(ar::launch_logits(p, st));
         }
+        join(r, m, pitch, ar::kStatColumns, 64);  // whole blocks of products
+    }
+
+    void join(uint64_t r, uint32_t m, uint64_t pitch, uint32_t columns, uint32_t round) {
         ar::JoinArgs j = {};
         j.stats = h->at<float2>(h->l.stats);
         j.pitch = pitch;
-        j.parts = static_cast<uint32_t>(up(h->vocab, ar::kStatColumns) / ar::kStatColumns);
+        j.parts = static_cast<uint32_t>(up(h->vocab, columns) / columns);
+        j.round = round;
         j.base = static_cast<uint32_t>(r);
         j.n = m;
         j.c = c;
-        j.t = static_cast<float>(t);
         j.t2 = static_cast<float>(t * t);
         j.lists = lists;
         j.rows = rows;
@@ -275,7 +350,7 @@ struct Call {
             j.z_pitch = h->l.wide;
             j.vocab = vocab;
             j.loss = h->at<float>(h->l.loss) + r;
-            j.g = grad(r);
+            j.g = grad(columns == ar::kFewColumns ? 0 : r);
             run(ar::launch_grad(j, st));
         } else {
             j.sums = h->at<double>(h->l.sums);
@@ -296,7 +371,7 @@ struct Call {
         p.n = width;
         p.k = m;
         p.count_k = 1;
-        p.run = a->grad_weight_dtype == AR_BFLOAT16 ? kLongRun : kExactRun;
+        p.run = run_of(a->grad_weight_dtype);
         p.out.out = a->grad_weight;
         p.out.stride = a->grad_weight_stride;
         p.out.bf16 = a->grad_weight_dtype == AR_BFLOAT16;
@@ -320,7 +395,7 @@ struct Call {
         p.count_m = 1;
         p.n = width;
         p.k = static_cast<uint32_t>(end - v);
-        p.run = a->grad_hidden_dtype == AR_BFLOAT16 ? kLongRun : kExactRun;
+        p.run = run_of(a->grad_hidden_dtype);
         p.out.out = a->grad_hidden;
         p.out.stride = a->grad_hidden_stride;
         p.out.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
@@ -363,7 +438,18 @@ struct Call {
         r.rows = rows;
         r.result = a->result;
         r.ticket = h->at<uint32_t>(h->l.ticket);
+        if (few()) {
+            r.losses = a->losses;
+            r.grad = a->accumulate ? nullptr : a->grad_hidden;
+            r.grad_stride = a->grad_hidden_stride;
+            r.grad_bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
+            r.width = width;
+        }
         run(ar::launch_rows(r, st));
+        if (few()) {
+            few_tokens();
+            return cuda_status(e);
+        }
         if (n > 0) {
             ar::PackArgs p = {};
             p.src = a->hidden;

@@ -5,7 +5,7 @@
 // With z = X W^T, y = z log2(e) / t and a token's shares p over a short list
 // of ids, the loss is t^2 (sum p log p - sum p z / t + log sum exp(z / t)) and
 // its gradient by z, with the factor f of the record,
-//   g = f t (2^(y - top) / sum 2^(y - top) - p),   dX = g W,   dW = g^T X.
+//   g = 2^(y - top) / sum 2^(y - top) - p,   dX = f t g W,   dW = f t g^T X.
 #include <cuda.h>  // the tensor map's types only: the driver call is resolved at run time
 
 #include <algorithm>
@@ -189,6 +189,17 @@ __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant
         const uint32_t who = __ballot_sync(kFull, counts);
         if (counts) a.rows.row[place + __popc(who & ((1u << lane) - 1))] = static_cast<int32_t>(i);
         place += __popc(who);
+    }
+    if (a.losses || a.grad) {  // a few tokens
+        __syncthreads();
+        for (uint32_t i = 0; i < a.n; ++i) {
+            if (a.lists.counted[i]) continue;
+            if (a.losses && tid == 0) a.losses[i] = 0.f;
+            for (uint32_t c = tid; a.grad && c < a.width; c += kRowThreads) {
+                if (a.grad_bf16) static_cast<uint16_t*>(a.grad)[i * a.grad_stride + c] = 0;
+                else static_cast<float*>(a.grad)[i * a.grad_stride + c] = 0.f;
+            }
+        }
     }
     if (tid == 0) {
         const uint32_t n = sums[31];
@@ -392,8 +403,10 @@ constexpr int kGradThreads = 256;
 
 // A CTA a place's `columns` columns: the statistics (of the whole row, in every
 // one of its CTAs), then
-//   g = 2^(y - top) factor t / sum - share factor t
-// from the logits, then the few columns of the row's list.  Bound by HBM: a logit's
+//   g = 2^(y - top) / sum - share
+// from the logits, then the few columns of the row's list.  The factor comes with
+// the products' float32 sums: in bf16 a token's largest gradients, near -1, would all
+// carry the factor's own rounding.  Bound by HBM: a logit's
 // 4 bytes in and its gradient's 2 (float32: 6) out.
 __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ JoinArgs a) {
     __shared__ float2 part[kGradThreads / 32];
@@ -402,9 +415,9 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t count = *a.rows.count, m = count > a.base ? min(a.n, count - a.base) : 0;
-    for (uint64_t r = blockIdx.y; r < (m + 63) / 64 * 64; r += gridDim.y) {
+    for (uint64_t r = blockIdx.y; r < (m + a.round - 1) / a.round * a.round; r += gridDim.y) {
         const bool in = r < m;
-        float top = 0.f, inv = 0.f, gain = 0.f;
+        float top = 0.f, inv = 0.f;
         uint64_t token = 0;
         if (in) {
             float sum;
@@ -417,8 +430,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             for (int w = 1; w < kGradThreads / 32; ++w) join_stat(top, sum, part[w].x, part[w].y);
             token = a.rows.row[a.base + r];
             const float entropy = a.lists.entropy[token];  // NaN: a list that is not valid
-            gain = entropy == entropy && sum > 0.f ? __fmul_rn(*a.rows.factor, a.t) : __int_as_float(0x7FC00000);
-            inv = __fdiv_rn(gain, sum);
+            inv = entropy == entropy && sum > 0.f ? __fdiv_rn(1.f, sum) : __int_as_float(0x7FC00000);
             if (blockIdx.x == 0 && warp == 0) {
                 const float loss = row_loss(a, token, top, sum, lane);
                 if (lane == 0) {
@@ -451,7 +463,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             const uint32_t v = static_cast<uint32_t>(a.lists.ids[list + k]);
             if (v < lo || v >= hi) continue;
             const float share = a.lists.shares ? a.lists.shares[list + k] : 1.f;
-            float x = __fsub_rn(value(a.lists.logits[list + k]), __fmul_rn(share, gain));
+            float x = __fsub_rn(value(a.lists.logits[list + k]), share);
             for (int q = 0; q < a.g.planes; ++q) g[q * a.g.plane + v] = split_plane(x);
         }
     }
@@ -469,7 +481,7 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int 
 // tile of 256 x 256, each holding 128 rows of A and of B in shared memory and 128
 // rows of C in its tensor memory, twice (the epilogue of one tile runs beside the
 // products of the next).  Persistent: pairs take tiles in turn.  Warp 0 loads (TMA,
-// a ring of kStages blocks of 64 products), warp 1 of the pair's first CTA issues
+// a ring of blocks of 64 products), warp 1 of the pair's first CTA issues
 // the products, warps 4 to 11 are the epilogue: a thread half a row.
 //
 // The tensor cores cut sums off where float32 would round them.  Products whose
@@ -479,8 +491,11 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int 
 constexpr int kSide = 256;             // rows and columns of a pair's tile
 constexpr int kHalf = kSide / 2;       // ... of A and of B in one CTA
 constexpr int kDeep = 64;              // products of a block: 128 bytes of bf16
-constexpr int kStages = 6;
-constexpr uint32_t kOperandBytes = kHalf * kDeep * 2, kStageBytes = 2 * kOperandBytes;
+constexpr uint32_t kOperandBytes = kHalf * kDeep * 2;  // of a block of A or B, one plane, in one CTA
+constexpr int kOperands = 12;          // of them in shared memory
+// Blocks in flight: of bf16 six, of float32 two of six operands each, whose six
+// products read them where they are.
+__host__ __device__ constexpr int stages_of(int planes) { return kOperands / (2 * planes); }
 constexpr int kProductThreads = 384, kEpilogueWarp = 4, kEpilogueWarps = 8;
 constexpr uint32_t kStagedBytes = 32 * 128;  // of an epilogue warp: 32 rows' part of a result on its way out
 constexpr int kTmemColumns = 512;
@@ -490,14 +505,14 @@ static_assert(kSide == static_cast<int>(kLossTile) && kHalf == static_cast<int>(
 // Barriers, in 8-byte words of shared memory.
 enum : uint32_t {
     kFullBar = 0,                      // a stage's blocks are there (the pair's; in its first CTA)
-    kEmptyBar = kFullBar + kStages,    // ... have been read
-    kReadyBar = kEmptyBar + kStages,   // an accumulator is complete
+    kEmptyBar = kFullBar + stages_of(1),  // ... have been read
+    kReadyBar = kEmptyBar + stages_of(1),  // an accumulator is complete
     kFreeBar = kReadyBar + 2,          // ... has been read (in the pair's first CTA)
     kDoneBar = kFreeBar + 2,           // the products issued are complete
     kTmemWord = kDoneBar + 1,
     kBarWords = kTmemWord + 1
 };
-constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
+constexpr uint32_t kProductSmem = kOperands * kOperandBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
 
 // One or two products in one launch.
 struct ProductParams {
@@ -593,13 +608,12 @@ __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.
 
 // The tiles of a product and the blocks of each.
 struct Tiles {
-    uint32_t m, blocks, splits, per;  // rows of A, blocks of k times passes, ... of a split
-    uint32_t k_blocks, tall, wide, group, total;  // the launch makes sure that total fits
+    uint32_t m, blocks, splits, per;  // rows of A, blocks of k, ... of a split
+    uint32_t tall, wide, group, total;  // the launch makes sure that total fits
     __device__ __forceinline__ void set(const ProductArgs& a) {
         const uint32_t count = *a.count, left = count > a.base ? count - a.base : 0;
         m = a.count_m ? min(a.m, left) : a.m;
-        k_blocks = ((a.count_k ? min(a.k, left) : a.k) + kDeep - 1) / kDeep;
-        blocks = k_blocks * (a.a.m.planes == 1 ? 1 : 6);
+        blocks = ((a.count_k ? min(a.k, left) : a.k) + kDeep - 1) / kDeep;
         tall = (m + kSide - 1) / kSide;
         wide = (a.n + a.width - 1) / a.width;
         group = a.group;
@@ -656,9 +670,9 @@ struct Work {
     }
 };
 
-// The planes of pass q of float32 operands, small products first.
-__device__ __forceinline__ int plane_a(uint32_t q) { return (0x001012 >> (4 * q)) & 3; }
-__device__ __forceinline__ int plane_b(uint32_t q) { return (0x010210 >> (4 * q)) & 3; }
+// The planes of product q of the six of a float32 block, small ones first.
+__host__ __device__ constexpr uint32_t plane_a(uint32_t q) { return (0x001012 >> (4 * q)) & 3; }
+__host__ __device__ constexpr uint32_t plane_b(uint32_t q) { return (0x010210 >> (4 * q)) & 3; }
 
 // A row's next id at or behind column v, as its place in the list.
 __device__ __forceinline__ int first_id(const int32_t* ids, int top, int32_t v) {
@@ -681,16 +695,26 @@ struct Place {
     uint32_t lane;
 };
 
-// The warp's 32 rows' 128 bytes each, word(0..31) this lane's, to shared memory; use() is
-// then given every row's 16 bytes by eight lanes a row: whole lines for memory.
-template <class Word, class Use>
-__device__ __forceinline__ void transposed(const Place& p, Word word, Use use) {
+// The warp's 32 rows' 128 bytes each, word(0..31) this lane's, to shared memory ...
+template <class Word>
+__device__ __forceinline__ void stage(const Place& p, Word word) {
     __syncwarp();
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j)
         sts128(p.staged + p.lane * 128 + ((j ^ (p.lane & 7)) << 4),
                make_uint4(word(4 * j), word(4 * j + 1), word(4 * j + 2), word(4 * j + 3)));
     __syncwarp();
+}
+
+// ... whose rows' words are then a lane's each,
+__device__ __forceinline__ uint32_t staged_word(const Place& p, uint32_t r) {
+    return lds32(p.staged + r * 128 + ((p.lane / 4 ^ (r & 7)) << 4) + p.lane % 4 * 4);
+}
+
+// or given to use() in 16 bytes by eight lanes a row: whole lines for memory.
+template <class Word, class Use>
+__device__ __forceinline__ void transposed(const Place& p, Word word, Use use) {
+    stage(p, word);
 #pragma unroll 4
     for (uint32_t i = 0; i < 8; ++i) {
         const uint32_t r = 4 * i + p.lane / 8, j = p.lane % 8;
@@ -769,22 +793,31 @@ struct LogitTile {
 
 // Four columns of a row of the caller's matrix.
 __device__ __forceinline__ void store_four(const OutArgs& o, uint64_t at, uint32_t cols, float4 x) {
-    const float v[4] = {x.x, x.y, x.z, x.w};
-    if (cols >= 4 && !o.accumulate) {
+    if (cols >= 4) {
         if (o.bf16) {
             uint16_t* p = static_cast<uint16_t*>(o.out) + at;
             if ((reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+                if (o.accumulate) {
+                    const uint2 y = *reinterpret_cast<const uint2*>(p);
+                    x = make_float4(__fadd_rn(x.x, bf_lo(y.x)), __fadd_rn(x.y, bf_hi(y.x)), __fadd_rn(x.z, bf_lo(y.y)),
+                                    __fadd_rn(x.w, bf_hi(y.y)));
+                }
                 *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
                 return;
             }
         } else {
             float* p = static_cast<float*>(o.out) + at;
             if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+                if (o.accumulate) {
+                    const float4 y = *reinterpret_cast<const float4*>(p);
+                    x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+                }
                 *reinterpret_cast<float4*>(p) = x;
                 return;
             }
         }
     }
+    const float v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (uint32_t j = 0; j < 4; ++j)
         if (j < cols) store_out(o.out, at + j, o.bf16, o.accumulate, v[j]);
@@ -793,54 +826,108 @@ __device__ __forceinline__ void store_four(const OutArgs& o, uint64_t at, uint32
 struct OutTile {
     const OutArgs& o;
     uint64_t to = 0;  // this lane's row in the caller's matrix
+    float scale;
 
     __device__ __forceinline__ OutTile(const ProductArgs& a, const Place& p) : o(a.out) {
+        scale = __fmul_rn(*o.factor, o.t);
         if (p.in) to = (o.row ? static_cast<uint64_t>(o.row[p.row]) : p.row) * o.stride;
     }
 
+    // Rows off a 16-byte boundary go row by row, a lane a word: lines are written
+    // whole but at their ends.  (By 4-byte stores of 16 bytes' lanes, 30 MB of float32
+    // rows of 515 took 60 us longer.)
     __device__ __forceinline__ void finish(const Place& p, float (&z)[4][32], float* part) const {
         if (p.cols == 0) return;
         const uint32_t rows = __popc(__ballot_sync(kFull, p.in));  // the warp's first ones
         const uint64_t row0 = p.row - p.lane;
         float* sum = part ? part : o.sum;
         const uint64_t pitch = part ? o.part_pitch : o.sum_pitch;
+        const uintptr_t mine = reinterpret_cast<uintptr_t>(o.out) + (to + p.n0) * (o.bf16 ? 2 : 4);
+        const bool aligned = __all_sync(kFull, (mine & 15) == 0 || !p.in);
         if (!sum && !o.add && o.bf16 && !o.accumulate) {
-            // two values a word: 64 columns at a time; off alignment or at the edge by pieces
+            // two values a word: 64 columns at a time
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 auto word = [&](uint32_t j) {
-                    return pack_bf16x2(z[2 * h + j / 16][2 * j % 32], z[2 * h + j / 16][2 * j % 32 + 1]);
+                    return pack_bf16x2(__fmul_rn(z[2 * h + j / 16][2 * j % 32], scale), __fmul_rn(z[2 * h + j / 16][2 * j % 32 + 1], scale));
                 };
-                transposed(p, word, [&](uint32_t r, uint32_t j, uint4 x) {
-                    const uint32_t c = 64 * h + 8 * j;
-                    uint16_t* q = static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, r) + p.n0 + c;
-                    if (r >= rows || c >= p.cols) return;
-                    if (c + 8 <= p.cols && (reinterpret_cast<uintptr_t>(q) & 15) == 0) {
-                        *reinterpret_cast<uint4*>(q) = x;
-                        return;
-                    }
-                    const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+                const uint32_t c0 = 64 * h;
+                if (c0 >= p.cols) break;
+                if (aligned && c0 + 64 <= p.cols) {
+                    transposed(p, word, [&](uint32_t r, uint32_t j, uint4 x) {
+                        uint16_t* q = static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, r) + p.n0 + c0 + 8 * j;
+                        if (r < rows) *reinterpret_cast<uint4*>(q) = x;
+                    });
+                    continue;
+                }
+                stage(p, word);
+                const uint32_t c = c0 + 2 * p.lane;
+                for (uint32_t r0 = 0; r0 < rows; r0 += 8) {  // eight rows' loads before their stores
+                    uint32_t x[8], before[8];
+                    uint16_t* q[8];
 #pragma unroll
-                    for (uint32_t i = 0; i < 8; ++i)
-                        if (c + i < p.cols) q[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
-                });
+                    for (uint32_t r = 0; r < 8; ++r) {
+                        x[r] = staged_word(p, r0 + r);
+                        q[r] = static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, r0 + r) + p.n0 + c;
+                    }
+#pragma unroll
+                    for (uint32_t r = 0; r < 8; ++r) before[r] = __shfl_up_sync(kFull, x[r], 1);
+#pragma unroll
+                    for (uint32_t r = 0; r < 8; ++r) {
+                        if (r0 + r >= rows) break;
+                        if ((reinterpret_cast<uintptr_t>(q[r]) & 2) == 0) {
+                            if (c + 1 < p.cols) *reinterpret_cast<uint32_t*>(q[r]) = x[r];
+                            else if (c < p.cols) *q[r] = static_cast<uint16_t>(x[r]);
+                        } else {
+                            // this lane's first value goes with the one before it
+                            if (p.lane == 0) *q[r] = static_cast<uint16_t>(x[r]);
+                            else if (c < p.cols) *reinterpret_cast<uint32_t*>(q[r] - 1) = (before[r] >> 16) | (x[r] << 16);
+                            else if (c - 1 < p.cols) q[r][-1] = static_cast<uint16_t>(before[r] >> 16);
+                            if (p.lane == 31 && c + 1 < p.cols) q[r][1] = static_cast<uint16_t>(x[r] >> 16);
+                        }
+                    }
+                }
             }
             return;
         }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-            transposed(p, [&](uint32_t j) { return __float_as_uint(z[h][j]); }, [&](uint32_t r, uint32_t j, uint4 bits) {
-                const uint32_t c = 32 * h + 4 * j;
-                const uint64_t at = __shfl_sync(kFull, to, r) + p.n0 + c;
-                if (r >= rows || c >= p.cols) return;
-                float4 x = floats(bits);
-                if (o.add) {
-                    const float4 y = *reinterpret_cast<const float4*>(o.add + (row0 + r) * o.sum_pitch + p.n0 + c);
-                    x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+            const uint32_t c0 = 32 * h;
+            auto word = [&](uint32_t j) { return __float_as_uint(__fmul_rn(z[h][j], scale)); };
+            if (c0 >= p.cols) break;
+            if (sum || (aligned && c0 + 32 <= p.cols)) {
+                transposed(p, word, [&](uint32_t r, uint32_t j, uint4 bits) {
+                    const uint32_t c = c0 + 4 * j;
+                    const uint64_t at = __shfl_sync(kFull, to, r) + p.n0 + c;
+                    if (r >= rows || c >= p.cols) return;
+                    float4 x = floats(bits);
+                    if (o.add) {
+                        const float4 y = *reinterpret_cast<const float4*>(o.add + (row0 + r) * o.sum_pitch + p.n0 + c);
+                        x = make_float4(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y), __fadd_rn(x.z, y.z), __fadd_rn(x.w, y.w));
+                    }
+                    if (sum) *reinterpret_cast<float4*>(sum + (row0 + r) * pitch + p.n0 + c) = x;  // whole tiles there
+                    else store_four(o, at, 4, x);
+                });
+                continue;
+            }
+            stage(p, word);
+            const uint32_t c = c0 + p.lane;
+            for (uint32_t r0 = 0; r0 < rows; r0 += 8) {
+                float x[8];
+                uint64_t at[8];
+#pragma unroll
+                for (uint32_t r = 0; r < 8; ++r) {
+                    x[r] = __uint_as_float(staged_word(p, r0 + r));
+                    at[r] = __shfl_sync(kFull, to, r0 + r) + p.n0 + c;
                 }
-                if (sum) *reinterpret_cast<float4*>(sum + (row0 + r) * pitch + p.n0 + c) = x;
-                else store_four(o, at, p.cols - c, x);
-            });
+                if (c >= p.cols) continue;
+#pragma unroll
+                for (uint32_t r = 0; r < 8; ++r) {
+                    if (r0 + r >= rows) break;
+                    if (o.add) x[r] = __fadd_rn(x[r], o.add[(row0 + r0 + r) * o.sum_pitch + p.n0 + c]);
+                    store_out(o.out, at[r], o.bf16, o.accumulate, x[r]);
+                }
+            }
         }
     }
 };
@@ -869,12 +956,13 @@ __device__ void write_record(const RecordArgs& a, uint32_t lane) {
 
 // LOGITS: one product of two matrices along k, the softmax's statistics in its
 // epilogue.  Otherwise one or two with B turned, into the caller's memory.
-template <bool LOGITS>
+template <bool LOGITS, int kPlanes>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p, int products) {
     extern __shared__ char raw[];
     __shared__ Work work;
     constexpr bool BT = !LOGITS;
+    constexpr uint32_t kStages = stages_of(kPlanes), kStageBytes = 2 * kPlanes * kOperandBytes;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;  // the same in both CTAs
     const uint32_t staged = base + kStages * kStageBytes, bars = staged + kEpilogueWarps * kStagedBytes;
     auto bar = [bars](uint32_t i) { return bars + 8 * i; };
@@ -915,46 +1003,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     uint32_t mt, nt, split, lo, n, which, t;
     bool ok = true;
     if (warp == 0 && lane == 0) {
-        uint32_t it = 0;
         const uint32_t full0 = in_first(bar(kFullBar));
+        uint32_t s = 0, round = 0;
         for (uint32_t j = 0; ok && work.pick(j, pair, which, t); ++j) {
-            const Tiles& tiles = work.tiles[which];
             const ProductArgs& a = p.args[which];
             const CUtensorMap *ma = &p.a[which], *mb = &p.b[which];
-            tiles.at(t, mt, nt, split, lo, n);
-            const bool planes = a.a.m.planes > 1, at = !LOGITS && a.a.turned;
+            work.tiles[which].at(t, mt, nt, split, lo, n);
+            const bool at = !LOGITS && a.a.turned;
             const int m0 = static_cast<int>(mt * kSide + rank * kHalf);
             const int n0 = static_cast<int>(nt * a.width + rank * (a.width / 2));
-            const uint32_t k_blocks = tiles.k_blocks;
-            uint32_t q = lo / max(1u, k_blocks), k = lo - q * k_blocks;
-            for (uint32_t i = 0; i < n; ++i, ++it) {
-                const uint32_t s = it % kStages, round = it / kStages;
+            for (uint32_t i = 0; i < n; ++i) {
                 if (round > 0 && !(ok = mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1))) break;
-                const int k0 = static_cast<int>(k * kDeep);
-                const int za = planes ? plane_a(q) : 0, zb = planes ? plane_b(q) : 0;
-                const uint32_t to = base + s * kStageBytes, full = full0 + 8 * s;
+                const int k0 = static_cast<int>((lo + i) * kDeep);
+                const uint32_t full = full0 + 8 * s;
+                uint32_t to = base + s * kStageBytes;
                 if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
-                if (at) {
-                    tma_load(to, ma, m0, k0, za, full);
-                    tma_load(to + kOperandBytes / 2, ma, m0 + 64, k0, za, full);
-                } else {
-                    tma_load(to, ma, k0, m0, za, full);
+                for (int q = 0; q < kPlanes; ++q, to += 2 * kOperandBytes) {
+                    if (at) {
+                        tma_load(to, ma, m0, k0, q, full);
+                        tma_load(to + kOperandBytes / 2, ma, m0 + 64, k0, q, full);
+                    } else {
+                        tma_load(to, ma, k0, m0, q, full);
+                    }
+                    if (BT) {
+                        tma_load(to + kOperandBytes, mb, n0, k0, q, full);
+                        tma_load(to + kOperandBytes + kOperandBytes / 2, mb, n0 + 64, k0, q, full);
+                    } else {
+                        tma_load(to + kOperandBytes, mb, k0, n0, q, full);
+                    }
                 }
-                if (BT) {
-                    tma_load(to + kOperandBytes, mb, n0, k0, zb, full);
-                    tma_load(to + kOperandBytes + kOperandBytes / 2, mb, n0 + 64, k0, zb, full);
-                } else {
-                    tma_load(to + kOperandBytes, mb, k0, n0, zb, full);
-                }
-                if (++k == k_blocks) k = 0, ++q;
+                if (++s == kStages) s = 0, ++round;
             }
         }
         // the last blocks have been read before the pair's memory goes
-        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-            if (!mbar_wait_here(bar(kEmptyBar + i % kStages), (i / kStages) & 1)) ok = false;
+        for (uint32_t i = 0; i < kStages; ++i) {
+            if (round > 0 && !mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1)) ok = false;
+            if (++s == kStages) s = 0, ++round;
+        }
         if (rank == 1 && !mbar_wait_here(bar(kDoneBar), 0)) ok = false;
     } else if (warp == 1 && lane == 0 && rank == 0) {
-        uint32_t it = 0, done = 0;
+        uint32_t s = 0, phase = 0, done = 0;
         for (uint32_t i0 = 0; ok && work.pick(i0, pair, which, t); ++i0) {
             const ProductArgs& a = p.args[which];
             work.tiles[which].at(t, mt, nt, split, lo, n);
@@ -967,15 +1055,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 if (done >= 2 && !(ok = mbar_wait_here(bar(kFreeBar + b), (done / 2 - 1) & 1))) break;
                 tmem_fence_after();
                 const uint32_t end = n - i > run ? i + run : n;
-                for (uint32_t j = i; j < end; ++j, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!(ok = mbar_wait_here(bar(kFullBar + s), (it / kStages) & 1))) break;
+                for (uint32_t j = i; j < end; ++j) {
+                    if (!(ok = mbar_wait_here(bar(kFullBar + s), phase))) break;
                     tmem_fence_after();
                     const uint32_t at = s * (kStageBytes / 16);
 #pragma unroll
-                    for (uint32_t k = 0; k < kDeep / 16; ++k)
-                        mma(acc, a0 + (at + k * a_step), b0 + (at + k * (BT ? 2048 / 16 : 32 / 16)), desc, j > i || k > 0);
+                    for (uint32_t q = 0; q < (kPlanes == 1 ? 1 : 6); ++q) {
+                        const uint32_t pa = at + (kPlanes == 1 ? 0 : plane_a(q) * (2 * kOperandBytes / 16));
+                        const uint32_t pb = at + (kPlanes == 1 ? 0 : plane_b(q) * (2 * kOperandBytes / 16));
+#pragma unroll
+                        for (uint32_t k = 0; k < kDeep / 16; ++k)
+                            mma(acc, a0 + (pa + k * a_step), b0 + (pb + k * (BT ? 2048 / 16 : 32 / 16)), desc,
+                                j > i || q > 0 || k > 0);
+                    }
                     mma_commit(bar(kEmptyBar + s));
+                    if (++s == kStages) s = 0, phase ^= 1;
                 }
                 if (!ok) break;
                 mma_commit(bar(kReadyBar + b));
@@ -1107,6 +1201,258 @@ cudaError_t make_map(const Operand& o, CUtensorMap* map) {
                : cudaErrorInvalidValue;
 }
 
+// ------------------------------------------------------------- a few tokens
+//
+// Up to eight tokens: the weights are read (and their gradient written) once by
+// plain loads and every sum is a float32 fused multiply-add, for float32 inputs
+// without the three planes of the tensor cores.  A CTA's 64 vocabulary entries are
+// eight rows of W a warp, 16 bytes of each a lane where rows are aligned, else a
+// value; eight rows' loads are in flight together.
+
+constexpr int kFewThreads = 256, kFewRows = kFewColumns / (kFewThreads / 32), kFewDeep = 1024;
+
+// VEC values of a row from i on.
+template <bool BF16, int VEC>
+__device__ __forceinline__ void few_load(const void* p, uint64_t i, float (&x)[VEC]) {
+    if constexpr (VEC == 1) {
+        x[0] = load_value(p, i, BF16);
+    } else if constexpr (!BF16) {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else if constexpr (VEC == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+        x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+        x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
+        x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
+    }
+}
+
+// Where value d of a token lies in shared memory: a lane's VEC values in fours, so
+// that a warp's reads of four are of consecutive addresses.
+template <int VEC>
+__device__ __forceinline__ uint32_t few_place(uint32_t d) {
+    if (VEC <= 4) return d;
+    return d / 256 * 256 + d % 8 / 4 * 128 + d % 256 / 8 * 4 + d % 4;
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t few_count(const FewArgs& a) {
+    const uint32_t count = *a.rows.count;
+    return count > a.base ? min(count - a.base, static_cast<uint32_t>(N)) : 0;
+}
+
+template <int N, bool BF16, int VEC>
+__global__ void __launch_bounds__(kFewThreads) few_logits_kernel(const __grid_constant__ FewArgs a) {
+    __shared__ __align__(16) float xs[N][kFewDeep];
+    __shared__ float zs[N][kFewColumns];
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const uint32_t v0 = blockIdx.x * kFewColumns;
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t count = few_count<N>(a);
+    const int32_t* row = a.rows.row + a.base;
+    float acc[kFewRows * N] = {};  // row by row
+    uint64_t at[kFewRows];
+#pragma unroll
+    for (int j = 0; j < kFewRows; ++j)  // behind the vocabulary: its last entry, not used
+        at[j] = min(v0 + warp * kFewRows + j, a.vocab - 1) * a.w_stride;
+    for (uint32_t d0 = 0; d0 < a.width; d0 += kFewDeep) {
+        const uint32_t deep = min(static_cast<uint32_t>(kFewDeep), a.width - d0);
+        __syncthreads();
+        for (uint32_t i = tid; i < N * kFewDeep; i += kFewThreads) {
+            const uint32_t r = i / kFewDeep, d = i % kFewDeep;
+            if (d < deep) xs[r][few_place<VEC>(d)] = r < count ? load_value(a.x, row[r] * a.x_stride + d0 + d, BF16) : 0.f;
+        }
+        __syncthreads();
+#pragma unroll(VEC == 1 ? 4 : 1)
+        for (uint32_t d = VEC * lane; d < deep; d += 32 * VEC) {
+            float w[kFewRows][VEC];
+#pragma unroll
+            for (int j = 0; j < kFewRows; ++j) few_load<BF16, VEC>(a.w, at[j] + d0 + d, w[j]);
+#pragma unroll
+            for (int i = 0; i < VEC; i += VEC == 1 ? 1 : 4)
+#pragma unroll
+                for (int r = 0; r < N; ++r) {
+                    float x[4];
+                    if constexpr (VEC == 1) {
+                        x[0] = xs[r][d];
+                    } else {
+                        const float4 v = *reinterpret_cast<const float4*>(&xs[r][few_place<VEC>(d + i)]);
+                        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+                    }
+#pragma unroll
+                    for (int q = 0; q < (VEC == 1 ? 1 : 4); ++q)
+#pragma unroll
+                        for (int j = 0; j < kFewRows; ++j) acc[j * N + r] = __fmaf_rn(w[j][i + q], x[q], acc[j * N + r]);
+                }
+        }
+    }
+    // the lanes' sums: each step hands half of the values to the other half of the lanes
+    int have = kFewRows * N, first = 0;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const bool upper = lane & o;
+        if (have > 1) {
+            have /= 2;
+#pragma unroll
+            for (int i = 0; i < kFewRows * N / 2; ++i) {
+                if (i >= have) break;
+                const float give = upper ? acc[i] : acc[i + have], keep = upper ? acc[i + have] : acc[i];
+                acc[i] = __fadd_rn(keep, __shfl_xor_sync(kFull, give, o));
+            }
+            first += upper ? have : 0;
+        } else {
+            acc[0] = __fadd_rn(acc[0], __shfl_xor_sync(kFull, acc[0], o));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < (N * kFewRows > 32 ? N * kFewRows / 32 : 1); ++i)
+        zs[(first + i) % N][warp * kFewRows + (first + i) / N] = acc[i];
+    __syncthreads();
+    if (warp < count) {
+        float top = -kInf, sum = 0.f;
+#pragma unroll
+        for (uint32_t i = lane; i < kFewColumns; i += 32) {
+            if (v0 + i >= a.vocab) break;
+            const float z = zs[warp][i];
+            if (a.z) a.z[warp * a.z_pitch + v0 + i] = z;
+            join_stat(top, sum, __fmul_rn(z, a.c), 1.f);
+        }
+        for (int o = 16; o > 0; o /= 2) {
+            const float t2 = __shfl_xor_sync(kFull, top, o), s2 = __shfl_xor_sync(kFull, sum, o);
+            join_stat(top, sum, t2, s2);
+        }
+        if (lane == 0) a.stats[warp * a.stats_pitch + blockIdx.x] = make_float2(top, sum);
+    }
+    for (uint32_t k = tid; k < count * a.lists.top; k += kFewThreads) {
+        const uint32_t r = k / a.lists.top;
+        const uint64_t i = static_cast<uint64_t>(row[r]) * a.lists.top + (k - r * a.lists.top);
+        const uint32_t v = static_cast<uint32_t>(a.lists.ids[i]) - v0;
+        if (v < kFewColumns) a.lists.logits[i] = zs[r][v];
+    }
+}
+
+// grad W = f t g^T X of the CTA's entries, and its part of grad X = f t g W: a thread
+// four columns (VEC 4: next to each other, else `lanes` apart), `lanes` threads a
+// row; the gradients of 64 entries' logits at a time.
+template <int N, bool BF16, int VEC>
+__global__ void __launch_bounds__(kFewThreads) few_gradients_kernel(const __grid_constant__ FewArgs a, uint32_t lanes,
+                                                                    const __grid_constant__ RecordArgs record) {
+    constexpr int kAhead = N <= 2 ? 8 : 4;  // rows of W whose loads are in flight
+    __shared__ float gs[N][kFewColumns];
+    __shared__ float sums[4 * kFewThreads];
+    const uint32_t tid = threadIdx.x, tx = tid % lanes, ty = tid / lanes, rows = kFewThreads / lanes;
+    const uint32_t c0 = VEC == 4 ? (blockIdx.x * lanes + tx) * 4 : blockIdx.x * 4 * lanes + tx, step = VEC == 4 ? 1 : lanes;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid < 32 && record.result) write_record(record, tid);
+    const uint32_t count = few_count<N>(a);
+    const int32_t* row = a.rows.row + a.base;
+    if (count == 0 && a.base > 0) return;  // nothing to add
+    const float scale = __fmul_rn(*a.rows.factor, a.t);
+    float x[N][4], acc[N][4] = {};
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t c = c0 + j * step;
+            x[r][j] = static_cast<uint32_t>(r) < count && c < a.width ? load_value(a.x, row[r] * a.x_stride + c, BF16) : 0.f;
+        }
+    const uint32_t lo = blockIdx.y * a.entries, hi = min(a.vocab, lo + a.entries);
+    for (uint32_t v0 = lo; v0 < hi; v0 += kFewColumns) {
+        __syncthreads();
+        for (uint32_t i = tid; i < N * kFewColumns; i += kFewThreads) {
+            const uint32_t r = i / kFewColumns, v = v0 + i % kFewColumns;
+            float g = 0.f;
+            if (r < count && v < hi)
+                for (int q = a.g.planes - 1; q >= 0; --q) g = __fadd_rn(g, bf16_value(a.g.p[q * a.g.plane + r * a.g.pitch + v]));
+            gs[r][i % kFewColumns] = g;
+        }
+        __syncthreads();
+        const uint32_t end = min(hi - v0, kFewColumns);
+        for (uint32_t i0 = ty; i0 < end; i0 += kAhead * rows) {
+            float w[kAhead][4] = {};
+            if (a.grad_x && c0 < a.width) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) {
+                    const uint64_t at = static_cast<uint64_t>(v0 + min(i0 + k * rows, end - 1)) * a.w_stride + c0;
+                    if constexpr (VEC == 4) {
+                        few_load<BF16, 4>(a.w, at, w[k]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (c0 + j * step < a.width) w[k][j] = load_value(a.w, at + j * step, BF16);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const uint32_t i = i0 + k * rows;
+                if (i >= end) break;
+                float y[4] = {};
+#pragma unroll
+                for (int r = 0; r < N; ++r) {
+                    const float g = gs[r][i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y[j] = __fmaf_rn(g, x[r][j], y[j]);
+                        acc[r][j] = __fmaf_rn(g, w[k][j], acc[r][j]);
+                    }
+                }
+                if (!a.grad_w || c0 >= a.width) continue;
+                const uint64_t to = static_cast<uint64_t>(v0 + i) * a.grad_w_stride + c0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(y[j], scale);
+                const bool add = a.accumulate || a.base > 0;
+                if (VEC == 4 && add && !a.grad_w_bf16) {
+                    const float4 old = *reinterpret_cast<const float4*>(static_cast<const float*>(a.grad_w) + to);
+                    y[0] = __fadd_rn(y[0], old.x), y[1] = __fadd_rn(y[1], old.y), y[2] = __fadd_rn(y[2], old.z), y[3] = __fadd_rn(y[3], old.w);
+                }
+                if (VEC == 4 && !(add && a.grad_w_bf16)) {
+                    if (a.grad_w_bf16)
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.grad_w) + to) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                    else
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.grad_w) + to) = make_float4(y[0], y[1], y[2], y[3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (c0 + j * step < a.width) store_out(a.grad_w, to + j * step, a.grad_w_bf16, add, y[j]);
+                }
+            }
+        }
+    }
+    if (!a.grad_x) return;
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[j * kFewThreads + tid] = acc[r][j];
+        __syncthreads();
+        if (ty != 0) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float s = 0.f;
+            for (uint32_t k = 0; k < rows; ++k) s = __fadd_rn(s, sums[j * kFewThreads + k * lanes + tx]);
+            if (c0 + j * step < a.width) a.parts[(static_cast<uint64_t>(blockIdx.y) * N + r) * a.width + c0 + j * step] = s;
+        }
+    }
+}
+
+// grad X from its parts, in their order.
+__global__ void __launch_bounds__(128) few_finish_kernel(const __grid_constant__ FewArgs a, uint32_t tokens, uint32_t splits) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t c = blockIdx.x * 128 + threadIdx.x, r = blockIdx.y;
+    if (c >= a.width || a.base + r >= *a.rows.count) return;
+    const float scale = __fmul_rn(*a.rows.factor, a.t);
+    float s = 0.f;
+#pragma unroll 8
+    for (uint32_t k = 0; k < splits; ++k) s = __fadd_rn(s, a.parts[(static_cast<uint64_t>(k) * tokens + r) * a.width + c]);
+    store_out(a.grad_x, a.rows.row[a.base + r] * a.grad_x_stride + c, a.grad_x_bf16, a.accumulate, __fmul_rn(s, scale));
+}
+
 template <class... Args>
 cudaError_t launch(void (*f)(Args...), dim3 grid, int block, size_t smem, cudaStream_t st, const Args&... a) {
     cudaLaunchConfig_t cfg = {};
@@ -1127,7 +1473,7 @@ uint32_t ctas(uint64_t n, uint64_t each) { return static_cast<uint32_t>((n + eac
 
 uint64_t tall_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.m) + kSide - 1) / kSide; }
 uint64_t wide_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.n) + a.width - 1) / a.width; }
-uint64_t blocks_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.k) + kDeep - 1) / kDeep * (a.a.m.planes == 1 ? 1 : 6); }
+uint64_t blocks_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.k) + kDeep - 1) / kDeep; }
 
 // Tiles as wide as they divide the columns evenly; rows of tiles side by side: all
 // of them while A's rows stay in L2, then eight.
@@ -1145,7 +1491,8 @@ void set_shape(ProductArgs& a) {
 uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t room) {
     const uint64_t pairs = kLossSms / 2, tiles = tall_of(a) * wide_of(a), blocks = blocks_of(a);
     if (tiles == 0 || tiles >= 8 * pairs) return 1;
-    const uint64_t most = std::min(blocks / 4, room / (tall_of(a) * kSide * a.out.part_pitch));
+    const uint64_t passes = a.a.m.planes == 1 ? 1 : 6;
+    const uint64_t most = std::min(blocks * passes / 4, room / (tall_of(a) * kSide * a.out.part_pitch));
     const uint64_t other = second ? blocks_of(*second) * second->width : 0;
     const uint64_t others = second ? tall_of(*second) * wide_of(*second) * other : 0;
     uint64_t best = 0;
@@ -1154,7 +1501,7 @@ uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t roo
         if (s > std::max<uint64_t>(1, most)) return;
         const uint64_t each = (blocks + s - 1) / s * a.width;
         const uint64_t fullest = std::max((tiles * s + pairs - 1) / pairs * each, (tiles * s * each + others) / pairs + other / 2);
-        const uint64_t cost = fullest + (s > 1 ? (8 + tiles * s / 4) * kSide : 0);
+        const uint64_t cost = fullest * passes + (s > 1 ? (8 + tiles * s / 4) * kSide : 0);
         if (splits == 0 || cost < best) {
             best = cost;
             splits = static_cast<uint32_t>(s);
@@ -1183,19 +1530,27 @@ cudaError_t launch_join(const JoinArgs& a, cudaStream_t st) {
 
 cudaError_t launch_grad(const JoinArgs& a0, cudaStream_t st) {
     JoinArgs a = a0;
-    const uint32_t rows = ctas(a.n, 64) * 64;
+    const uint32_t rows = ctas(a.n, a.round) * a.round;
     a.columns = 128 * kGradThreads;  // less while a few waves of CTAs are not full
     while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 40 * kLossSms) a.columns /= 2;
     return launch(grad_kernel, dim3(ctas(a.vocab, a.columns), std::min(rows, 32768u)), kGradThreads, 0, st, a);
 }
 
+using ProductKernel = void (*)(ProductParams, int);
+
+ProductKernel product_of(bool logits, int planes) {
+    if (planes == 1) return logits ? product_kernel<true, 1> : product_kernel<false, 1>;
+    return logits ? product_kernel<true, kMaxPlanes> : product_kernel<false, kMaxPlanes>;
+}
+
 cudaError_t prepare_products() {
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&product_kernel<true>),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&product_kernel<false>),
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
-    return e;
+    for (const bool logits : {false, true})
+        for (const int planes : {1, kMaxPlanes}) {
+            const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(product_of(logits, planes)),
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
 }
 
 namespace {
@@ -1211,7 +1566,7 @@ cudaError_t launch_tiles(ProductParams& p, int n, bool logits, cudaStream_t st) 
     }
     if (tiles > 0x7FFFFFFFu) return cudaErrorInvalidValue;  // 2^22 tokens and 2^24 entries make 2^30
     const uint32_t pairs = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(1, tiles), kLossSms / 2));
-    return launch(logits ? product_kernel<true> : product_kernel<false>, 2 * pairs, kProductThreads, kProductSmem, st, p, n);
+    return launch(product_of(logits, p.args[0].a.m.planes), 2 * pairs, kProductThreads, kProductSmem, st, p, n);
 }
 
 }  // namespace
@@ -1236,6 +1591,52 @@ cudaError_t launch_products(const ProductArgs* a, int n, uint64_t room, const Re
     if (e != cudaSuccess || p.args[0].splits == 1) return e;
     return launch(finish_kernel, std::min<uint32_t>(std::max<uint32_t>(1, ctas(static_cast<uint64_t>(a[0].m) * ctas(a[0].n, 4), 256)), 8 * kLossSms),
                   256, 0, st, p.args[0]);
+}
+
+namespace {
+
+bool aligned(const void* p, uint64_t stride, int es, uint32_t width, uint32_t bytes) {
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * es % bytes == 0 && static_cast<uint64_t>(width) * es % bytes == 0;
+}
+
+template <int N>
+cudaError_t few_logits(const FewArgs& a, cudaStream_t st) {
+    const bool whole = aligned(a.w, a.w_stride, a.bf16 ? 2 : 4, a.width, 16);
+    return launch(a.bf16 ? (whole ? few_logits_kernel<N, true, 8> : few_logits_kernel<N, true, 1>)
+                         : (whole ? few_logits_kernel<N, false, 4> : few_logits_kernel<N, false, 1>),
+                  ctas(a.vocab, kFewColumns), kFewThreads, 0, st, a);
+}
+
+template <int N>
+cudaError_t few_gradients(FewArgs a, const RecordArgs& r, cudaStream_t st) {
+    uint32_t lanes = 32;
+    while (lanes < kFewThreads && 4 * lanes < a.width) lanes *= 2;
+    const uint32_t wide = ctas(a.width, 4 * lanes);
+    // four CTAs an SM
+    const uint32_t most = std::min<uint64_t>(std::max(1u, 4 * kLossSms / wide), a.room / (static_cast<uint64_t>(N) * a.width));
+    a.entries = ctas(ctas(a.vocab, std::max(1u, most)), kFewColumns) * kFewColumns;
+    const uint32_t splits = ctas(a.vocab, a.entries);
+    const bool whole = (!a.grad_x || aligned(a.w, a.w_stride, a.bf16 ? 2 : 4, a.width, a.bf16 ? 8 : 16)) &&
+                       (!a.grad_w || aligned(a.grad_w, a.grad_w_stride, a.grad_w_bf16 ? 2 : 4, a.width, a.grad_w_bf16 ? 8 : 16)) &&
+                       a.width % 4 == 0;
+    cudaError_t e = launch(a.bf16 ? (whole ? few_gradients_kernel<N, true, 4> : few_gradients_kernel<N, true, 1>)
+                                  : (whole ? few_gradients_kernel<N, false, 4> : few_gradients_kernel<N, false, 1>),
+                           dim3(wide, splits), kFewThreads, 0, st, a, lanes, r);
+    if (e == cudaSuccess && a.grad_x) e = launch(few_finish_kernel, dim3(ctas(a.width, 128), a.n), 128, 0, st, a, static_cast<uint32_t>(N), splits);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_few_logits(const FewArgs& a, cudaStream_t st) {
+    return a.n <= 1 ? few_logits<1>(a, st) : a.n <= 2 ? few_logits<2>(a, st) : a.n <= 4 ? few_logits<4>(a, st) : few_logits<8>(a, st);
+}
+
+cudaError_t launch_few_gradients(FewArgs a, const RecordArgs& r, cudaStream_t st) {
+    return a.n <= 1   ? few_gradients<1>(a, r, st)
+           : a.n <= 2 ? few_gradients<2>(a, r, st)
+           : a.n <= 4 ? few_gradients<4>(a, r, st)
+                      : few_gradients<8>(a, r, st);
 }
 
 }  // namespace ar

@@ -69,6 +69,13 @@ struct RowsArgs {
     Counted rows;
     float* result;     // written here where nothing counts
     uint32_t* ticket;  // of the joins of this call
+    // of a call on few tokens (others' are cleared as they are packed): what those that
+    // do not count are given; null: none
+    float* losses;
+    void* grad;
+    uint64_t grad_stride;
+    int grad_bf16;
+    uint32_t width;
 };
 
 // Rows of a caller's matrix into planes: row i from row rows.row[i] of src
@@ -96,7 +103,7 @@ struct JoinArgs {
     uint64_t pitch;
     uint32_t parts, base, n;
     float c;               // log2(e) / t
-    float t, t2;           // t, t^2
+    float t2;              // t^2
     Lists lists;
     Counted rows;
     float* losses;         // by token; null: none
@@ -105,11 +112,11 @@ struct JoinArgs {
     uint32_t* bad;
     uint32_t *ticket, tickets;
     float* result;
-    // with gradients: the piece's logits and the place of every loss and logit gradient;
-    // zeros in the rows behind the last up to a block of products
+    // with gradients: the piece's logits and the place of every loss and logit gradient
     const float* z;
     uint64_t z_pitch;
     uint32_t vocab, columns;  // ..., of a CTA
+    uint32_t round;           // zeros in the rows up to a multiple of this
     float* loss;
     Planes g;
 };
@@ -136,11 +143,13 @@ struct LogitArgs {
     uint64_t z_pitch;
 };
 
-// Where a product goes: `add` (float32, null: nothing) is added to it, and it is
+// Where a product goes: it is scaled, `add` (float32, null: nothing) is added to it, and it is
 // stored in `sum` (float32), or if that is null in the caller's rows (row i into
 // row[i] if row is not null).  Products of several splits go to parts, a matrix of
 // whole tiles each, and are finished by launch_finish; they have no add and sum.
 struct OutArgs {
+    const float* factor;  // the product times *factor t
+    float t;
     const float* add;
     float* sum;
     uint64_t sum_pitch;
@@ -175,6 +184,35 @@ struct RecordArgs {
     float* result;      // null: none
 };
 
+// Calls of a few tokens, whose time is that of reading the weights: no tiles, no
+// packing.  Of the counted tokens those at places [base, base + n), n <= kFewTokens;
+// z, stats and g start at the first of them.
+constexpr uint32_t kFewTokens = 8, kFewColumns = 64;
+
+struct FewArgs {
+    const void *x, *w;
+    uint64_t x_stride, w_stride;
+    int bf16;
+    uint32_t base, n, width, vocab;
+    Counted rows;
+    // logits
+    float c;
+    Lists lists;
+    float2* stats;
+    uint64_t stats_pitch;
+    float* z;  // null: the statistics alone
+    uint64_t z_pitch;
+    // gradients from the logits' (null: not wanted)
+    Planes g;
+    float t;
+    void *grad_x, *grad_w;
+    uint64_t grad_x_stride, grad_w_stride;
+    int grad_x_bf16, grad_w_bf16, accumulate;
+    float* parts;  // of grad_x
+    uint64_t room;
+    uint32_t entries;  // vocabulary entries of a CTA, a multiple of kFewColumns
+};
+
 cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
 cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
@@ -186,5 +224,8 @@ cudaError_t launch_logits(ProductArgs a, cudaStream_t st);
 // One or two products in one launch (and the finish of the first, if it is worth
 // splitting: its parts have room for `room` values).
 cudaError_t launch_products(const ProductArgs* a, int n, uint64_t room, const RecordArgs& r, cudaStream_t st);
+
+cudaError_t launch_few_logits(const FewArgs& a, cudaStream_t st);
+cudaError_t launch_few_gradients(FewArgs a, const RecordArgs& r, cudaStream_t st);
 
 }  // namespace ar

@@ -217,6 +217,46 @@ def test_cross_entropy(n, d, v, dtype, keep):
 
 @gpu
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("n, d, v", [(1, 1, 65), (2, 1030, 300), (3, 515, 64), (4, 2050, 63), (5, 33, 1), (6, 640, 1003),
+                                     (7, 129, 2003), (8, 4097, 130), (9, 4097, 130), (12, 1100, 2003)])
+@pytest.mark.parametrize("keep", [1.0, 0.5])
+def test_few_tokens(n, d, v, dtype, keep):
+    """Calls of a few tokens take kernels of their own (float32 in groups of eight),
+    also on odd and accumulating rows, with lists and in float32 results."""
+    import torch
+    x, w, g = make(n, d, v, dtype, seed=n * d)
+    t = targets_of(n, v, g, keep)
+    h = ar.OutputLoss(20, d, v, dtype, top=5)
+    Expected(x, w, *one_hot_lists(t), dtype=dtype).check(*run_ce(h, x, w, t, dtype))
+    want = Expected(x, w, *one_hot_lists(t), reduction="sum", scale=1.0 / 300, dtype=dtype)
+    want.check(*run_ce(h, x, w, t, dtype, gtype="float32", reduction="sum", scale=1.0 / 300))
+    for grads in ((), ("hidden",), ("weight",)):
+        want.check(*run_ce(h, x, w, t, dtype, grads, reduction="sum", scale=1.0 / 300))
+    k = min(5, v)
+    ids, logits = teacher(n, k, v, g, dtype, 0.4, twice=True)
+    lists, shares, spread = teacher_lists(ids, logits, 2.0)
+    big = torch.zeros(n, d + 3, dtype=x.dtype, device="cuda")
+    big[:, 1:-2] = x
+    dx = torch.ones(n, d + 1, dtype=x.dtype, device="cuda")[:, 1:]
+    dw = (0.01 * torch.randn(v, d, generator=g)).to(tdt(dtype)).cuda()
+    x0, w0 = dx.clone(), dw.clone()
+    rec = h.distill(big[:, 1:-2], w, ids.cuda(), logits.cuda(), temperature=2.0, grad_hidden=dx, grad_weight=dw, accumulate=True)
+    Expected(x, w, lists, shares, 2.0, dtype=dtype, spread=spread).check(rec, None, dx, dw, x0, w0)
+
+
+@gpu
+@pytest.mark.parametrize("keep", [1.0, 0.3])
+def test_few_tokens_of_large_float32_weights(keep):
+    x, w, g = make(21, 4100, 4100, "float32", seed=7)
+    t = targets_of(21, 4100, g, keep)
+    h = ar.OutputLoss(21, 4100, 4100, "float32")
+    want = Expected(x, w, *one_hot_lists(t), dtype="float32")
+    want.check(*run_ce(h, x, w, t, "float32"))
+    want.check(*run_ce(h, x, w, t, "float32", ()))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 @pytest.mark.parametrize("n, d, v, piece", [(700, 40, 303, 256), (1100, 136, 500, 512), (257, 1000, 77, 256)])
 def test_pieces(n, d, v, piece, dtype):
     x, w, g = make(n, d, v, dtype, seed=3)
