@@ -693,6 +693,41 @@ def test_loss_then_norm_then_update():
 
 
 @gpu
+@pytest.mark.parametrize("teacher_k", [0, 6])
+def test_sharded_step_of_an_output_layer(teacher_k):
+    """examples/zero_step.py with ar.OutputLoss: every rank's float32 gradient,
+    the update that follows from them, and the same bits from its graph."""
+    import sys
+    import torch
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import zero_step
+    P, n, d, v = 3, 70, 40, 331
+    eager, graphed = (zero_step.OutputLayerStep(P, n, d, v, teacher_k, weight_decay=0.01) for _ in range(2))
+    graph = graphed.capture()
+    for _ in range(3):
+        before = [w.clone().view(v, d) for w in eager.weights]
+        eager.backward()
+        for r in range(P):
+            if teacher_k:
+                lists, shares, spread = teacher_lists(eager.ids[r].cpu(), eager.top[r].cpu(), 1.0)
+                want = Expected(eager.states[r], before[r], lists, shares, spread=spread)
+            else:
+                want = Expected(eager.states[r], before[r], *one_hot_lists(eager.next[r].cpu()))
+            want.check(eager.records[r], None, None, eager.grads[r].view(v, d))
+        mean = sum(g.double() for g in eager.grads) / P
+        record = eager.step()
+        assert record[0].item() == pytest.approx(float(mean.norm()), rel=(10 + 2 * P) * U)
+        assert all(torch.equal(eager.weights[0], w) for w in eager.weights)
+        assert not torch.equal(eager.weights[0].view(v, d), before[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(eager.records, graphed.records)
+        assert all(torch.equal(p, q) for p, q in zip(eager.weights + eager.master, graphed.weights + graphed.master))
+    eager.loss.check()
+    graphed.loss.check()
+
+
+@gpu
 def test_closing_twice_and_dropping_during_a_capture():
     import torch
     x, w, g = make(20, 64, 300, "bfloat16")
