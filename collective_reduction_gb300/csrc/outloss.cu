@@ -491,28 +491,26 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int 
 constexpr int kSide = 256;             // rows and columns of a pair's tile
 constexpr int kHalf = kSide / 2;       // ... of A and of B in one CTA
 constexpr int kDeep = 64;              // products of a block: 128 bytes of bf16
-constexpr uint32_t kOperandBytes = kHalf * kDeep * 2;  // of a block of A or B, one plane, in one CTA
-constexpr int kOperands = 12;          // of them in shared memory
-// Blocks in flight: of bf16 six, of float32 two of six operands each, whose six
-// products read them where they are.
-__host__ __device__ constexpr int stages_of(int planes) { return kOperands / (2 * planes); }
+constexpr uint32_t kStages = 6;        // blocks of A and B (of float32 a plane's) in flight
+constexpr uint32_t kOperandBytes = kHalf * kDeep * 2, kStageBytes = 2 * kOperandBytes;
 constexpr int kProductThreads = 384, kEpilogueWarp = 4, kEpilogueWarps = 8;
 constexpr uint32_t kStagedBytes = 32 * 128;  // of an epilogue warp: 32 rows' part of a result on its way out
 constexpr int kTmemColumns = 512;
 
+static_assert(kStages % kMaxPlanes == 0, "a float32 block's stages follow each other");
 static_assert(kSide == static_cast<int>(kLossTile) && kHalf == static_cast<int>(kStatColumns), "statistics are of an epilogue thread's columns");
 
 // Barriers, in 8-byte words of shared memory.
 enum : uint32_t {
     kFullBar = 0,                      // a stage's blocks are there (the pair's; in its first CTA)
-    kEmptyBar = kFullBar + stages_of(1),  // ... have been read
-    kReadyBar = kEmptyBar + stages_of(1),  // an accumulator is complete
+    kEmptyBar = kFullBar + kStages,    // ... have been read
+    kReadyBar = kEmptyBar + kStages,   // an accumulator is complete
     kFreeBar = kReadyBar + 2,          // ... has been read (in the pair's first CTA)
     kDoneBar = kFreeBar + 2,           // the products issued are complete
     kTmemWord = kDoneBar + 1,
     kBarWords = kTmemWord + 1
 };
-constexpr uint32_t kProductSmem = kOperands * kOperandBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
+constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
 
 // One or two products in one launch.
 struct ProductParams {
@@ -670,9 +668,8 @@ struct Work {
     }
 };
 
-// The planes of product q of the six of a float32 block, small ones first.
-__host__ __device__ constexpr uint32_t plane_a(uint32_t q) { return (0x001012 >> (4 * q)) & 3; }
-__host__ __device__ constexpr uint32_t plane_b(uint32_t q) { return (0x010210 >> (4 * q)) & 3; }
+// The plane in the q-th of a float32 block's three stages.
+__device__ __forceinline__ int plane_at(int q) { return q == 0 ? 1 : q == 1 ? 0 : 2; }
 
 // A row's next id at or behind column v, as its place in the list.
 __device__ __forceinline__ int first_id(const int32_t* ids, int top, int32_t v) {
@@ -962,7 +959,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     extern __shared__ char raw[];
     __shared__ Work work;
     constexpr bool BT = !LOGITS;
-    constexpr uint32_t kStages = stages_of(kPlanes), kStageBytes = 2 * kPlanes * kOperandBytes;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;  // the same in both CTAs
     const uint32_t staged = base + kStages * kStageBytes, bars = staged + kEpilogueWarps * kStagedBytes;
     auto bar = [bars](uint32_t i) { return bars + 8 * i; };
@@ -1012,27 +1008,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             const bool at = !LOGITS && a.a.turned;
             const int m0 = static_cast<int>(mt * kSide + rank * kHalf);
             const int n0 = static_cast<int>(nt * a.width + rank * (a.width / 2));
-            for (uint32_t i = 0; i < n; ++i) {
-                if (round > 0 && !(ok = mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1))) break;
+            for (uint32_t i = 0; i < n && ok; ++i) {
                 const int k0 = static_cast<int>((lo + i) * kDeep);
-                const uint32_t full = full0 + 8 * s;
-                uint32_t to = base + s * kStageBytes;
-                if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
-                for (int q = 0; q < kPlanes; ++q, to += 2 * kOperandBytes) {
+                for (int q = 0; q < kPlanes; ++q) {
+                    if (round > 0 && !(ok = mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1))) break;
+                    const int plane = kPlanes == 1 ? 0 : plane_at(q);
+                    const uint32_t full = full0 + 8 * s, to = base + s * kStageBytes;
+                    if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
                     if (at) {
-                        tma_load(to, ma, m0, k0, q, full);
-                        tma_load(to + kOperandBytes / 2, ma, m0 + 64, k0, q, full);
+                        tma_load(to, ma, m0, k0, plane, full);
+                        tma_load(to + kOperandBytes / 2, ma, m0 + 64, k0, plane, full);
                     } else {
-                        tma_load(to, ma, k0, m0, q, full);
+                        tma_load(to, ma, k0, m0, plane, full);
                     }
                     if (BT) {
-                        tma_load(to + kOperandBytes, mb, n0, k0, q, full);
-                        tma_load(to + kOperandBytes + kOperandBytes / 2, mb, n0 + 64, k0, q, full);
+                        tma_load(to + kOperandBytes, mb, n0, k0, plane, full);
+                        tma_load(to + kOperandBytes + kOperandBytes / 2, mb, n0 + 64, k0, plane, full);
                     } else {
-                        tma_load(to + kOperandBytes, mb, k0, n0, q, full);
+                        tma_load(to + kOperandBytes, mb, k0, n0, plane, full);
                     }
+                    if (++s == kStages) s = 0, ++round;
                 }
-                if (++s == kStages) s = 0, ++round;
             }
         }
         // the last blocks have been read before the pair's memory goes
@@ -1055,21 +1051,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 if (done >= 2 && !(ok = mbar_wait_here(bar(kFreeBar + b), (done / 2 - 1) & 1))) break;
                 tmem_fence_after();
                 const uint32_t end = n - i > run ? i + run : n;
-                for (uint32_t j = i; j < end; ++j) {
-                    if (!(ok = mbar_wait_here(bar(kFullBar + s), phase))) break;
+                // the products of A's block in one stage and B's in another
+                auto multiply = [&](uint32_t sa, uint32_t sb, bool add) {
+#pragma unroll
+                    for (uint32_t k = 0; k < kDeep / 16; ++k)
+                        mma(acc, a0 + (sa * (kStageBytes / 16) + k * a_step),
+                            b0 + (sb * (kStageBytes / 16) + k * (BT ? 2048 / 16 : 32 / 16)), desc, add || k > 0);
+                };
+                auto full = [&](uint32_t stage) {
+                    if (!mbar_wait_here(bar(kFullBar + stage), phase)) return false;
                     tmem_fence_after();
-                    const uint32_t at = s * (kStageBytes / 16);
-#pragma unroll
-                    for (uint32_t q = 0; q < (kPlanes == 1 ? 1 : 6); ++q) {
-                        const uint32_t pa = at + (kPlanes == 1 ? 0 : plane_a(q) * (2 * kOperandBytes / 16));
-                        const uint32_t pb = at + (kPlanes == 1 ? 0 : plane_b(q) * (2 * kOperandBytes / 16));
-#pragma unroll
-                        for (uint32_t k = 0; k < kDeep / 16; ++k)
-                            mma(acc, a0 + (pa + k * a_step), b0 + (pb + k * (BT ? 2048 / 16 : 32 / 16)), desc,
-                                j > i || q > 0 || k > 0);
+                    return true;
+                };
+                for (uint32_t j = i; j < end; ++j) {
+                    if constexpr (kPlanes == 1) {
+                        if (!(ok = full(s))) break;
+                        multiply(s, s, j > i);
+                        mma_commit(bar(kEmptyBar + s));
+                    } else {
+                        // planes 1, 0, 2: the first one's stage is free for the next block but one
+                        // while the others are still read
+                        if (!(ok = full(s))) break;
+                        multiply(s, s, j > i);
+                        if (!(ok = full(s + 1))) break;
+                        multiply(s, s + 1, true);
+                        multiply(s + 1, s, true);
+                        mma_commit(bar(kEmptyBar + s));
+                        multiply(s + 1, s + 1, true);
+                        if (!(ok = full(s + 2))) break;
+                        multiply(s + 1, s + 2, true);
+                        multiply(s + 2, s + 1, true);
+                        mma_commit(bar(kEmptyBar + s + 1));
+                        mma_commit(bar(kEmptyBar + s + 2));
                     }
-                    mma_commit(bar(kEmptyBar + s));
-                    if (++s == kStages) s = 0, phase ^= 1;
+                    s += kPlanes;
+                    if (s == kStages) s = 0, phase ^= 1;
                 }
                 if (!ok) break;
                 mma_commit(bar(kReadyBar + b));
