@@ -821,13 +821,13 @@ __device__ __forceinline__ void store_four(const OutArgs& o, uint64_t at, uint32
 }
 
 struct OutTile {
-    const OutArgs& o;
+    const OutArgs& args;
     uint64_t to = 0;  // this lane's row in the caller's matrix
     float scale;
 
-    __device__ __forceinline__ OutTile(const ProductArgs& a, const Place& p) : o(a.out) {
-        scale = __fmul_rn(*o.factor, o.t);
-        if (p.in) to = (o.row ? static_cast<uint64_t>(o.row[p.row]) : p.row) * o.stride;
+    __device__ __forceinline__ OutTile(const ProductArgs& a, const Place& p) : args(a.out) {
+        scale = __fmul_rn(*args.factor, args.t);
+        if (p.in) to = (args.row ? static_cast<uint64_t>(args.row[p.row]) : p.row) * args.stride;
     }
 
     // Rows off a 16-byte boundary go row by row, a lane a word: lines are written
@@ -835,10 +835,18 @@ struct OutTile {
     // rows of 515 took 60 us longer.)
     __device__ __forceinline__ void finish(const Place& p, float (&z)[4][32], float* part) const {
         if (p.cols == 0) return;
+        // copies: read through the reference again after every store, they made a tile of
+        // 256 x 192 float32 off alignment take 13 us
+        OutArgs o;
+        o.out = args.out;
+        o.add = args.add;
+        o.bf16 = args.bf16;
+        o.accumulate = args.accumulate;
+        o.sum_pitch = args.sum_pitch;
         const uint32_t rows = __popc(__ballot_sync(kFull, p.in));  // the warp's first ones
         const uint64_t row0 = p.row - p.lane;
-        float* sum = part ? part : o.sum;
-        const uint64_t pitch = part ? o.part_pitch : o.sum_pitch;
+        float* sum = part ? part : args.sum;
+        const uint64_t pitch = part ? args.part_pitch : o.sum_pitch;
         const uintptr_t mine = reinterpret_cast<uintptr_t>(o.out) + (to + p.n0) * (o.bf16 ? 2 : 4);
         const bool aligned = __all_sync(kFull, (mine & 15) == 0 || !p.in);
         if (!sum && !o.add && o.bf16 && !o.accumulate) {
