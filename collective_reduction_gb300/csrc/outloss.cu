@@ -848,7 +848,7 @@ struct OutTile {
         float* sum = part ? part : args.sum;
         const uint64_t pitch = part ? args.part_pitch : o.sum_pitch;
         const uintptr_t mine = reinterpret_cast<uintptr_t>(o.out) + (to + p.n0) * (o.bf16 ? 2 : 4);
-        const bool aligned = __all_sync(kFull, (mine & 15) == 0 || !p.in);
+        const bool aligned = __all_sync(kFull, (mine & 15) == 0 || !p.in), mapped = args.row != nullptr;
         if (!sum && !o.add && o.bf16 && !o.accumulate) {
             // two values a word: 64 columns at a time
 #pragma unroll
@@ -867,29 +867,21 @@ struct OutTile {
                 }
                 stage(p, word);
                 const uint32_t c = c0 + 2 * p.lane;
-                for (uint32_t r0 = 0; r0 < rows; r0 += 8) {  // eight rows' loads before their stores
-                    uint32_t x[8], before[8];
-                    uint16_t* q[8];
-#pragma unroll
-                    for (uint32_t r = 0; r < 8; ++r) {
-                        x[r] = staged_word(p, r0 + r);
-                        q[r] = static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, r0 + r) + p.n0 + c;
-                    }
-#pragma unroll
-                    for (uint32_t r = 0; r < 8; ++r) before[r] = __shfl_up_sync(kFull, x[r], 1);
-#pragma unroll
-                    for (uint32_t r = 0; r < 8; ++r) {
-                        if (r0 + r >= rows) break;
-                        if ((reinterpret_cast<uintptr_t>(q[r]) & 2) == 0) {
-                            if (c + 1 < p.cols) *reinterpret_cast<uint32_t*>(q[r]) = x[r];
-                            else if (c < p.cols) *q[r] = static_cast<uint16_t>(x[r]);
-                        } else {
-                            // this lane's first value goes with the one before it
-                            if (p.lane == 0) *q[r] = static_cast<uint16_t>(x[r]);
-                            else if (c < p.cols) *reinterpret_cast<uint32_t*>(q[r] - 1) = (before[r] >> 16) | (x[r] << 16);
-                            else if (c - 1 < p.cols) q[r][-1] = static_cast<uint16_t>(before[r] >> 16);
-                            if (p.lane == 31 && c + 1 < p.cols) q[r][1] = static_cast<uint16_t>(x[r] >> 16);
-                        }
+                // a row's address: one addition from row to row where they follow each other
+                uint16_t* q = static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, 0) + p.n0 + c;
+#pragma unroll 4
+                for (uint32_t r = 0; r < rows; ++r, q += args.stride) {
+                    const uint32_t x = staged_word(p, r), before = __shfl_up_sync(kFull, x, 1);
+                    uint16_t* at = mapped ? static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, r) + p.n0 + c : q;
+                    if ((reinterpret_cast<uintptr_t>(at) & 2) == 0) {
+                        if (c + 1 < p.cols) *reinterpret_cast<uint32_t*>(at) = x;
+                        else if (c < p.cols) *at = static_cast<uint16_t>(x);
+                    } else {
+                        // this lane's first value goes with the one before it
+                        if (p.lane == 0) *at = static_cast<uint16_t>(x);
+                        else if (c < p.cols) *reinterpret_cast<uint32_t*>(at - 1) = (before >> 16) | (x << 16);
+                        else if (c - 1 < p.cols) at[-1] = static_cast<uint16_t>(before >> 16);
+                        if (p.lane == 31 && c + 1 < p.cols) at[1] = static_cast<uint16_t>(x >> 16);
                     }
                 }
             }
@@ -917,21 +909,20 @@ struct OutTile {
             }
             stage(p, word);
             const uint32_t c = c0 + p.lane;
-            for (uint32_t r0 = 0; r0 < rows; r0 += 8) {
-                float x[8];
-                uint64_t at[8];
-#pragma unroll
-                for (uint32_t r = 0; r < 8; ++r) {
-                    x[r] = __uint_as_float(staged_word(p, r0 + r));
-                    at[r] = __shfl_sync(kFull, to, r0 + r) + p.n0 + c;
-                }
+            if (!mapped && !o.add && !o.bf16 && !o.accumulate) {
+                float* q = static_cast<float*>(o.out) + __shfl_sync(kFull, to, 0) + p.n0 + c;
+                const uint64_t stride = args.stride;
                 if (c >= p.cols) continue;
-#pragma unroll
-                for (uint32_t r = 0; r < 8; ++r) {
-                    if (r0 + r >= rows) break;
-                    if (o.add) x[r] = __fadd_rn(x[r], o.add[(row0 + r0 + r) * o.sum_pitch + p.n0 + c]);
-                    store_out(o.out, at[r], o.bf16, o.accumulate, x[r]);
-                }
+#pragma unroll 8
+                for (uint32_t r = 0; r < rows; ++r, q += stride) *q = __uint_as_float(staged_word(p, r));
+                continue;
+            }
+            for (uint32_t r = 0; r < rows; ++r) {
+                const uint64_t at = __shfl_sync(kFull, to, r) + p.n0 + c;
+                float x = __uint_as_float(staged_word(p, r));
+                if (c >= p.cols) continue;
+                if (o.add) x = __fadd_rn(x, o.add[(row0 + r) * o.sum_pitch + p.n0 + c]);
+                store_out(o.out, at, o.bf16, o.accumulate, x);
             }
         }
     }
