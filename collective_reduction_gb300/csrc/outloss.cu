@@ -719,6 +719,21 @@ __device__ __forceinline__ void transposed(const Place& p, Word word, Use use) {
     }
 }
 
+// The same for rows that follow each other `pitch` elements apart, from `to` on (the
+// first row's first of these columns): use(address of a row's 16 bytes, they).
+template <class T, class Word, class Use>
+__device__ __forceinline__ void walked(const Place& p, Word word, T* to, uint64_t pitch, uint32_t rows, Use use) {
+    stage(p, word);
+    const uint32_t r0 = p.lane / 8, j = p.lane % 8;
+    T* q = to + r0 * pitch + j * (16 / sizeof(T));
+    const uint64_t step = 4 * pitch;
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i, q += step) {
+        const uint4 x = lds128(p.staged + (4 * i + r0) * 128 + ((j ^ (4 * i + r0 & 7)) << 4));
+        if (4 * i + r0 < rows) use(q, x);
+    }
+}
+
 __device__ __forceinline__ float4 floats(uint4 v) {
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
@@ -748,9 +763,8 @@ struct LogitTile {
         const int32_t v = static_cast<int32_t>(g.v0 + p.n0 + c0);
         if (g.z) {
             float* to = g.z + (p.row - p.lane) * g.z_pitch + p.n0 + c0;  // rows behind the last are the workspace's too
-            transposed(p, [&](uint32_t j) { return __float_as_uint(z[j]); }, [&](uint32_t r, uint32_t j, uint4 x) {
-                *reinterpret_cast<uint4*>(to + r * g.z_pitch + 4 * j) = x;
-            });
+            walked(p, [&](uint32_t j) { return __float_as_uint(z[j]); }, to, g.z_pitch, 32,
+                   [&](float* q, uint4 x) { *reinterpret_cast<uint4*>(q) = x; });
         }
         if (c0 + 32 > p.cols) {
 #pragma unroll
@@ -858,6 +872,11 @@ struct OutTile {
                 };
                 const uint32_t c0 = 64 * h;
                 if (c0 >= p.cols) break;
+                if (aligned && !mapped && c0 + 64 <= p.cols) {
+                    walked(p, word, static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, 0) + p.n0 + c0, args.stride, rows,
+                           [&](uint16_t* q, uint4 x) { *reinterpret_cast<uint4*>(q) = x; });
+                    continue;
+                }
                 if (aligned && c0 + 64 <= p.cols) {
                     transposed(p, word, [&](uint32_t r, uint32_t j, uint4 x) {
                         uint16_t* q = static_cast<uint16_t*>(o.out) + __shfl_sync(kFull, to, r) + p.n0 + c0 + 8 * j;
@@ -892,6 +911,13 @@ struct OutTile {
             const uint32_t c0 = 32 * h;
             auto word = [&](uint32_t j) { return __float_as_uint(__fmul_rn(z[h][j], scale)); };
             if (c0 >= p.cols) break;
+            const bool fresh = !o.add && (sum || (!mapped && !o.bf16 && !o.accumulate));
+            if (fresh && (sum || (aligned && c0 + 32 <= p.cols))) {
+                // float32 as it is, into the workspace (whole tiles there) or the caller's rows
+                float* first = sum ? sum + row0 * pitch + p.n0 + c0 : static_cast<float*>(o.out) + __shfl_sync(kFull, to, 0) + p.n0 + c0;
+                walked(p, word, first, sum ? pitch : args.stride, rows, [&](float* q, uint4 x) { *reinterpret_cast<uint4*>(q) = x; });
+                continue;
+            }
             if (sum || (aligned && c0 + 32 <= p.cols)) {
                 transposed(p, word, [&](uint32_t r, uint32_t j, uint4 bits) {
                     const uint32_t c = c0 + 4 * j;
