@@ -301,12 +301,13 @@ __device__ __forceinline__ void join_stat(float& top, float& sum, float top2, fl
 // all of them.  With y = z c and shares that add up to 1
 //   log sum exp(z / t) - sum p z / t = ln 2 (log2 sum 2^(y - top) + sum p (top - y)),
 // whose terms do not cancel, so float32 does.
-__device__ __forceinline__ float row_loss(const JoinArgs& a, uint64_t token, float top, float sum, uint32_t lane) {
+__device__ __forceinline__ float row_loss(const JoinArgs& a, uint64_t r, uint64_t token, float top, float sum, uint32_t lane) {
     const uint64_t at = token * a.lists.top;
     float dot = 0.f;  // sum p (top - y)
     for (int j = lane; j < a.lists.top; j += 32) {
-        if (a.lists.ids[at + j] == kNoId) break;  // nothing behind it
-        const float d = -__fmaf_rn(a.lists.logits[at + j], a.c, -top);
+        const int32_t id = a.lists.ids[at + j];
+        if (id == kNoId) break;  // nothing behind it
+        const float d = -__fmaf_rn(a.z ? a.z[r * a.z_pitch + id] : a.lists.logits[at + j], a.c, -top);
         const float share = a.lists.shares ? a.lists.shares[at + j] : 1.f;
         if (share != 0.f) dot = __fmaf_rn(share, d, dot);
     }
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_const
         float top, sum;
         row_stat(a, r, lane, 32, top, sum);
         const uint64_t token = a.rows.row[a.base + r];
-        loss = row_loss(a, token, top, sum, lane);
+        loss = row_loss(a, r, token, top, sum, lane);
         if (a.losses && lane == 0) a.losses[token] = loss;
     }
     if (lane == 0) {
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             const float entropy = a.lists.entropy[token];  // NaN: a list that is not valid
             inv = entropy == entropy && sum > 0.f ? __fdiv_rn(1.f, sum) : __int_as_float(0x7FC00000);
             if (blockIdx.x == 0 && warp == 0) {
-                const float loss = row_loss(a, token, top, sum, lane);
+                const float loss = row_loss(a, r, token, top, sum, lane);
                 if (lane == 0) {
                     a.loss[r] = loss;
                     if (a.losses) a.losses[token] = loss;
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             const uint32_t v = static_cast<uint32_t>(a.lists.ids[list + k]);
             if (v < lo || v >= hi) continue;
             const float share = a.lists.shares ? a.lists.shares[list + k] : 1.f;
-            float x = __fsub_rn(value(a.lists.logits[list + k]), share);
+            float x = __fsub_rn(value(z[v]), share);
             for (int q = 0; q < a.g.planes; ++q) g[q * a.g.plane + v] = split_plane(x);
         }
     }
@@ -738,20 +739,17 @@ __device__ __forceinline__ float4 floats(uint4 v) {
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-// Logits: the largest and the sum of a thread's 128 columns, the logits at its
-// row's ids, and the logits.
+// Logits: the largest and the sum of a thread's 128 columns, and the logits (where
+// the gradients' kernel finds those at the row's ids), or those at the ids alone.
 struct LogitTile {
     const LogitArgs& g;
     uint64_t list = 0;
     int next = 0;
     int32_t next_id = kNoId;
-    float top, sum;
 
     // Before the products are complete: the row's place in its list.
     __device__ __forceinline__ LogitTile(const ProductArgs& a, const Place& p) : g(a.logit) {
-        top = -kInf;
-        sum = 0.f;
-        if (!p.in) return;
+        if (!p.in || g.z) return;
         list = static_cast<uint64_t>(g.row[p.row]) * g.lists.top;
         next = first_id(g.lists.ids + list, g.lists.top, static_cast<int32_t>(g.v0 + p.n0));
         if (next < g.lists.top) next_id = g.lists.ids[list + next];
@@ -760,7 +758,6 @@ struct LogitTile {
     template <int C>
     __device__ __forceinline__ void chunk(const Place& p, float (&z)[32]) {
         const uint32_t c0 = 32 * C;
-        const int32_t v = static_cast<int32_t>(g.v0 + p.n0 + c0);
         if (g.z) {
             float* to = g.z + (p.row - p.lane) * g.z_pitch + p.n0 + c0;  // rows behind the last are the workspace's too
             walked(p, [&](uint32_t j) { return __float_as_uint(z[j]); }, to, g.z_pitch, 32,
@@ -771,6 +768,7 @@ struct LogitTile {
             for (int j = 0; j < 32; ++j)
                 if (c0 + j >= p.cols) z[j] = -kInf;
         }
+        const int32_t v = static_cast<int32_t>(g.v0 + p.n0 + c0);
         while (next_id < v + 32) {  // a list ends at kNoId, or with its places
             const int at = next_id - v;
             float x = 0.f;
@@ -781,16 +779,6 @@ struct LogitTile {
             ++next;
             next_id = next < g.lists.top ? g.lists.ids[list + next] : kNoId;
         }
-        float m = top;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) m = fmaxf(m, __fmul_rn(z[j], g.c));
-        const float base = m == -kInf ? 0.f : m;
-        sum = __fmul_rn(sum, exp2_fast(__fsub_rn(top, base)));
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < 32; ++j) part[j % 4] = __fadd_rn(part[j % 4], exp2_fast(__fmaf_rn(z[j], g.c, -base)));
-        sum = __fadd_rn(sum, __fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])));
-        top = m;
     }
 
     __device__ __forceinline__ void finish(const Place& p, float (&z)[4][32]) {
@@ -798,7 +786,20 @@ struct LogitTile {
         chunk<1>(p, z[1]);
         chunk<2>(p, z[2]);
         chunk<3>(p, z[3]);
-        if (p.in && p.cols) g.stats[p.row * g.stats_pitch + p.n0 / kStatColumns] = make_float2(top, sum);
+        float m[4] = {-kInf, -kInf, -kInf, -kInf}, part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) m[h] = fmaxf(m[h], z[h][j]);
+        // c > 0: the largest y is the largest z's
+        const float top = __fmul_rn(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), g.c), base = top == -kInf ? 0.f : top;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) part[h] = __fadd_rn(part[h], exp2_fast(__fmaf_rn(z[h][j], g.c, -base)));
+        if (p.in && p.cols)
+            g.stats[p.row * g.stats_pitch + p.n0 / kStatColumns] =
+                make_float2(top, __fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])));
     }
 };
 
