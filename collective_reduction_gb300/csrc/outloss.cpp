@@ -599,7 +599,9 @@ ar_status ar_output_distill(ar_output_loss_t h, const ar_output_loss_args* args,
                             int k, double temperature, void* stream) {
     ar::TraceRange trace("ar_output_distill");
     if (!h || !args || (id_bytes != 4 && id_bytes != 8) || !float_dtype(logit_dtype)) return AR_ERR_INVALID_ARG;
-    if (k < 1 || k > h->top || !float_normal(temperature) || !float_normal(1.0 / temperature)) return AR_ERR_INVALID_ARG;
+    if (k < 1 || k > h->top || !float_normal(temperature) || !float_normal(1.0 / temperature) ||
+        !float_normal(temperature * temperature))
+        return AR_ERR_INVALID_ARG;
     try {
         const uint64_t width = static_cast<uint64_t>(k);
         const ar_status s = check_args(h, args, {{ids, args->tokens, width, ids_stride, id_bytes},

@@ -582,8 +582,8 @@ typedef struct {
 ar_status ar_output_cross_entropy(ar_output_loss_t h, const ar_output_loss_args* args, const void* targets,
                                   int target_bytes, int64_t ignore_index, void* stream);
 /* Distillation from each token's k <= top largest teacher logits: the teacher's
- * shares p are their softmax at temperature t (a float32-normal number > 0), and
- * the loss is t^2 times the Kullback-Leibler divergence of the student's softmax
+ * shares p are their softmax at temperature t (> 0, float32-normal with its square
+ * and its reciprocal), and the loss is t^2 times the Kullback-Leibler divergence of the student's softmax
  * over the whole vocabulary from p.  ids: n x k integers of id_bytes 4 or 8,
  * negative for no entry; logits: n x k of logit_dtype, -infinity for no entry (with
  * an entry absent, its logit is not looked at); strides in elements between

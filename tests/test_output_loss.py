@@ -201,7 +201,7 @@ def run_ce(h, x, w, targets, dtype, grads=("hidden", "weight"), gtype=None, **mo
 
 
 SIZES = [(1, 1, 1), (1, 8, 2), (3, 5, 7), (37, 129, 203), (255, 64, 256), (256, 64, 257), (257, 72, 511),
-         (300, 515, 1003), (513, 96, 2003), (129, 640, 130)]
+         (300, 515, 1003), (513, 96, 2003), (129, 640, 130), (40, 1, 1), (300, 2, 70), (26, 7, 300)]
 
 
 @gpu
@@ -625,7 +625,7 @@ def test_refusals():
     refused(ce, hidden=x, weight=w, targets=t, losses=torch.zeros(19, device="cuda"))
     refused(ce, hidden=x, weight=w, targets=t, result=torch.zeros(3, device="cuda"))
     ids, logits = torch.zeros(20, 4, dtype=torch.int64, device="cuda"), torch.zeros(20, 4, device="cuda")
-    for k in (dict(temperature=0.0), dict(temperature=math.inf), dict(ids=ids[:, :3]), dict(logits=logits.half()),
+    for k in (dict(temperature=0.0), dict(temperature=math.inf), dict(temperature=1e30), dict(temperature=1e-30), dict(ids=ids[:, :3]), dict(logits=logits.half()),
               dict(ids=torch.zeros(20, 5, dtype=torch.int64, device="cuda"), logits=torch.zeros(20, 5, device="cuda")),
               dict(ids=ids[:, :0], logits=logits[:, :0])):
         refused(h.distill, **{**dict(hidden=x, weight=w, ids=ids, logits=logits), **k})
