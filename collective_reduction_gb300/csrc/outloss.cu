@@ -515,7 +515,7 @@ constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStag
 
 // One or two products in one launch.
 struct ProductParams {
-    CUtensorMap a[2], b[2];
+    CUtensorMap a[2], b[2];  // of logits a[1] is theirs
     ProductArgs args[2];
     RecordArgs record;
 };
@@ -748,7 +748,9 @@ struct LogitTile {
     int32_t next_id = kNoId;
 
     // Before the products are complete: the row's place in its list.
-    __device__ __forceinline__ LogitTile(const ProductArgs& a, const Place& p) : g(a.logit) {
+    const CUtensorMap* z_map;
+
+    __device__ __forceinline__ LogitTile(const ProductArgs& a, const Place& p, const CUtensorMap* z_map_) : g(a.logit), z_map(z_map_) {
         if (!p.in || g.z) return;
         list = static_cast<uint64_t>(g.row[p.row]) * g.lists.top;
         next = first_id(g.lists.ids + list, g.lists.top, static_cast<int32_t>(g.v0 + p.n0));
@@ -759,9 +761,17 @@ struct LogitTile {
     __device__ __forceinline__ void chunk(const Place& p, float (&z)[32]) {
         const uint32_t c0 = 32 * C;
         if (g.z) {
-            float* to = g.z + (p.row - p.lane) * g.z_pitch + p.n0 + c0;  // rows behind the last are the workspace's too
-            walked(p, [&](uint32_t j) { return __float_as_uint(z[j]); }, to, g.z_pitch, 32,
-                   [&](float* q, uint4 x) { *reinterpret_cast<uint4*>(q) = x; });
+            // rows behind the last are the workspace's too
+            if (p.lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the buffer before
+            stage(p, [&](uint32_t j) { return __float_as_uint(z[j]); });
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (p.lane == 0) {
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(z_map),
+                             "r"(static_cast<int>(p.n0 + c0)), "r"(static_cast<int>(p.row)), "r"(p.staged)
+                             : "memory");
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
         }
         if (c0 + 32 > p.cols) {
 #pragma unroll
@@ -1137,7 +1147,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             at.n0 = nt * a.width + half * kHalf;
             const uint32_t end = min(a.n, (nt + 1) * a.width);
             at.cols = end > at.n0 ? min(static_cast<uint32_t>(kHalf), end - at.n0) : 0;
-            std::conditional_t<LOGITS, LogitTile, OutTile> tile(a, at);
+            auto tile = [&] {
+                if constexpr (LOGITS) return LogitTile(a, at, &p.a[1]);
+                else return OutTile(a, at);
+            }();
             float z[4][32];
 #pragma unroll
             for (int h = 0; h < 4; ++h)
@@ -1172,6 +1185,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
             }
         }
     }
+    // the logits are in memory before the CTA's end
+    if (LOGITS && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!ok) atomicOr(p.args[0].status, 1u);
     __syncwarp();
     tmem_fence_before();
@@ -1595,6 +1610,18 @@ cudaError_t prepare_products() {
     return cudaSuccess;
 }
 
+// The piece's logits, 32 rows of 32 columns a store.
+cudaError_t make_logit_map(const LogitArgs& g, uint64_t rows, uint64_t columns, CUtensorMap* map) {
+    const EncodeFn encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {columns, rows}, strides[1] = {g.z_pitch * 4};
+    const cuuint32_t box[2] = {32, 32}, steps[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, g.z, dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
 namespace {
 
 cudaError_t launch_tiles(ProductParams& p, int n, bool logits, cudaStream_t st) {
@@ -1618,6 +1645,10 @@ cudaError_t launch_logits(ProductArgs a, cudaStream_t st) {
     set_shape(a);
     a.width = std::min<uint32_t>(kSide, ctas(a.n, 32) * 32);  // statistics are of whole tiles' halves
     p.args[0] = a;
+    if (a.logit.z) {
+        const cudaError_t e = make_logit_map(a.logit, tall_of(a) * kSide, wide_of(a) * kSide, &p.a[1]);
+        if (e != cudaSuccess) return e;
+    }
     return launch_tiles(p, 1, true, st);
 }
 
