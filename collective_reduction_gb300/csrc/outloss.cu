@@ -1589,7 +1589,7 @@ cudaError_t launch_grad(const JoinArgs& a0, cudaStream_t st) {
     JoinArgs a = a0;
     const uint32_t rows = ctas(a.n, a.round) * a.round;
     a.columns = 128 * kGradThreads;  // less while a few waves of CTAs are not full
-    while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 40 * kLossSms) a.columns /= 2;
+    while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 16 * kLossSms) a.columns /= 2;
     return launch(grad_kernel, dim3(ctas(a.vocab, a.columns), std::min(rows, 32768u)), kGradThreads, 0, st, a);
 }
 
