@@ -49,7 +49,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 constexpr int kTeacherWarps = 4;
 
 // A warp a token: the softmax of its entries, entries of one id added up, sorted
-// by id.  The k^2 comparisons of a list stay in shared memory.
+// by id.  The k^2 comparisons of a list stay in shared memory: 17 us for 2048 lists
+// of 64, 2% of what follows.
 __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const __grid_constant__ TeacherArgs a) {
     extern __shared__ char smem[];
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -144,7 +145,8 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const __gri
 constexpr int kRowThreads = 1024;
 
 // One CTA: targets into lists of one id, and the tokens that count in their
-// order; every warp has a run of tokens, 32 at a time.
+// order; every warp has a run of tokens, 32 at a time (14 us for 16384: latency; a
+// thread a run of its own took 45).
 __global__ void __launch_bounds__(kRowThreads) rows_kernel(const __grid_constant__ RowsArgs a) {
     __shared__ uint32_t sums[32];
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -253,7 +255,8 @@ __device__ __forceinline__ uint4 pack_eight(const float (&x)[8]) {
     return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
-// A warp a row (and a token), over the rows up to a tile's end.
+// A warp a row (and a token), over the rows up to a tile's end.  Bound by HBM at
+// size: 65 MB of odd bf16 rows 26 us, 16384 rows of 1024 15 us.
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
     const uint32_t lane = threadIdx.x % 32;
     const uint64_t r = blockIdx.x * 8ull + threadIdx.x / 32;
@@ -407,8 +410,10 @@ constexpr int kGradThreads = 256;
 //   g = 2^(y - top) / sum - share
 // from the logits, then the few columns of the row's list.  The factor comes with
 // the products' float32 sums: in bf16 a token's largest gradients, near -1, would all
-// carry the factor's own rounding.  Bound by HBM: a logit's
-// 4 bytes in and its gradient's 2 (float32: 6) out.
+// carry the factor's own rounding.  Bound by HBM: a logit's 4 bytes in and its
+// gradient's 2 (float32: 6) out, 6.2 TB/s on cold caches at 4096 x 50001, 7 among the
+// other launches.  A row's statistics cost each of its CTAs a round trip, so ranges are
+// long: 281 us for 2048 x 128000 in 8192 columns, 215 as here.
 __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ JoinArgs a) {
     __shared__ float2 part[kGradThreads / 32];
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -488,6 +493,13 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int 
 // The tensor cores cut sums off where float32 would round them.  Products whose
 // result is float32 are therefore summed there for a run of blocks only, and runs
 // are added up in the epilogue's registers.
+//
+// Bound by the tensor cores: 256 x 256 is the largest tile whose accumulators fit
+// TMEM twice and halves what each CTA loads of B; 64 products a block is a swizzle's
+// 128 bytes, six blocks in flight all that shared memory holds beside 32 KB on its way
+// out.  4096 tokens of 2048 x 50001: logits 482 us (1.74 PFLOP/s; tensor cores 81%
+// busy, the logits' way out takes shared memory's bandwidth), both gradients 882 us
+// (1.90 PFLOP/s, 94%).
 
 constexpr int kSide = 256;             // rows and columns of a pair's tile
 constexpr int kHalf = kSide / 2;       // ... of A and of B in one CTA
@@ -1533,7 +1545,10 @@ uint64_t wide_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.n) + a.
 uint64_t blocks_of(const ProductArgs& a) { return (static_cast<uint64_t>(a.k) + kDeep - 1) / kDeep; }
 
 // Tiles as wide as they divide the columns evenly; rows of tiles side by side: all
-// of them while A's rows stay in L2, then eight.
+// of them while A's rows stay in L2, then eight.  Measured, all against eight: logits
+// of 4096 tokens of 2048 x 50001 460 against 468 us (16 MB of A), of 8192 of 4096 x
+// 128000 4.49 against 4.48 ms (64 MB); dW of the two (410 MB and 2.1 GB) with its
+// logits 1298 against 1204 us and 12.0 against 11.3 ms.
 void set_shape(ProductArgs& a) {
     const uint32_t wide = ctas(a.n, kSide);
     a.width = (ctas(a.n, wide) + 31) / 32 * 32;
@@ -1544,7 +1559,8 @@ void set_shape(ProductArgs& a) {
 
 // Parts of the first product's k: the number that leaves the fullest pair the least
 // to do, in columns of blocks, with what the parts cost (8 blocks' time for their
-// launch, one for four parts of a tile).
+// launch, one for four parts of a tile).  37 tokens' dX of 129 x 2003 float32: one
+// tile of 32 blocks, 13 us in 8 parts and more, 67 us in one.
 uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t room) {
     const uint64_t pairs = kLossSms / 2, tiles = tall_of(a) * wide_of(a), blocks = blocks_of(a);
     if (tiles == 0 || tiles >= 8 * pairs) return 1;
