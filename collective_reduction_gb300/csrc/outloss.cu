@@ -413,7 +413,7 @@ constexpr int kGradThreads = 256;
 // carry the factor's own rounding.  Bound by HBM: a logit's 4 bytes in and its
 // gradient's 2 (float32: 6) out, 6.2 TB/s on cold caches at 4096 x 50001, 7 among the
 // other launches.  A row's statistics cost each of its CTAs a round trip, so ranges are
-// long: 281 us for 2048 x 128000 in 8192 columns, 215 as here.
+// long: 281 us for 2048 x 128000 in 8192 columns, 247 in 32768.
 __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constant__ JoinArgs a) {
     __shared__ float2 part[kGradThreads / 32];
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -497,9 +497,9 @@ __device__ __forceinline__ void store_out(void* out, uint64_t at, int bf16, int 
 // Bound by the tensor cores: 256 x 256 is the largest tile whose accumulators fit
 // TMEM twice and halves what each CTA loads of B; 64 products a block is a swizzle's
 // 128 bytes, six blocks in flight all that shared memory holds beside 32 KB on its way
-// out.  4096 tokens of 2048 x 50001: logits 482 us (1.74 PFLOP/s; tensor cores 81%
-// busy, the logits' way out takes shared memory's bandwidth), both gradients 882 us
-// (1.90 PFLOP/s, 94%).
+// out.  4096 tokens of 2048 x 50001: logits 511 us (1.64 PFLOP/s; tensor cores 81%
+// busy, the logits' way out takes shared memory's bandwidth), both gradients 846 us
+// (1.98 PFLOP/s, 94%).
 
 constexpr int kSide = 256;             // rows and columns of a pair's tile
 constexpr int kHalf = kSide / 2;       // ... of A and of B in one CTA
@@ -1559,8 +1559,9 @@ void set_shape(ProductArgs& a) {
 
 // Parts of the first product's k: the number that leaves the fullest pair the least
 // to do, in columns of blocks, with what the parts cost (8 blocks' time for their
-// launch, one for four parts of a tile).  37 tokens' dX of 129 x 2003 float32: one
-// tile of 32 blocks, 13 us in 8 parts and more, 67 us in one.
+// launch, one for four parts of a tile).  Whole calls of float32 tokens with parts
+// and without: 37 of 129 x 2003 40 and 87 us, 300 of 256 x 5003 60 and 180, 515 of
+// 515 x 10007 173 and 363.
 uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t room) {
     const uint64_t pairs = kLossSms / 2, tiles = tall_of(a) * wide_of(a), blocks = blocks_of(a);
     if (tiles == 0 || tiles >= 8 * pairs) return 1;
