@@ -109,22 +109,24 @@ def bound_of_sum(k, dtype):
 
 
 class Expected:
-    """The definition in 64 bits on the host, and how far float32 may be off."""
+    """The definition in 64 bits (on the host unless told), and how far float32
+    may be off."""
 
-    def __init__(self, x, w, ids, shares, t=1.0, scale=1.0, reduction="mean", dtype="bfloat16", spread=None):
+    def __init__(self, x, w, ids, shares, t=1.0, scale=1.0, reduction="mean", dtype="bfloat16", spread=None, on="cpu"):
         """ids: lists of each token (empty: does not count); shares likewise;
         spread: the largest teacher difference / t of each token."""
         import torch
-        x, w = x.double().cpu(), w.double().cpu()
+        x, w = x.double().to(on), w.double().to(on)
+        self.on = on
         n, v = x.shape[0], w.shape[0]
         keep = [i for i in range(n) if ids[i]]
         self.counted = len(keep)
         self.factor = scale / max(1, len(keep)) if reduction == "mean" else scale
-        p = torch.zeros(n, v, dtype=torch.float64)
+        p = torch.zeros(n, v, dtype=torch.float64, device=on)
         for i in keep:
             for j, s in zip(ids[i], shares[i]):
                 p[i, j] += s
-        mask = torch.zeros(n, 1, dtype=torch.float64)
+        mask = torch.zeros(n, 1, dtype=torch.float64, device=on)
         mask[keep] = 1.0
         xs = torch.where(mask > 0, x, 0.0)
         zt = xs @ w.t() / t
@@ -156,14 +158,14 @@ class Expected:
         assert factor == pytest.approx(self.factor, rel=2 * U)
         assert abs(loss - self.loss) <= self.loss_tol + 1e-40
         if losses is not None:
-            assert bool(((losses.double().cpu() - self.losses).abs() <= self.losses_tol).all())
+            assert bool(((losses.double().to(self.on) - self.losses).abs() <= self.losses_tol).all())
         for got, want, tol, old in ((dx, self.dx, self.dx_tol, x0), (dw, self.dw, self.dw_tol, w0)):
             if got is None:
                 continue
             h = half_step(str(got.dtype).replace("torch.", ""))
             if old is not None:
-                want = want + old.double().cpu()
-            off = (got.double().cpu() - want).abs()
+                want = want + old.double().to(self.on)
+            off = (got.double().to(self.on) - want).abs()
             room = tol * (1 + 2 * h) + 2 * h * want.abs() + 1e-38  # the sum with what was there rounds in float32 too
             assert bool((off <= room).all()), float((off / room).max())
 
@@ -265,6 +267,26 @@ def test_pieces(n, d, v, piece, dtype):
     assert h.info()["pieces"] > 1
     want = Expected(x, w, *one_hot_lists(t), reduction="sum", scale=0.25, dtype=dtype)
     want.check(*run_ce(h, x, w, t.int(), dtype, reduction="sum", scale=0.25))
+
+
+@gpu
+@pytest.mark.parametrize("dtype, gtype", [("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float32", "float32")])
+@pytest.mark.parametrize("n, d, v", [(1700, 40, 303), (2400, 270, 130)])
+@pytest.mark.parametrize("keep", [1.0, 0.3])
+def test_more_pieces_than_are_kept(n, d, v, keep, dtype, gtype):
+    """The weights' gradient is summed in memory over several runs of pieces; the
+    last ones may hold no token that counts."""
+    import torch
+    x, w, g = make(n, d, v, dtype, seed=25)
+    t = targets_of(n, v, g, keep)
+    h = ar.OutputLoss(n, d, v, dtype, piece=256)
+    assert h.info()["pieces"] > 4
+    want = Expected(x, w, *one_hot_lists(t), dtype=dtype)
+    want.check(*run_ce(h, x, w, t, dtype, gtype=gtype))
+    dx, dw = (0.01 * torch.randn(a.shape, generator=g).to(tdt(gtype)).cuda() for a in (x, w))
+    x0, w0 = dx.clone(), dw.clone()
+    rec = h.cross_entropy(x, w, t.cuda(), grad_hidden=dx, grad_weight=dw, accumulate=True)
+    want.check(rec, None, dx, dw, x0, w0)
 
 
 @gpu
@@ -543,9 +565,9 @@ def test_gradients_against_differences():
 
 
 @gpu
-def test_in_a_graph_on_its_stream_with_new_inputs():
+@pytest.mark.parametrize("n, d, v", [(640, 72, 500), (4, 72, 500)])
+def test_in_a_graph_on_its_stream_with_new_inputs(n, d, v):
     import torch
-    n, d, v = 640, 72, 500
     x, w, g = make(n, d, v, "bfloat16", seed=17)
     t = targets_of(n, v, g, 0.8).cuda()
     h = ar.OutputLoss(n, d, v, top=4, piece=512)
@@ -569,6 +591,80 @@ def test_in_a_graph_on_its_stream_with_new_inputs():
         Expected(x2, w2, *one_hot_lists(t2)).check(*got)
         eager = run_ce(h, x2, w2, t2, "bfloat16")  # the same bits as the graph's
         assert all(torch.equal(p, q) for p, q in zip(got, eager))
+
+
+@gpu
+def test_weights_packed_in_turn():
+    """Float32 rows so long that the workspace holds a part of the weights at a
+    time: logits and the gradient of the hidden states go part by part."""
+    n, d, v = 40, 65536, 2900
+    x, w, g = make(n, d, v, "float32", seed=23)
+    t = targets_of(n, v, g, 0.8)
+    h = ar.OutputLoss(n, d, v, "float32")
+    want = Expected(x, w, *one_hot_lists(t), dtype="float32", on="cuda")
+    want.check(*run_ce(h, x, w, t, "float32"))
+    want.check(*run_ce(h, x, w, t, "float32", ()))
+
+
+@gpu
+@pytest.mark.parametrize("n", [3, 30])
+def test_weights_of_more_than_2_to_the_31_elements(n):
+    """Losses, the hidden states' gradient and rows of the weights' from both ends,
+    against the definition in pieces of the vocabulary."""
+    import torch
+    d, v, step = 8192, 270000, 30000
+    g = torch.Generator(device="cuda").manual_seed(24)
+    x = torch.randn(n, d, generator=g, device="cuda").bfloat16()
+    w = torch.empty(v, d, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, v, step):
+        w[a:a + step] = torch.randn(step, d, generator=g, device="cuda") * (1.3 / math.sqrt(d))
+    t = torch.randint(v, (n,), generator=g, device="cuda")
+    t[0], t[1] = v - 1, 0
+    dw, dx, losses = torch.empty_like(w), torch.empty_like(x), torch.empty(n, device="cuda")
+    h = ar.OutputLoss(n, d, v)
+    rec = h.cross_entropy(x, w, t, grad_hidden=dx, grad_weight=dw, losses=losses)
+    h.check()
+    z = torch.cat([x.double() @ w[a:a + step].double().t() for a in range(0, v, step)], 1)
+    q = torch.softmax(z, 1)
+    want = torch.logsumexp(z, 1) - z.gather(1, t[:, None])[:, 0]
+    e = bound_of_sum(d, "bfloat16") * float((x.double().abs().sum(1) * float(w.abs().max())).max())
+    dq = 2 * e + 8 * U * (float(z.abs().max()) + 2) + 2 * U * (v + 4) + 16 * U
+    assert bool(((losses.double() - want).abs() <= 2 * dq + 4 * U * want).all())
+    assert abs(rec[0].item() - float(want.mean())) <= 2 * dq + 8 * U * float(want.mean())
+    gz = q.clone()
+    gz.scatter_add_(1, t[:, None], torch.full((n, 1), -1.0, dtype=torch.float64, device="cuda"))
+    gz /= n
+    off = q * dq / n + 2.0 ** -8 * gz.abs() + bound_of_sum(v, "bfloat16") * gz.abs()
+    dx_want, room = torch.zeros(n, d, dtype=torch.float64, device="cuda"), torch.zeros(n, d, dtype=torch.float64, device="cuda")
+    for a in range(0, v, step):
+        part = w[a:a + step].double()
+        dx_want += gz[:, a:a + step] @ part
+        room += off[:, a:a + step] @ part.abs()
+    assert bool(((dx.double() - dx_want).abs() <= room * 1.01 + 2.0 ** -8 * dx_want.abs() + 1e-38).all())
+    for rows in (slice(0, 300), slice(262000, 262300), slice(v - 300, v)):
+        dw_want = gz[:, rows].t() @ x.double()
+        room = off[:, rows].t() @ x.double().abs()
+        assert bool(((dw[rows].double() - dw_want).abs() <= room * 1.01 + 2.0 ** -8 * dw_want.abs() + 1e-38).all())
+
+
+@gpu
+def test_two_handles_on_two_streams():
+    import torch
+    cases = []
+    for n, d, v, dtype in ((700, 264, 3000, "bfloat16"), (300, 129, 2003, "float32")):
+        x, w, g = make(n, d, v, dtype, seed=n)
+        t = targets_of(n, v, g, 0.8)
+        h = ar.OutputLoss(n, d, v, dtype)
+        alone = run_ce(h, x, w, t, dtype)
+        cases.append((h, x, w, t.cuda(), alone, torch.cuda.Stream(), [torch.zeros_like(a) for a in (x, w)]))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for h, x, w, t, _, stream, (dx, dw) in cases:
+            h.cross_entropy(x, w, t, grad_hidden=dx, grad_weight=dw, stream=stream)
+    torch.cuda.synchronize()
+    for h, x, w, t, (rec, _, dx0, dw0), _, (dx, dw) in cases:
+        h.check()
+        assert torch.equal(h.record, rec) and torch.equal(dx, dx0) and torch.equal(dw, dw0)
 
 
 @gpu
