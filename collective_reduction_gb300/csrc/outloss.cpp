@@ -208,21 +208,25 @@ struct Call {
                a->weight_stride % 8 == 0 && a->weight_stride < (1ull << 38);
     }
     // Vocabulary entries that are at hand at a time, [v0, v1) as planes: where they are, or packed.
-    uint64_t entries() const { return weight_as_is() ? h->vocab : h->l.pack; }
+    uint64_t entries() const { return weight_as_is() ? h->vocab : std::min(h->vocab, h->l.pack); }
     // All of them stay packed for the call.
     ar::Planes weight(uint64_t v0, uint64_t v1) {
-        const char* from = static_cast<const char*>(a->weight) + v0 * a->weight_stride * esize(h->dtype);
-        if (weight_as_is()) return {reinterpret_cast<uint16_t*>(const_cast<char*>(from)), 0, a->weight_stride, 1};
+        if (weight_as_is())
+            return {static_cast<uint16_t*>(const_cast<void*>(a->weight)) + v0 * a->weight_stride, 0, a->weight_stride, 1};
+        const ar::PackArgs p = pack_weight(v0, v1);
+        if (!packed) run(ar::launch_pack(p, nullptr, st));
+        packed = v0 == 0 && v1 == h->vocab;
+        return p.out;
+    }
+    ar::PackArgs pack_weight(uint64_t v0, uint64_t v1) const {
         ar::PackArgs p = {};
-        p.src = from;
+        p.src = static_cast<const char*>(a->weight) + v0 * a->weight_stride * esize(h->dtype);
         p.stride = a->weight_stride;
         p.bf16 = h->dtype == AR_BFLOAT16;
         p.n = static_cast<uint32_t>(v1 - v0);
         p.width = width;
         p.out = {h->at<uint16_t>(h->l.weight), h->l.pack * h->l.pitch, h->l.pitch, h->l.planes};
-        if (!packed) run(ar::launch_pack(p, st));
-        packed = v0 == 0 && v1 == h->vocab;
-        return p.out;
+        return p;
     }
     void run(cudaError_t next) {
         if (e == cudaSuccess) e = next;
@@ -467,7 +471,10 @@ struct Call {
             p.grad = a->accumulate ? nullptr : a->grad_hidden;
             p.grad_stride = a->grad_hidden_stride;
             p.grad_bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
-            run(ar::launch_pack(p, st));
+            // with the weights, where all of them are packed at a time
+            packed = !weight_as_is() && entries() == h->vocab;
+            const ar::PackArgs w = packed ? pack_weight(0, h->vocab) : ar::PackArgs{};
+            run(ar::launch_pack(p, packed ? &w : nullptr, st));
         }
         for (uint64_t first = 0; first < n || first == 0; first += h->l.kept) {
             const uint32_t all = static_cast<uint32_t>(std::min<uint64_t>(n - first, h->l.kept));

@@ -257,11 +257,7 @@ __device__ __forceinline__ uint4 pack_eight(const float (&x)[8]) {
 
 // A warp a row (and a token), over the rows up to a tile's end.  Bound by HBM at
 // size: 65 MB of odd bf16 rows 26 us, 16384 rows of 1024 15 us.
-__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a) {
-    const uint32_t lane = threadIdx.x % 32;
-    const uint64_t r = blockIdx.x * 8ull + threadIdx.x / 32;
-    griddep_launch_dependents();
-    griddep_wait();
+__device__ __forceinline__ void pack_row(const PackArgs& a, uint64_t r, uint32_t lane) {
     if (a.counted && r < a.n && !a.counted[r]) {
         if (a.losses && lane == 0) a.losses[r] = 0.f;
         if (a.grad)
@@ -285,6 +281,16 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
             for (int q = 0; q < a.out.planes; ++q) *reinterpret_cast<uint4*>(out + q * a.out.plane + c) = split_eight(x);
         }
     }
+}
+
+// One matrix, or two of which the second begins with CTA `second`.
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackArgs a, const __grid_constant__ PackArgs b,
+                                                   uint32_t second) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (blockIdx.x < second) pack_row(a, blockIdx.x * 8ull + warp, lane);
+    else pack_row(b, (blockIdx.x - second) * 8ull + warp, lane);
 }
 
 // ------------------------------------------------------------------- joins
@@ -1594,8 +1600,9 @@ cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st) {
 
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) { return launch(rows_kernel, 1, kRowThreads, 0, st, a); }
 
-cudaError_t launch_pack(const PackArgs& a, cudaStream_t st) {
-    return launch(pack_kernel, ctas(a.n, kLossTile) * (kLossTile / 8), 256, 0, st, a);
+cudaError_t launch_pack(const PackArgs& a, const PackArgs* b, cudaStream_t st) {
+    const uint32_t first = ctas(a.n, kLossTile) * (kLossTile / 8), more = b ? ctas(b->n, kLossTile) * (kLossTile / 8) : 0;
+    return launch(pack_kernel, first + more, 256, 0, st, a, b ? *b : a, first);
 }
 
 cudaError_t launch_join(const JoinArgs& a, cudaStream_t st) {

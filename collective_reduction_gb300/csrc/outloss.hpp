@@ -215,7 +215,7 @@ struct FewArgs {
 
 cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st);
-cudaError_t launch_pack(const PackArgs& a, cudaStream_t st);
+cudaError_t launch_pack(const PackArgs& a, const PackArgs* b, cudaStream_t st);  // b: null, or a second matrix
 cudaError_t launch_join(const JoinArgs& a, cudaStream_t st);  // losses alone
 cudaError_t launch_grad(const JoinArgs& a, cudaStream_t st);  // losses and the logits' gradients
 // What the products' kernels need once on a device before their first launch.

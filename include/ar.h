@@ -533,8 +533,8 @@ ar_status ar_output_loss_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab
 /* A handle for up to `tokens` tokens of hidden size D over V vocabulary entries,
  * X and W of `dtype`.  top: entries of a teacher's list at most (0: cross entropy
  * alone).  piece: tokens at a time (rounded up to 256; 0: as many as make 2^28
- * logits, 256 at least): the workspace is mostly 6 bytes for each of their logits
- * (float32: 10).  gradients: 0 for losses alone, with a small workspace.
+ * logits, 256 at least): the workspace is mostly 4 bytes for each of a piece's
+ * logits and 2 (float32: 6) for each of up to four pieces'.  gradients: 0 for losses alone, with a small workspace.
  * AR_ERR_INVALID_ARG: null out, D or V of 0, top < 0, unknown types.
  * AR_ERR_UNSUPPORTED: AR_INT32, more than 2^22 tokens, D > 2^16, V > 2^24, top >
  * 1024, more than 2^31 list entries.  AR_ERR_NOMEM, AR_ERR_CUDA. */
