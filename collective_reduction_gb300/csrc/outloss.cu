@@ -623,6 +623,13 @@ __device__ __forceinline__ void tmem_read16(uint32_t taddr, float* v) {
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// No use of 16 values read from tensor memory before the wait that precedes this.
+__device__ __forceinline__ void tmem_arrived(float* v) {
+    asm volatile(""
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+
 // The tiles of a product and the blocks of each.
 struct Tiles {
     uint32_t m, blocks, splits, per;  // rows of A, blocks of k, ... of a split
@@ -1170,29 +1177,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 else return OutTile(a, at);
             }();
             float z[4][32];
-#pragma unroll
-            for (int h = 0; h < 4; ++h)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) z[h][j] = 0.f;
-            for (uint32_t i = 0; i < n;) {
-                const uint32_t b = done & 1;
-                ok = __all_sync(kFull, mbar_wait_here(bar(kReadyBar + b), (done / 2) & 1));
-                if (!ok) break;
+            uint32_t i = 0;
+            // a run's accumulators, waited for; its buffer, given back
+            auto ready = [&] {
+                ok = __all_sync(kFull, mbar_wait_here(bar(kReadyBar + (done & 1)), (done / 2) & 1));
                 tmem_fence_after();
+                return ok;
+            };
+            auto release = [&] {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(in_first(bar(kFreeBar + (done & 1))));
+                ++done;
+                i = n - i > a.run ? i + a.run : n;
+            };
+            if (n > 0) {
+                if (!ready()) break;
+#pragma unroll
+                for (int h = 0; h < 8; ++h) tmem_read16(lanes + (done & 1) * kSide + 16 * h, z[h / 2] + 16 * (h & 1));
+                tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 8; ++h) tmem_arrived(z[h / 2] + 16 * (h & 1));
+                release();
+            } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[h][j] = 0.f;
+            }
+            while (i < n) {
+                if (!ready()) break;
 #pragma unroll
                 for (int h = 0; h < 8; ++h) {
                     float x[16];
-                    tmem_read16(lanes + b * kSide + 16 * h, x);
+                    tmem_read16(lanes + (done & 1) * kSide + 16 * h, x);
                     tmem_wait_ld();
+                    tmem_arrived(x);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         z[h / 2][16 * (h & 1) + j] = __fadd_rn(z[h / 2][16 * (h & 1) + j], x[j]);
                 }
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive_cluster(in_first(bar(kFreeBar + b)));
-                ++done;
-                i = n - i > a.run ? i + a.run : n;
+                release();
             }
             if (!ok) break;
             if constexpr (LOGITS) {
