@@ -1205,17 +1205,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[h][j] = 0.f;
             }
+            // 32 columns at a time where registers are left for them (515 float32 tokens'
+            // gradients spill: 173 us instead of 167)
+            constexpr int kAhead = LOGITS ? 2 : 1;
             while (i < n) {
                 if (!ready()) break;
 #pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                    float x[16];
-                    tmem_read16(lanes + (done & 1) * kSide + 16 * h, x);
-                    tmem_wait_ld();
-                    tmem_arrived(x);
+                for (int h = 0; h < 8; h += kAhead) {
+                    float x[kAhead][16];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        z[h / 2][16 * (h & 1) + j] = __fadd_rn(z[h / 2][16 * (h & 1) + j], x[j]);
+                    for (int k = 0; k < kAhead; ++k) tmem_read16(lanes + (done & 1) * kSide + 16 * (h + k), x[k]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < kAhead; ++k) {
+                        float* to = z[(h + k) / 2] + 16 * ((h + k) & 1);
+                        tmem_arrived(x[k]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) to[j] = __fadd_rn(to[j], x[k][j]);
+                    }
                 }
                 release();
             }
