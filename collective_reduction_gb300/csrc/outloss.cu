@@ -310,7 +310,8 @@ __device__ __forceinline__ void join_stat(float& top, float& sum, float top2, fl
 // all of them.  With y = z c and shares that add up to 1
 //   log sum exp(z / t) - sum p z / t = ln 2 (log2 sum 2^(y - top) + sum p (top - y)),
 // whose terms do not cancel, so float32 does.
-__device__ __forceinline__ float row_loss(const JoinArgs& a, uint64_t r, uint64_t token, float top, float sum, uint32_t lane) {
+__device__ __forceinline__ float row_loss(const JoinArgs& a, uint64_t r, uint64_t token, float top, float sum,
+                                          uint32_t lane) {
     const uint64_t at = token * a.lists.top;
     float dot = 0.f;  // sum p (top - y)
     for (int j = lane; j < a.lists.top; j += 32) {
@@ -325,7 +326,8 @@ __device__ __forceinline__ float row_loss(const JoinArgs& a, uint64_t r, uint64_
 }
 
 // The statistics of a place by the lanes of a warp, from part `first` on in steps of `step`.
-__device__ __forceinline__ void row_stat(const JoinArgs& a, uint64_t r, uint32_t first, uint32_t step, float& top, float& sum) {
+__device__ __forceinline__ void row_stat(const JoinArgs& a, uint64_t r, uint32_t first, uint32_t step, float& top,
+                                         float& sum) {
     const float2* at = a.stats + r * a.pitch;
     top = -kInf;
     sum = 0.f;
@@ -517,7 +519,8 @@ constexpr uint32_t kStagedBytes = 32 * 128;  // of an epilogue warp: 32 rows' pa
 constexpr int kTmemColumns = 512;
 
 static_assert(kStages % kMaxPlanes == 0, "a float32 block's stages follow each other");
-static_assert(kSide == static_cast<int>(kLossTile) && kHalf == static_cast<int>(kStatColumns), "statistics are of an epilogue thread's columns");
+static_assert(kSide == static_cast<int>(kLossTile) && kHalf == static_cast<int>(kStatColumns),
+              "statistics are of an epilogue thread's columns");
 
 // Barriers, in 8-byte words of shared memory.
 enum : uint32_t {
@@ -529,7 +532,8 @@ enum : uint32_t {
     kTmemWord = kDoneBar + 1,
     kBarWords = kTmemWord + 1
 };
-constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;  // 1024: to a swizzle's boundary
+// (1024: to a swizzle's boundary)
+constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStagedBytes + kBarWords * 8 + 1024;
 
 // One or two products in one launch.
 struct ProductParams {
@@ -646,7 +650,8 @@ struct Tiles {
         total = tall * wide * splits;
     }
     // Tile t: in each split, groups of `group` rows of tiles, column by column.
-    __device__ __forceinline__ void at(uint32_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo, uint32_t& n) const {
+    __device__ __forceinline__ void at(uint32_t t, uint32_t& mt, uint32_t& nt, uint32_t& split, uint32_t& lo,
+                                       uint32_t& n) const {
         const uint32_t each = tall * wide;
         split = splits == 1 ? 0 : t / each;
         const uint32_t r = t - split * each;
@@ -775,7 +780,8 @@ struct LogitTile {
     // Before the products are complete: the row's place in its list.
     const CUtensorMap* z_map;
 
-    __device__ __forceinline__ LogitTile(const ProductArgs& a, const Place& p, const CUtensorMap* z_map_) : g(a.logit), z_map(z_map_) {
+    __device__ __forceinline__ LogitTile(const ProductArgs& a, const Place& p, const CUtensorMap* z_map_)
+        : g(a.logit), z_map(z_map_) {
         if (!p.in || g.z) return;
         list = static_cast<uint64_t>(g.row[p.row]) * g.lists.top;
         next = first_id(g.lists.ids + list, g.lists.top, static_cast<int32_t>(g.v0 + p.n0));
@@ -904,7 +910,8 @@ struct OutTile {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 auto word = [&](uint32_t j) {
-                    return pack_bf16x2(__fmul_rn(z[2 * h + j / 16][2 * j % 32], scale), __fmul_rn(z[2 * h + j / 16][2 * j % 32 + 1], scale));
+                    const float(&x)[32] = z[2 * h + j / 16];
+                    return pack_bf16x2(__fmul_rn(x[2 * j % 32], scale), __fmul_rn(x[2 * j % 32 + 1], scale));
                 };
                 const uint32_t c0 = 64 * h;
                 if (c0 >= p.cols) break;
@@ -950,8 +957,9 @@ struct OutTile {
             const bool fresh = !o.add && (sum || (!mapped && !o.bf16 && !o.accumulate));
             if (fresh && (sum || (aligned && c0 + 32 <= p.cols))) {
                 // float32 as it is, into the workspace (whole tiles there) or the caller's rows
-                float* first = sum ? sum + row0 * pitch + p.n0 + c0 : static_cast<float*>(o.out) + __shfl_sync(kFull, to, 0) + p.n0 + c0;
-                walked(p, word, first, sum ? pitch : args.stride, rows, [&](float* q, uint4 x) { *reinterpret_cast<uint4*>(q) = x; });
+                float* first = sum ? sum + row0 * pitch : static_cast<float*>(o.out) + __shfl_sync(kFull, to, 0);
+                walked(p, word, first + p.n0 + c0, sum ? pitch : args.stride, rows,
+                       [&](float* q, uint4 x) { *reinterpret_cast<uint4*>(q) = x; });
                 continue;
             }
             if (sum || (aligned && c0 + 32 <= p.cols)) {
@@ -1231,7 +1239,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 tile.finish(at, z);
             } else {
                 const Tiles& tiles = work.tiles[which];
-                tile.finish(at, z, tiles.splits > 1 ? a.out.parts + split * (static_cast<uint64_t>(tiles.tall) * kSide * a.out.part_pitch) : nullptr);
+                const uint64_t part = static_cast<uint64_t>(tiles.tall) * kSide * a.out.part_pitch;
+                tile.finish(at, z, tiles.splits > 1 ? a.out.parts + split * part : nullptr);
             }
         }
     }
@@ -1474,7 +1483,8 @@ __global__ void __launch_bounds__(kFewThreads) few_gradients_kernel(const __grid
             const uint32_t r = i / kFewColumns, v = v0 + i % kFewColumns;
             float g = 0.f;
             if (r < count && v < hi)
-                for (int q = a.g.planes - 1; q >= 0; --q) g = __fadd_rn(g, bf16_value(a.g.p[q * a.g.plane + r * a.g.pitch + v]));
+                for (int q = a.g.planes - 1; q >= 0; --q)
+                    g = __fadd_rn(g, bf16_value(a.g.p[q * a.g.plane + r * a.g.pitch + v]));
             gs[r][i % kFewColumns] = g;
         }
         __syncthreads();
@@ -1515,11 +1525,13 @@ __global__ void __launch_bounds__(kFewThreads) few_gradients_kernel(const __grid
                 const bool add = a.accumulate || a.base > 0;
                 if (VEC == 4 && add && !a.grad_w_bf16) {
                     const float4 old = *reinterpret_cast<const float4*>(static_cast<const float*>(a.grad_w) + to);
-                    y[0] = __fadd_rn(y[0], old.x), y[1] = __fadd_rn(y[1], old.y), y[2] = __fadd_rn(y[2], old.z), y[3] = __fadd_rn(y[3], old.w);
+                    y[0] = __fadd_rn(y[0], old.x), y[1] = __fadd_rn(y[1], old.y);
+                    y[2] = __fadd_rn(y[2], old.z), y[3] = __fadd_rn(y[3], old.w);
                 }
                 if (VEC == 4 && !(add && a.grad_w_bf16)) {
                     if (a.grad_w_bf16)
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.grad_w) + to) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.grad_w) + to) =
+                            make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
                     else
                         *reinterpret_cast<float4*>(static_cast<float*>(a.grad_w) + to) = make_float4(y[0], y[1], y[2], y[3]);
                 } else {
@@ -1548,7 +1560,8 @@ __global__ void __launch_bounds__(kFewThreads) few_gradients_kernel(const __grid
 }
 
 // grad X from its parts, in their order.
-__global__ void __launch_bounds__(128) few_finish_kernel(const __grid_constant__ FewArgs a, uint32_t tokens, uint32_t splits) {
+__global__ void __launch_bounds__(128) few_finish_kernel(const __grid_constant__ FewArgs a, uint32_t tokens,
+                                                         uint32_t splits) {
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t c = blockIdx.x * 128 + threadIdx.x, r = blockIdx.y;
@@ -1612,7 +1625,8 @@ uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t roo
     auto look = [&](uint64_t s) {
         if (s > std::max<uint64_t>(1, most)) return;
         const uint64_t each = (blocks + s - 1) / s * a.width;
-        const uint64_t fullest = std::max((tiles * s + pairs - 1) / pairs * each, (tiles * s * each + others) / pairs + other / 2);
+        const uint64_t even = (tiles * s * each + others) / pairs + other / 2;
+        const uint64_t fullest = std::max((tiles * s + pairs - 1) / pairs * each, even);
         const uint64_t cost = fullest * passes + (s > 1 ? (8 + tiles * s / 4) * kSide : 0);
         if (splits == 0 || cost < best) {
             best = cost;
@@ -1627,7 +1641,8 @@ uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t roo
 }  // namespace
 
 cudaError_t launch_teacher(const TeacherArgs& a, cudaStream_t st) {
-    return launch(teacher_kernel, ctas(a.n, kTeacherWarps), 32 * kTeacherWarps, static_cast<size_t>(kTeacherWarps) * 2 * a.k * 4, st, a);
+    const size_t smem = static_cast<size_t>(kTeacherWarps) * 2 * a.k * 4;
+    return launch(teacher_kernel, ctas(a.n, kTeacherWarps), 32 * kTeacherWarps, smem, st, a);
 }
 
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t st) { return launch(rows_kernel, 1, kRowThreads, 0, st, a); }
@@ -1645,7 +1660,8 @@ cudaError_t launch_grad(const JoinArgs& a0, cudaStream_t st) {
     JoinArgs a = a0;
     const uint32_t rows = ctas(a.n, a.round) * a.round;
     a.columns = 128 * kGradThreads;  // less while a few waves of CTAs are not full
-    while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 16 * kLossSms) a.columns /= 2;
+    while (a.columns > 8 * kGradThreads && static_cast<uint64_t>(a.n) * ctas(a.vocab, a.columns) < 16 * kLossSms)
+        a.columns /= 2;
     return launch(grad_kernel, dim3(ctas(a.vocab, a.columns), std::min(rows, 32768u)), kGradThreads, 0, st, a);
 }
 
@@ -1718,14 +1734,15 @@ cudaError_t launch_products(const ProductArgs* a, int n, uint64_t room, const Re
     if (p.args[0].out.parts) p.args[0].splits = splits_of(p.args[0], n > 1 ? &p.args[1] : nullptr, room);
     const cudaError_t e = launch_tiles(p, n, false, st);
     if (e != cudaSuccess || p.args[0].splits == 1) return e;
-    return launch(finish_kernel, std::min<uint32_t>(std::max<uint32_t>(1, ctas(static_cast<uint64_t>(a[0].m) * ctas(a[0].n, 4), 256)), 8 * kLossSms),
-                  256, 0, st, p.args[0]);
+    const uint32_t whole = ctas(static_cast<uint64_t>(a[0].m) * ctas(a[0].n, 4), 256);
+    return launch(finish_kernel, std::min(std::max(1u, whole), 8 * kLossSms), 256, 0, st, p.args[0]);
 }
 
 namespace {
 
 bool aligned(const void* p, uint64_t stride, int es, uint32_t width, uint32_t bytes) {
-    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * es % bytes == 0 && static_cast<uint64_t>(width) * es % bytes == 0;
+    return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * es % bytes == 0 &&
+           static_cast<uint64_t>(width) * es % bytes == 0;
 }
 
 template <int N>
@@ -1742,7 +1759,8 @@ cudaError_t few_gradients(FewArgs a, const RecordArgs& r, cudaStream_t st) {
     while (lanes < kFewThreads && 4 * lanes < a.width) lanes *= 2;
     const uint32_t wide = ctas(a.width, 4 * lanes);
     // four CTAs an SM
-    const uint32_t most = std::min<uint64_t>(std::max(1u, 4 * kLossSms / wide), a.room / (static_cast<uint64_t>(N) * a.width));
+    const uint32_t most =
+        std::min<uint64_t>(std::max(1u, 4 * kLossSms / wide), a.room / (static_cast<uint64_t>(N) * a.width));
     a.entries = ctas(ctas(a.vocab, std::max(1u, most)), kFewColumns) * kFewColumns;
     const uint32_t splits = ctas(a.vocab, a.entries);
     const bool whole = (!a.grad_x || aligned(a.w, a.w_stride, a.bf16 ? 2 : 4, a.width, a.bf16 ? 8 : 16)) &&
@@ -1751,14 +1769,18 @@ cudaError_t few_gradients(FewArgs a, const RecordArgs& r, cudaStream_t st) {
     cudaError_t e = launch(a.bf16 ? (whole ? few_gradients_kernel<N, true, 4> : few_gradients_kernel<N, true, 1>)
                                   : (whole ? few_gradients_kernel<N, false, 4> : few_gradients_kernel<N, false, 1>),
                            dim3(wide, splits), kFewThreads, 0, st, a, lanes, r);
-    if (e == cudaSuccess && a.grad_x) e = launch(few_finish_kernel, dim3(ctas(a.width, 128), a.n), 128, 0, st, a, static_cast<uint32_t>(N), splits);
+    if (e == cudaSuccess && a.grad_x)
+        e = launch(few_finish_kernel, dim3(ctas(a.width, 128), a.n), 128, 0, st, a, static_cast<uint32_t>(N), splits);
     return e;
 }
 
 }  // namespace
 
 cudaError_t launch_few_logits(const FewArgs& a, cudaStream_t st) {
-    return a.n <= 1 ? few_logits<1>(a, st) : a.n <= 2 ? few_logits<2>(a, st) : a.n <= 4 ? few_logits<4>(a, st) : few_logits<8>(a, st);
+    return a.n <= 1   ? few_logits<1>(a, st)
+           : a.n <= 2 ? few_logits<2>(a, st)
+           : a.n <= 4 ? few_logits<4>(a, st)
+                      : few_logits<8>(a, st);
 }
 
 cudaError_t launch_few_gradients(FewArgs a, const RecordArgs& r, cudaStream_t st) {

@@ -164,8 +164,7 @@ def main():
     stop.record()
     torch.cuda.synchronize()
     us = start.elapsed_time(stop) / 20 * 1e3
-    what = "losses, gradients, reduce-scatter, norm, AdamW, all-gather" if layer else "reduce-scatter, norm, AdamW, all-gather"
-    print(f"one step ({what}) in a CUDA graph: {us:.1f} us")
+    print(f"one step ({'losses, gradients, ' if layer else ''}reduce-scatter, norm, AdamW, all-gather) in a CUDA graph: {us:.1f} us")
 
 
 if __name__ == "__main__":

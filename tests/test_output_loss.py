@@ -242,7 +242,8 @@ def test_few_tokens(n, d, v, dtype, keep):
     dx = torch.ones(n, d + 1, dtype=x.dtype, device="cuda")[:, 1:]
     dw = (0.01 * torch.randn(v, d, generator=g)).to(tdt(dtype)).cuda()
     x0, w0 = dx.clone(), dw.clone()
-    rec = h.distill(big[:, 1:-2], w, ids.cuda(), logits.cuda(), temperature=2.0, grad_hidden=dx, grad_weight=dw, accumulate=True)
+    rec = h.distill(big[:, 1:-2], w, ids.cuda(), logits.cuda(), temperature=2.0, grad_hidden=dx, grad_weight=dw,
+                    accumulate=True)
     Expected(x, w, lists, shares, 2.0, dtype=dtype, spread=spread).check(rec, None, dx, dw, x0, w0)
 
 
@@ -635,7 +636,7 @@ def test_weights_of_more_than_2_to_the_31_elements(n):
     gz.scatter_add_(1, t[:, None], torch.full((n, 1), -1.0, dtype=torch.float64, device="cuda"))
     gz /= n
     off = q * dq / n + 2.0 ** -8 * gz.abs() + bound_of_sum(v, "bfloat16") * gz.abs()
-    dx_want, room = torch.zeros(n, d, dtype=torch.float64, device="cuda"), torch.zeros(n, d, dtype=torch.float64, device="cuda")
+    dx_want, room = (torch.zeros(n, d, dtype=torch.float64, device="cuda") for _ in range(2))
     for a in range(0, v, step):
         part = w[a:a + step].double()
         dx_want += gz[:, a:a + step] @ part
@@ -721,7 +722,8 @@ def test_refusals():
     refused(ce, hidden=x, weight=w, targets=t, losses=torch.zeros(19, device="cuda"))
     refused(ce, hidden=x, weight=w, targets=t, result=torch.zeros(3, device="cuda"))
     ids, logits = torch.zeros(20, 4, dtype=torch.int64, device="cuda"), torch.zeros(20, 4, device="cuda")
-    for k in (dict(temperature=0.0), dict(temperature=math.inf), dict(temperature=1e30), dict(temperature=1e-30), dict(ids=ids[:, :3]), dict(logits=logits.half()),
+    for k in (dict(temperature=0.0), dict(temperature=math.inf), dict(temperature=1e30),
+              dict(temperature=1e-30), dict(ids=ids[:, :3]), dict(logits=logits.half()),
               dict(ids=torch.zeros(20, 5, dtype=torch.int64, device="cuda"), logits=torch.zeros(20, 5, device="cuda")),
               dict(ids=ids[:, :0], logits=logits[:, :0])):
         refused(h.distill, **{**dict(hidden=x, weight=w, ids=ids, logits=logits), **k})
