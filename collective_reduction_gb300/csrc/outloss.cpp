@@ -257,12 +257,15 @@ struct Call {
     //   192 x 4001             3 MB    16   34 :   25   49    15  25 :  17   33    14  27 :  17   33    16   35 :  17   33
     // The tiles' float32 pays for packing the weights in planes, their odd bf16 rows for
     // packing them at all.  More than eight tokens of float32 are taken in groups.
+    // Where both take as long these kernels do it: they keep the logits' gradient in
+    // float32, where a handful of bf16 roundings do not average out.
     bool few() const {
         const uint64_t bytes = static_cast<uint64_t>(vocab) * width * esize(h->dtype), mb = 1u << 20;
         if (n == 0) return false;
         if (h->dtype == AR_FLOAT32) return n <= 8 || (n <= 16 && bytes >= 8 * mb) || (n <= 24 && grads && bytes >= 64 * mb);
         if (!weight_as_is()) return n <= 8;
-        return n <= 2 || (n <= 4 && (grads || bytes < 64 * mb)) || (n <= 8 && grads && bytes >= 64 * mb);
+        if (n <= 2) return true;
+        return n <= 4 ? grads || bytes < 64 * mb : n <= 8 && (bytes >= 64 * mb ? grads : bytes < 8 * mb);
     }
 
     ar::FewArgs few_args(uint64_t r) const {
@@ -286,8 +289,14 @@ struct Call {
         return f;
     }
 
+    // A few tokens' logits' gradients: 24 bits of them, whatever the inputs' type.
+    ar::Planes few_grad() const {
+        static_assert(ar::kFewTokens * ar::kMaxPlanes <= ar::kLossTile, "they fit the tiles' place");
+        return {h->at<uint16_t>(h->l.grad), ar::kFewTokens * h->l.wide, h->l.wide, ar::kMaxPlanes};
+    }
+
     ar::FewArgs few_gradients(ar::FewArgs f) const {
-        f.g = grad(0);
+        f.g = few_grad();
         f.t = static_cast<float>(t);
         f.grad_x = a->grad_hidden;
         f.grad_w = a->grad_weight;
@@ -357,7 +366,7 @@ struct Call {
             j.z_pitch = h->l.wide;
             j.vocab = vocab;
             j.loss = h->at<float>(h->l.loss) + r;
-            j.g = grad(columns == ar::kFewColumns ? 0 : r);
+            j.g = columns == ar::kFewColumns ? few_grad() : grad(r);
             run(ar::launch_grad(j, st));
         } else {
             j.sums = h->at<double>(h->l.sums);

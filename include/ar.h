@@ -573,8 +573,8 @@ typedef struct {
  *   [2] nonfinite  1 if a counted token's loss is an infinity or NaN, else 0
  *   [3] factor     scale / max(1, counted) (AR_LOSS_MEAN), scale (AR_LOSS_SUM)
  * The gradients are the loss's.  They are computed from bf16 inputs with the
- * logits' gradient rounded to bf16 once (float32 inputs: in float32), summed in
- * float32 and rounded to their type once.  Outputs may overlap neither each
+ * logits' gradient rounded to bf16 once (float32 inputs, and a few tokens: in
+ * float32), summed in float32 and rounded to their type once.  Outputs may overlap neither each
  * other nor the inputs.  Errors: AR_ERR_INVALID_ARG for null or misaligned (to
  * their element) pointers, memory that is not the handle's device's or ends too
  * early, overlaps, strides below D, a gradient type that is neither, a scale
