@@ -295,13 +295,15 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ PackA
 
 // ------------------------------------------------------------------- joins
 
-// (top, sum 2^(y - top)) of two parts of a row; a part of -infinities alone adds
-// nothing, +infinity or NaN make the sum NaN.
+// (top, sum 2^(y - top)) of two parts of a row.  A part of -infinities alone has sum
+// 0 and adds nothing; +infinity and NaN make the sum NaN, also where they are all
+// that a part has: fmaxf leaves NaN out, so such a part's top is -infinity, and it
+// keeps its sum.
 __device__ __forceinline__ void join_stat(float& top, float& sum, float top2, float sum2) {
     const float m = fmaxf(top, top2);
     const float low = -kInf;
-    const float a = top == low ? 0.f : __fmul_rn(sum, exp2_fast(__fsub_rn(top, m)));
-    const float b = top2 == low ? 0.f : __fmul_rn(sum2, exp2_fast(__fsub_rn(top2, m)));
+    const float a = top == low ? sum : __fmul_rn(sum, exp2_fast(__fsub_rn(top, m)));
+    const float b = top2 == low ? sum2 : __fmul_rn(sum2, exp2_fast(__fsub_rn(top2, m)));
     top = m;
     sum = __fadd_rn(a, b);
 }
@@ -1434,7 +1436,8 @@ __global__ void __launch_bounds__(kFewThreads) few_logits_kernel(const __grid_co
             if (v0 + i >= a.vocab) break;
             const float z = zs[warp][i];
             if (a.z) a.z[warp * a.z_pitch + v0 + i] = z;
-            join_stat(top, sum, __fmul_rn(z, a.c), 1.f);
+            const float y = __fmul_rn(z, a.c);
+            join_stat(top, sum, y, y == -kInf ? 0.f : 1.f);
         }
         for (int o = 16; o > 0; o /= 2) {
             const float t2 = __shfl_xor_sync(kFull, top, o), s2 = __shfl_xor_sync(kFull, sum, o);

@@ -513,7 +513,10 @@ ar_status ar_adamw_step_counted(ar_adamw_t h, const ar_adamw_params* params, uin
  * entries) have loss 0 and gradient 0, and their hidden states are not read:
  * products run over the tokens that count alone.  A target or id outside the
  * vocabulary makes its token's loss and the gradients it enters NaN, and the
- * record says nonfinite. */
+ * record says nonfinite.  So does a NaN among the weights, for every token that
+ * counts, or in a token's hidden state.  A logit of -infinity adds nothing, one of
+ * +infinity makes the loss NaN or an infinity; float32 inputs that are infinite
+ * may make their logits NaN (they are multiplied as sums of three bf16 values). */
 typedef struct ar_output_loss_s* ar_output_loss_t;
 typedef enum { AR_LOSS_MEAN = 0, AR_LOSS_SUM = 1 } ar_loss_reduction;
 

@@ -1,0 +1,163 @@
+"""The output layer's losses where what is read could make them go wrong: NaN and
+infinities in the weights and hidden states.
+
+Tolerances as derived in test_output_loss.py, with the products of a logit that
+are not zero in the place of all of them (adding a zero rounds nothing), and on
+the gradient of a logit the rounding that the call makes: to bf16, or none
+beyond float32's."""
+
+import math
+
+import pytest
+
+import collective_reduction_gb300 as ar
+from test_output_loss import U, bound_of_sum, half_step, make, run_ce, run_distill, targets_of, teacher
+
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from gpu_util import ensure_built
+    return ensure_built()
+
+
+class Tight:
+    """Softmax cross entropy in 64 bits and how far a call may be off it.  `terms`:
+    products of a logit that are not zero; `half`: half a step, relative, of the
+    logits' gradients; `out`: entry whose logit is -infinity."""
+
+    def __init__(self, x, w, targets, dtype, terms=None, half=U, ignore=-100, reduction="mean", scale=1.0, out=None):
+        import torch
+        x, w, t = x.double(), w.double(), targets.cuda()
+        n, v = x.shape[0], w.shape[0]
+        counted = t != ignore
+        mask = counted.double()[:, None]
+        x = torch.where(counted[:, None], x, 0.0)
+        self.counted = int(counted.sum())
+        self.factor = scale / max(1, self.counted) if reduction == "mean" else scale
+        z = x @ w.t()
+        if out is not None:
+            z[:, out] = -math.inf
+        at = torch.where(counted, t, 0).long()[:, None]
+        p = torch.zeros_like(z).scatter_(1, at, 1.0)
+        lse = torch.logsumexp(z, 1, keepdim=True)
+        self.losses = ((lse - z.gather(1, at)) * mask)[:, 0]
+        self.loss = float(self.losses.sum()) * self.factor
+        q = (z - lse).exp()
+        g = self.factor * (q - p) * mask
+        if out is None:
+            e = bound_of_sum(terms or x.shape[1], dtype) * (x.abs() @ w.abs().t()).amax(1, keepdim=True)
+            big = z.abs().amax(1, keepdim=True)
+        else:
+            keep = torch.arange(v, device="cuda") != out
+            e = bound_of_sum(terms or x.shape[1], dtype) * (x.abs() @ w[keep].abs().t()).amax(1, keepdim=True)
+            big = z[:, keep].abs().amax(1, keepdim=True)
+        d = 2 * e + 8 * U * (big + 2) + 2 * U * (v + 4) + 16 * U
+        self.losses_tol = (2 * d * mask)[:, 0] + 4 * U * self.losses
+        self.loss_tol = float(self.losses_tol.sum()) * self.factor + 4 * U * abs(self.loss)
+        if out is not None:
+            return
+        g_tol = self.factor * (q * d + p * 4 * U) * mask + (half + 4 * U) * g.abs()
+        kind = "float32" if half == U else dtype  # the planes' products are as many as float32's at most
+        self.dx, self.dw = g @ w, g.t() @ x
+        self.dx_tol = g_tol @ w.abs() + bound_of_sum(v, kind) * (g.abs() @ w.abs())
+        self.dw_tol = g_tol.t() @ x.abs() + bound_of_sum(n, kind) * (g.abs().t() @ x.abs())
+
+    def check(self, record, losses=None, dx=None, dw=None, old=0.0, telling=0.5):
+        """`telling`: the part of the gradients' elements at least that results of
+        zeros would fail at."""
+        loss, counted, nonfinite, factor = record.tolist()
+        assert counted == self.counted and nonfinite == 0.0 and factor == pytest.approx(self.factor, rel=2 * U)
+        assert abs(loss - self.loss) <= self.loss_tol < abs(self.loss)
+        if losses is not None:
+            assert bool(((losses.double() - self.losses).abs() <= self.losses_tol).all())
+        for got, want, tol in ((dx, self.dx, self.dx_tol), (dw, self.dw, self.dw_tol)):
+            if got is None:
+                continue
+            want = want + old
+            half = half_step(str(got.dtype).replace("torch.", ""))
+            room = tol + (half + 2 * U) * (want.abs() + tol) + 1e-38
+            assert float((want.abs() > room)[want != 0].double().mean()) >= telling
+            off = (got.double() - want).abs()
+            assert bool((off <= room).all()), float((off / room).max())
+
+
+# ------------------------------------------------- what is not a number
+
+def avoid(t, entry, v):
+    t = t.clone()
+    t[t == entry] = (entry + 1) % v
+    return t
+
+
+def columns_of(v):
+    return sorted({c for c in (0, 5, 31, 32, 63, 64, 127, 128, 255, 256, v - 1) if c < v})
+
+
+FEW_AND_TILES = [("bfloat16", 1, 64, 65), ("bfloat16", 2, 33, 129), ("bfloat16", 3, 64, 257), ("bfloat16", 8, 40, 300),
+                 ("float32", 1, 33, 129), ("float32", 8, 64, 257), ("float32", 12, 1100, 2003),
+                 ("bfloat16", 40, 64, 129), ("bfloat16", 300, 40, 257), ("bfloat16", 40, 33, 65), ("float32", 40, 64, 129),
+                 ("float32", 300, 33, 257), ("float32", 300, 40, 300)]
+
+
+@gpu
+@pytest.mark.parametrize("dtype, n, d, v", FEW_AND_TILES)
+@pytest.mark.parametrize("grads", [(), ("hidden", "weight")])
+def test_a_nan_weight_makes_every_loss_nan(dtype, n, d, v, grads):
+    """Also where it is the only entry of a part of the vocabulary, or its first."""
+    x, w, g = make(n, d, v, dtype, seed=n + v)
+    t0 = targets_of(n, v, g, 0.8)
+    t0[0] = 1
+    h = ar.OutputLoss(n, d, v, dtype, top=2)
+    ids, logits = teacher(n, 2, v, g, "float32")
+    for c in columns_of(v):
+        w2, t = w.clone(), avoid(t0, c, v)
+        w2[c, d // 2] = math.nan
+        rec, losses, dx, dw = run_ce(h, x, w2, t, dtype, grads)
+        counts = (t != -100).cuda()
+        assert math.isnan(rec[0].item()) and rec[1].item() == int(counts.sum()) and rec[2].item() == 1.0, c
+        assert bool(losses[counts].isnan().all()) and bool((losses[~counts] == 0).all()), c
+        if grads:
+            assert bool(dw.isnan().all()) and bool(dx[counts].isnan().all()) and bool((dx[~counts] == 0).all()), c
+        rec, losses, _, _ = run_distill(h, x, w2, avoid(ids, c, v), logits, dtype)
+        assert rec[2].item() == 1.0 and bool(losses.isnan().all()), c
+
+
+@gpu
+@pytest.mark.parametrize("dtype, n, d, v", FEW_AND_TILES)
+def test_an_infinite_weight(dtype, n, d, v):
+    """A logit of -infinity adds nothing, one of +infinity leaves no finite loss.  The
+    tensor cores' float32 products of an infinity may be NaN instead: never a
+    finite loss that is wrong."""
+    import torch
+    x, w, g = make(n, d, v, dtype, seed=n + v)
+    x[:, 0] = torch.where(torch.rand(n, generator=g).cuda() < 0.5, x[:, 0].abs() + 0.1, -x[:, 0].abs() - 0.1)
+    t0 = targets_of(n, v, g)
+    planes = dtype == "float32" and n > 24
+    h = ar.OutputLoss(n, d, v, dtype)
+    for c in columns_of(v):
+        t = avoid(t0, c, v)
+        want = Tight(x, w, t, dtype, out=c)
+        for sign in (1.0, -1.0):
+            w2 = w.clone()
+            w2[c, 0] = sign * math.inf
+            up = x[:, 0] * sign > 0
+            rec, losses, _, _ = run_ce(h, x, w2, t, dtype, ())
+            assert not bool(losses[up].isfinite().any()) and rec[2].item() == float(bool((~losses.isfinite()).any())), c
+            off = (losses.double() - want.losses).abs()
+            right = off <= want.losses_tol
+            assert bool((right | up | (planes & ~losses.isfinite())).all()), c
+
+
+@gpu
+@pytest.mark.parametrize("dtype, n", [("bfloat16", 3), ("bfloat16", 40), ("float32", 3), ("float32", 40)])
+def test_a_nan_hidden_state_is_its_tokens_alone(dtype, n):
+    import torch
+    x, w, g = make(n, 64, 257, dtype, seed=n)
+    t = targets_of(n, 257, g)
+    x[1, 5] = math.nan
+    rec, losses, dx, dw = run_ce(ar.OutputLoss(n, 64, 257, dtype), x, w, t, dtype)
+    others = torch.arange(n, device="cuda") != 1
+    assert rec[2].item() == 1.0 and math.isnan(losses[1].item()) and bool(losses[others].isfinite().all())
+    assert bool(dx[1].isnan().all()) and bool(dx[others].isfinite().all()) and bool(dw.isnan().all())
