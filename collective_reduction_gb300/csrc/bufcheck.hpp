@@ -42,6 +42,17 @@ struct Span {
 // and all pairwise disjoint.  A span of no bytes is not looked at.
 ar_status check_spans(const std::vector<Span>& spans, int device);
 
+// Bytes from a matrix's first element to behind its last: `rows` rows of `width`
+// es-byte elements, `stride` >= width elements apart.  kTooManyBytes instead of
+// 2^62 or more, so that nothing wraps.
+constexpr uint64_t kTooManyBytes = ~0ull;
+constexpr uint64_t matrix_bytes(uint64_t rows, uint64_t width, uint64_t stride, uint64_t es) {
+    if (rows == 0 || width == 0) return 0;
+    const uint64_t most = (1ull << 62) / es;  // elements
+    if (width >= most || (rows > 1 && (rows - 1) > (most - 1 - width) / stride)) return kTooManyBytes;
+    return ((rows - 1) * stride + width) * es;
+}
+
 // Device (or managed) memory of `device` that holds `bytes` bytes from p on.
 bool device_resident(const void* p, uint64_t bytes, int device);
 

@@ -141,7 +141,7 @@ struct Matrix {
     const void* p;
     uint64_t rows, width, stride;
     int es;
-    uint64_t bytes() const { return rows == 0 || width == 0 ? 0 : ((rows - 1) * stride + width) * es; }
+    uint64_t bytes() const { return ar::matrix_bytes(rows, width, stride, static_cast<uint64_t>(es)); }
 };
 
 bool on_device(int device) {
@@ -155,7 +155,7 @@ ar_status check_matrices(const std::vector<Matrix>& in, const std::vector<Matrix
     all.insert(all.end(), in.begin(), in.end());
     for (size_t i = 0; i < all.size(); ++i) {
         const Matrix& m = all[i];
-        if (m.stride < m.width || m.stride > (1ull << 40)) return AR_ERR_INVALID_ARG;
+        if (m.stride < m.width || m.stride > (1ull << 40) || m.bytes() == ar::kTooManyBytes) return AR_ERR_INVALID_ARG;
         if (m.bytes() == 0) continue;
         const uintptr_t a = reinterpret_cast<uintptr_t>(m.p);
         if (!a || a % m.es || a + m.bytes() < a) return AR_ERR_INVALID_ARG;

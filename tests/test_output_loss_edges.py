@@ -1,12 +1,15 @@
 """The output layer's losses where what is read could make them go wrong: NaN and
-infinities in the weights and hidden states.
+infinities in the weights and hidden states, rows that are far apart.
 
 Tolerances as derived in test_output_loss.py, with the products of a logit that
 are not zero in the place of all of them (adding a zero rounds nothing), and on
 the gradient of a logit the rounding that the call makes: to bf16, or none
 beyond float32's."""
 
+import ctypes
 import math
+import os
+import subprocess
 
 import pytest
 
@@ -161,3 +164,48 @@ def test_a_nan_hidden_state_is_its_tokens_alone(dtype, n):
     others = torch.arange(n, device="cuda") != 1
     assert rec[2].item() == 1.0 and math.isnan(losses[1].item()) and bool(losses[others].isfinite().all())
     assert bool(dx[1].isnan().all()) and bool(dx[others].isfinite().all()) and bool(dw.isnan().all())
+
+
+# ------------------------------------------------- rows that are far apart
+
+FAR = [(4, 1 << 22, 1 << 40), (2, 1 << 23, 1 << 40), (2, 1 << 24, 1 << 39), (8, 1 << 21, 1 << 40), (4, 3, (1 << 63) - 1),
+       (2, 2, (1 << 64) - 1)]
+
+
+def test_bytes_of_rows_that_are_far_apart_do_not_wrap(tmp_path):
+    """Sizes whose rows times stride times element are a multiple of 2^64, and
+    ordinary ones, as the checks of a call compute them, on the host alone."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    cases = [(r + 1, 8, s, e) for e, r, s in FAR] + [(0, 8, 8, 2), (5, 0, 8, 2), (1, 8, 1 << 60, 4), (1, 1 << 62, 1 << 62, 4),
+                                                     (3, 5, 7, 2), (1 << 24, 1 << 16, 1 << 16, 4), (1 << 21, 1, 1 << 39, 4)]
+    lines = "\n".join(f'    std::printf("%llu\\n", (unsigned long long)ar::matrix_bytes({r}ull, {w}ull, {s}ull, {e}ull));'
+                      for r, w, s, e in cases)
+    source = tmp_path / "bytes.cpp"
+    source.write_text(f'#include <cstdio>\n#include "bufcheck.hpp"\nint main() {{\n{lines}\n}}\n')
+    program = tmp_path / "bytes"
+    subprocess.run(["g++", "-std=c++17", "-I" + os.path.join(root, "include"), "-I/usr/local/cuda/include",
+                    "-I" + os.path.join(root, "collective_reduction_gb300", "csrc"), str(source), "-o", str(program)],
+                   check=True)
+    got = subprocess.run([str(program)], check=True, capture_output=True, text=True).stdout.split()
+    for (r, w, s, e), b in zip(cases, got):
+        exact = ((r - 1) * s + w) * e if r and w else 0
+        assert int(b) == (exact if exact < 1 << 62 else (1 << 64) - 1), (r, w, s, e)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_weights_whose_rows_are_far_apart_are_refused(dtype):
+    """By the host, before any launch."""
+    import torch
+    v = (1 << (23 if dtype == "bfloat16" else 22)) + 1
+    x, w = (torch.zeros(8 * k, dtype=getattr(torch, dtype), device="cuda") for k in (1, 64))
+    targets = torch.zeros(1, dtype=torch.int64, device="cuda")
+    h = ar.OutputLoss(1, 8, v, dtype, grads=False)
+    a = ar.OutputLossArgs()
+    a.tokens, a.hidden, a.hidden_stride, a.scale, a.result = 1, x.data_ptr(), 8, 1.0, h.record.data_ptr()
+    a.weight = w.data_ptr()
+    for stride in (1 << 40, 1 << 39, (1 << 64) - 1):
+        a.weight_stride = stride
+        assert ar.lib().ar_output_cross_entropy(h._h, ctypes.byref(a), targets.data_ptr(), 8, -100, None) == 1
+    h.check()
+    assert bool((h.record == 0).all())
