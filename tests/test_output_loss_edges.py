@@ -209,3 +209,54 @@ def test_weights_whose_rows_are_far_apart_are_refused(dtype):
         assert ar.lib().ar_output_cross_entropy(h._h, ctypes.byref(a), targets.data_ptr(), 8, -100, None) == 1
     h.check()
     assert bool((h.record == 0).all())
+
+
+# ------------------------------------------------- long sums
+
+def rows_near_two(rows, width, seed):
+    """Random bf16 in [1.8, 2)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    y = torch.empty(rows, width, dtype=torch.bfloat16, device="cuda")
+    for part in y.split(1 << 18):
+        part.copy_(1.8 + 0.19 * torch.rand(part.shape, generator=g, device="cuda"))
+    return y
+
+
+# 65536 additions in the tensor cores, each cut off below 2^-23, are 0.13% of such sums: 0.6 of half
+# a step of bf16 at values just below a power of two.  Runs of at most 256 blocks of four additions:
+LONG_SUM = 256 * 4 * 2 * U + (1 << 20) // (256 * 64) * U + 16 * U
+
+
+@gpu
+def test_bf16_gradient_of_weights_over_a_million_tokens():
+    """Terms of one sign: every logit is 0, so a row that is no target is the sum of all
+    hidden states / 1024.  76 tiles: nothing is gained by splitting the sums."""
+    import torch
+    n, d, v = 1 << 20, 4864, 1024
+    x = rows_near_two(n, d, 31)
+    w, dw = (torch.zeros(v, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    h = ar.OutputLoss(n, d, v)
+    rec = h.cross_entropy(x, w, torch.zeros(n, dtype=torch.int32, device="cuda"), reduction="sum", grad_weight=dw)
+    h.check()
+    want = sum(part.double().sum(0) for part in x.split(1 << 18)) / v
+    assert 1024.0 < float(want.min()) and float(want.max()) < 2048.0
+    assert bool(((dw[1:].double() - want).abs() <= 4.0 + LONG_SUM * want).all())  # half a step
+    assert rec[0].item() == pytest.approx(n * math.log(v), rel=1e-6)
+
+
+@gpu
+def test_bf16_gradient_of_hidden_states_over_a_million_entries():
+    """Hidden states of 0 and a target's row of 0: the mean of the other rows."""
+    import torch
+    n, d, v = 1024, 4864, 1 << 20
+    w = rows_near_two(v, d, 32)
+    w[7] = 0
+    x, dx = (torch.zeros(n, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    h = ar.OutputLoss(n, d, v)
+    rec = h.cross_entropy(x, w, torch.full((n,), 7, device="cuda"), reduction="sum", scale=16.0, grad_hidden=dx)
+    h.check()
+    want = 16.0 * sum(part.double().sum(0) for part in w.split(1 << 18)) / v
+    assert 16.0 < float(want.min()) and float(want.max()) < 32.0
+    assert bool(((dx.double() - want).abs() <= 0.0625 + LONG_SUM * want).all())
+    assert rec[0].item() == pytest.approx(16 * n * math.log(v), rel=1e-6)
