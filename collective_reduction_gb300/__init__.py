@@ -615,7 +615,9 @@ class OutputLoss:
     counted, nonfinite, factor.  Without `result` that is `self.record`, which
     the next call overwrites.  loss = factor * sum of the counted tokens' losses,
     factor = scale / counted (reduction "mean") or scale ("sum"); the gradients are
-    the loss's, in the dtype or float32, written or (accumulate) added to what is
+    the loss's, in the dtype or float32 (of bfloat16 inputs: bfloat16 gradients of
+    more than 8 tokens come from logits' gradients rounded to bfloat16, float32 ones
+    from float32's and take up to three times as long), written or (accumulate) added to what is
     there.  `losses` (float32, n) takes every token's loss, 0 for tokens that do
     not count.  The written gradients' autograd versions are raised (a replay of
     a captured call does not).  Calls on one handle share its workspace: order

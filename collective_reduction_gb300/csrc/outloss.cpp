@@ -31,14 +31,14 @@ constexpr uint64_t kPackBytes = 1ull << 30;
 // take over: of float32 inputs (six products a block), of bf16 inputs for logits
 // and float32 results, and for bf16 results (whose rounding is 2^-8).  The tensor
 // cores cut every sum off, always downwards, so the error grows with the run: with 1
-// and 8 losses and float32 gradients are as far from 64 bits as float32 products
-// are (2 to 5e-7 relative); with 2 and 16 they are twice as far, and 515 tokens of
+// and 8 (3, where A has three planes) losses and float32 gradients are as far from 64
+// bits as float32 products are (2 to 7e-7 relative); with 2 and 16 they are twice as far, and 515 tokens of
 // 515 x 10007 float32 take 154 us instead of 173, 4096 of 2048 x 50001 bf16 1592
 // instead of 1633; with 4 for bf16 1739.  Sums of a million equal terms for a bf16
 // result were 0.65% low (1.5 of its steps) in one run; in runs of 256 blocks they are
 // 0.01% low.  8192 tokens of 4096 x 128000 take 17.5 ms so and 17.3 in one run, other
 // cases as long: from 128 to 512 blocks there is no difference beyond the noise.
-constexpr uint32_t kFloatRun = 1, kExactRun = 8, kLongRun = 256;
+constexpr uint32_t kFloatRun = 1, kExactRun = 8, kPlanesRun = 3, kLongRun = 256;
 
 ar_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;
@@ -113,7 +113,8 @@ ar_status make_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab, ar_dtype
         // parts for each pair of SMs
         l.part_room = std::max(l.kept * l.sum_pitch, 8 * ar::kLossSms / 2 * tile * tile);
         l.part = l.add(4 * l.part_room);
-        if (l.kept < l.rows) l.sum = l.add(4 * l.wide * l.sum_pitch);
+        // float32 gradients of weights are summed where the caller wants them
+        if (l.kept < l.rows && dtype == AR_BFLOAT16) l.sum = l.add(4 * l.wide * l.sum_pitch);
     }
     return AR_OK;
 }
@@ -179,6 +180,11 @@ struct Call {
     cudaStream_t st;
     uint32_t n, width, vocab;
     bool grads, packed = false;
+    // of the pass at hand: the gradients that it makes, the logits' gradients' planes, and the
+    // tokens whose logits' gradients are kept
+    bool to_hidden = false, to_weight = false;
+    int planes = 1;
+    uint64_t kept = 0;
     float c = 0.f;
     double t = 1.0;
     ar::Lists lists = {};
@@ -203,7 +209,9 @@ struct Call {
         return {h->at<uint16_t>(h->l.hidden) + r * h->l.pitch, h->l.rows * h->l.pitch, h->l.pitch, h->l.planes};
     }
     ar::Planes grad(uint64_t r) const {
-        return {h->at<uint16_t>(h->l.grad) + r % h->l.kept * h->l.wide, h->l.kept * h->l.wide, h->l.wide, h->l.planes};
+        ar::Planes g = {h->at<uint16_t>(h->l.grad) + r % kept * h->l.wide, kept * h->l.wide, h->l.wide, planes};
+        if (planes != h->l.planes) g.low = h->at<uint16_t>(h->l.z);  // a piece at a time: r is its first
+        return g;
     }
     // TMA reads rows that start on 16-byte boundaries
     bool weight_as_is() const {
@@ -235,8 +243,9 @@ struct Call {
         if (e == cudaSuccess) e = next;
     }
 
-    uint32_t run_of(ar_dtype result) const {
-        return h->dtype == AR_FLOAT32 ? kFloatRun : result == AR_FLOAT32 ? kExactRun : kLongRun;
+    uint32_t run_of(ar_dtype result, int planes_a) const {
+        if (h->dtype == AR_FLOAT32) return kFloatRun;
+        return result == AR_FLOAT32 ? (planes_a == 1 ? kExactRun : kPlanesRun) : kLongRun / planes_a;
     }
 
     // Of the counted tokens at places [r, r + m).
@@ -337,7 +346,7 @@ struct Call {
             p.count_m = 1;
             p.n = static_cast<uint32_t>(end - v);
             p.k = width;
-            p.run = run_of(AR_FLOAT32);
+            p.run = run_of(AR_FLOAT32, 1);
             p.logit.c = c;
             p.logit.v0 = static_cast<uint32_t>(v);
             p.logit.lists = lists;
@@ -345,6 +354,7 @@ struct Call {
             p.logit.stats = h->at<float2>(h->l.stats) + v / ar::kStatColumns;
             p.logit.stats_pitch = pitch;
             if (grads) p.logit.z = h->at<float>(h->l.z) + v;
+            p.logit.at_ids = !grads || planes != h->l.planes;
             p.logit.z_pitch = h->l.wide;
             run(ar::launch_logits(p, st));
         }
@@ -381,7 +391,8 @@ struct Call {
         }
     }
 
-    // The last tokens' product goes to the caller, with the sum of those before.
+    // The last tokens' product goes to the caller, with the sum of those before; in
+    // float32 every product does.
     ar::ProductArgs grad_weight(uint64_t r, uint32_t m, bool last) const {
         ar::ProductArgs p = product(r);
         p.a = {grad(r), true, m, h->vocab};
@@ -390,14 +401,14 @@ struct Call {
         p.n = width;
         p.k = m;
         p.count_k = 1;
-        p.run = run_of(a->grad_weight_dtype);
+        p.run = run_of(a->grad_weight_dtype, planes);
         p.out.out = a->grad_weight;
         p.out.stride = a->grad_weight_stride;
         p.out.bf16 = a->grad_weight_dtype == AR_BFLOAT16;
-        p.out.accumulate = a->accumulate;
+        p.out.accumulate = a->accumulate || (!p.out.bf16 && r > 0);
         p.out.sum_pitch = p.out.part_pitch = h->l.sum_pitch;
-        if (r > 0) p.out.add = h->at<float>(h->l.sum);
-        if (!last) p.out.sum = h->at<float>(h->l.sum);
+        if (p.out.bf16 && r > 0) p.out.add = h->at<float>(h->l.sum);
+        if (p.out.bf16 && !last) p.out.sum = h->at<float>(h->l.sum);
         if (!p.out.add && !p.out.sum) p.out.parts = h->at<float>(h->l.part);
         return p;
     }
@@ -408,13 +419,14 @@ struct Call {
         ar::ProductArgs p = product(r);
         ar::Planes g = grad(r);
         g.p += v;
+        if (g.low) g.low += 2 * v;  // v is of whole tiles
         p.a = {g, false, m, end - v};
         p.b = {weight(v, end), true, end - v, h->hidden};
         p.m = m;
         p.count_m = 1;
         p.n = width;
         p.k = static_cast<uint32_t>(end - v);
-        p.run = run_of(a->grad_hidden_dtype);
+        p.run = run_of(a->grad_hidden_dtype, planes);
         p.out.out = a->grad_hidden;
         p.out.stride = a->grad_hidden_stride;
         p.out.bf16 = a->grad_hidden_dtype == AR_BFLOAT16;
@@ -432,7 +444,7 @@ struct Call {
         ar::RecordArgs record = {h->at<float>(h->l.loss), rows, last && m > 0 ? a->result : nullptr};
         ar::ProductArgs p[2];
         int k = 0;
-        if (a->grad_hidden && m > 0) {
+        if (to_hidden && m > 0) {
             uint64_t v = 0;
             for (; v + entries() < h->vocab; v += entries()) {
                 const ar::ProductArgs q = grad_hidden(r, m, v, v + entries());
@@ -440,8 +452,30 @@ struct Call {
             }
             p[k++] = grad_hidden(r, m, v, h->vocab);
         }
-        if (a->grad_weight) p[k++] = grad_weight(r, m, last);
+        if (to_weight) p[k++] = grad_weight(r, m, last);
         run(ar::launch_products(p, k, h->l.part_room, record, st));
+    }
+
+    // Losses and the gradients asked for.  Of bf16 inputs logits' gradients are float32's 24
+    // bits in three planes where a result is float32, and of a few tokens, whose products
+    // cost what reading the weights does; else bf16, rounded once.  The planes that the
+    // workspace has no place for take that of the piece's logits, so pieces are not kept:
+    // the gradient of weights is summed piece by piece.  4096 tokens of 2048 x 50001 take
+    // 3.76 ms for both gradients in float32, 7e-7 off the definition; of rounded logits'
+    // gradients they took 1.84 and were 1.1e-3 off.
+    void pass(bool hidden, bool weight) {
+        to_hidden = hidden;
+        to_weight = weight;
+        const bool exact = (hidden && a->grad_hidden_dtype == AR_FLOAT32) || (weight && a->grad_weight_dtype == AR_FLOAT32);
+        planes = exact || (grads && n <= ar::kFewTokens) ? ar::kMaxPlanes : h->l.planes;
+        kept = h->l.kept;
+        if (planes != h->l.planes) kept = h->l.piece;
+        for (uint64_t first = 0; first < n || first == 0; first += kept) {
+            const uint32_t all = static_cast<uint32_t>(std::min<uint64_t>(n - first, kept));
+            for (uint64_t at = first; at < first + all; at += h->l.piece)
+                losses(at, static_cast<uint32_t>(std::min<uint64_t>(first + all - at, h->l.piece)));
+            if (to_weight || (to_hidden && all > 0)) gradients(first, all, first + kept >= n);
+        }
     }
 
     // Everything after the lists: the tokens that count, then in pieces of them
@@ -488,11 +522,14 @@ struct Call {
             const ar::PackArgs w = packed ? pack_weight(0, h->vocab) : ar::PackArgs{};
             run(ar::launch_pack(p, packed ? &w : nullptr, st));
         }
-        for (uint64_t first = 0; first < n || first == 0; first += h->l.kept) {
-            const uint32_t all = static_cast<uint32_t>(std::min<uint64_t>(n - first, h->l.kept));
-            for (uint64_t at = first; at < first + all; at += h->l.piece)
-                losses(at, static_cast<uint32_t>(std::min<uint64_t>(first + all - at, h->l.piece)));
-            if (a->grad_weight || (a->grad_hidden && all > 0)) gradients(first, all, first + h->l.kept >= n);
+        // one gradient in each type: two passes, so that the float32 one is of float32 and the
+        // bf16 one's sums need no more runs
+        if (grads && h->dtype == AR_BFLOAT16 && n > ar::kFewTokens && a->grad_hidden && a->grad_weight &&
+            a->grad_hidden_dtype != a->grad_weight_dtype) {
+            pass(true, false);
+            pass(false, true);
+        } else {
+            pass(a->grad_hidden, a->grad_weight);
         }
         return cuda_status(e);
     }

@@ -319,7 +319,9 @@ __device__ __forceinline__ float row_loss(const JoinArgs& a, uint64_t r, uint64_
     for (int j = lane; j < a.lists.top; j += 32) {
         const int32_t id = a.lists.ids[at + j];
         if (id == kNoId) break;  // nothing behind it
-        const float d = -__fmaf_rn(a.z ? a.z[r * a.z_pitch + id] : a.lists.logits[at + j], a.c, -top);
+        // logits that other CTAs may be overwriting are not read
+        const float z = a.z && !a.g.low ? a.z[r * a.z_pitch + id] : a.lists.logits[at + j];
+        const float d = -__fmaf_rn(z, a.c, -top);
         const float share = a.lists.shares ? a.lists.shares[at + j] : 1.f;
         if (share != 0.f) dot = __fmaf_rn(share, d, dot);
     }
@@ -415,6 +417,11 @@ __global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_const
 
 constexpr int kGradThreads = 256;
 
+// The second plane's value of a row's column; the third's is kLowGroup on.
+__device__ __forceinline__ uint16_t* low_place(const Planes& g, uint64_t r, uint32_t v) {
+    return g.low + 2 * r * g.pitch + v / kLowGroup * (2 * kLowGroup) + v % kLowGroup;
+}
+
 // A CTA a place's `columns` columns: the statistics (of the whole row, in every
 // one of its CTAs), then
 //   g = 2^(y - top) / sum - share
@@ -458,8 +465,26 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
         const float* z = a.z + r * a.z_pitch;
         uint16_t* g = a.g.p + r * a.g.pitch;
         auto value = [&](float x) { return __fmul_rn(exp2_fast(__fmaf_rn(x, a.c, -top)), inv); };
+        // a warp's 256 columns' low planes are their logits' place
+        for (uint32_t v = lo + 8 * tid; a.g.low && v - 8 * lane < hi; v += 8 * kGradThreads) {
+            float x[8] = {};
+            if (in && v < hi) {
+                const float4 p = *reinterpret_cast<const float4*>(z + v), q = *reinterpret_cast<const float4*>(z + v + 4);
+                x[0] = value(p.x), x[1] = value(p.y), x[2] = value(p.z), x[3] = value(p.w);
+                x[4] = value(q.x), x[5] = value(q.y), x[6] = value(q.z), x[7] = value(q.w);
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j)
+                    if (v + j >= hi) x[j] = 0.f;
+            }
+            __syncwarp();
+            if (v >= (hi + kLowGroup - 1) / kLowGroup * kLowGroup) continue;
+            uint16_t* low = low_place(a.g, r, v);
+            *reinterpret_cast<uint4*>(g + v) = split_eight(x);
+            *reinterpret_cast<uint4*>(low) = split_eight(x);
+            *reinterpret_cast<uint4*>(low + kLowGroup) = split_eight(x);
+        }
 #pragma unroll 2
-        for (uint32_t v = lo + 8 * tid; v < hi; v += 8 * kGradThreads) {  // the pitch is of whole tiles
+        for (uint32_t v = lo + 8 * tid; !a.g.low && v < hi; v += 8 * kGradThreads) {  // the pitch is of whole tiles
             float x[8] = {};
             if (in) {
                 const float4 p = *reinterpret_cast<const float4*>(z + v), q = *reinterpret_cast<const float4*>(z + v + 4);
@@ -479,6 +504,15 @@ __global__ void __launch_bounds__(kGradThreads) grad_kernel(const __grid_constan
             const uint32_t v = static_cast<uint32_t>(a.lists.ids[list + k]);
             if (v < lo || v >= hi) continue;
             const float share = a.lists.shares ? a.lists.shares[list + k] : 1.f;
+            if (a.g.low) {
+                uint16_t* low = low_place(a.g, r, v);  // the planes' sum is the value
+                float x = __fadd_rn(__fadd_rn(bf16_value(low[kLowGroup]), bf16_value(low[0])), bf16_value(g[v]));
+                x = __fsub_rn(x, share);
+                g[v] = split_plane(x);
+                low[0] = split_plane(x);
+                low[kLowGroup] = split_plane(x);
+                continue;
+            }
             float x = __fsub_rn(value(z[v]), share);
             for (int q = 0; q < a.g.planes; ++q) g[q * a.g.plane + v] = split_plane(x);
         }
@@ -540,6 +574,7 @@ constexpr uint32_t kProductSmem = kStages * kStageBytes + kEpilogueWarps * kStag
 // One or two products in one launch.
 struct ProductParams {
     CUtensorMap a[2], b[2];  // of logits a[1] is theirs
+    CUtensorMap low[2];      // A's second and third plane, if they are in a float32 matrix's place
     ProductArgs args[2];
     RecordArgs record;
 };
@@ -581,6 +616,16 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
         "%4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// The same of a group of columns of a low plane.
+__device__ __forceinline__ void tma_load_low(uint32_t dst, const CUtensorMap* map, int plane, int group, int y,
+                                             uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+        "%4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(0), "r"(plane), "r"(group), "r"(y), "r"(bar)
         : "memory");
 }
 
@@ -771,8 +816,8 @@ __device__ __forceinline__ float4 floats(uint4 v) {
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
 }
 
-// Logits: the largest and the sum of a thread's 128 columns, and the logits (where
-// the gradients' kernel finds those at the row's ids), or those at the ids alone.
+// Logits: the largest and the sum of a thread's 128 columns, the logits, and those at
+// the row's ids (where the gradients' kernel does not find them among the others).
 struct LogitTile {
     const LogitArgs& g;
     uint64_t list = 0;
@@ -784,7 +829,7 @@ struct LogitTile {
 
     __device__ __forceinline__ LogitTile(const ProductArgs& a, const Place& p, const CUtensorMap* z_map_)
         : g(a.logit), z_map(z_map_) {
-        if (!p.in || g.z) return;
+        if (!p.in || !g.at_ids) return;
         list = static_cast<uint64_t>(g.row[p.row]) * g.lists.top;
         next = first_id(g.lists.ids + list, g.lists.top, static_cast<int32_t>(g.v0 + p.n0));
         if (next < g.lists.top) next_id = g.lists.ids[list + next];
@@ -1023,8 +1068,9 @@ __device__ void write_record(const RecordArgs& a, uint32_t lane) {
 }
 
 // LOGITS: one product of two matrices along k, the softmax's statistics in its
-// epilogue.  Otherwise one or two with B turned, into the caller's memory.
-template <bool LOGITS, int kPlanes>
+// epilogue.  Otherwise one or two with B turned, into the caller's memory.  A and B
+// are of one plane each, of three each (six products a term), or A of three and B of one.
+template <bool LOGITS, int kPlanes, int kPlanesB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p, int products) {
     extern __shared__ char raw[];
@@ -1083,19 +1129,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                 const int k0 = static_cast<int>((lo + i) * kDeep);
                 for (int q = 0; q < kPlanes; ++q) {
                     if (round > 0 && !(ok = mbar_wait_here(bar(kEmptyBar + s), (round - 1) & 1))) break;
-                    const int plane = kPlanes == 1 ? 0 : plane_at(q);
+                    const int plane = kPlanesB == 1 ? 0 : plane_at(q);
                     const uint32_t full = full0 + 8 * s, to = base + s * kStageBytes;
-                    if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * kStageBytes);
-                    if (at) {
+                    const bool with_b = q < kPlanesB;  // one plane of B: in the first of A's stages
+                    if (rank == 0) mbar_expect_tx(bar(kFullBar + s), 2 * (with_b ? kStageBytes : kOperandBytes));
+                    if (kPlanes > kPlanesB && q > 0) {
+                        if (at) {
+                            tma_load_low(to, &p.low[which], q - 1, m0 / kDeep, k0, full);
+                            tma_load_low(to + kOperandBytes / 2, &p.low[which], q - 1, m0 / kDeep + 1, k0, full);
+                        } else {
+                            tma_load_low(to, &p.low[which], q - 1, k0 / kDeep, m0, full);
+                        }
+                    } else if (at) {
                         tma_load(to, ma, m0, k0, plane, full);
                         tma_load(to + kOperandBytes / 2, ma, m0 + 64, k0, plane, full);
                     } else {
                         tma_load(to, ma, k0, m0, plane, full);
                     }
-                    if (BT) {
+                    if (with_b && BT) {
                         tma_load(to + kOperandBytes, mb, n0, k0, plane, full);
                         tma_load(to + kOperandBytes + kOperandBytes / 2, mb, n0 + 64, k0, plane, full);
-                    } else {
+                    } else if (with_b) {
                         tma_load(to + kOperandBytes, mb, k0, n0, plane, full);
                     }
                     if (++s == kStages) s = 0, ++round;
@@ -1139,6 +1193,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
                         if (!(ok = full(s))) break;
                         multiply(s, s, j > i);
                         mma_commit(bar(kEmptyBar + s));
+                    } else if constexpr (kPlanesB == 1) {
+                        if (!(ok = full(s))) break;
+                        multiply(s, s, j > i);
+                        if (!(ok = full(s + 1))) break;
+                        multiply(s + 1, s, true);
+                        if (!(ok = full(s + 2))) break;
+                        multiply(s + 2, s, true);
+                        mma_commit(bar(kEmptyBar + s));
+                        mma_commit(bar(kEmptyBar + s + 1));
+                        mma_commit(bar(kEmptyBar + s + 2));
                     } else {
                         // planes 1, 0, 2: the first one's stage is free for the next block but one
                         // while the others are still read
@@ -1307,12 +1371,29 @@ EncodeFn encode_tiled() {
 cudaError_t make_map(const Operand& o, CUtensorMap* map) {
     const EncodeFn encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
-    const cuuint64_t row = 2 * o.m.pitch, plane = o.m.planes > 1 ? 2 * o.m.plane : row;
-    const cuuint64_t dims[3] = {o.cols, std::max<uint64_t>(1, o.rows), static_cast<cuuint64_t>(o.m.planes)};
+    const int planes = o.m.low ? 1 : o.m.planes;
+    const cuuint64_t row = 2 * o.m.pitch, plane = planes > 1 ? 2 * o.m.plane : row;
+    const cuuint64_t dims[3] = {o.cols, std::max<uint64_t>(1, o.rows), static_cast<cuuint64_t>(planes)};
     const cuuint64_t strides[2] = {row, plane};
     const cuuint32_t box[3] = {kDeep, static_cast<cuuint32_t>(o.turned ? kDeep : kHalf), 1}, steps[3] = {1, 1, 1};
     static_assert(kDeep == 64, "a block's rows are one swizzle wide, turned or not");
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, o.m.p, dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+// The same blocks of the low planes: 64 columns, plane, group of columns, row.  Columns
+// behind the last up to a group's end are zeros there.
+cudaError_t make_low_map(const Operand& o, CUtensorMap* map) {
+    const EncodeFn encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    static_assert(kLowGroup == kDeep, "a group of columns is a block's");
+    const cuuint64_t dims[4] = {kDeep, 2, (o.cols + kDeep - 1) / kDeep, std::max<uint64_t>(1, o.rows)};
+    const cuuint64_t strides[3] = {2 * kDeep, 4 * kDeep, 4 * o.m.pitch};
+    const cuuint32_t box[4] = {kDeep, 1, 1, static_cast<cuuint32_t>(o.turned ? kDeep : kHalf)}, steps[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, o.m.low, dims, strides, box, steps,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
@@ -1619,7 +1700,7 @@ void set_shape(ProductArgs& a) {
 uint32_t splits_of(const ProductArgs& a, const ProductArgs* second, uint64_t room) {
     const uint64_t pairs = kLossSms / 2, tiles = tall_of(a) * wide_of(a), blocks = blocks_of(a);
     if (tiles == 0 || tiles >= 8 * pairs) return 1;
-    const uint64_t passes = a.a.m.planes == 1 ? 1 : 6;
+    const uint64_t passes = a.a.m.planes == 1 ? 1 : a.b.m.planes == 1 ? 3 : 6;
     const uint64_t most = std::min(blocks * passes / 4, room / (tall_of(a) * kSide * a.out.part_pitch));
     const uint64_t other = second ? blocks_of(*second) * second->width : 0;
     const uint64_t others = second ? tall_of(*second) * wide_of(*second) * other : 0;
@@ -1670,18 +1751,20 @@ cudaError_t launch_grad(const JoinArgs& a0, cudaStream_t st) {
 
 using ProductKernel = void (*)(ProductParams, int);
 
-ProductKernel product_of(bool logits, int planes) {
-    if (planes == 1) return logits ? product_kernel<true, 1> : product_kernel<false, 1>;
-    return logits ? product_kernel<true, kMaxPlanes> : product_kernel<false, kMaxPlanes>;
+// By the planes of A and of B.
+ProductKernel product_of(bool logits, int a, int b) {
+    if (a == 1) return logits ? product_kernel<true, 1, 1> : product_kernel<false, 1, 1>;
+    if (b == 1) return product_kernel<false, kMaxPlanes, 1>;
+    return logits ? product_kernel<true, kMaxPlanes, kMaxPlanes> : product_kernel<false, kMaxPlanes, kMaxPlanes>;
 }
 
 cudaError_t prepare_products() {
-    for (const bool logits : {false, true})
-        for (const int planes : {1, kMaxPlanes}) {
-            const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(product_of(logits, planes)),
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
-            if (e != cudaSuccess) return e;
-        }
+    for (const ProductKernel f : {product_of(true, 1, 1), product_of(false, 1, 1), product_of(false, kMaxPlanes, 1),
+                                  product_of(true, kMaxPlanes, kMaxPlanes), product_of(false, kMaxPlanes, kMaxPlanes)}) {
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(f),
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kProductSmem);
+        if (e != cudaSuccess) return e;
+    }
     return cudaSuccess;
 }
 
@@ -1705,12 +1788,14 @@ cudaError_t launch_tiles(ProductParams& p, int n, bool logits, cudaStream_t st) 
         const ProductArgs& a = p.args[i];
         cudaError_t e = make_map(a.a, &p.a[i]);
         if (e == cudaSuccess) e = make_map(a.b, &p.b[i]);
+        if (e == cudaSuccess && a.a.m.low) e = make_low_map(a.a, &p.low[i]);
         if (e != cudaSuccess) return e;
         tiles += tall_of(a) * wide_of(a) * a.splits;
     }
     if (tiles > 0x7FFFFFFFu) return cudaErrorInvalidValue;  // 2^22 tokens and 2^24 entries make 2^30
     const uint32_t pairs = static_cast<uint32_t>(std::min<uint64_t>(std::max<uint64_t>(1, tiles), kLossSms / 2));
-    return launch(product_of(logits, p.args[0].a.m.planes), 2 * pairs, kProductThreads, kProductSmem, st, p, n);
+    const ProductKernel f = product_of(logits, p.args[0].a.m.planes, p.args[0].b.m.planes);
+    return launch(f, 2 * pairs, kProductThreads, kProductSmem, st, p, n);
 }
 
 }  // namespace

@@ -26,7 +26,11 @@ struct Planes {
     uint64_t plane;  // elements from one plane to the next
     uint64_t pitch;  // ... and from one row to the next
     int planes;
+    // null, or where the second and the third plane are instead: in the place of a float32
+    // matrix of this pitch, of every kLowGroup columns the second plane's and then the third's
+    uint16_t* low = nullptr;
 };
+constexpr uint32_t kLowGroup = 64;
 
 // What every token has, by its place among the n of the call: its list of ids
 // (ascending, kNoId behind the last) with their shares.
@@ -112,7 +116,8 @@ struct JoinArgs {
     uint32_t* bad;
     uint32_t *ticket, tickets;
     float* result;
-    // with gradients: the piece's logits and the place of every loss and logit gradient
+    // with gradients: the piece's logits (overwritten where they are g.low's place) and the place
+    // of every loss and logit gradient
     const float* z;
     uint64_t z_pitch;
     uint32_t vocab, columns;  // ..., of a CTA
@@ -135,6 +140,7 @@ struct Operand {
 struct LogitArgs {
     float c;
     uint32_t v0;         // the first column's vocabulary entry (stats and z start there)
+    bool at_ids;         // whether lists.logits is to be written
     Lists lists;
     const int32_t* row;  // the token at each place
     float2* stats;

@@ -575,10 +575,13 @@ typedef struct {
  *   [1] counted    tokens that count
  *   [2] nonfinite  1 if a counted token's loss is an infinity or NaN, else 0
  *   [3] factor     scale / max(1, counted) (AR_LOSS_MEAN), scale (AR_LOSS_SUM)
- * The gradients are the loss's.  They are computed from bf16 inputs with the
- * logits' gradient rounded to bf16 once (float32 inputs, and a few tokens: in
- * float32), summed in float32 and rounded to their type once.  Outputs may overlap neither each
- * other nor the inputs.  Errors: AR_ERR_INVALID_ARG for null or misaligned (to
+ * The gradients are the loss's.  Gradients in float32, and those of a call of up
+ * to 8 tokens, are sums of float32 logits' gradients (24 bits); for bf16 gradients of
+ * more tokens the logits' gradients are rounded to bf16 once, which leaves results
+ * within 2^-8 of the sum of their terms' magnitudes.  Sums are float32, rounded to
+ * the result's type once.  Float32 gradients of bf16 inputs take three times the
+ * products of bf16 ones, and a call for one gradient of each type makes the
+ * logits twice.  Outputs may overlap neither each other nor the inputs.  Errors: AR_ERR_INVALID_ARG for null or misaligned (to
  * their element) pointers, memory that is not the handle's device's or ends too
  * early, overlaps, strides below D, a gradient type that is neither, a scale
  * that is not a float32-normal positive number, gradients of a handle without. */

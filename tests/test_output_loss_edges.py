@@ -1,5 +1,6 @@
 """The output layer's losses where what is read could make them go wrong: NaN and
-infinities in the weights and hidden states, rows that are far apart.
+infinities in the weights and hidden states, rows that are far apart, float32
+gradients of bf16 inputs, sums over a million products.
 
 Tolerances as derived in test_output_loss.py, with the products of a logit that
 are not zero in the place of all of them (adding a zero rounds nothing), and on
@@ -14,9 +15,10 @@ import subprocess
 import pytest
 
 import collective_reduction_gb300 as ar
-from test_output_loss import U, bound_of_sum, half_step, make, run_ce, run_distill, targets_of, teacher
+from test_output_loss import U, bound_of_sum, half_step, make, run_ce, run_distill, targets_of, tdt, teacher
 
 gpu = pytest.mark.gpu
+HALF = 2.0 ** -8  # of a step of bf16, relative
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -84,6 +86,15 @@ class Tight:
             assert float((want.abs() > room)[want != 0].double().mean()) >= telling
             off = (got.double() - want).abs()
             assert bool((off <= room).all()), float((off / room).max())
+
+
+def sparse_states(n, d, cols, g, dtype):
+    """Hidden states that are zero but in `cols` columns, spread from the first to the last."""
+    import torch
+    at = torch.linspace(0, d - 1, cols).round().long().cuda()
+    x = torch.zeros(n, d, dtype=tdt(dtype), device="cuda")
+    x[:, at] = torch.randn(n, cols, generator=g, device="cuda").to(x.dtype)
+    return x, at
 
 
 # ------------------------------------------------- what is not a number
@@ -209,6 +220,60 @@ def test_weights_whose_rows_are_far_apart_are_refused(dtype):
         assert ar.lib().ar_output_cross_entropy(h._h, ctypes.byref(a), targets.data_ptr(), 8, -100, None) == 1
     h.check()
     assert bool((h.record == 0).all())
+
+
+# ------------------------------------------------- float32 gradients of bf16 inputs
+
+@gpu
+@pytest.mark.parametrize("n, d, v, piece", [(20, 64, 300, 0), (300, 515, 1003, 0), (900, 72, 700, 0), (900, 72, 700, 256),
+                                            (2400, 136, 257, 256)])
+@pytest.mark.parametrize("grads", [("hidden", "weight"), ("hidden",), ("weight",)])
+def test_float32_gradients_of_bf16_inputs_are_of_float32_logit_gradients(n, d, v, piece, grads):
+    import torch
+    x, w, g = make(n, d, v, "bfloat16", seed=n)
+    t = targets_of(n, v, g, 0.8)
+    h = ar.OutputLoss(n, d, v, piece=piece)
+    want = Tight(x, w, t, "bfloat16")
+    rec, losses, dx, dw = run_ce(h, x, w, t, "bfloat16", grads, "float32")
+    want.check(rec, losses, dx, dw)
+    old = {k: 0.25 for k in grads}
+    more = {"grad_" + k: torch.full(y.shape, old[k], device="cuda") for k, y in (("hidden", x), ("weight", w)) if k in grads}
+    rec = h.cross_entropy(x, w, t.cuda(), accumulate=True, **more)
+    h.check()
+    want.check(rec, None, more.get("grad_hidden"), more.get("grad_weight"), old=0.25)
+
+
+@gpu
+@pytest.mark.parametrize("wide", ["hidden", "weight"])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_one_gradient_in_float32_and_one_in_bf16(wide, piece):
+    import torch
+    n, d, v = 900, 72, 700
+    x, w, g = make(n, d, v, "bfloat16", seed=3)
+    t = targets_of(n, v, g, 0.8)
+    h = ar.OutputLoss(n, d, v, piece=piece)
+    dx = torch.full((n, d), 7.0, device="cuda", dtype=torch.float32 if wide == "hidden" else torch.bfloat16)
+    dw = torch.full((v, d), 7.0, device="cuda", dtype=torch.float32 if wide == "weight" else torch.bfloat16)
+    losses = torch.full((n,), 7.0, device="cuda")
+    rec = h.cross_entropy(x, w, t.cuda(), grad_hidden=dx, grad_weight=dw, losses=losses).clone()
+    h.check()
+    exact, rounded = Tight(x, w, t, "bfloat16"), Tight(x, w, t, "bfloat16", half=HALF)
+    exact.check(rec, losses, dx if wide == "hidden" else None, dw if wide == "weight" else None)
+    rounded.check(rec, losses, dx if wide != "hidden" else None, dw if wide != "weight" else None)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 2, 5, 8])
+@pytest.mark.parametrize("d, v", [(64, 300), (129, 517), (1024, 600), (8192, 520), (16384, 700), (65536, 560)])
+def test_a_few_tokens_gradients_are_rounded_once(n, d, v):
+    """Whatever the weights' size: 0.04 to 73 MB."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    x, _ = sparse_states(n, d, 16, g, "bfloat16")
+    w = (0.4 * torch.randn(v, d, generator=g, device="cuda")).bfloat16()
+    t = torch.randint(v, (n,), generator=g, device="cuda")
+    rec, losses, dx, dw = run_ce(ar.OutputLoss(n, d, v), x, w, t, "bfloat16")
+    Tight(x, w, t, "bfloat16", terms=16).check(rec, losses, dx, dw)
 
 
 # ------------------------------------------------- long sums
