@@ -538,6 +538,9 @@ ar_status ar_output_loss_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab
  * alone).  piece: tokens at a time (rounded up to 256; 0: as many as make 2^28
  * logits, 256 at least): the workspace is mostly 4 bytes for each of a piece's
  * logits and 2 (float32: 6) for each of up to four pieces'.  gradients: 0 for losses alone, with a small workspace.
+ * Weights whose rows do not start on 16 bytes, and float32 ones, are packed up to
+ * 1 GB (odd views of bf16 rows of whole 16 bytes: 256 MB) at a time; handles of up
+ * to 8 tokens need no place for it.
  * AR_ERR_INVALID_ARG: null out, D or V of 0, top < 0, unknown types.
  * AR_ERR_UNSUPPORTED: AR_INT32, more than 2^22 tokens, D > 2^16, V > 2^24, top >
  * 1024, more than 2^31 list entries.  AR_ERR_NOMEM, AR_ERR_CUDA. */

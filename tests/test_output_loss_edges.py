@@ -1,6 +1,6 @@
 """The output layer's losses where what is read could make them go wrong: NaN and
 infinities in the weights and hidden states, rows that are far apart, float32
-gradients of bf16 inputs, sums over a million products.
+gradients of bf16 inputs, sums over a million products, odd views of weights.
 
 Tolerances as derived in test_output_loss.py, with the products of a logit that
 are not zero in the place of all of them (adding a zero rounds nothing), and on
@@ -325,3 +325,45 @@ def test_bf16_gradient_of_hidden_states_over_a_million_entries():
     assert 16.0 < float(want.min()) and float(want.max()) < 32.0
     assert bool(((dx.double() - want).abs() <= 0.0625 + LONG_SUM * want).all())
     assert rec[0].item() == pytest.approx(16 * n * math.log(v), rel=1e-6)
+
+
+# ------------------------------------------------- memory
+
+def test_workspace_is_that_of_what_calls_use():
+    """Handles for a few tokens pack no weights, others of bf16 rows of whole 16 bytes
+    256 MB of them at most; the weights' gradient takes a sum of its own only where
+    bf16 is asked of runs of pieces."""
+    mb = 1 << 20
+    for dtype in ("bfloat16", "float32"):
+        few = ar.output_loss_layout(8, 4096, 128000, dtype, grads=False)["workspace_bytes"]
+        assert few < 256 * 4096 * 6 * 2 + 16 * mb  # a tile of states and of weights
+    scored = ar.output_loss_layout(16384, 4096, 128000, grads=False)["workspace_bytes"]
+    assert scored < 2 * 16384 * 4096 + 256 * mb + 8 * 16384 * 1000 + 8 * mb  # states, odd views, statistics
+    assert ar.output_loss_layout(37, 129, 2003, "float32")["workspace_bytes"] < 32 * mb
+    bf16, f32 = (ar.output_loss_layout(4096, 1024, 50001, t, piece=256)["workspace_bytes"] for t in ("bfloat16", "float32"))
+    wide = 50176  # logits of 256 tokens, gradients of 1024, hidden states, weights (packed: all), parts, the sum
+    assert bf16 < wide * (4 * 256 + 2 * 1024) + 4096 * 1024 * 2 + 256 * mb + 160 * mb + wide * 1024 * 4
+    assert f32 < wide * (4 * 256 + 6 * 1024) + 4096 * 1024 * 6 + wide * 1024 * 6 + 160 * mb
+
+
+@gpu
+@pytest.mark.parametrize("gtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("n", [3, 300])
+def test_odd_views_of_weights_are_packed_in_turn(n, gtype):
+    """328 MB of bf16 rows whose pitch is no multiple of 16 bytes."""
+    import torch
+    d, v = 2048, 80000
+    g = torch.Generator(device="cuda").manual_seed(35)
+    x, _ = sparse_states(n, d, 24, g, "bfloat16")
+    w = (0.3 * torch.randn(v, d, generator=g, device="cuda")).bfloat16()
+    odd = torch.full((v, d + 1), math.nan, dtype=torch.bfloat16, device="cuda")[:, 1:]
+    odd.copy_(w)
+    t = torch.randint(v, (n,), generator=g, device="cuda")
+    part = (1 << 28) // (2 * d) // 256 * 256  # entries at a time
+    t[:3] = torch.tensor([part - 1, part, v - 1], device="cuda")
+    h = ar.OutputLoss(n, d, v)
+    assert 0 < part < v
+    half = U if n <= 8 or gtype == "float32" else HALF
+    want = Tight(x, w, t, "bfloat16", terms=24, half=half)
+    want.check(*run_ce(h, x, odd, t, "bfloat16", gtype=gtype), telling=0.2)
+    want.check(*run_ce(h, x, odd, t, "bfloat16", (), gtype))
