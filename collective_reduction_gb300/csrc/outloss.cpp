@@ -268,24 +268,34 @@ struct Call {
     }
 
     // Whether the call is on few enough tokens for the kernels that read the weights
-    // as they are, of eight tokens at a time.  Losses alone / with gradients, us, those
-    // kernels against tiles:
-    //                       float32 W   n = 8             bf16 W   n = 2           n = 4            n = 8
-    //   4096 x 128000       2097 MB   658 1513 : 1798 6272   257 720 : 287 1843   291 913 : 225 1789   569 1328 : 229 1783
-    //   1023 x 32003         131 MB    64  214 :  142  656    27 120 :  66  363    39 150 :  65  357    50  174 :  64  356
-    //   640 x 10007           26 MB    23   62 :   49  156    17  43 :  23   53    17  51 :  22   51    31   70 :  21   51
-    //   192 x 4001             3 MB    16   34 :   25   49    15  25 :  17   33    14  27 :  17   33    16   35 :  17   33
-    // The tiles' float32 pays for packing the weights in planes, their odd bf16 rows for
-    // packing them at all.  More than eight tokens of float32 are taken in groups.
-    // Where both take as long these kernels do it: they keep the logits' gradient in
-    // float32, where a handful of bf16 roundings do not average out.
+    // as they are, of eight tokens at a time.  Losses alone / with gradients in a captured
+    // graph, us, those kernels against tiles:
+    //   bf16 W                n = 2              n = 4              n = 5              n = 8
+    //   4096 x 128000   208  730 : 304 1840  298  997 : 303 1843  485 1320 : 297 1834  545 1400 : 291 1841
+    //   2048 x 50000     56  189 :  84  401   76  253 :  72  387  125  349 :  74  389  139  374 :  69  389
+    //   1024 x 32000     23  104 :  35  149   30  125 :  31  147   47  160 :  31  148   51  167 :  31  150
+    //   640 x 10007      15   43 :  21   66   18   54 :  23   66   27   68 :  23   66   29   72 :  21   66
+    //   192 x 4001       12   25 :  17   31   14   29 :  17   31   15   33 :  17   33   17   35 :  17   33
+    //   1023 x 32003     27  121 :  61  376   39  153 :  60  375   45  174 :  56  372   49  181 :  54  373
+    //   float32 W             n = 8              n = 9              n = 16             n = 24
+    //   4096 x 128000   653 1537 :1933 6525 1023 2930 :1934 6536 1303 3853 :1933 6540 1972 6185 :1934 6558
+    //   2048 x 50000    146  378 : 358  848  223  688 : 358  849  286  909 : 359  848  426 1441 : 359  851
+    //   1024 x 32000     52  190 : 135  309   87  334 : 135  309  110  427 : 135  310  162  664 : 136  312
+    //   1024 x 4096      25   51 :  49   84   35   99 :  50   85   41  107 :  50   86   58  169 :  51   86
+    //   192 x 4001       17   35 :  23   39   23   64 :  23   39   25   66 :  23   39   33   98 :  23   40
+    // The tiles' float32 pays for packing the weights in planes, twice (for the logits and
+    // for the gradient of hidden states) where they are packed in turn; their odd bf16 rows
+    // for packing them at all.  More than eight tokens of float32 are taken in groups, each
+    // of which reads the weights and adds to their gradient.
     bool few() const {
         const uint64_t bytes = static_cast<uint64_t>(vocab) * width * esize(h->dtype), mb = 1u << 20;
         if (n == 0) return false;
-        if (h->dtype == AR_FLOAT32) return n <= 8 || (n <= 16 && bytes >= 8 * mb) || (n <= 24 && grads && bytes >= 64 * mb);
-        if (!weight_as_is()) return n <= 8;
-        if (n <= 2) return true;
-        return n <= 4 ? grads || bytes < 64 * mb : n <= 8 && (bytes >= 64 * mb ? grads : bytes < 8 * mb);
+        if (h->dtype == AR_FLOAT32) {
+            if (n <= 8) return true;
+            return grads ? n <= 24 && entries() < vocab : n <= 16 && bytes >= 8 * mb;
+        }
+        if (n <= 2 || (n <= 8 && (!weight_as_is() || bytes < 4 * mb))) return true;
+        return n <= 4 ? grads || bytes < 128 * mb : n <= 8 && grads && bytes >= 128 * mb;
     }
 
     ar::FewArgs few_args(uint64_t r) const {

@@ -367,3 +367,26 @@ def test_odd_views_of_weights_are_packed_in_turn(n, gtype):
     want = Tight(x, w, t, "bfloat16", terms=24, half=half)
     want.check(*run_ce(h, x, odd, t, "bfloat16", gtype=gtype), telling=0.2)
     want.check(*run_ce(h, x, odd, t, "bfloat16", (), gtype))
+
+
+@gpu
+@pytest.mark.parametrize("n, keep", [(12, 1.0), (21, 0.6), (24, 1.0), (25, 1.0), (40, 1.0), (40, 0.6)])
+def test_weights_packed_in_turn_element_by_element(n, keep):
+    """Float32 rows of 65536: a part of 2560 entries is packed at a time, or up to 24
+    tokens go in groups that read them as they are.  The states' 24 values a row
+    leave logits that are off by 1e-4 at most."""
+    import torch
+    d, v = 65536, 2900
+    g = torch.Generator(device="cuda").manual_seed(33)
+    x, at = sparse_states(n, d, 24, g, "float32")
+    w = torch.randn(v, d, generator=g, device="cuda") * 0.4
+    t = torch.randint(v, (n,), generator=g, device="cuda")
+    t[torch.rand(n, generator=g, device="cuda") >= keep] = -100
+    t[:4] = torch.tensor([0, 2559, 2560, v - 1], device="cuda")
+    h = ar.OutputLoss(n, d, v, "float32")
+    want = Tight(x, w, t, "float32", terms=24)
+    rec, losses, dx, dw = run_ce(h, x, w, t, "float32")
+    want.check(rec, losses, dx, dw)
+    want.check(*run_ce(h, x, w, t, "float32", ()))
+    dx0 = torch.ones_like(dx)
+    want.check(h.cross_entropy(x, w, t, grad_hidden=dx0, accumulate=True), None, dx0, old=1.0)
