@@ -1,6 +1,7 @@
-"""The output layer's losses where what is read could make them go wrong: NaN and
-infinities in the weights and hidden states, rows that are far apart, float32
-gradients of bf16 inputs, sums over a million products, odd views of weights.
+"""The output layer's losses where what is read, asked for or summed could make
+them go wrong: NaN and infinities in the weights and hidden states, rows that are
+far apart, float32 gradients of bf16 inputs, sums over a million products, odd
+views of weights, parts of them in turn, elements behind 2^31.
 
 Tolerances as derived in test_output_loss.py, with the products of a logit that
 are not zero in the place of all of them (adding a zero rounds nothing), and on
@@ -15,7 +16,8 @@ import subprocess
 import pytest
 
 import collective_reduction_gb300 as ar
-from test_output_loss import U, bound_of_sum, half_step, make, run_ce, run_distill, targets_of, tdt, teacher
+from test_output_loss import (Expected, U, bound_of_sum, half_step, make, run_ce, run_distill, targets_of, tdt, teacher,
+                              teacher_lists)
 
 gpu = pytest.mark.gpu
 HALF = 2.0 ** -8  # of a step of bf16, relative
@@ -177,6 +179,26 @@ def test_a_nan_hidden_state_is_its_tokens_alone(dtype, n):
     assert bool(dx[1].isnan().all()) and bool(dx[others].isfinite().all()) and bool(dw.isnan().all())
 
 
+# ------------------------------------------------- what counts
+
+@gpu
+@pytest.mark.parametrize("n", [5, 300])
+@pytest.mark.parametrize("ignore, size", [(7, 4), (7, 8), (-1, 4), (0, 8), (1 << 40, 8)])
+def test_another_ignore_index(n, ignore, size):
+    import torch
+    x, w, g = make(n, 64, 300, "bfloat16", seed=n)
+    t = targets_of(n, 300, g)
+    t[::3] = ignore
+    h = ar.OutputLoss(n, 64, 300)
+    rec, losses, dx, dw = run_ce(h, x, w, t if size == 8 else t.int(), "bfloat16", ignore_index=ignore)
+    Tight(x, w, t, "bfloat16", half=HALF, ignore=ignore).check(rec, losses, dx, dw)
+    assert bool((losses[(t == ignore).cuda()] == 0).all())
+    if ignore >= 0:  # and -100 is a target like others then: outside the vocabulary
+        t[1] = -100
+        rec, losses, _, _ = run_ce(h, x, w, t if size == 8 else t.int(), "bfloat16", ignore_index=ignore)
+        assert rec[2].item() == 1.0 and math.isnan(losses[1].item())
+
+
 # ------------------------------------------------- rows that are far apart
 
 FAR = [(4, 1 << 22, 1 << 40), (2, 1 << 23, 1 << 40), (2, 1 << 24, 1 << 39), (8, 1 << 21, 1 << 40), (4, 3, (1 << 63) - 1),
@@ -274,6 +296,69 @@ def test_a_few_tokens_gradients_are_rounded_once(n, d, v):
     t = torch.randint(v, (n,), generator=g, device="cuda")
     rec, losses, dx, dw = run_ce(ar.OutputLoss(n, d, v), x, w, t, "bfloat16")
     Tight(x, w, t, "bfloat16", terms=16).check(rec, losses, dx, dw)
+
+
+@gpu
+@pytest.mark.parametrize("n, d, v, k", [(6, 1024, 3000, 5), (300, 72, 2003, 33), (900, 40, 300, 300)])
+def test_float32_gradients_of_a_distillation(n, d, v, k):
+    """Entries of one id add up, some are absent; twice the same bits, also from a graph
+    that is given new inputs."""
+    import torch
+    x, w, g = make(n, d, v, "bfloat16", seed=k)
+    h = ar.OutputLoss(n, d, v, top=k, piece=512)
+    dx, dw, losses = (torch.zeros(s, device="cuda") for s in ((n, d), (v, d), (n,)))
+    ids, logits = (y.cuda() for y in teacher(n, k, v, g, "float32", 0.3, twice=True))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rec = h.distill(x, w, ids, logits, temperature=2.0, grad_hidden=dx, grad_weight=dw, losses=losses)
+    for seed in (41, 42):
+        ids2, logits2 = teacher(n, k, v, g.manual_seed(seed), "float32", 0.3, twice=True)
+        ids.copy_(ids2)
+        logits.copy_(logits2)
+        graph.replay()
+        h.check()
+        lists, shares, spread = teacher_lists(ids2, logits2, 2.0)
+        want = Expected(x, w, lists, shares, 2.0, dtype="float32", spread=spread)
+        want.check(rec, losses, dx, dw)
+        assert bool((want.dw.abs() > want.dw_tol)[want.dw != 0].double().mean() > 0.5)
+        first = [y.clone() for y in (rec, losses, dx, dw)]
+        h.distill(x, w, ids, logits, temperature=2.0, grad_hidden=dx, grad_weight=dw, losses=losses)
+        assert all(torch.equal(a, b) for a, b in zip(first, (rec, losses, dx, dw)))
+
+
+@gpu
+@pytest.mark.parametrize("n", [6, 70, 700])
+def test_float32_gradients_of_a_target_outside_the_vocabulary(n):
+    import torch
+    x, w, g = make(n, 1024, 3001, "bfloat16", seed=n)
+    t = targets_of(n, 3001, g)
+    t[4] = 3001
+    rec, losses, dx, dw = run_ce(ar.OutputLoss(n, 1024, 3001, piece=256), x, w, t, "bfloat16", gtype="float32")
+    others = torch.arange(n, device="cuda") != 4
+    assert rec[2].item() == 1.0 and losses.isnan().nonzero().tolist() == [[4]]
+    assert bool(dx[4].isnan().all()) and bool(dx[others].isfinite().all()) and bool(dw.isnan().all())
+
+
+@gpu
+def test_float32_and_bf16_gradients_on_two_streams_are_as_alone():
+    import torch
+    n, d, v = 700, 264, 3000
+    x, w, g = make(n, d, v, "bfloat16", seed=6)
+    t = targets_of(n, v, g, 0.8)
+    cases = []
+    for gtype in ("float32", "bfloat16"):
+        h = ar.OutputLoss(n, d, v)
+        alone = run_ce(h, x, w, t, "bfloat16", gtype=gtype)
+        cases.append((h, alone, torch.cuda.Stream(), [torch.zeros_like(a) for a in alone[2:]]))
+    t = t.cuda()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for h, _, stream, (dx, dw) in cases:
+            h.cross_entropy(x, w, t, grad_hidden=dx, grad_weight=dw, stream=stream)
+    torch.cuda.synchronize()
+    for h, (rec, _, dx0, dw0), _, (dx, dw) in cases:
+        h.check()
+        assert torch.equal(h.record, rec) and torch.equal(dx, dx0) and torch.equal(dw, dw0)
 
 
 # ------------------------------------------------- long sums
@@ -390,3 +475,47 @@ def test_weights_packed_in_turn_element_by_element(n, keep):
     want.check(*run_ce(h, x, w, t, "float32", ()))
     dx0 = torch.ones_like(dx)
     want.check(h.cross_entropy(x, w, t, grad_hidden=dx0, accumulate=True), None, dx0, old=1.0)
+
+
+@gpu
+@pytest.mark.parametrize("n", [3, 30])
+def test_rows_around_element_2_to_the_31(n):
+    """Losses, the hidden states' gradient and every row of the weights', with targets
+    on both sides of the boundary and at both ends."""
+    import torch
+    d, v, step = 8192, 270000, 30000
+    edge = (1 << 31) // d
+    g = torch.Generator(device="cuda").manual_seed(34)
+    x, at = sparse_states(n, d, 16, g, "bfloat16")
+    w = torch.empty(v, d, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, v, step):
+        w[a:a + step] = torch.randn(step, d, generator=g, device="cuda")
+    t = torch.randint(v, (n,), generator=g, device="cuda")
+    t[:3] = torch.tensor([edge - 1, edge, v - 1], device="cuda")
+    if n > 3:
+        t[3] = 0
+    dw, dx, losses = torch.full_like(w, 7.0), torch.empty_like(x), torch.empty(n, device="cuda")
+    h = ar.OutputLoss(n, d, v)
+    rec = h.cross_entropy(x, w, t, reduction="sum", grad_hidden=dx, grad_weight=dw, losses=losses)
+    h.check()
+    # the definition with the columns that are not zero, but for the states' gradient
+    half = U if n <= 8 else HALF
+    small = Tight(x[:, at], w[:, at], t, "bfloat16", half=half, reduction="sum")
+    small.check(rec, losses, None, dw[:, at])
+    rest = torch.ones(d, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    z = x[:, at].double() @ w[:, at].double().t()
+    q = torch.softmax(z, 1)
+    gz = q.scatter_add(1, t[:, None], torch.full((n, 1), -1.0, dtype=torch.float64, device="cuda"))
+    e = bound_of_sum(16, "bfloat16") * float((x[:, at].double().abs() @ w[:, at].double().abs().t()).max())
+    dq = 2 * e + 8 * U * (float(z.abs().max()) + 2) + 2 * U * (v + 4) + 16 * U
+    off = q * dq + gz.abs() * (half + bound_of_sum(v, "bfloat16") + 4 * U)
+    want, room = (torch.zeros(n, d, dtype=torch.float64, device="cuda") for _ in range(2))
+    for a in range(0, v, step):
+        assert bool((dw[a:a + step][:, rest] == 0).all())
+        part = w[a:a + step].double()
+        want += gz[:, a:a + step] @ part
+        room += off[:, a:a + step] @ part.abs()
+    room += HALF * (want.abs() + room) + 1e-38
+    assert float((want.abs() > room).double().mean()) > 0.5
+    assert bool(((dx.double() - want).abs() <= room).all())
