@@ -605,20 +605,21 @@ def _rows_of(t, what, rows, width, dtypes):
 
 class OutputLoss:
     """The losses of an output layer, logits = hidden @ weight.T, for up to
-    `tokens` tokens, without an array of tokens x vocab; with the gradients of
+    `tokens` tokens, in pieces of up to 2^28 logits; with the gradients of
     hidden states and weights.  hidden and weight are bfloat16 or float32
     (`dtype`), as (n, hidden) and (vocab, hidden) tensors with any row stride.
     `top`: entries of a teacher's list at most; `piece`: tokens worked
-    on at a time (0: chosen); `grads=False`: losses alone, little workspace.
+    on at a time (0: chosen); `grads=False`: losses alone, little workspace
+    (output_loss_layout tells how much, and of what the other handles hold).
 
     Both calls return the record, four floats on the device: loss, tokens
     counted, nonfinite, factor.  Without `result` that is `self.record`, which
     the next call overwrites.  loss = factor * sum of the counted tokens' losses,
     factor = scale / counted (reduction "mean") or scale ("sum"); the gradients are
-    the loss's, in the dtype or float32 (of bfloat16 inputs: bfloat16 gradients of
-    more than 8 tokens come from logits' gradients rounded to bfloat16, float32 ones
-    from float32's and take up to three times as long), written or (accumulate) added to what is
-    there.  `losses` (float32, n) takes every token's loss, 0 for tokens that do
+    the loss's, in the dtype or float32, written or (accumulate) added to what is
+    there.  Of bfloat16 inputs, bfloat16 gradients of more than 8 tokens come from
+    logits' gradients rounded to bfloat16; float32 ones from float32's, in about
+    twice the time.  `losses` (float32, n) takes every token's loss, 0 for tokens that do
     not count.  The written gradients' autograd versions are raised (a replay of
     a captured call does not).  Calls on one handle share its workspace: order
     them on one stream.  A CUDA graph that captured calls does not keep the

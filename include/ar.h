@@ -495,8 +495,10 @@ ar_status ar_adamw_step_counted(ar_adamw_t h, const ar_adamw_params* params, uin
  * of each token's softmax over the V logits, and the gradients of X and W.  The
  * pages take gradients as given; these calls have no counterpart on them.
  *
- * No n x V array is made: logits and their gradients are worked on in pieces
- * of the tokens that fit the handle's workspace (losses alone store no logits).  Both losses are, for a
+ * Losses alone store no logits.  With gradients logits are worked on in pieces of
+ * the tokens, of up to 2^28 of them in float32, and their gradients are kept for up
+ * to four pieces (in bf16; float32 inputs: as three bf16 values): a call with fewer
+ * logits holds them all, one with more never more than that.  Both losses are, for a
  * token with teacher shares p over a short list of ids at temperature t,
  *   loss = t^2 [ sum_k p_k log p_k - sum_k p_k z_k / t + log sum_v exp(z_v / t) ]
  * whose gradient by z is t (softmax(z / t) - p); cross entropy has one id of
@@ -536,8 +538,13 @@ ar_status ar_output_loss_layout(uint64_t tokens, uint64_t hidden, uint64_t vocab
 /* A handle for up to `tokens` tokens of hidden size D over V vocabulary entries,
  * X and W of `dtype`.  top: entries of a teacher's list at most (0: cross entropy
  * alone).  piece: tokens at a time (rounded up to 256; 0: as many as make 2^28
- * logits, 256 at least): the workspace is mostly 4 bytes for each of a piece's
- * logits and 2 (float32: 6) for each of up to four pieces'.  gradients: 0 for losses alone, with a small workspace.
+ * logits, 256 at least).  gradients: 0 for losses alone, with a small workspace.
+ * The workspace with gradients is 4 bytes for each of a piece's logits, 2 (float32:
+ * 6) for each of up to four pieces', a copy of the hidden states, parts of the
+ * gradients' sums (4 bytes for each value of four pieces' states at least), and,
+ * for bf16 weights' gradients of more tokens than four pieces, 4 bytes for each of
+ * the weights.  Where that is too much, call it for some of the tokens at a time:
+ * AR_LOSS_SUM, accumulated in float32, adds up to the same gradients.
  * Weights whose rows do not start on 16 bytes, and float32 ones, are packed up to
  * 1 GB (odd views of bf16 rows of whole 16 bytes: 256 MB) at a time; handles of up
  * to 8 tokens need no place for it.
