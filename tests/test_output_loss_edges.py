@@ -199,6 +199,28 @@ def test_another_ignore_index(n, ignore, size):
         assert rec[2].item() == 1.0 and math.isnan(losses[1].item())
 
 
+@gpu
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("n, d, v", [(1, 64, 300), (7, 129, 2003), (12, 1100, 2003), (40, 33, 65), (513, 96, 2003),
+                                     (2000, 40, 257)])
+@pytest.mark.parametrize("keep", [1.0, 0.5])
+def test_handles_for_losses_alone(n, d, v, dtype, keep):
+    """Also for fewer tokens than the handle's, and with a teacher's lists."""
+    import torch
+    x, w, g = make(n, d, v, dtype, seed=n + d)
+    t = targets_of(n, v, g, keep)
+    t[0] = 1
+    h = ar.OutputLoss(n + 300, d, v, dtype, top=5, grads=False)
+    assert h.info()["pieces"] == 1
+    Tight(x, w, t, dtype).check(*run_ce(h, x, w, t, dtype, ()))
+    ids, logits = teacher(n, 5, v, g, dtype, 1.0 - keep, twice=True)
+    losses = torch.full((n,), 7.0, device="cuda")
+    rec = h.distill(x, w, ids.cuda(), logits.cuda(), temperature=2.0, losses=losses)
+    h.check()
+    lists, shares, spread = teacher_lists(ids, logits, 2.0)
+    Expected(x, w, lists, shares, 2.0, dtype=dtype, spread=spread).check(rec, losses)
+
+
 # ------------------------------------------------- rows that are far apart
 
 FAR = [(4, 1 << 22, 1 << 40), (2, 1 << 23, 1 << 40), (2, 1 << 24, 1 << 39), (8, 1 << 21, 1 << 40), (4, 3, (1 << 63) - 1),
