@@ -37,10 +37,10 @@ constexpr uint64_t kPackBytes = 1ull << 30, kStrayBytes = 1ull << 28;
 // and float32 results, and for bf16 results (whose rounding is 2^-8).  The tensor
 // cores cut every sum off, always downwards, so the error grows with the run: with 1
 // and 8 (3, where A has three planes) losses and float32 gradients are as far from 64
-// bits as float32 products are (2 to 7e-7 relative); with 2 and 16 they are twice as far, and 515 tokens of
-// 515 x 10007 float32 take 154 us instead of 173, 4096 of 2048 x 50001 bf16 1592
-// instead of 1633; with 4 for bf16 1739.  Sums of a million equal terms for a bf16
-// result were 0.65% low (1.5 of its steps) in one run; in runs of 256 blocks they are
+// bits as float32 products are (2 to 7e-7 relative); with 2 and 16 they are twice as
+// far, and 515 tokens of 515 x 10007 float32 take 154 us instead of 173, 4096 of
+// 2048 x 50001 bf16 1592 instead of 1633; with 4 for bf16 1739.  Sums of a million
+// terms of one sign for a bf16 result were 0.65% low (1.5 of its steps) in one run; in runs of 256 blocks they are
 // 0.01% low.  8192 tokens of 4096 x 128000 take 17.5 ms so and 17.3 in one run, other
 // cases as long: from 128 to 512 blocks there is no difference beyond the noise.
 constexpr uint32_t kFloatRun = 1, kExactRun = 8, kPlanesRun = 3, kLongRun = 256;
